@@ -1,0 +1,743 @@
+// kvq_paged_decode.cuh — attention over the E4M3 pages for few query rows per
+// kv head (kvq_paged_attention): a split of the token axis over warps.
+//
+// Mathematics.  With key codes a_t, value codes c_t and the page scales sk,
+// sv of token t, in log2 units (kappa = softmax scale * log2 e):
+//   s_t = kappa * sk_t * (q . a_t) + log2(sv_t)
+//   m   = max s_t,  w_t = 2^(s_t - m) <= 1
+//   out = (sum_t w_t c_t) / (sum_t w_t / sv_t)
+// The value scale rides in the exponent, so it costs one FMA a score and the
+// codes themselves are the matrix operands: E4M3 converts to fp16 exactly,
+// and w_t in fp16 is full precision for the tokens that carry the result,
+// whatever their pages' scales are.  Weights, sums and outputs accumulate in
+// fp32; the fp16 rounding of w_t is the only one besides the output's.
+//
+// Split.  Every warp streams a contiguous, equal range of units of UT = 32
+// (D = 128) or 64 (D = 64) tokens: 4 KB of key and 4 KB of value codes that
+// TMA copies into one of its NS stages, with the 128- or 64-byte swizzle that
+// makes the fragment reads free of bank conflicts.  A unit that belongs to
+// several pages is several boxes.  A warp's last item stays in shared memory
+// and the CTA joins its warps' shares; an item that crosses CTAs is joined by
+// the CTA that arrives last, in CTA order, so results do not depend on timing.
+//
+// Tensor-core operands (mma.sync m16n8k16, fp16 in, fp32 out).  Scores:
+// A = 16 tokens x 16 channels of codes, B = 8 query rows.  Lane (g, t) reads
+// 16-byte chunks of tokens g and g + 8; a 4-byte word gives the four
+// channels of one k-step, and the query registers hold the same channels, so
+// no data moves between lanes.  Values: A = 16 channels x 16 tokens; a byte
+// permute pairs the codes of two tokens.  The scores' C fragment becomes the
+// weights' B fragment by an 8x8 transpose (movmatrix).
+#pragma once
+
+#include <atomic>
+#include <type_traits>
+
+#include "kvq_decode_mma.cuh"
+#include "kvq_paged.cuh"
+
+namespace kvq {
+
+__device__ __forceinline__ uint32_t movmatrix(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+
+__device__ __forceinline__ float fast_log2(float x) {
+  float y;
+  asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+template <int D, int NT>
+struct PagedCfg {
+  static constexpr int NW = kPagedWarps;
+  static constexpr int UT = paged_unit_tokens(D);  // tokens of a unit
+  static constexpr int GR = UT / 16;               // 16-token granules of a unit
+  static constexpr int NS = 3;                     // stages of a warp
+  static constexpr int RG = 8 * NT;                // query rows of a group
+  static constexpr int STAGE = 8192;
+  static constexpr int PART = RG * (D + 2);        // floats of a partial: O, then m, l
+  static constexpr int RING = 64;                  // granule records of a warp
+  static constexpr int OFF_BAR = NW * NS * STAGE;
+  static constexpr int OFF_RING = OFF_BAR + round_up(NW * NS * 8, 128);
+  static constexpr int OFF_SEG = OFF_RING + NW * RING * 16;
+  static constexpr int OFF_CUM = OFF_SEG + 1024;
+  static constexpr int smem(int batch) { return OFF_CUM + 4 * (batch + 1); }
+  static_assert(PART * 4 <= NS * STAGE, "a warp's partial fits in its stages");
+};
+
+// An item's place: request, kv head, row group, and its units.
+struct PagedItem {
+  int b, h, grp;
+  int u0, nu;      // first global unit, units
+  int tok0;        // first token of unit 0 of the item
+  int q0, rows;    // first row of q, query rows of the group
+  int seq;
+  int n;           // new tokens of the request
+};
+
+// A warp's part of an item, for the join.
+struct PagedSeg {
+  int u0, u1;      // the item's global units (u0 < 0: no segment)
+  int b, h, grp;
+  int where;       // 0: the warp's global slot, 1: its stages
+};
+
+template <int D, int NT, bool BF16>
+__global__ void __launch_bounds__(PagedCfg<D, NT>::NW * 32, 1)
+    paged_decode_kernel(const __grid_constant__ PagedAttnParams p,
+                        const __grid_constant__ CUtensorMap kmap,
+                        const __grid_constant__ CUtensorMap vmap) {
+  using C = PagedCfg<D, NT>;
+  constexpr int NW = C::NW, UT = C::UT, GR = C::GR, NS = C::NS, RG = C::RG, PART = C::PART;
+  constexpr int KC = D / 64;   // 16-byte chunks of a key row a lane reads
+  constexpr int KS = D / 16;   // k-steps of the scores
+  constexpr int MT = D / 16;   // m-tiles of the values
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int g = lane >> 2, t = lane & 3;
+  uint8_t* stages = smem + warp * NS * C::STAGE;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR) + warp * NS;
+  float4* ring = reinterpret_cast<float4*>(smem + C::OFF_RING) + warp * C::RING;
+  PagedSeg* segs = reinterpret_cast<PagedSeg*>(smem + C::OFF_SEG);  // [NW][2]
+  int* flags = reinterpret_cast<int*>(smem + C::OFF_SEG + NW * 2 * sizeof(PagedSeg));
+  int* cum = reinterpret_cast<int*>(smem + C::OFF_CUM);
+  if (lane == 0) {
+    for (int s = 0; s < NS; ++s) mbar_init(&bars[s], 1);
+    fence_barrier_init();
+    segs[2 * warp].u0 = segs[2 * warp + 1].u0 = -1;
+  }
+  grid_dep_wait();
+
+  // ---- units of every request: prefix sum over the batch -------------------
+  auto groups_of = [&](const PagedReq& r) { return (r.n * p.R + RG - 1) / RG; };
+  auto units_of = [&](const PagedReq& r) {
+    const int nu = (r.seq + UT - 1) / UT - first_seen(p, r) / UT;
+    return nu > 1 ? nu : 1;  // an empty request still has its zero rows written
+  };
+  auto load_req = [&](int b, int* bad) {
+    PagedReq r = paged_req(p, b, bad);
+    const int rows = r.n * p.R;
+    if (rows < p.row_min || rows > p.row_max) r.n = 0;
+    return r;
+  };
+  {
+    const int per = (p.batch + NW * 32 - 1) / (NW * 32);
+    const int b0 = min(tid * per, p.batch), b1 = min(b0 + per, p.batch);
+    int mine = 0;
+    bool any_bad = false;
+    for (int b = b0; b < b1; ++b) {
+      int bad;
+      const PagedReq r = load_req(b, &bad);
+      any_bad |= bad != 0;
+      if (r.n > 0) mine += p.H * groups_of(r) * units_of(r);
+    }
+    int incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int x = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += x;
+    }
+    if (lane == 31) flags[warp] = incl;
+    __syncthreads();
+    int base = 0;
+    for (int w = 0; w < warp; ++w) base += flags[w];
+    int at = base + incl - mine;
+    for (int b = b0; b < b1; ++b) {
+      int bad;
+      const PagedReq r = load_req(b, &bad);
+      cum[b] = at;
+      if (r.n > 0) at += p.H * groups_of(r) * units_of(r);
+    }
+    if (b1 == p.batch && b0 < b1) cum[p.batch] = at;
+    if (any_bad && blockIdx.x == 0) set_err(p.err, KVQ_PAGED_ERR_LENGTH);
+    __syncthreads();
+  }
+  grid_dep_launch();
+  const int U = cum[p.batch];
+  if (U == 0) return;
+  // warps in use: at least one unit each, packed into the first CTAs
+  const int W = min(p.n_warps, U);
+  const int gw = blockIdx.x * NW + warp;
+  auto first_of = [&](int w) { return static_cast<int>(static_cast<long long>(w) * U / W); };
+  if (static_cast<int>(blockIdx.x) * NW >= W) return;
+  const int ua = gw < W ? first_of(gw) : U, ub = gw < W ? first_of(gw + 1) : U;
+
+  auto find_item = [&](int u, PagedItem& it) {
+    int lo = 0, hi = p.batch;  // the last request with cum[b] <= u
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (cum[mid] <= u) lo = mid;
+      else hi = mid;
+    }
+    int bad;
+    const PagedReq r = load_req(lo, &bad);
+    const int G = groups_of(r), nu = units_of(r);
+    const int i = (u - cum[lo]) / nu;
+    it.b = lo;
+    it.h = i / G;
+    it.grp = i - it.h * G;
+    it.u0 = cum[lo] + i * nu;
+    it.nu = nu;
+    it.tok0 = first_seen(p, r) / UT * UT;
+    it.q0 = r.q0;
+    it.rows = min(RG, r.n * p.R - it.grp * RG);
+    it.seq = r.seq;
+    it.n = r.n;
+  };
+  // Tokens [lo, hi) that any row of the group sees.
+  auto seen_lo = [&](const PagedItem& it) {
+    if (p.window == 0) return 0;
+    const int lo = it.seq - it.n + it.grp * RG / p.R + 1 - p.window;
+    return lo > 0 ? lo : 0;
+  };
+  auto seen_hi = [&](const PagedItem& it) {
+    return max(0, it.seq - it.n + (it.grp * RG + it.rows - 1) / p.R + 1);
+  };
+
+  // ---- the load cursor, NS units ahead -------------------------------------
+  PagedItem li;
+  int lu = ua, lend = ua;      // next unit to load, end of its item
+  int gbase = 0, grec = 0;     // granule records: read so far of this batch, ring position
+  int llo = 0, lhi = 0;
+  int my_page = -1;            // lane's granule of the current batch of 32
+  // Refills the lanes' granule records from unit lu of item li on.
+  auto fetch_granules = [&]() {
+    const int tok = li.tok0 + (lu - li.u0) * UT + lane * 16;
+    my_page = -1;
+    float ks = 0.f, lv = 0.f, iv = 0.f;
+    // (records beyond this warp's range or the item are never used)
+    if (tok < lhi && tok + 16 > llo && lu + lane / GR < min(lend, ub)) {
+      const int page = p.table[static_cast<size_t>(li.b) * p.max_pages + (tok >> p.lg_ps)];
+      if (page >= 0 && page < p.n_pages) {
+        my_page = page;
+        const size_t at = static_cast<size_t>(page) * p.H + li.h;
+        ks = p.k_scale[at];
+        const float vs = p.v_scale[at];
+        lv = fast_log2(vs);
+        iv = 1.f / vs;
+      } else {
+        set_err(p.err, KVQ_PAGED_ERR_BAD_PAGE);
+      }
+    }
+    ring[(grec + lane) & (C::RING - 1)] = make_float4(ks, lv, iv, my_page >= 0 ? 1.f : 0.f);
+    gbase = 0;
+  };
+  auto issue = [&](int s) {
+    if (lu == lend) {
+      find_item(lu, li);
+      lend = li.u0 + li.nu;
+      llo = seen_lo(li);
+      lhi = seen_hi(li);
+      fetch_granules();
+    } else if (gbase == 32) {
+      fetch_granules();
+    }
+    uint8_t* st = stages + s * C::STAGE;
+    const int nbox = UT / p.box_rows, gpb = p.box_rows / 16;  // boxes of a side, granules of a box
+    // lane i < nbox copies key box i, lane nbox + i value box i
+    const int bx = lane < nbox ? lane : lane - nbox;
+    int page = -1;
+    if (p.box_rows == 16) page = __shfl_sync(0xffffffffu, my_page, gbase + (bx & (GR - 1)));
+    else {
+      // a box spans granules of one page; any of them that is needed names it
+      for (int i = 0; i < gpb; ++i) {
+        const int x = __shfl_sync(0xffffffffu, my_page, gbase + ((bx * gpb + i) & (GR - 1)));
+        page = x >= 0 ? x : page;
+      }
+    }
+    const bool mine = lane < 2 * nbox && page >= 0;
+    const uint32_t box_bytes = static_cast<uint32_t>(p.box_rows) * D;
+    const int n = __popc(__ballot_sync(0xffffffffu, mine));
+    if (lane == 0) mbar_arrive_expect_tx(&bars[s], n * box_bytes);
+    __syncwarp();
+    if (mine) {
+      const int tok = li.tok0 + (lu - li.u0) * UT + bx * p.box_rows;
+      const int row = ((page * p.H + li.h) << p.lg_ps) + (tok & ((1 << p.lg_ps) - 1));
+      const bool key = lane < nbox;
+      tma_load_2d(st + (key ? 0 : 4096) + bx * box_bytes, key ? &kmap : &vmap, 0, row, &bars[s]);
+    }
+    gbase += GR;
+    grec += GR;
+    ++lu;
+  };
+#pragma unroll
+  for (int s = 0; s < NS; ++s)
+    if (lu < ub) issue(s);
+
+  // ---- compute ---------------------------------------------------------------
+  uint32_t qf[NT][KS][2];
+  float acc[MT][NT][4];
+  float m[NT][2], l[NT][2], cq[NT][2];
+  PagedItem it;
+  int iend = ua;               // end of the current item
+  int lo = 0, hi = 0, full_lo = 0, full_hi = 0;
+  int crec = 0;                // ring position of the unit's first granule
+  bool failed = false;
+
+  auto enter = [&](int u) {
+    find_item(u, it);
+    iend = it.u0 + it.nu;
+    lo = seen_lo(it);
+    hi = seen_hi(it);
+    // tokens [full_lo, full_hi) are seen by every row of the group
+    full_hi = it.seq - it.n + it.grp * RG / p.R + 1;
+    full_lo = p.window == 0 ? 0 : hi - p.window;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const int r = nt * 8 + g;  // this lane's query row
+      float c = p.qscale;
+      uint32_t w[KS * 2];
+#pragma unroll
+      for (int i = 0; i < KS * 2; ++i) w[i] = 0;
+      if (r < it.rows) {
+        const int row = it.grp * RG + r;
+        const int j = row / p.R;
+        const uint4* src = reinterpret_cast<const uint4*>(
+            static_cast<const uint16_t*>(p.q) + static_cast<long long>(it.q0 + j) * p.q_stride +
+            (static_cast<long long>(it.h) * p.R + (row - j * p.R)) * D + t * (D / 4));
+#pragma unroll
+        for (int i = 0; i < KS / 2; ++i) {
+          const uint4 v = src[i];
+          w[4 * i] = v.x;
+          w[4 * i + 1] = v.y;
+          w[4 * i + 2] = v.z;
+          w[4 * i + 3] = v.w;
+        }
+      }
+      if constexpr (BF16) {
+        // The row times a power of two as fp16: its largest element comes to
+        // [2^14, 2^15), so elements down to 2^-22 of it keep all their bits
+        // and the rest an absolute error below 2^-40 of it.
+        uint32_t mg = 0;
+#pragma unroll
+        for (int i = 0; i < KS * 2; ++i) mg = __vmaxu2(mg, w[i] & 0x7fff7fffu);
+        uint32_t mx = max(mg & 0xffffu, mg >> 16);
+        mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+        mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+        const int e = max(static_cast<int>(mx >> 7) - 127, -100);
+        const float up = __uint_as_float(static_cast<uint32_t>(127 + 14 - e) << 23);
+        c *= __uint_as_float(static_cast<uint32_t>(127 - 14 + e) << 23);
+#pragma unroll
+        for (int i = 0; i < KS * 2; ++i)
+          w[i] = pack_half2(__uint_as_float(w[i] << 16) * up,
+                            __uint_as_float(w[i] & 0xffff0000u) * up);
+      }
+#pragma unroll
+      for (int i = 0; i < KS; ++i) {
+        qf[nt][i][0] = w[2 * i];
+        qf[nt][i][1] = w[2 * i + 1];
+      }
+      // columns 2t, 2t + 1 of the score fragment are rows of other lanes
+      cq[nt][0] = __shfl_sync(0xffffffffu, c, 8 * t);
+      cq[nt][1] = __shfl_sync(0xffffffffu, c, 8 * t + 4);
+#pragma unroll
+      for (int c2 = 0; c2 < 2; ++c2) {
+        m[nt][c2] = -INFINITY;
+        l[nt][c2] = 0.f;
+      }
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[mt][nt][i] = 0.f;
+    }
+  };
+
+  // One unit from stage memory.  MASK: some of its tokens are hidden from
+  // some rows (or not there at all).
+  auto compute = [&](const uint8_t* st, int tok, auto masked) {
+    constexpr bool MASK = decltype(masked)::value;
+    uint32_t pw[GR][NT][2];
+    float s[GR][NT][4];
+    float4 rec[GR];
+#pragma unroll
+    for (int mt = 0; mt < GR; ++mt) {
+      rec[mt] = ring[(crec + mt) & (C::RING - 1)];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s[mt][nt][i] = 0.f;
+      const int r0 = mt * 16 + g, r1 = r0 + 8;
+#pragma unroll
+      for (int c = 0; c < KC; ++c) {
+        uint4 a, b;
+        if constexpr (D == 128) {
+          const int ch = ((2 * t + c) ^ (r0 & 7)) << 4;  // r1 & 7 is the same
+          a = *reinterpret_cast<const uint4*>(st + r0 * 128 + ch);
+          b = *reinterpret_cast<const uint4*>(st + r1 * 128 + ch);
+        } else {
+          const int ch = (t ^ ((r0 >> 1) & 3)) << 4;
+          a = *reinterpret_cast<const uint4*>(st + r0 * 64 + ch);
+          b = *reinterpret_cast<const uint4*>(st + r1 * 64 + ch);
+        }
+        const uint32_t aw[4] = {a.x, a.y, a.z, a.w}, bw[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          const uint32_t a0 = e4m3x2_to_half2(aw[w]), a1 = e4m3x2_to_half2(bw[w]);
+          const uint32_t a2 = e4m3x2_to_half2(aw[w] >> 16), a3 = e4m3x2_to_half2(bw[w] >> 16);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+            mma_16816(s[mt][nt], a0, a1, a2, a3, qf[nt][4 * c + w][0], qf[nt][4 * c + w][1]);
+        }
+      }
+    }
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      float mx[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+      for (int mt = 0; mt < GR; ++mt) {
+        const float f0 = rec[mt].x * cq[nt][0], f1 = rec[mt].x * cq[nt][1];
+        float* x = s[mt][nt];
+        x[0] = fmaf(x[0], f0, rec[mt].y);
+        x[1] = fmaf(x[1], f1, rec[mt].y);
+        x[2] = fmaf(x[2], f0, rec[mt].y);
+        x[3] = fmaf(x[3], f1, rec[mt].y);
+        if constexpr (MASK) {
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            const int row = it.grp * RG + nt * 8 + 2 * t + c;
+            const int pos = it.seq - it.n + row / p.R;
+            const int first = p.window == 0 ? 0 : pos - p.window + 1;
+            const int ta = tok + mt * 16 + g, tb = ta + 8;
+            const bool there = rec[mt].w != 0.f;
+            if (!there || ta > pos || ta < first) x[c] = -INFINITY;
+            if (!there || tb > pos || tb < first) x[2 + c] = -INFINITY;
+          }
+        }
+        mx[0] = fmaxf(mx[0], fmaxf(x[0], x[2]));
+        mx[1] = fmaxf(mx[1], fmaxf(x[1], x[3]));
+      }
+      float al[2], mb[2];
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        mx[c] = fmaxf(mx[c], __shfl_xor_sync(0xffffffffu, mx[c], 4));
+        mx[c] = fmaxf(mx[c], __shfl_xor_sync(0xffffffffu, mx[c], 8));
+        mx[c] = fmaxf(mx[c], __shfl_xor_sync(0xffffffffu, mx[c], 16));
+        const float mn = fmaxf(m[nt][c], mx[c]);
+        mb[c] = mn == -INFINITY ? 0.f : mn;
+        al[c] = fast_exp2(m[nt][c] - mb[c]);
+        m[nt][c] = mn;
+        l[nt][c] *= al[c];
+      }
+#pragma unroll
+      for (int mt = 0; mt < GR; ++mt) {
+        float* x = s[mt][nt];
+        x[0] = fast_exp2(x[0] - mb[0]);
+        x[1] = fast_exp2(x[1] - mb[1]);
+        x[2] = fast_exp2(x[2] - mb[0]);
+        x[3] = fast_exp2(x[3] - mb[1]);
+        l[nt][0] = fmaf(x[0] + x[2], rec[mt].z, l[nt][0]);
+        l[nt][1] = fmaf(x[1] + x[3], rec[mt].z, l[nt][1]);
+        pw[mt][nt][0] = movmatrix(pack_half2(x[0], x[1]));
+        pw[mt][nt][1] = movmatrix(pack_half2(x[2], x[3]));
+      }
+      if (__any_sync(0xffffffffu, al[0] != 1.f || al[1] != 1.f)) {
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+          acc[mt][nt][0] *= al[0];
+          acc[mt][nt][1] *= al[1];
+          acc[mt][nt][2] *= al[0];
+          acc[mt][nt][3] *= al[1];
+        }
+      }
+    }
+    const uint8_t* sv = st + 4096;
+#pragma unroll
+    for (int mt = 0; mt < GR; ++mt) {
+      // value rows of tokens 2t, 2t + 1, 2t + 8, 2t + 9 of the granule:
+      // channels [D/8 * g, D/8 * (g + 1))
+      constexpr int VW = D / 32;  // words of a lane's row
+      uint32_t v[4][VW];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int r = mt * 16 + 2 * t + (i & 1) + 8 * (i >> 1);
+        if constexpr (D == 128) {
+          const uint4 x = *reinterpret_cast<const uint4*>(sv + r * 128 + ((g ^ (r & 7)) << 4));
+          v[i][0] = x.x;
+          v[i][1] = x.y;
+          v[i][2] = x.z;
+          v[i][3] = x.w;
+        } else {
+          const uint2 x = *reinterpret_cast<const uint2*>(
+              sv + r * 64 + (((g >> 1) ^ ((r >> 1) & 3)) << 4) + 8 * (g & 1));
+          v[i][0] = x.x;
+          v[i][1] = x.y;
+        }
+        if constexpr (MASK) {
+          // what lies in hidden rows may decode to NaN, which a weight of 0
+          // would not cancel
+          const int tk = tok + r;
+          if (tk < lo || tk >= hi || rec[mt].w == 0.f) {
+#pragma unroll
+            for (int w = 0; w < VW; ++w) v[i][w] = 0;
+          }
+        }
+      }
+#pragma unroll
+      for (int w = 0; w < VW; ++w) {
+        const uint32_t x0 = __byte_perm(v[0][w], v[1][w], 0x5140), x1 = __byte_perm(v[0][w], v[1][w], 0x7362);
+        const uint32_t y0 = __byte_perm(v[2][w], v[3][w], 0x5140), y1 = __byte_perm(v[2][w], v[3][w], 0x7362);
+        const uint32_t a0 = e4m3x2_to_half2(x0), a1 = e4m3x2_to_half2(x0 >> 16);
+        const uint32_t a2 = e4m3x2_to_half2(y0), a3 = e4m3x2_to_half2(y0 >> 16);
+        const uint32_t b0 = e4m3x2_to_half2(x1), b1 = e4m3x2_to_half2(x1 >> 16);
+        const uint32_t b2 = e4m3x2_to_half2(y1), b3 = e4m3x2_to_half2(y1 >> 16);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          mma_16816(acc[2 * w][nt], a0, a1, a2, a3, pw[mt][nt][0], pw[mt][nt][1]);
+          mma_16816(acc[2 * w + 1][nt], b0, b1, b2, b3, pw[mt][nt][0], pw[mt][nt][1]);
+        }
+      }
+    }
+  };
+
+  // Leaves the current item after unit u - 1: a finished output, or a partial.
+  auto leave = [&](bool last) {
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        l[nt][c] += __shfl_xor_sync(0xffffffffu, l[nt][c], 4);
+        l[nt][c] += __shfl_xor_sync(0xffffffffu, l[nt][c], 8);
+        l[nt][c] += __shfl_xor_sync(0xffffffffu, l[nt][c], 16);
+      }
+    const bool whole = it.u0 >= ua && iend <= ub;
+    if (whole) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const int r = nt * 8 + 2 * t + c;
+          if (r >= it.rows) continue;
+          const int row = it.grp * RG + r, j = row / p.R;
+          const float inv = l[nt][c] > 0.f ? 1.f / l[nt][c] : (l[nt][c] == 0.f ? 0.f : l[nt][c]);
+          uint32_t w[D / 16];
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt) {
+            const float x = acc[mt][nt][c] * inv, y = acc[mt][nt][2 + c] * inv;
+            if constexpr (BF16) {
+              const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
+              w[mt] = *reinterpret_cast<const uint32_t*>(&h);
+            } else {
+              w[mt] = pack_half2(x, y);
+            }
+          }
+          uint4* dst = reinterpret_cast<uint4*>(
+              static_cast<uint16_t*>(p.out) + static_cast<long long>(it.q0 + j) * p.out_stride +
+              (static_cast<long long>(it.h) * p.R + (row - j * p.R)) * D + g * (D / 8));
+#pragma unroll
+          for (int i = 0; i < D / 64; ++i)
+            dst[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+        }
+      return;
+    }
+    float* dst = last ? reinterpret_cast<float*>(stages)
+                      : p.warp_part + static_cast<size_t>(gw) * PART;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const int r = nt * 8 + 2 * t + c;
+#pragma unroll
+        for (int mt = 0; mt < MT; mt += 2) {
+          *reinterpret_cast<float4*>(dst + r * D + g * (D / 8) + 2 * mt) =
+              make_float4(acc[mt][nt][c], acc[mt][nt][2 + c], acc[mt + 1][nt][c], acc[mt + 1][nt][2 + c]);
+        }
+        if (g == 0) {
+          dst[RG * D + 2 * r] = m[nt][c];
+          dst[RG * D + 2 * r + 1] = l[nt][c];
+        }
+      }
+    if (lane == 0) {
+      PagedSeg& sg = segs[2 * warp + (last ? 1 : 0)];
+      sg.u0 = it.u0;
+      sg.u1 = iend;
+      sg.b = it.b;
+      sg.h = it.h;
+      sg.grp = it.grp;
+      sg.where = last ? 1 : 0;
+    }
+  };
+
+  int st = 0;
+  uint32_t phase = 0;
+  for (int u = ua; u < ub; ++u) {
+    if (u == iend) {
+      if (u > ua) leave(false);
+      enter(u);
+    }
+    if (!mbar_wait_bounded(&bars[st], phase)) {
+      failed = true;
+      break;
+    }
+    const int tok = it.tok0 + (u - it.u0) * UT;
+    if (tok < hi && tok + UT > lo) {
+      const uint8_t* sp = stages + st * C::STAGE;
+      bool there = true;
+#pragma unroll
+      for (int i = 0; i < GR; ++i) there &= ring[(crec + i) & (C::RING - 1)].w != 0.f;
+      if (there && tok >= full_lo && tok + UT <= full_hi) compute(sp, tok, std::false_type{});
+      else compute(sp, tok, std::true_type{});
+    }
+    crec += GR;
+    __syncwarp();
+    if (lu < ub) issue(st);
+    if (++st == NS) {
+      st = 0;
+      phase ^= 1;
+    }
+  }
+  if (failed) {
+    // a copy did not arrive in time: record it, let the others land (bounded)
+    set_err(p.err, KVQ_PAGED_ERR_WAIT);
+    for (int i = 0; i < NS; ++i) {
+      mbar_wait_bounded(&bars[st], phase);
+      if (++st == NS) {
+        st = 0;
+        phase ^= 1;
+      }
+    }
+  } else if (ua < ub) {
+    leave(true);
+  }
+
+  // ---- the CTA's join ---------------------------------------------------------
+  __syncthreads();
+  const int cu0 = first_of(min(static_cast<int>(blockIdx.x) * NW, W));
+  const int cu1 = first_of(min((static_cast<int>(blockIdx.x) + 1) * NW, W));
+  auto finish = [&](const PagedSeg& sg, int r, int ch, float M, float L, float4 o) {
+    int bad;
+    const PagedReq rq = load_req(sg.b, &bad);
+    const int row = sg.grp * RG + r;
+    if (row >= rq.n * p.R) return;
+    const int j = row / p.R;
+    const float inv = L > 0.f ? 1.f / L : (L == 0.f ? 0.f : L);
+    uint2 w;
+    if constexpr (BF16) {
+      const __nv_bfloat162 a = __floats2bfloat162_rn(o.x * inv, o.y * inv);
+      const __nv_bfloat162 b = __floats2bfloat162_rn(o.z * inv, o.w * inv);
+      w = make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+    } else {
+      w = make_uint2(pack_half2(o.x * inv, o.y * inv), pack_half2(o.z * inv, o.w * inv));
+    }
+    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) +
+                              static_cast<long long>(rq.q0 + j) * p.out_stride +
+                              (static_cast<long long>(sg.h) * p.R + (row - j * p.R)) * D + ch) = w;
+  };
+  for (int i0 = 0; i0 < 2 * NW;) {
+    const PagedSeg sg = segs[i0];
+    if (sg.u0 < 0) {
+      ++i0;
+      continue;
+    }
+    int i1 = i0 + 1;
+    while (i1 < 2 * NW && (segs[i1].u0 < 0 || segs[i1].u0 == sg.u0)) ++i1;
+    const bool starts = sg.u0 >= cu0, ends = sg.u1 <= cu1;
+    const bool whole = starts && ends;
+    const int cta = blockIdx.x;
+    float* slot = p.cta_part + static_cast<size_t>(2 * cta + (starts ? 1 : 0)) * PART;
+    for (int e = tid; e < RG * D / 4; e += NW * 32) {
+      const int r = e / (D / 4), ch = e % (D / 4) * 4;
+      auto part = [&](int i) {
+        return segs[i].where ? reinterpret_cast<const float*>(smem + (i >> 1) * NS * C::STAGE)
+                             : p.warp_part + static_cast<size_t>(cta * NW + (i >> 1)) * PART;
+      };
+      float M = -INFINITY;
+      for (int i = i0; i < i1; ++i)
+        if (segs[i].u0 >= 0) M = fmaxf(M, part(i)[RG * D + 2 * r]);
+      const float mb = M == -INFINITY ? 0.f : M;
+      float L = 0.f;
+      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int i = i0; i < i1; ++i) {
+        if (segs[i].u0 < 0) continue;
+        const float* s = part(i);
+        const float w = fast_exp2(s[RG * D + 2 * r] - mb);
+        const float4 x = *reinterpret_cast<const float4*>(s + r * D + ch);
+        L = fmaf(s[RG * D + 2 * r + 1], w, L);
+        o.x = fmaf(x.x, w, o.x);
+        o.y = fmaf(x.y, w, o.y);
+        o.z = fmaf(x.z, w, o.z);
+        o.w = fmaf(x.w, w, o.w);
+      }
+      if (whole) {
+        finish(sg, r, ch, M, L, o);
+      } else {
+        *reinterpret_cast<float4*>(slot + r * D + ch) = o;
+        if (ch == 0) {
+          slot[RG * D + 2 * r] = M;
+          slot[RG * D + 2 * r + 1] = L;
+        }
+      }
+    }
+    if (!whole) {
+      // CTAs that hold units of the item: its first unit's to its last unit's
+      auto owner = [&](int u) {
+        return static_cast<int>(((static_cast<long long>(u) + 1) * W - 1) / U) / NW;
+      };
+      const int ca = owner(sg.u0), cb = owner(sg.u1 - 1);
+      __threadfence();
+      __syncthreads();
+      if (tid == 0) {
+        const int seen = atomicAdd(&p.tickets[ca], 1);
+        flags[8] = seen == cb - ca;
+        if (seen == cb - ca) p.tickets[ca] = 0;  // nobody else comes: ready for the next launch
+      }
+      __syncthreads();
+      if (flags[8]) {
+        __threadfence();
+        for (int e = tid; e < RG * D / 4; e += NW * 32) {
+          const int r = e / (D / 4), ch = e % (D / 4) * 4;
+          auto part = [&](int c) { return p.cta_part + static_cast<size_t>(2 * c + (c == ca ? 1 : 0)) * PART; };
+          float M = -INFINITY;
+          for (int c = ca; c <= cb; ++c) M = fmaxf(M, __ldcg(part(c) + RG * D + 2 * r));
+          const float mb = M == -INFINITY ? 0.f : M;
+          float L = 0.f;
+          float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+          for (int c = ca; c <= cb; ++c) {
+            const float* s = part(c);
+            const float2 ml = __ldcg(reinterpret_cast<const float2*>(s + RG * D + 2 * r));
+            const float4 x = __ldcg(reinterpret_cast<const float4*>(s + r * D + ch));
+            const float w = fast_exp2(ml.x - mb);
+            L = fmaf(ml.y, w, L);
+            o.x = fmaf(x.x, w, o.x);
+            o.y = fmaf(x.y, w, o.y);
+            o.z = fmaf(x.z, w, o.z);
+            o.w = fmaf(x.w, w, o.w);
+          }
+          finish(sg, r, ch, M, L, o);
+        }
+      }
+      __syncthreads();
+    }
+    i0 = i1;
+  }
+}
+
+template <int D, int NT, bool BF16>
+cudaError_t launch_paged_decode_t(const PagedAttnParams& p, const CUtensorMap& km,
+                                  const CUtensorMap& vm, cudaStream_t st) {
+  using C = PagedCfg<D, NT>;
+  auto fn = paged_decode_kernel<D, NT, BF16>;
+  const int smem = C::smem(p.batch);
+  const cudaError_t e = allow_smem(reinterpret_cast<const void*>(fn), C::smem(kPagedMaxBatch));
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(p.n_warps / C::NW);
+  cfg.blockDim = dim3(C::NW * 32);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, fn, p, km, vm);
+}
+
+}  // namespace kvq

@@ -1,0 +1,351 @@
+// kvq_paged_store.cu — new keys and values into the E4M3 pages
+// (kvq_paged_store).
+//
+// For every page and kv head that receives rows, with amax over the new rows'
+// finite elements:
+//   e     = the least exponent in [-15, 40] with amax <= 448 * 2^e
+//   scale = max(2^e, the page's scale when it holds older rows)
+//   code  = E4M3(x / scale), nearest even, saturating (NaN: code 0)
+// and when the scale grows, the older rows' codes c become E4M3(c * old /
+// scale).  Scales are powers of two, so x / scale is exact in fp32 and every
+// code is rounded once; E4M3 keeps the same relative precision at any power
+// of two, which is why a finer scale would gain nothing above its subnormals.
+//
+// A run is a maximal sequence of tokens whose slots are consecutive rows of
+// one page; its first token leads it and whoever finds a leader stores the
+// whole run, so no two CTAs touch the same page and head.
+//
+// Bound: HBM for prompts (6 bytes a value: 2 read and 1 written, K and V),
+// latency for single tokens.
+#include "kvq_paged.cuh"
+
+namespace kvq {
+namespace {
+
+// Magnitude bits of two 16-bit floats: ordered as unsigned halves, NaN above
+// infinity above the finite values.
+__device__ __forceinline__ uint32_t mag2(uint32_t w) { return w & 0x7fff7fffu; }
+
+template <bool BF16>
+__device__ __forceinline__ uint32_t inf_bits() {
+  return BF16 ? 0x7f80u : 0x7c00u;
+}
+
+template <bool BF16>
+__device__ __forceinline__ float2 to_float2(uint32_t w) {
+  if constexpr (BF16) {
+    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+  } else {
+    const __half2 h = *reinterpret_cast<const __half2*>(&w);
+    return __half22float2(h);
+  }
+}
+
+// Largest of a 16-byte vector's eight magnitudes, as bits.
+__device__ __forceinline__ uint32_t vec_max(uint4 v, uint32_t m2) {
+  m2 = __vmaxu2(m2, mag2(v.x));
+  m2 = __vmaxu2(m2, mag2(v.y));
+  m2 = __vmaxu2(m2, mag2(v.z));
+  return __vmaxu2(m2, mag2(v.w));
+}
+// The same over the finite elements only.
+template <bool BF16>
+__device__ __forceinline__ uint32_t vec_max_finite(uint4 v, uint32_t m2) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    uint32_t a = mag2(w[i]);
+    if ((a & 0xffffu) >= inf_bits<BF16>()) a &= 0xffff0000u;
+    if ((a >> 16) >= inf_bits<BF16>()) a &= 0xffffu;
+    m2 = __vmaxu2(m2, a);
+  }
+  return m2;
+}
+__device__ __forceinline__ uint32_t fold2(uint32_t m2) { return max(m2 & 0xffffu, m2 >> 16); }
+
+// The least exponent in range with |value| <= 448 * 2^e = 1.75 * 2^(e + 8).
+__device__ __forceinline__ int exp_for(float amax) {
+  const uint32_t b = __float_as_uint(amax);
+  const int e = static_cast<int>(b >> 23) - 127 - 8 + ((b & 0x7fffffu) > 0x600000u ? 1 : 0);
+  return min(max(e, kPagedMinExp), kPagedMaxExp);
+}
+template <bool BF16>
+__device__ __forceinline__ int exp_for_bits(uint32_t mag) {
+  float a;
+  if constexpr (BF16) a = __uint_as_float(mag << 16);
+  else a = __half2float(__ushort_as_half(static_cast<unsigned short>(mag)));
+  return exp_for(a);
+}
+// Exponent of a stored scale, rounded up to a power of two of the range;
+// kPagedMinExp when it is no positive finite number (a page nothing was
+// stored into).
+__device__ __forceinline__ int exp_of_scale(float s) {
+  if (!(s > 0.f) || !isfinite(s)) return kPagedMinExp;
+  const uint32_t b = __float_as_uint(s);
+  const int e = static_cast<int>(b >> 23) - 127 + ((b & 0x7fffffu) ? 1 : 0);
+  return min(max(e, kPagedMinExp), kPagedMaxExp);
+}
+__device__ __forceinline__ float exp2i(int e) { return __uint_as_float(static_cast<uint32_t>(127 + e) << 23); }
+
+__device__ __forceinline__ uint32_t codes2(float2 x) {
+  return __nv_cvt_float2_to_fp8x2(x, __NV_SATFINITE, __NV_E4M3);
+}
+
+// Eight values times `inv` (a power of two) as E4M3 codes.  `clean` replaces
+// NaN by 0 first (the conversion would keep it).
+template <bool BF16>
+__device__ __forceinline__ uint2 codes8(uint4 v, float inv, bool clean) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  uint32_t c[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float2 f = to_float2<BF16>(w[i]);
+    f.x *= inv;
+    f.y *= inv;
+    if (clean) {
+      f.x = f.x == f.x ? f.x : 0.f;
+      f.y = f.y == f.y ? f.y : 0.f;
+    }
+    c[i] = codes2(f);
+  }
+  return make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
+}
+
+// Eight E4M3 codes times `f` (a power of two <= 1), rounded again.
+__device__ __forceinline__ uint2 rescale8(uint2 v, float f) {
+  const uint32_t w[4] = {v.x & 0xffffu, v.x >> 16, v.y & 0xffffu, v.y >> 16};
+  uint32_t c[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t h = e4m3x2_to_half2(w[i]);
+    float2 x = __half22float2(*reinterpret_cast<const __half2*>(&h));
+    x.x *= f;
+    x.y *= f;
+    c[i] = codes2(x);
+  }
+  return make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
+}
+
+// True when token t leads a run: it has a slot, and the token before it is
+// not the page's row before it.
+__device__ __forceinline__ bool leads(const PagedStoreParams& p, int t, int slot, int prev) {
+  return slot >= 0 && (t == 0 || prev != slot - 1 || (slot & ((1 << p.lg_ps) - 1)) == 0);
+}
+
+__device__ __forceinline__ const uint4* vec_ptr(const PagedStoreParams& p, int side, long long t,
+                                                int h, int D, int vec) {
+  return reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(side ? p.x[1] : p.x[0]) +
+                                        t * (side ? p.stride[1] : p.stride[0]) + h * D) + vec;
+}
+
+// ---- single tokens: a warp looks at one token and one head ------------------
+//
+// Lanes [0, 16) serve K and [16, 32) V; a side's lanes hold a row as 16-byte
+// vectors (D / 8 of them, 16 / (D / 8) rows at a time).
+constexpr int kRowWarps = 4;
+
+template <int D, bool BF16>
+__global__ void __launch_bounds__(kRowWarps * 32) paged_store_rows_kernel(const PagedStoreParams p) {
+  constexpr int VPR = D / 8, RPS = 16 / VPR;  // vectors of a row, rows a step
+  grid_dep_wait();
+  grid_dep_launch();
+  const int lane = threadIdx.x & 31;
+  const long long gw = static_cast<long long>(blockIdx.x) * kRowWarps + (threadIdx.x >> 5);
+  const int t = static_cast<int>(gw / p.H), h = static_cast<int>(gw % p.H);
+  if (t >= p.n_tokens) return;
+  const int slot = p.slots[t];
+  const int prev = t > 0 ? p.slots[t - 1] : -1;
+  if (!leads(p, t, slot, prev)) return;
+  const int page = slot >> p.lg_ps, row0 = slot & ((1 << p.lg_ps) - 1);
+  if (page >= p.n_pages) {
+    if (lane == 0) set_err(p.err, KVQ_PAGED_ERR_BAD_PAGE);
+    return;
+  }
+  const int side = lane >> 4, l = lane & 15, sub = l / VPR, vec = l % VPR;
+  // rows of the run: until the page ends or the slots stop following
+  const int most = min((1 << p.lg_ps) - row0, p.n_tokens - t);
+  int n = 1;
+  while (n < most) {
+    const int i = n + lane;
+    const bool ok = i < most && p.slots[t + i] == slot + i;
+    const uint32_t m = __ballot_sync(0xffffffffu, !ok);
+    if (m) {
+      n += __ffs(m) - 1;
+      break;
+    }
+    n += 32;
+  }
+  float* scale = (side ? p.scale[1] : p.scale[0]) + static_cast<size_t>(page) * p.H + h;
+  const float was = *scale;
+  const uint4 zero = make_uint4(0, 0, 0, 0);
+  const uint4 first = sub < n ? *vec_ptr(p, side, t + sub, h, D, vec) : zero;
+  uint32_t m2 = vec_max(first, 0);
+  for (int i = sub + RPS; i < n; i += RPS) m2 = vec_max(*vec_ptr(p, side, t + i, h, D, vec), m2);
+  auto side_max = [](uint32_t x) {  // over the side's sixteen lanes
+#pragma unroll
+    for (int o = 1; o < 16; o <<= 1) x = max(x, __shfl_xor_sync(0xffffffffu, x, o));
+    return x;
+  };
+  uint32_t mag = side_max(fold2(m2));
+  const bool odd = mag >= inf_bits<BF16>();  // the side holds a NaN or an infinity
+  if (__any_sync(0xffffffffu, odd)) {
+    m2 = 0;
+    for (int i = sub; i < n; i += RPS)
+      m2 = vec_max_finite<BF16>(*vec_ptr(p, side, t + i, h, D, vec), m2);
+    mag = side_max(fold2(m2));
+    if (odd && l == 0) set_err(p.err, KVQ_PAGED_ERR_NONFINITE);
+  }
+  int e = exp_for_bits<BF16>(mag);
+  uint8_t* base = (side ? p.pages[1] : p.pages[0]) + ((static_cast<size_t>(page) * p.H + h) << p.lg_ps) * D + vec * 8;
+  if (row0 > 0) {
+    const int eo = exp_of_scale(was);
+    e = max(e, eo);
+    const float now = exp2i(e);
+    if (was != now && was > 0.f) {
+      const float f = was / now;
+      for (int i = sub; i < row0; i += RPS) {
+        uint2* c = reinterpret_cast<uint2*>(base + static_cast<size_t>(i) * D);
+        *c = rescale8(*c, f);
+      }
+    }
+  }
+  const float inv = exp2i(-e);
+  if (sub < n) *reinterpret_cast<uint2*>(base + static_cast<size_t>(row0 + sub) * D) = codes8<BF16>(first, inv, odd);
+  for (int i = sub + RPS; i < n; i += RPS)
+    *reinterpret_cast<uint2*>(base + static_cast<size_t>(row0 + i) * D) =
+        codes8<BF16>(*vec_ptr(p, side, t + i, h, D, vec), inv, odd);
+  if (l == 0) *scale = exp2i(e);
+}
+
+// ---- prompts: a CTA looks at a chunk of tokens and one head -----------------
+//
+// The run's vectors stay in registers between the maximum and the codes, so
+// every input byte is read once: 128 threads a side, 128 / (D / 8) rows a
+// step, at most kMaxSteps steps (a whole 128-row page).
+constexpr int kChunkThreads = 256;
+constexpr int kChunk = 32;  // tokens a CTA looks for leaders in
+
+template <int D, bool BF16>
+__global__ void __launch_bounds__(kChunkThreads) paged_store_chunk_kernel(const PagedStoreParams p) {
+  constexpr int VPR = D / 8, RPS = 128 / VPR, STEPS = 128 / RPS;
+  __shared__ uint32_t s_lead;
+  __shared__ int s_len;
+  __shared__ uint32_t s_max[2][2][4];  // [pass][side][warp]
+  grid_dep_wait();
+  grid_dep_launch();
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int side = tid >> 7, l = tid & 127, sub = l / VPR, vec = l % VPR;
+  const int tb = blockIdx.x * kChunk, h = blockIdx.y;
+  const int ps = 1 << p.lg_ps;
+  if (tid < 32) {
+    const int t = tb + lane;
+    bool lead = false;
+    if (t < p.n_tokens) lead = leads(p, t, p.slots[t], t > 0 ? p.slots[t - 1] : -1);
+    const uint32_t m = __ballot_sync(0xffffffffu, lead);
+    if (lane == 0) s_lead = m;
+  }
+  __syncthreads();
+  uint32_t todo = s_lead;
+  while (todo) {
+    const int t = tb + __ffs(todo) - 1;
+    todo &= todo - 1;
+    const int slot = p.slots[t];
+    const int page = slot >> p.lg_ps, row0 = slot & (ps - 1);
+    if (page >= p.n_pages) {
+      if (tid == 0) set_err(p.err, KVQ_PAGED_ERR_BAD_PAGE);
+      continue;
+    }
+    // rows of the run: the first token that does not follow
+    const int most = min(ps - row0, p.n_tokens - t);
+    if (tid == 0) s_len = most;
+    __syncthreads();
+    if (tid < most && p.slots[t + tid] != slot + tid) atomicMin(&s_len, tid);
+    float* scale = (side ? p.scale[1] : p.scale[0]) + static_cast<size_t>(page) * p.H + h;
+    const float was = *scale;
+    __syncthreads();
+    const int n = s_len;
+    uint4 x[STEPS];
+    uint32_t m2 = 0;
+#pragma unroll
+    for (int s = 0; s < STEPS; ++s) {
+      const int i = s * RPS + sub;
+      x[s] = make_uint4(0, 0, 0, 0);
+      if (i < n) x[s] = __ldg(vec_ptr(p, side, t + i, h, D, vec));
+    }
+#pragma unroll
+    for (int s = 0; s < STEPS; ++s) m2 = vec_max(x[s], m2);
+    uint32_t mag = __reduce_max_sync(0xffffffffu, fold2(m2));
+    if (lane == 0) s_max[0][side][(tid >> 5) & 3] = mag;
+    __syncthreads();
+    mag = 0;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) mag = max(mag, s_max[0][side][w]);
+    const bool odd = mag >= inf_bits<BF16>();
+    if (__syncthreads_or(odd)) {
+      m2 = 0;
+#pragma unroll
+      for (int s = 0; s < STEPS; ++s) m2 = vec_max_finite<BF16>(x[s], m2);
+      const uint32_t mw = __reduce_max_sync(0xffffffffu, fold2(m2));
+      if (lane == 0) s_max[1][side][(tid >> 5) & 3] = mw;
+      __syncthreads();
+      mag = 0;
+#pragma unroll
+      for (int w = 0; w < 4; ++w) mag = max(mag, s_max[1][side][w]);
+      if (odd && l == 0) set_err(p.err, KVQ_PAGED_ERR_NONFINITE);
+    }
+    int e = exp_for_bits<BF16>(mag);
+    uint8_t* base = (side ? p.pages[1] : p.pages[0]) + ((static_cast<size_t>(page) * p.H + h) << p.lg_ps) * D + vec * 8;
+    if (row0 > 0) {
+      e = max(e, exp_of_scale(was));
+      const float now = exp2i(e);
+      if (was != now && was > 0.f) {
+        const float f = was / now;
+        for (int i = sub; i < row0; i += RPS) {
+          uint2* c = reinterpret_cast<uint2*>(base + static_cast<size_t>(i) * D);
+          *c = rescale8(*c, f);
+        }
+      }
+    }
+    const float inv = exp2i(-e);
+#pragma unroll
+    for (int s = 0; s < STEPS; ++s) {
+      const int i = s * RPS + sub;
+      if (i < n)
+        *reinterpret_cast<uint2*>(base + static_cast<size_t>(row0 + i) * D) =
+            codes8<BF16>(x[s], inv, odd);
+    }
+    if (l == 0) *scale = exp2i(e);
+    __syncthreads();  // s_len, s_max and `was` of the next run
+  }
+}
+
+template <int D, bool BF16>
+cudaError_t launch(const PagedStoreParams& p, cudaStream_t st) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (p.n_tokens <= 1024) {
+    const long long warps = static_cast<long long>(p.n_tokens) * p.H;
+    cfg.gridDim = dim3(static_cast<unsigned>((warps + kRowWarps - 1) / kRowWarps));
+    cfg.blockDim = dim3(kRowWarps * 32);
+    return cudaLaunchKernelEx(&cfg, paged_store_rows_kernel<D, BF16>, p);
+  }
+  cfg.gridDim = dim3((p.n_tokens + kChunk - 1) / kChunk, p.H);
+  cfg.blockDim = dim3(kChunkThreads);
+  return cudaLaunchKernelEx(&cfg, paged_store_chunk_kernel<D, BF16>, p);
+}
+
+}  // namespace
+
+cudaError_t launch_paged_store(const PagedStoreParams& p, int D, int dtype, cudaStream_t st) {
+  const bool bf = dtype == KVQ_DTYPE_BF16;
+  if (D == 128) return bf ? launch<128, true>(p, st) : launch<128, false>(p, st);
+  if (D == 64) return bf ? launch<64, true>(p, st) : launch<64, false>(p, st);
+  return cudaErrorInvalidValue;
+}
+
+}  // namespace kvq

@@ -345,6 +345,146 @@ KVQ_API kvq_status kvq_decode_attention_noalloc(const kvq_config* cfg, const voi
                                                 float softmax_scale, int* device_error,
                                                 void* stream);
 
+/* ---------------------------------------------------------------------------
+ * Paged 8-bit cache: the operators of a serving step.
+ *
+ * A server that batches requests of different lengths, which come and go,
+ * keeps its tokens in pages of a pool instead of one buffer per row.  Three
+ * calls make a step: kvq_paged_plan (block tables and slots from the
+ * requests' lengths), kvq_paged_store (new keys and values into the pages),
+ * kvq_paged_attention (the new tokens' attention).  Lengths, tables and slots
+ * stay on the device, so a captured step can be replayed with other lengths.
+ *
+ * Pool.  E4M3 codes [n_pages][n_kv_heads][page_size][head_dim] (one byte
+ * each) for K and for V, and one fp32 scale for each page and kv head; a
+ * value is code * scale.  Token `pos` of request b lies in page
+ * block_table[b][pos / page_size], row pos % page_size; its slot is
+ * page * page_size + row.  The buffers are the caller's.
+ *
+ * Arithmetic of the store, exactly, per page and kv head that receives rows:
+ *   amax  = max |x| over the new rows' finite elements
+ *   scale = max(2^e, the page's scale if it holds older rows), e the least
+ *           exponent in [-15, 40] with amax <= 448 * 2^e
+ *   code  = E4M3(x / scale): nearest, ties to even, saturating at +-448
+ * Scales are powers of two, so x / scale is exact and a code is rounded once;
+ * a floating-point code loses no precision to a coarser power of two above
+ * its subnormals.  When a page's scale grows from s to s', its older rows'
+ * codes c become E4M3(c * s / s') (exact but for codes that become
+ * subnormal).  Elements below 2^-25 in magnitude become 0, as 2^-15 * 2^-9 is
+ * the smallest value a page can hold.  Infinities saturate, NaN is stored as
+ * 0, and either sets KVQ_PAGED_ERR_NONFINITE.
+ *
+ * Conventions, besides those at the top of this header.
+ *   - Sizes with an upper bound: head_dim 64 or 128; page_size 16, 32, 64 or
+ *     128; batch <= 4096; n_q_heads a multiple of n_kv_heads, at most 16
+ *     times; n_pages * n_kv_heads * page_size < 2^31 (KVQ_ERR_UNSUPPORTED
+ *     beyond).  Buffers may be larger than 4 GB.
+ *   - 16-bit inputs are fp16 or bf16 (kvq_dtype), one row of heads x head_dim
+ *     contiguous elements per token; `stride` is the distance between tokens
+ *     in elements, a multiple of 8 (slices of a fused projection fit).
+ *   - int arrays are 32-bit and 4-byte aligned (slots: 16).
+ *   - The calls launch on the current device, which holds every buffer.
+ *   - device_error is an optional device int that kernels OR the
+ *     KVQ_PAGED_ERR_* bits into; the caller clears it.  What a kernel flags it
+ *     also skips: no call reads or writes outside its buffers, whatever the
+ *     tables and lengths hold.
+ *   - Two calls that may overlap on the GPU must not write the same pages, nor
+ *     share a workspace.  One call must not write a page from two places of
+ *     the batch: the rows of a page that it writes are consecutive tokens.
+ * ------------------------------------------------------------------------ */
+
+typedef enum { KVQ_DTYPE_FP16 = 0, KVQ_DTYPE_BF16 = 1 } kvq_dtype;
+
+#define KVQ_PAGED_ERR_WAIT 1      /* a bounded wait ran out; the output is not complete
+                                     and the workspace's first 1024 bytes have to be
+                                     zeroed before its next use                         */
+#define KVQ_PAGED_ERR_BAD_PAGE 2  /* a needed page id is outside the pool: its rows are
+                                     not stored, its tokens not attended                */
+#define KVQ_PAGED_ERR_NO_PAGES 4  /* the free stack did not hold a request's pages       */
+#define KVQ_PAGED_ERR_LENGTH 8    /* a length breaks the call's contract                 */
+#define KVQ_PAGED_ERR_NONFINITE 16 /* a stored key or value was infinite or NaN          */
+
+typedef struct {
+  void* k_pages;   /* E4M3 [n_pages][n_kv_heads][page_size][head_dim], 16-byte aligned */
+  void* v_pages;
+  float* k_scale;  /* [n_pages][n_kv_heads] */
+  float* v_scale;
+  int n_pages, n_kv_heads, page_size, head_dim;
+} kvq_paged_pool;
+
+/* Validates a pool's sizes on the host (the pointers are not looked at). */
+KVQ_API kvq_status kvq_paged_pool_check(const kvq_paged_pool* pool);
+
+/* The bookkeeping of a step.  Request b holds ctx_len[b] cached tokens and
+ * brings new_len[b] (0 allowed) new ones; its first ceil(ctx / page_size)
+ * table entries are valid.  Fresh pages come from the top of the stack
+ * free_pages[0 .. *n_free): request b, in order of b, takes the next ones.
+ *   block_table  [batch][max_pages]: the fresh entries are written, the others
+ *                left as they are.
+ *   cu_new       [batch + 1]: offsets of the requests' new tokens.
+ *   seq_len      [batch]: ctx + new.
+ *   slots        [n_tokens]: the slot of every new token; -1 behind the last
+ *                one (n_tokens may exceed their number) and where there is no
+ *                page.
+ *   n_left       [1]: stack entries left (the new *n_free).
+ * A request whose pages the stack does not hold (KVQ_PAGED_ERR_NO_PAGES), or
+ * that needs more than max_pages or has a negative length
+ * (KVQ_PAGED_ERR_LENGTH), takes nothing: seq_len[b] = ctx_len[b], its tokens
+ * keep their places in cu_new and get slot -1.  Requests behind one that the
+ * stack could not serve get no fresh pages either (the order of admission is
+ * kept).  *n_free above n_free_pages, or more new tokens than n_tokens, set
+ * KVQ_PAGED_ERR_LENGTH too; the stack is then read to n_free_pages, the slots
+ * are written to n_tokens.
+ * All arrays are device int32; seq_len, cu_new and n_left may not be the
+ * input arrays themselves. */
+KVQ_API kvq_status kvq_paged_plan(const int* ctx_len, const int* new_len, int batch,
+                                  int* block_table, int max_pages, const int* free_pages,
+                                  int n_free_pages, const int* n_free, int page_size, int n_tokens,
+                                  int* cu_new, int* seq_len, int* slots, int* n_left,
+                                  int* device_error, void* stream);
+
+/* Stores n_tokens new keys and values: token t goes to slots[t] (negative:
+ * nowhere).  k, v: device fp16 or bf16 [n_tokens][n_kv_heads][head_dim] at
+ * k_stride / v_stride elements a token.  Rows below the first one written to a
+ * page are its older rows.  Rows and pages without a slot are left as they
+ * are. */
+KVQ_API kvq_status kvq_paged_store(const kvq_paged_pool* pool, const void* k, const void* v,
+                                   int dtype, long long k_stride, long long v_stride,
+                                   const int* slots, int n_tokens, int* device_error,
+                                   void* stream);
+
+/* Bytes of kvq_paged_attention's workspace for this pool (host only).  The
+ * first 1024 bytes must be zero before the first call with it; every call
+ * leaves them zero. */
+KVQ_API kvq_status kvq_paged_workspace_bytes(const kvq_paged_pool* pool, size_t* bytes);
+
+/* Attention of the new tokens over the pages.  New token j of request b, row
+ * cu_new[b] + j of q and out, has position p = seq_len[b] - n + j (n =
+ * cu_new[b + 1] - cu_new[b] <= max_new) and sees the tokens t of its request
+ * with t <= p and, when window > 0, t > p - window:
+ *   out = sum_t softmax_t(softmax_scale * q . k_t) * v_t
+ * with query head hq reading kv head hq / (n_q_heads / n_kv_heads); zeros when
+ * it sees nothing.  max_new = 1 is a decode step, larger ones cover drafted
+ * tokens, prompts and chunks of prompts, mixed in one batch.
+ *   q, out       device fp16 or bf16 (dtype) [n_tokens][n_q_heads][head_dim]
+ *                at q_stride / out_stride elements a token.  Rows of no request
+ *                (behind cu_new[batch]) are left as they are.
+ *   block_table  [batch][max_pages]; only entries of pages that a new token
+ *                sees are read.  Rows of a page beyond the request's tokens may
+ *                hold anything.
+ *   workspace    kvq_paged_workspace_bytes(pool), 16-byte aligned.
+ * A request whose cu_new or seq_len break the contract (n > max_new, offsets
+ * outside [0, n_tokens], seq_len outside [0, max_pages * page_size]) is
+ * skipped, with KVQ_PAGED_ERR_LENGTH.  Sums run in fp32 in an order that does
+ * not depend on timing: equal calls give equal bits. */
+KVQ_API kvq_status kvq_paged_attention(const kvq_paged_pool* pool, const void* q, int dtype,
+                                       long long q_stride, void* out, long long out_stride,
+                                       int n_tokens, int n_q_heads, const int* block_table,
+                                       int max_pages, const int* cu_new, const int* seq_len,
+                                       int batch, int max_new, float softmax_scale, int window,
+                                       void* workspace, size_t n_workspace, int* device_error,
+                                       void* stream);
+
 /* Host-side lengths: quantized tokens and tail tokens per pair
  * (KVQ_ERR_UNSUPPORTED for a ragged cache). */
 KVQ_API kvq_status kvq_get_state(const kvq_cache* cache, int* T_q,
