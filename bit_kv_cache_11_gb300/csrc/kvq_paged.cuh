@@ -86,6 +86,14 @@ __device__ __forceinline__ void grid_dep_launch() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
+// Four E4M3 codes -> exact fp16 pairs: bytes 0 and 1, bytes 2 and 3.
+__device__ __forceinline__ void e4m3x4_to_half2x2(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(w));
+}
+
 // Tiled copy of one box of a 2-D tensor map into shared memory.
 __device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* map, int x, int y,
                                             uint64_t* bar) {
@@ -132,13 +140,19 @@ cudaError_t paged_decode_d64(const PagedAttnParams& p, const CUtensorMap& km, co
                              bool bf16, int nt, cudaStream_t st);
 cudaError_t paged_decode_d128(const PagedAttnParams& p, const CUtensorMap& km,
                               const CUtensorMap& vm, bool bf16, int nt, cudaStream_t st);
+cudaError_t launch_paged_prompt(const PagedAttnParams& a, int items_max, const CUtensorMap& km,
+                                const CUtensorMap& vm, int D, bool bf16, cudaStream_t st);
 // Lets kernel `fn` use `bytes` of dynamic shared memory on the current device
 // (set once per kernel and device).
 cudaError_t allow_smem(const void* fn, int bytes);
 // Warps per CTA of the decode kernel, its most CTAs (one per SM of a GB300) and
 // the tokens of a unit.
-constexpr int kPagedWarps = 8;
+constexpr int paged_warps(int) { return 8; }
 constexpr int kPagedMaxCtas = 152;
+// A request with at most this many query rows per kv head (new tokens * R) is
+// served by the decode kernel, which splits its tokens over the SMs and reads
+// them once per 16 rows; one with more rows by the prompt kernel.
+constexpr int kDecodeRows = 64;
 constexpr int paged_unit_tokens(int D) { return 4096 / D; }
 // Requests a call may have: the prefix sums of the batch live in shared memory.
 constexpr int kPagedMaxBatch = 4096;

@@ -112,8 +112,10 @@ bool row_map(CUtensorMap* m, void* pages, const kvq_paged_pool* c, int box_rows)
 constexpr size_t kTicketBytes = 1024;
 constexpr size_t part_floats(int rg, int D) { return static_cast<size_t>(rg) * (D + 2); }
 size_t workspace_bytes(int D) {
-  const size_t slots = static_cast<size_t>(kPagedMaxCtas) * (kPagedWarps + 2);
-  return kTicketBytes + slots * part_floats(16, D) * sizeof(float);
+  size_t most = 0;  // per CTA: a slot for each warp and two of its own
+  for (int nt = 1; nt <= 2; ++nt)
+    most = std::max(most, (paged_warps(nt) + 2) * part_floats(8 * nt, D) * sizeof(float));
+  return kTicketBytes + kPagedMaxCtas * most;
 }
 static_assert(kPagedMaxCtas * sizeof(int) <= kTicketBytes, "a ticket per CTA");
 
@@ -236,11 +238,18 @@ kvq_status kvq_paged_attention(const kvq_paged_pool* pool, const void* q, int dt
     return KVQ_ERR_UNSUPPORTED;
   max_new = std::min(max_new, n_tokens);
   const int nt = static_cast<long long>(max_new) * R <= 8 ? 1 : 2;
-  // units of all items are counted in 31 bits
+  // units of the decode kernel's items are counted in 31 bits
   const int ut = paged_unit_tokens(D);
   const long long span = static_cast<long long>(max_pages) * pool->page_size;
-  const double items = static_cast<double>(H) * (static_cast<double>(n_tokens) * R / (8 * nt) + batch);
-  if (items * (static_cast<double>(span) / ut + 2) >= 2147483647.0) return KVQ_ERR_UNSUPPORTED;
+  const long long rows_all = static_cast<long long>(n_tokens) * R;
+  const long long groups = std::min<long long>(static_cast<long long>(batch) * (kDecodeRows / (8 * nt)),
+                                               rows_all / (8 * nt) + batch);
+  if (static_cast<double>(H) * groups * (static_cast<double>(span) / ut + 2) >= 2147483647.0)
+    return KVQ_ERR_UNSUPPORTED;
+  // row-tile pairs of the prompt kernel, at most
+  const bool prompts = static_cast<long long>(max_new) * R > kDecodeRows;
+  const long long pairs = rows_all / 256 + std::min<long long>(batch, rows_all / (kDecodeRows + 1));
+  if (prompts && pairs * H > INT_MAX) return KVQ_ERR_UNSUPPORTED;
 
   int dev = 0, sms = 0;
   if (cudaGetDevice(&dev) != cudaSuccess ||
@@ -264,25 +273,39 @@ kvq_status kvq_paged_attention(const kvq_paged_pool* pool, const void* q, int dt
   p.R = R;
   p.lg_ps = log2_of(pool->page_size);
   p.n_pages = pool->n_pages;
-  p.box_rows = std::min(pool->page_size, ut);
   p.k_scale = pool->k_scale;
   p.v_scale = pool->v_scale;
   p.qscale = softmax_scale * 1.4426950408889634f;
   p.window = window;
   p.row_min = 1;
-  p.row_max = INT_MAX;
-  p.n_warps = std::min(sms, kPagedMaxCtas) * kPagedWarps;
+  p.row_max = kDecodeRows;
+  p.n_warps = std::min(sms, kPagedMaxCtas) * paged_warps(nt);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   p.tickets = reinterpret_cast<int*>(ws);
   p.warp_part = reinterpret_cast<float*>(ws + kTicketBytes);
   p.cta_part = p.warp_part + static_cast<size_t>(p.n_warps) * part_floats(8 * nt, D);
   p.err = device_error;
+  const bool bf = dtype == KVQ_DTYPE_BF16;
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
   CUtensorMap km, vm;
+  if (prompts && pairs > 0) {
+    PagedAttnParams a = p;
+    a.row_min = kDecodeRows + 1;
+    a.row_max = INT_MAX;
+    a.box_rows = pool->page_size;
+    if (!row_map(&km, pool->k_pages, pool, a.box_rows) ||
+        !row_map(&vm, pool->v_pages, pool, a.box_rows))
+      return KVQ_ERR_CUDA;
+    if (launch_paged_prompt(a, static_cast<int>(pairs), km, vm, D, bf, st) != cudaSuccess) {
+      cudaGetLastError();
+      return KVQ_ERR_CUDA;
+    }
+    count_launches(1);
+  }
+  p.box_rows = std::min(pool->page_size, ut);
   if (!row_map(&km, pool->k_pages, pool, p.box_rows) ||
       !row_map(&vm, pool->v_pages, pool, p.box_rows))
     return KVQ_ERR_CUDA;
-  const bool bf = dtype == KVQ_DTYPE_BF16;
-  const cudaStream_t st = static_cast<cudaStream_t>(stream);
   const cudaError_t e = D == 128 ? paged_decode_d128(p, km, vm, bf, nt, st)
                                  : paged_decode_d64(p, km, vm, bf, nt, st);
   if (e != cudaSuccess) {

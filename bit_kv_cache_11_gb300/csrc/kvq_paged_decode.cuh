@@ -54,9 +54,25 @@ __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(a));
+  return v;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t a) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
+  return v;
+}
+
+// No page is needed (a table entry is never this: ids are below 2^31 - 1).
+constexpr int kNoPage = 0x7fffffff;
+
 template <int D, int NT>
 struct PagedCfg {
-  static constexpr int NW = kPagedWarps;
+  static constexpr int NW = paged_warps(NT);
   static constexpr int UT = paged_unit_tokens(D);  // tokens of a unit
   static constexpr int GR = UT / 16;               // 16-token granules of a unit
   static constexpr int NS = 3;                     // stages of a warp
@@ -202,66 +218,82 @@ __global__ void __launch_bounds__(PagedCfg<D, NT>::NW * 32, 1)
   };
 
   // ---- the load cursor, NS units ahead -------------------------------------
-  PagedItem li;
+  PagedItem li = {};
   int lu = ua, lend = ua;      // next unit to load, end of its item
   int gbase = 0, grec = 0;     // granule records: read so far of this batch, ring position
   int llo = 0, lhi = 0;
-  int my_page = -1;            // lane's granule of the current batch of 32
-  // Refills the lanes' granule records from unit lu of item li on.
-  auto fetch_granules = [&]() {
-    const int tok = li.tok0 + (lu - li.u0) * UT + lane * 16;
-    my_page = -1;
-    float ks = 0.f, lv = 0.f, iv = 0.f;
-    // (records beyond this warp's range or the item are never used)
-    if (tok < lhi && tok + 16 > llo && lu + lane / GR < min(lend, ub)) {
-      const int page = p.table[static_cast<size_t>(li.b) * p.max_pages + (tok >> p.lg_ps)];
-      if (page >= 0 && page < p.n_pages) {
-        my_page = page;
-        const size_t at = static_cast<size_t>(page) * p.H + li.h;
-        ks = p.k_scale[at];
-        const float vs = p.v_scale[at];
-        lv = fast_log2(vs);
-        iv = 1.f / vs;
-      } else {
-        set_err(p.err, KVQ_PAGED_ERR_BAD_PAGE);
-      }
-    }
-    ring[(grec + lane) & (C::RING - 1)] = make_float4(ks, lv, iv, my_page >= 0 ? 1.f : 0.f);
-    gbase = 0;
+  // The lanes hold 32 granules at a time: their pages, and in the ring their
+  // scales.  The next 32 pages are requested as the current ones start, the
+  // next scales half way, so neither wait stops the stream.
+  int my_page = -1;
+  int nx_page = -1;
+  float nx_ks = 0.f, nx_vs = 1.f;
+  // Page of the lane's granule when the batch starts at unit u (-1: none).
+  auto granule_page = [&](int u) {
+    const int tok = li.tok0 + (u - li.u0) * UT + lane * 16;
+    // the granule's box, named by its first token that a row may see
+    const int box = tok & ~(p.box_rows - 1);
+    const int rep = max(box, llo);
+    // (granules beyond this warp's range or the item are never used)
+    if (rep < lhi && box + p.box_rows > llo && u + lane / GR < min(lend, ub))
+      return p.table[static_cast<size_t>(li.b) * p.max_pages + (rep >> p.lg_ps)];
+    return kNoPage;
   };
+  auto check_page = [&](int page) {
+    if (page == kNoPage) return -1;
+    if (page >= 0 && page < p.n_pages) return page;
+    set_err(p.err, KVQ_PAGED_ERR_BAD_PAGE);
+    return -1;
+  };
+  auto granule_scales = [&](int page, float* ks, float* vs) {
+    if (page < 0) return;
+    const size_t at = static_cast<size_t>(page) * p.H + li.h;
+    *ks = p.k_scale[at];
+    *vs = p.v_scale[at];
+  };
+  // The lane's record of the batch that starts at unit lu.
+  auto start_batch = [&](int page, float ks, float vs) {
+    const int tok = li.tok0 + (lu - li.u0) * UT + lane * 16;
+    my_page = page;
+    const bool seen = page >= 0 && tok < lhi && tok + 16 > llo;
+    ring[(grec + lane) & (C::RING - 1)] = make_float4(ks, fast_log2(vs), 1.f / vs, seen ? 1.f : 0.f);
+    gbase = 0;
+    nx_page = granule_page(lu + 32 / GR);
+  };
+  const int nbox = UT / p.box_rows;  // boxes of a side
+  // lane i < nbox copies key box i, lane nbox + i value box i
+  const bool key = lane < nbox;
+  const int bx = key ? lane : lane - nbox;
+  const uint32_t box_bytes = static_cast<uint32_t>(p.box_rows) * D;
+  const int box_g = bx * (p.box_rows / 16) & (GR - 1);  // first granule of the lane's box
   auto issue = [&](int s) {
     if (lu == lend) {
       find_item(lu, li);
       lend = li.u0 + li.nu;
       llo = seen_lo(li);
       lhi = seen_hi(li);
-      fetch_granules();
+      const int page = check_page(granule_page(lu));
+      float ks = 0.f, vs = 1.f;
+      granule_scales(page, &ks, &vs);
+      start_batch(page, ks, vs);
     } else if (gbase == 32) {
-      fetch_granules();
+      start_batch(nx_page, nx_ks, nx_vs);
+    } else if (gbase == 16) {
+      nx_page = check_page(nx_page);
+      nx_ks = 0.f;
+      nx_vs = 1.f;
+      granule_scales(nx_page, &nx_ks, &nx_vs);
     }
-    uint8_t* st = stages + s * C::STAGE;
-    const int nbox = UT / p.box_rows, gpb = p.box_rows / 16;  // boxes of a side, granules of a box
-    // lane i < nbox copies key box i, lane nbox + i value box i
-    const int bx = lane < nbox ? lane : lane - nbox;
-    int page = -1;
-    if (p.box_rows == 16) page = __shfl_sync(0xffffffffu, my_page, gbase + (bx & (GR - 1)));
-    else {
-      // a box spans granules of one page; any of them that is needed names it
-      for (int i = 0; i < gpb; ++i) {
-        const int x = __shfl_sync(0xffffffffu, my_page, gbase + ((bx * gpb + i) & (GR - 1)));
-        page = x >= 0 ? x : page;
-      }
-    }
+    const int page = __shfl_sync(0xffffffffu, my_page, gbase + box_g);
     const bool mine = lane < 2 * nbox && page >= 0;
-    const uint32_t box_bytes = static_cast<uint32_t>(p.box_rows) * D;
     const int n = __popc(__ballot_sync(0xffffffffu, mine));
     if (lane == 0) mbar_arrive_expect_tx(&bars[s], n * box_bytes);
     __syncwarp();
     if (mine) {
       const int tok = li.tok0 + (lu - li.u0) * UT + bx * p.box_rows;
       const int row = ((page * p.H + li.h) << p.lg_ps) + (tok & ((1 << p.lg_ps) - 1));
-      const bool key = lane < nbox;
-      tma_load_2d(st + (key ? 0 : 4096) + bx * box_bytes, key ? &kmap : &vmap, 0, row, &bars[s]);
+      tma_load_2d(stages + s * C::STAGE + (key ? 0 : 4096) + bx * box_bytes, key ? &kmap : &vmap,
+                  0, row, &bars[s]);
     }
     gbase += GR;
     grec += GR;
@@ -275,7 +307,7 @@ __global__ void __launch_bounds__(PagedCfg<D, NT>::NW * 32, 1)
   uint32_t qf[NT][KS][2];
   float acc[MT][NT][4];
   float m[NT][2], l[NT][2], cq[NT][2];
-  PagedItem it;
+  PagedItem it = {};
   int iend = ua;               // end of the current item
   int lo = 0, hi = 0, full_lo = 0, full_hi = 0;
   int crec = 0;                // ring position of the unit's first granule
@@ -349,38 +381,41 @@ __global__ void __launch_bounds__(PagedCfg<D, NT>::NW * 32, 1)
     }
   };
 
+  // This lane's places in a stage: its key chunks of token g (token g + 8 is
+  // 8 rows on, under the same swizzle), its value chunk of tokens 2t, 2t + 1.
+  uint32_t koff[KC], voff[2];
+#pragma unroll
+  for (int c = 0; c < KC; ++c)
+    koff[c] = D == 128 ? g * 128 + (((2 * t + c) ^ g) << 4) : g * 64 + ((t ^ (g >> 1)) << 4);
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    voff[i] = 4096 + (D == 128 ? (2 * t + i) * 128 + ((g ^ (2 * t + i)) << 4)
+                               : (2 * t + i) * 64 + (((g >> 1) ^ t) << 4) + 8 * (g & 1));
+  const uint32_t stages_s = smem_addr(stages);
+
   // One unit from stage memory.  MASK: some of its tokens are hidden from
   // some rows (or not there at all).
-  auto compute = [&](const uint8_t* st, int tok, auto masked) {
+  float4 rec[GR];  // the unit's granule records
+  auto compute = [&](uint32_t st, int tok, auto masked) {
     constexpr bool MASK = decltype(masked)::value;
     uint32_t pw[GR][NT][2];
     float s[GR][NT][4];
-    float4 rec[GR];
 #pragma unroll
     for (int mt = 0; mt < GR; ++mt) {
-      rec[mt] = ring[(crec + mt) & (C::RING - 1)];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int i = 0; i < 4; ++i) s[mt][nt][i] = 0.f;
-      const int r0 = mt * 16 + g, r1 = r0 + 8;
 #pragma unroll
       for (int c = 0; c < KC; ++c) {
-        uint4 a, b;
-        if constexpr (D == 128) {
-          const int ch = ((2 * t + c) ^ (r0 & 7)) << 4;  // r1 & 7 is the same
-          a = *reinterpret_cast<const uint4*>(st + r0 * 128 + ch);
-          b = *reinterpret_cast<const uint4*>(st + r1 * 128 + ch);
-        } else {
-          const int ch = (t ^ ((r0 >> 1) & 3)) << 4;
-          a = *reinterpret_cast<const uint4*>(st + r0 * 64 + ch);
-          b = *reinterpret_cast<const uint4*>(st + r1 * 64 + ch);
-        }
+        const uint4 a = lds128(st + koff[c] + mt * 16 * D);
+        const uint4 b = lds128(st + koff[c] + (mt * 16 + 8) * D);
         const uint32_t aw[4] = {a.x, a.y, a.z, a.w}, bw[4] = {b.x, b.y, b.z, b.w};
 #pragma unroll
         for (int w = 0; w < 4; ++w) {
-          const uint32_t a0 = e4m3x2_to_half2(aw[w]), a1 = e4m3x2_to_half2(bw[w]);
-          const uint32_t a2 = e4m3x2_to_half2(aw[w] >> 16), a3 = e4m3x2_to_half2(bw[w] >> 16);
+          uint32_t a0, a1, a2, a3;
+          e4m3x4_to_half2x2(aw[w], a0, a2);
+          e4m3x4_to_half2x2(bw[w], a1, a3);
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
             mma_16816(s[mt][nt], a0, a1, a2, a3, qf[nt][4 * c + w][0], qf[nt][4 * c + w][1]);
@@ -447,7 +482,6 @@ __global__ void __launch_bounds__(PagedCfg<D, NT>::NW * 32, 1)
         }
       }
     }
-    const uint8_t* sv = st + 4096;
 #pragma unroll
     for (int mt = 0; mt < GR; ++mt) {
       // value rows of tokens 2t, 2t + 1, 2t + 8, 2t + 9 of the granule:
@@ -456,23 +490,22 @@ __global__ void __launch_bounds__(PagedCfg<D, NT>::NW * 32, 1)
       uint32_t v[4][VW];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const int r = mt * 16 + 2 * t + (i & 1) + 8 * (i >> 1);
+        const uint32_t at = st + voff[i & 1] + (mt * 16 + 8 * (i >> 1)) * D;
         if constexpr (D == 128) {
-          const uint4 x = *reinterpret_cast<const uint4*>(sv + r * 128 + ((g ^ (r & 7)) << 4));
+          const uint4 x = lds128(at);
           v[i][0] = x.x;
           v[i][1] = x.y;
           v[i][2] = x.z;
           v[i][3] = x.w;
         } else {
-          const uint2 x = *reinterpret_cast<const uint2*>(
-              sv + r * 64 + (((g >> 1) ^ ((r >> 1) & 3)) << 4) + 8 * (g & 1));
+          const uint2 x = lds64(at);
           v[i][0] = x.x;
           v[i][1] = x.y;
         }
         if constexpr (MASK) {
           // what lies in hidden rows may decode to NaN, which a weight of 0
           // would not cancel
-          const int tk = tok + r;
+          const int tk = tok + mt * 16 + 2 * t + (i & 1) + 8 * (i >> 1);
           if (tk < lo || tk >= hi || rec[mt].w == 0.f) {
 #pragma unroll
             for (int w = 0; w < VW; ++w) v[i][w] = 0;
@@ -483,10 +516,11 @@ __global__ void __launch_bounds__(PagedCfg<D, NT>::NW * 32, 1)
       for (int w = 0; w < VW; ++w) {
         const uint32_t x0 = __byte_perm(v[0][w], v[1][w], 0x5140), x1 = __byte_perm(v[0][w], v[1][w], 0x7362);
         const uint32_t y0 = __byte_perm(v[2][w], v[3][w], 0x5140), y1 = __byte_perm(v[2][w], v[3][w], 0x7362);
-        const uint32_t a0 = e4m3x2_to_half2(x0), a1 = e4m3x2_to_half2(x0 >> 16);
-        const uint32_t a2 = e4m3x2_to_half2(y0), a3 = e4m3x2_to_half2(y0 >> 16);
-        const uint32_t b0 = e4m3x2_to_half2(x1), b1 = e4m3x2_to_half2(x1 >> 16);
-        const uint32_t b2 = e4m3x2_to_half2(y1), b3 = e4m3x2_to_half2(y1 >> 16);
+        uint32_t a0, a1, a2, a3, b0, b1, b2, b3;
+        e4m3x4_to_half2x2(x0, a0, a1);
+        e4m3x4_to_half2x2(y0, a2, a3);
+        e4m3x4_to_half2x2(x1, b0, b1);
+        e4m3x4_to_half2x2(y1, b2, b3);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
           mma_16816(acc[2 * w][nt], a0, a1, a2, a3, pw[mt][nt][0], pw[mt][nt][1]);
@@ -577,10 +611,13 @@ __global__ void __launch_bounds__(PagedCfg<D, NT>::NW * 32, 1)
     }
     const int tok = it.tok0 + (u - it.u0) * UT;
     if (tok < hi && tok + UT > lo) {
-      const uint8_t* sp = stages + st * C::STAGE;
+      const uint32_t sp = stages_s + st * C::STAGE;
       bool there = true;
 #pragma unroll
-      for (int i = 0; i < GR; ++i) there &= ring[(crec + i) & (C::RING - 1)].w != 0.f;
+      for (int i = 0; i < GR; ++i) {
+        rec[i] = ring[(crec + i) & (C::RING - 1)];
+        there &= rec[i].w != 0.f;
+      }
       if (there && tok >= full_lo && tok + UT <= full_hi) compute(sp, tok, std::false_type{});
       else compute(sp, tok, std::true_type{});
     }
@@ -684,11 +721,11 @@ __global__ void __launch_bounds__(PagedCfg<D, NT>::NW * 32, 1)
       __syncthreads();
       if (tid == 0) {
         const int seen = atomicAdd(&p.tickets[ca], 1);
-        flags[8] = seen == cb - ca;
+        flags[31] = seen == cb - ca;
         if (seen == cb - ca) p.tickets[ca] = 0;  // nobody else comes: ready for the next launch
       }
       __syncthreads();
-      if (flags[8]) {
+      if (flags[31]) {
         __threadfence();
         for (int e = tid; e < RG * D / 4; e += NW * 32) {
           const int r = e / (D / 4), ch = e % (D / 4) * 4;

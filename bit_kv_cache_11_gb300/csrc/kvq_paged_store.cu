@@ -113,12 +113,12 @@ __device__ __forceinline__ uint2 codes8(uint4 v, float inv, bool clean) {
 
 // Eight E4M3 codes times `f` (a power of two <= 1), rounded again.
 __device__ __forceinline__ uint2 rescale8(uint2 v, float f) {
-  const uint32_t w[4] = {v.x & 0xffffu, v.x >> 16, v.y & 0xffffu, v.y >> 16};
-  uint32_t c[4];
+  uint32_t w[4], c[4];
+  e4m3x4_to_half2x2(v.x, w[0], w[1]);
+  e4m3x4_to_half2x2(v.y, w[2], w[3]);
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const uint32_t h = e4m3x2_to_half2(w[i]);
-    float2 x = __half22float2(*reinterpret_cast<const __half2*>(&h));
+    float2 x = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
     x.x *= f;
     x.y *= f;
     c[i] = codes2(x);

@@ -277,232 +277,16 @@ def kvq_debug_set_wait_limit(handle, limit: int) -> None:
 
 
 # ---- the paged 8-bit cache ----------------------------------------------------
-#
-# The calls take the tensors a serving program keeps: E4M3 pages
-# [n_pages][n_kv_heads][page_size][head_dim] with fp32 scales
-# [n_pages][n_kv_heads], int32 tables and lengths (include/kvq.h has the
-# arithmetic and the contracts).  They run on the tensors' device, on torch's
-# current stream of it unless `stream` is given, and can be captured.
 
-def _bad(call: str, what: str):
-    raise KvqError(KVQ_ERR_INVALID_ARG, f"{call}: {what}")
-
-
-def _paged_device(call: str, device):
-    """Checks that `device` is a CUDA device; returns its index."""
-    if device.type != "cuda":
-        _bad(call, f"tensors must be on a CUDA device, not {device}")
-    return device.index
-
-
-def _ints_of(call: str, name: str, x, device, size: int, ndim: int = 1):
-    """x: contiguous int32 on `device` with at least `size` elements."""
-    import torch
-    if (x.dtype is not torch.int32 or x.dim() != ndim or x.device != device
-            or x.numel() < size or not x.is_contiguous()):
-        _bad(call, f"{name} must be a contiguous int32 tensor of {ndim} dimension(s) and at least "
-                   f"{size} elements on {device}")
-    return x.data_ptr()
-
-
-def _on_device(index: int, fn, *args):
-    """Runs fn(*args) with CUDA device `index` current."""
-    import torch
-    if torch.cuda.current_device() == index:
-        return fn(*args)
-    with torch.cuda.device(index):
-        return fn(*args)
-
-
-def _raw_stream(index: int, stream):
-    if stream is None:
-        import torch
-        return torch._C._cuda_getCurrentRawStream(index) or None
-    if isinstance(stream, int):
-        return stream or None
-    return stream.cuda_stream or None
-
-
-def _error_ptr(call: str, error, device):
-    return None if error is None else _ints_of(call, "error", error, device, 1)
-
-
-def _pool_of(call: str, k_pages, v_pages, k_scale, v_scale) -> kvq_paged_pool:
-    import torch
-    if (k_pages.dtype is not torch.float8_e4m3fn or v_pages.dtype is not torch.float8_e4m3fn
-            or k_pages.dim() != 4 or v_pages.shape != k_pages.shape
-            or not k_pages.is_contiguous() or not v_pages.is_contiguous()):
-        _bad(call, "k_pages and v_pages must be contiguous float8_e4m3fn tensors "
-                   "[n_pages][n_kv_heads][page_size][head_dim]")
-    n, h, ps, d = k_pages.shape
-    device = k_pages.device
-    for x in (k_scale, v_scale):
-        if (x.dtype is not torch.float32 or x.shape != (n, h) or not x.is_contiguous()
-                or x.device != device):
-            _bad(call, f"scales must be contiguous float32 tensors [{n}][{h}] on {device}")
-    if v_pages.device != device:
-        _bad(call, f"v_pages must be on {device}")
-    return kvq_paged_pool(k_pages.data_ptr(), v_pages.data_ptr(), k_scale.data_ptr(),
-                          v_scale.data_ptr(), n, h, ps, d)
-
-
-def _rows_of(call: str, name: str, x, heads: int, dim: int, device):
-    """x: [tokens][heads][dim], heads and dims contiguous; returns its token stride."""
-    import torch
-    if x.dim() != 3 or x.shape[1] != heads or x.shape[2] != dim or x.device != device:
-        _bad(call, f"{name} must be [tokens][{heads}][{dim}] on {device}")
-    st, sh, sd = x.stride()
-    if sd != 1 or (sh != dim and heads > 1):
-        _bad(call, f"{name}: the heads and channels of a token must be contiguous")
-    return st if x.shape[0] > 1 else heads * dim
-
-
-def _dtype_of(call: str, name: str, x) -> int:
-    import torch
-    if x.dtype is torch.float16:
-        return KVQ_DTYPE_FP16
-    if x.dtype is torch.bfloat16:
-        return KVQ_DTYPE_BF16
-    _bad(call, f"{name} must be float16 or bfloat16, not {x.dtype}")
-
-
-def kvq_paged_pool_check(n_pages: int, n_kv_heads: int, page_size: int, head_dim: int) -> int:
-    pool = kvq_paged_pool(None, None, None, None, int(n_pages), int(n_kv_heads), int(page_size),
-                          int(head_dim))
-    return _lib.kvq_paged_pool_check(ctypes.byref(pool))
-
-
-def kvq_paged_plan(ctx_len, new_len, block_table, free_pages, n_free, page_size: int,
-                   n_tokens: int, cu_new=None, seq_len=None, slots=None, n_left=None, error=None,
-                   stream=None):
-    """Block tables and slots of a serving step.
-
-    ctx_len, new_len: int32 [batch], cached and new tokens of each request;
-    block_table: int32 [batch][max_pages], written in place; free_pages: int32
-    stack of free page ids of which n_free[0] are left.  Returns (cu_new
-    [batch + 1], seq_len [batch], slots [n_tokens], n_left [1])."""
-    import torch
-    call = "kvq_paged_plan"
-    device = ctx_len.device
-    index = _paged_device(call, device)
-    batch, n_tokens = ctx_len.numel(), int(n_tokens)
-    if block_table.dim() != 2 or block_table.shape[0] != batch or n_tokens < 0:
-        _bad(call, f"block_table must be [{batch}][max_pages] and n_tokens >= 0")
-    made = [n for n, x in ((n_tokens, slots), (batch + 1, cu_new), (batch, seq_len), (1, n_left))
-            if x is None]
-    if made:
-        parts = iter(torch.empty(sum(made), dtype=torch.int32, device=device).split(made))
-        slots = next(parts) if slots is None else slots
-        cu_new = next(parts) if cu_new is None else cu_new
-        seq_len = next(parts) if seq_len is None else seq_len
-        n_left = next(parts) if n_left is None else n_left
-    i = _ints_of
-    status = _on_device(
-        index, _lib.kvq_paged_plan, i(call, "ctx_len", ctx_len, device, batch),
-        i(call, "new_len", new_len, device, batch), batch,
-        i(call, "block_table", block_table, device, 1, 2), block_table.shape[1],
-        i(call, "free_pages", free_pages, device, 0), free_pages.numel(),
-        i(call, "n_free", n_free, device, 1), int(page_size), n_tokens,
-        i(call, "cu_new", cu_new, device, batch + 1), i(call, "seq_len", seq_len, device, batch),
-        i(call, "slots", slots, device, n_tokens), i(call, "n_left", n_left, device, 1),
-        _error_ptr(call, error, device), _raw_stream(index, stream))
-    if status:
-        _check(status, call)
-    return cu_new, seq_len, slots, n_left
-
-
-def kvq_paged_store(k, v, slots, k_pages, v_pages, k_scale, v_scale, error=None,
-                    stream=None) -> None:
-    """Stores keys and values k, v (fp16 or bf16 [tokens][n_kv_heads][head_dim],
-    any token stride that is a multiple of 8) at their slots (int32 [tokens])."""
-    call = "kvq_paged_store"
-    device = k_pages.device
-    index = _paged_device(call, device)
-    pool = _pool_of(call, k_pages, v_pages, k_scale, v_scale)
-    dtype = _dtype_of(call, "k", k)
-    if v.dtype is not k.dtype or v.shape != k.shape:
-        _bad(call, "k and v must have the same type and shape")
-    ks = _rows_of(call, "k", k, pool.n_kv_heads, pool.head_dim, device)
-    vs = _rows_of(call, "v", v, pool.n_kv_heads, pool.head_dim, device)
-    n = k.shape[0]
-    status = _on_device(index, _lib.kvq_paged_store, ctypes.byref(pool), k.data_ptr(),
-                        v.data_ptr(), dtype, ks, vs, _ints_of(call, "slots", slots, device, n), n,
-                        _error_ptr(call, error, device), _raw_stream(index, stream))
-    if status:
-        _check(status, call)
-
-
-_paged_workspaces: dict = {}
-
-
-def _paged_workspace(pool: kvq_paged_pool, index: int, stream):
-    """The attention's workspace.  Calls on one stream run one after the other
-    and share one; a captured call gets its own from the capture's memory,
-    with the counters cleared by the graph, so graphs share nothing."""
-    import torch
-    key = (index, stream, pool.head_dim)
-    capturing = torch.cuda.is_current_stream_capturing()
-    ws = None if capturing else _paged_workspaces.get(key)
-    if ws is None:
-        n = ctypes.c_size_t(0)
-        _check(_lib.kvq_paged_workspace_bytes(ctypes.byref(pool), ctypes.byref(n)),
-               "kvq_paged_workspace_bytes")
-        ws = torch.empty(n.value, dtype=torch.uint8, device=f"cuda:{index}")
-        ws[:1024].zero_()
-        if not capturing:
-            torch.cuda.current_stream(index).synchronize()  # `stream` may be another one
-            _paged_workspaces[key] = ws
-    return ws
-
-
-def kvq_paged_attention(q, k_pages, v_pages, k_scale, v_scale, block_table, cu_new, seq_len,
-                        max_new: int = 1, softmax_scale: float | None = None, window: int = 0,
-                        out=None, workspace=None, error=None, stream=None):
-    """Attention of the new tokens over the pages; returns out, in q's type.
-
-    q: fp16 or bf16 [tokens][n_q_heads][head_dim]; request b's new tokens are
-    rows cu_new[b] .. cu_new[b + 1], the last of its seq_len[b] tokens;
-    max_new: the most new tokens of a request; window: how many tokens back a
-    token sees (0: all).  `workspace`: a uint8 tensor of
-    kvq_paged_workspace_bytes whose first 1024 bytes are zero, for callers
-    that overlap calls on streams of their own."""
-    import torch
-    call = "kvq_paged_attention"
-    device = k_pages.device
-    index = _paged_device(call, device)
-    pool = _pool_of(call, k_pages, v_pages, k_scale, v_scale)
-    dtype = _dtype_of(call, "q", q)
-    heads = q.shape[1] if q.dim() == 3 else 0
-    qs = _rows_of(call, "q", q, heads, pool.head_dim, device)
-    n = q.shape[0]
-    if out is None:
-        out = torch.empty(n, heads, pool.head_dim, dtype=q.dtype, device=device)
-        os_ = heads * pool.head_dim
-    else:
-        if out.dtype is not q.dtype or out.shape != q.shape:
-            _bad(call, "out must have q's type and shape")
-        os_ = _rows_of(call, "out", out, heads, pool.head_dim, device)
-    batch = seq_len.numel()
-    if block_table.dim() != 2 or block_table.shape[0] != batch:
-        _bad(call, f"block_table must be [{batch}][max_pages]")
-    if softmax_scale is None:
-        softmax_scale = pool.head_dim ** -0.5
-    st = _raw_stream(index, stream)
-    if workspace is None:
-        workspace = _on_device(index, _paged_workspace, pool, index, st)
-    elif workspace.dtype is not torch.uint8 or workspace.device != device \
-            or not workspace.is_contiguous():
-        _bad(call, f"workspace must be a contiguous uint8 tensor on {device}")
-    i = _ints_of
-    status = _on_device(
-        index, _lib.kvq_paged_attention, ctypes.byref(pool), q.data_ptr(), dtype, qs,
-        out.data_ptr(), os_, n, heads, i(call, "block_table", block_table, device, 1, 2),
-        block_table.shape[1], i(call, "cu_new", cu_new, device, batch + 1),
-        i(call, "seq_len", seq_len, device, batch), batch, int(max_new), softmax_scale,
-        int(window), workspace.data_ptr(), workspace.numel(), _error_ptr(call, error, device), st)
-    if status:
-        _check(status, call)
-    return out
+def __getattr__(name):
+    """kvq_paged_plan, kvq_paged_store, kvq_paged_attention and PagedCache live
+    in paged.py, which needs torch; it is imported at their first use."""
+    if name.startswith("kvq_paged_") or name == "PagedCache":
+        from . import paged
+        if hasattr(paged, name):
+            globals()[name] = getattr(paged, name)
+            return globals()[name]
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
 
 
 # ---- convenience -------------------------------------------------------------
@@ -654,73 +438,3 @@ class KVCache:
     def check(self, stream=None) -> None:
         _check(kvq_check_device_error(self.handle, stream), "kvq_check_device_error")
 
-
-class PagedCache:
-    """One layer's paged 8-bit KV cache: a pool of E4M3 pages with a
-    power-of-two scale for each page and kv head.
-
-    The requests' tables and lengths are the caller's; a serving step is::
-
-        cache = PagedCache(n_pages=4096, page_size=64, n_q_heads=32, n_kv_heads=8,
-                           head_dim=128)
-        cu, seq, slots, left = cache.plan(ctx_len, new_len, block_table, free_pages, n_free,
-                                          n_tokens)
-        cache.store(k, v, slots)        # [n_tokens][n_kv_heads][head_dim] fp16 or bf16
-        out = cache.attention(q, block_table, cu, seq, max_new=1)
-
-    The step's plan serves every layer's cache.  ``check`` raises for what the
-    kernels flagged since the last check (a page id outside the pool, a free
-    stack that ran out, a non-finite key or value)."""
-
-    def __init__(self, n_pages, page_size, n_q_heads, n_kv_heads, head_dim, device="cuda"):
-        import torch
-        _check(kvq_paged_pool_check(n_pages, n_kv_heads, page_size, head_dim),
-               "kvq_paged_pool_check")
-        if n_q_heads < 1 or n_q_heads % n_kv_heads:
-            _bad("PagedCache", "n_q_heads must be a multiple of n_kv_heads")
-        self.n_q_heads = int(n_q_heads)
-        self.page_size = int(page_size)
-        shape = (n_pages, n_kv_heads, page_size, head_dim)
-        zeros = lambda s, t: torch.zeros(s, dtype=t, device=device)  # noqa: E731
-        self.k_pages = zeros(shape, torch.uint8).view(torch.float8_e4m3fn)
-        self.v_pages = zeros(shape, torch.uint8).view(torch.float8_e4m3fn)
-        self.k_scale = zeros(shape[:2], torch.float32).fill_(2.0 ** -15)
-        self.v_scale = zeros(shape[:2], torch.float32).fill_(2.0 ** -15)
-        self.error = zeros(1, torch.int32)
-
-    def plan(self, ctx_len, new_len, block_table, free_pages, n_free, n_tokens, stream=None):
-        return kvq_paged_plan(ctx_len, new_len, block_table, free_pages, n_free, self.page_size,
-                              n_tokens, error=self.error, stream=stream)
-
-    def store(self, k, v, slots, stream=None):
-        kvq_paged_store(k, v, slots, self.k_pages, self.v_pages, self.k_scale, self.v_scale,
-                        error=self.error, stream=stream)
-
-    def attention(self, q, block_table, cu_new, seq_len, max_new=1, softmax_scale=None, window=0,
-                  out=None, stream=None):
-        if q.dim() == 3 and q.shape[1] != self.n_q_heads:
-            _bad("PagedCache.attention", f"q must have {self.n_q_heads} heads")
-        return kvq_paged_attention(q, self.k_pages, self.v_pages, self.k_scale, self.v_scale,
-                                   block_table, cu_new, seq_len, max_new=max_new,
-                                   softmax_scale=softmax_scale, window=window, out=out,
-                                   error=self.error, stream=stream)
-
-    def check(self) -> None:
-        """Synchronizes the device; raises KvqError for what the kernels flagged."""
-        import torch
-        torch.cuda.synchronize(self.error.device)
-        bits = int(self.error.item())
-        if not bits:
-            return
-        self.error.zero_()
-        if bits & KVQ_PAGED_ERR_WAIT:  # a split that did not finish leaves its counters
-            for ws in _paged_workspaces.values():
-                if ws.device == self.error.device:
-                    ws[:1024].zero_()
-        names = ((KVQ_PAGED_ERR_WAIT, "a bounded wait ran out"),
-                 (KVQ_PAGED_ERR_BAD_PAGE, "a page id outside the pool"),
-                 (KVQ_PAGED_ERR_NO_PAGES, "the free stack ran out"),
-                 (KVQ_PAGED_ERR_LENGTH, "a length breaks the call's contract"),
-                 (KVQ_PAGED_ERR_NONFINITE, "a non-finite key or value"))
-        what = ", ".join(n for b, n in names if bits & b)
-        raise KvqError(KVQ_ERR_DEVICE_CHECK, f"PagedCache.check: {what}")
