@@ -104,6 +104,11 @@ __device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* map, i
       : "memory");
 }
 
+// Brings a tensor map of the kernel's parameters into the descriptor cache.
+__device__ __forceinline__ void tensormap_prefetch(const CUtensorMap* map) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
+}
+
 // Lengths of request b as the attention uses them: new tokens, first new
 // token's row of q, all tokens.  Values that break the contract of
 // include/kvq.h serve nothing (n = 0) and set the error word.

@@ -83,7 +83,8 @@ struct PagedCfg {
   static constexpr int OFF_BAR = NW * NS * STAGE;
   static constexpr int OFF_RING = OFF_BAR + round_up(NW * NS * 8, 128);
   static constexpr int OFF_SEG = OFF_RING + NW * RING * 16;
-  static constexpr int OFF_CUM = OFF_SEG + 1024;
+  static constexpr int OFF_ITEM = OFF_SEG + 1024;
+  static constexpr int OFF_CUM = OFF_ITEM + NW * 4 * 48;
   static constexpr int smem(int batch) { return OFF_CUM + 4 * (batch + 1); }
   static_assert(PART * 4 <= NS * STAGE, "a warp's partial fits in its stages");
 };
@@ -101,8 +102,7 @@ struct PagedItem {
 // A warp's part of an item, for the join.
 struct PagedSeg {
   int u0, u1;      // the item's global units (u0 < 0: no segment)
-  int b, h, grp;
-  int where;       // 0: the warp's global slot, 1: its stages
+  int h, grp, q0, rows;
 };
 
 template <int D, int NT, bool BF16>
@@ -122,12 +122,17 @@ __global__ void __launch_bounds__(PagedCfg<D, NT>::NW * 32, 1)
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR) + warp * NS;
   float4* ring = reinterpret_cast<float4*>(smem + C::OFF_RING) + warp * C::RING;
   PagedSeg* segs = reinterpret_cast<PagedSeg*>(smem + C::OFF_SEG);  // [NW][2]
+  PagedItem* items = reinterpret_cast<PagedItem*>(smem + C::OFF_ITEM) + warp * 4;
   int* flags = reinterpret_cast<int*>(smem + C::OFF_SEG + NW * 2 * sizeof(PagedSeg));
   int* cum = reinterpret_cast<int*>(smem + C::OFF_CUM);
   if (lane == 0) {
     for (int s = 0; s < NS; ++s) mbar_init(&bars[s], 1);
     fence_barrier_init();
     segs[2 * warp].u0 = segs[2 * warp + 1].u0 = -1;
+    if (warp == 0) {
+      tensormap_prefetch(&kmap);
+      tensormap_prefetch(&vmap);
+    }
   }
   grid_dep_wait();
 
@@ -148,12 +153,13 @@ __global__ void __launch_bounds__(PagedCfg<D, NT>::NW * 32, 1)
     const int b0 = min(tid * per, p.batch), b1 = min(b0 + per, p.batch);
     int mine = 0;
     bool any_bad = false;
-    for (int b = b0; b < b1; ++b) {
+    auto cost = [&](int b) {
       int bad;
       const PagedReq r = load_req(b, &bad);
       any_bad |= bad != 0;
-      if (r.n > 0) mine += p.H * groups_of(r) * units_of(r);
-    }
+      return r.n > 0 ? p.H * groups_of(r) * units_of(r) : 0;
+    };
+    for (int b = b0; b < b1; ++b) mine += cost(b);
     int incl = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -166,10 +172,8 @@ __global__ void __launch_bounds__(PagedCfg<D, NT>::NW * 32, 1)
     for (int w = 0; w < warp; ++w) base += flags[w];
     int at = base + incl - mine;
     for (int b = b0; b < b1; ++b) {
-      int bad;
-      const PagedReq r = load_req(b, &bad);
       cum[b] = at;
-      if (r.n > 0) at += p.H * groups_of(r) * units_of(r);
+      at += per == 1 ? mine : cost(b);
     }
     if (b1 == p.batch && b0 < b1) cum[p.batch] = at;
     if (any_bad && blockIdx.x == 0) set_err(p.err, KVQ_PAGED_ERR_LENGTH);
@@ -251,14 +255,12 @@ __global__ void __launch_bounds__(PagedCfg<D, NT>::NW * 32, 1)
     *ks = p.k_scale[at];
     *vs = p.v_scale[at];
   };
-  // The lane's record of the batch that starts at unit lu.
-  auto start_batch = [&](int page, float ks, float vs) {
-    const int tok = li.tok0 + (lu - li.u0) * UT + lane * 16;
-    my_page = page;
-    const bool seen = page >= 0 && tok < lhi && tok + 16 > llo;
-    ring[(grec + lane) & (C::RING - 1)] = make_float4(ks, fast_log2(vs), 1.f / vs, seen ? 1.f : 0.f);
-    gbase = 0;
-    nx_page = granule_page(lu + 32 / GR);
+  int n_items = 0;  // items entered by the load cursor
+  // The lane's record of the batch that started at unit u0b, ring place rec0.
+  auto put_record = [&](int u0b, int rec0, float ks, float vs) {
+    const int tok = li.tok0 + (u0b - li.u0) * UT + lane * 16;
+    const bool seen = my_page >= 0 && tok < lhi && tok + 16 > llo;
+    ring[(rec0 + lane) & (C::RING - 1)] = make_float4(ks, fast_log2(vs), 1.f / vs, seen ? 1.f : 0.f);
   };
   const int nbox = UT / p.box_rows;  // boxes of a side
   // lane i < nbox copies key box i, lane nbox + i value box i
@@ -267,17 +269,23 @@ __global__ void __launch_bounds__(PagedCfg<D, NT>::NW * 32, 1)
   const uint32_t box_bytes = static_cast<uint32_t>(p.box_rows) * D;
   const int box_g = bx * (p.box_rows / 16) & (GR - 1);  // first granule of the lane's box
   auto issue = [&](int s) {
-    if (lu == lend) {
+    const int u_first = lu, rec_first = grec;
+    const bool fresh = lu == lend;
+    float ks = 0.f, vs = 1.f;
+    if (fresh) {
       find_item(lu, li);
       lend = li.u0 + li.nu;
       llo = seen_lo(li);
       lhi = seen_hi(li);
-      const int page = check_page(granule_page(lu));
-      float ks = 0.f, vs = 1.f;
-      granule_scales(page, &ks, &vs);
-      start_batch(page, ks, vs);
+      if (lane == 0) items[n_items & 3] = li;
+      ++n_items;
+      my_page = check_page(granule_page(lu));
+      granule_scales(my_page, &ks, &vs);  // on their way while the copies start
+      gbase = 0;
     } else if (gbase == 32) {
-      start_batch(nx_page, nx_ks, nx_vs);
+      my_page = nx_page;
+      put_record(lu, grec, nx_ks, nx_vs);
+      gbase = 0;
     } else if (gbase == 16) {
       nx_page = check_page(nx_page);
       nx_ks = 0.f;
@@ -295,9 +303,12 @@ __global__ void __launch_bounds__(PagedCfg<D, NT>::NW * 32, 1)
       tma_load_2d(stages + s * C::STAGE + (key ? 0 : 4096) + bx * box_bytes, key ? &kmap : &vmap,
                   0, row, &bars[s]);
     }
+    if (fresh) put_record(u_first, rec_first, ks, vs);
+    if (gbase == 0) nx_page = granule_page(lu + 32 / GR);
     gbase += GR;
     grec += GR;
     ++lu;
+    __syncwarp();
   };
 #pragma unroll
   for (int s = 0; s < NS; ++s)
@@ -313,8 +324,10 @@ __global__ void __launch_bounds__(PagedCfg<D, NT>::NW * 32, 1)
   int crec = 0;                // ring position of the unit's first granule
   bool failed = false;
 
-  auto enter = [&](int u) {
-    find_item(u, it);
+  int k_items = 0;  // items entered here
+  auto enter = [&]() {
+    it = items[k_items & 3];
+    ++k_items;
     iend = it.u0 + it.nu;
     lo = seen_lo(it);
     hi = seen_hi(it);
@@ -591,10 +604,10 @@ __global__ void __launch_bounds__(PagedCfg<D, NT>::NW * 32, 1)
       PagedSeg& sg = segs[2 * warp + (last ? 1 : 0)];
       sg.u0 = it.u0;
       sg.u1 = iend;
-      sg.b = it.b;
       sg.h = it.h;
       sg.grp = it.grp;
-      sg.where = last ? 1 : 0;
+      sg.q0 = it.q0;
+      sg.rows = it.rows;
     }
   };
 
@@ -603,7 +616,7 @@ __global__ void __launch_bounds__(PagedCfg<D, NT>::NW * 32, 1)
   for (int u = ua; u < ub; ++u) {
     if (u == iend) {
       if (u > ua) leave(false);
-      enter(u);
+      enter();
     }
     if (!mbar_wait_bounded(&bars[st], phase)) {
       failed = true;
@@ -644,15 +657,29 @@ __global__ void __launch_bounds__(PagedCfg<D, NT>::NW * 32, 1)
   }
 
   // ---- the CTA's join ---------------------------------------------------------
+  // Every warp lists the segments (two a warp: the partial it left on its way,
+  // in global memory, and its last one, in its stages) and their groups, runs
+  // of segments of one item; then each takes (group, row) tasks in turn.
   __syncthreads();
   const int cu0 = first_of(min(static_cast<int>(blockIdx.x) * NW, W));
   const int cu1 = first_of(min((static_cast<int>(blockIdx.x) + 1) * NW, W));
-  auto finish = [&](const PagedSeg& sg, int r, int ch, float M, float L, float4 o) {
-    int bad;
-    const PagedReq rq = load_req(sg.b, &bad);
-    const int row = sg.grp * RG + r;
-    if (row >= rq.n * p.R) return;
-    const int j = row / p.R;
+  const int cta = blockIdx.x;
+  PagedSeg sg = {-1, -1, 0, 0, 0, 0};
+  if (lane < 2 * NW) sg = segs[lane];
+  const uint32_t valid = __ballot_sync(0xffffffffu, sg.u0 >= 0);
+  const uint32_t below = valid & ((1u << lane) - 1);
+  const int before = __shfl_sync(0xffffffffu, sg.u0, below ? 31 - __clz(below) : 0);
+  const uint32_t leaders = __ballot_sync(0xffffffffu, sg.u0 >= 0 && (!below || before != sg.u0));
+  const int n_groups = __popc(leaders);
+  const float* mine = lane & 1 ? reinterpret_cast<const float*>(smem + (lane >> 1) * NS * C::STAGE)
+                               : p.warp_part + static_cast<size_t>(cta * NW + (lane >> 1)) * PART;
+  constexpr int VL = D / 4;     // lanes that hold a row as float4
+  const int ch = lane % VL * 4;
+  const bool writes = lane < VL;
+
+  // Row r of a finished item.
+  auto finish = [&](int h, int grp, int q0, int r, float L, float4 o) {
+    const int row = grp * RG + r, j = row / p.R;
     const float inv = L > 0.f ? 1.f / L : (L == 0.f ? 0.f : L);
     uint2 w;
     if constexpr (BF16) {
@@ -662,97 +689,170 @@ __global__ void __launch_bounds__(PagedCfg<D, NT>::NW * 32, 1)
     } else {
       w = make_uint2(pack_half2(o.x * inv, o.y * inv), pack_half2(o.z * inv, o.w * inv));
     }
-    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) +
-                              static_cast<long long>(rq.q0 + j) * p.out_stride +
-                              (static_cast<long long>(sg.h) * p.R + (row - j * p.R)) * D + ch) = w;
+    if (writes)
+      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) +
+                                static_cast<long long>(q0 + j) * p.out_stride +
+                                (static_cast<long long>(h) * p.R + (row - j * p.R)) * D + ch) = w;
   };
-  for (int i0 = 0; i0 < 2 * NW;) {
-    const PagedSeg sg = segs[i0];
-    if (sg.u0 < 0) {
-      ++i0;
+
+  uint32_t open = 0;  // leaders of groups that other CTAs share
+  for (int k = 0, task = 0; k < n_groups; ++k) {
+    uint32_t rest = leaders;
+    for (int i = 0; i < k; ++i) rest &= rest - 1;
+    const int lead = __ffs(rest) - 1;
+    rest &= rest - 1;
+    const uint32_t upto = rest ? (1u << (__ffs(rest) - 1)) - 1 : 0xffffffffu;
+    const uint32_t members = valid & upto & ~((1u << lead) - 1);
+    const int u0 = __shfl_sync(0xffffffffu, sg.u0, lead), u1 = __shfl_sync(0xffffffffu, sg.u1, lead);
+    const int h = __shfl_sync(0xffffffffu, sg.h, lead), grp = __shfl_sync(0xffffffffu, sg.grp, lead);
+    const int q0 = __shfl_sync(0xffffffffu, sg.q0, lead), rows = __shfl_sync(0xffffffffu, sg.rows, lead);
+    const bool starts = u0 >= cu0, whole = starts && u1 <= cu1;
+    if (!whole) open |= 1u << lead;
+    float* slot = p.cta_part + static_cast<size_t>(2 * cta + (starts ? 1 : 0)) * PART;
+    auto put = [&](int r, float M, float L, float4 o) {
+      if (whole) {
+        finish(h, grp, q0, r, L, o);
+      } else {
+        if (writes) *reinterpret_cast<float4*>(slot + r * D + ch) = o;
+        if (lane == 0) *reinterpret_cast<float2*>(slot + RG * D + 2 * r) = make_float2(M, L);
+      }
+    };
+    if (__popc(members) <= 2) {
+      // One or two members (many short items): one warp joins the group's
+      // rows, all their loads on their way at once.  Lane 16 i + r weighs row
+      // r of member i.
+      if (task++ % NW != warp) continue;
+      const int ma = lead, mb_ = 31 - __clz(members);
+      const bool two = mb_ != ma;
+      const float* pa = reinterpret_cast<const float*>(
+          __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(mine), ma));
+      const float* pb = reinterpret_cast<const float*>(
+          __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(mine), mb_));
+      float2 ml = make_float2(-INFINITY, 0.f);
+      const int rr = lane & 15;
+      if (rr < RG && (lane < 16 || two))
+        ml = *reinterpret_cast<const float2*>((lane < 16 ? pa : pb) + RG * D + 2 * rr);
+      const float M = fmaxf(ml.x, __shfl_xor_sync(0xffffffffu, ml.x, 16));
+      const float w = lane < 16 || two ? fast_exp2(ml.x - (M == -INFINITY ? 0.f : M)) : 0.f;
+      float L = ml.y * w;
+      L += __shfl_xor_sync(0xffffffffu, L, 16);
+#pragma unroll
+      for (int r0 = 0; r0 < RG; r0 += 4) {
+        if (r0 >= rows) break;
+        float4 a[4], b[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          a[i] = *reinterpret_cast<const float4*>(pa + (r0 + i) * D + ch);
+          b[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (two) b[i] = *reinterpret_cast<const float4*>(pb + (r0 + i) * D + ch);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int r = r0 + i;
+          const float wa = __shfl_sync(0xffffffffu, w, r), wb = __shfl_sync(0xffffffffu, w, 16 + r);
+          const float Mr = __shfl_sync(0xffffffffu, M, r), Lr = __shfl_sync(0xffffffffu, L, r);
+          if (r < rows)
+            put(r, Mr, Lr, make_float4(fmaf(a[i].x, wa, b[i].x * wb), fmaf(a[i].y, wa, b[i].y * wb),
+                                       fmaf(a[i].z, wa, b[i].z * wb), fmaf(a[i].w, wa, b[i].w * wb)));
+        }
+      }
       continue;
     }
-    int i1 = i0 + 1;
-    while (i1 < 2 * NW && (segs[i1].u0 < 0 || segs[i1].u0 == sg.u0)) ++i1;
-    const bool starts = sg.u0 >= cu0, ends = sg.u1 <= cu1;
-    const bool whole = starts && ends;
-    const int cta = blockIdx.x;
-    float* slot = p.cta_part + static_cast<size_t>(2 * cta + (starts ? 1 : 0)) * PART;
-    for (int e = tid; e < RG * D / 4; e += NW * 32) {
-      const int r = e / (D / 4), ch = e % (D / 4) * 4;
-      auto part = [&](int i) {
-        return segs[i].where ? reinterpret_cast<const float*>(smem + (i >> 1) * NS * C::STAGE)
-                             : p.warp_part + static_cast<size_t>(cta * NW + (i >> 1)) * PART;
-      };
-      float M = -INFINITY;
-      for (int i = i0; i < i1; ++i)
-        if (segs[i].u0 >= 0) M = fmaxf(M, part(i)[RG * D + 2 * r]);
-      const float mb = M == -INFINITY ? 0.f : M;
-      float L = 0.f;
+    for (int r = 0; r < rows; ++r, ++task) {
+      if (task % NW != warp) continue;
+      const bool in = (members >> lane) & 1;
+      float2 ml = make_float2(-INFINITY, 0.f);
+      if (in) ml = *reinterpret_cast<const float2*>(mine + RG * D + 2 * r);
+      float M = ml.x;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+      const float w = in ? fast_exp2(ml.x - (M == -INFINITY ? 0.f : M)) : 0.f;
+      const float L = warp_sum(in ? ml.y * w : 0.f);
       float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-      for (int i = i0; i < i1; ++i) {
-        if (segs[i].u0 < 0) continue;
-        const float* s = part(i);
-        const float w = fast_exp2(s[RG * D + 2 * r] - mb);
-        const float4 x = *reinterpret_cast<const float4*>(s + r * D + ch);
-        L = fmaf(s[RG * D + 2 * r + 1], w, L);
-        o.x = fmaf(x.x, w, o.x);
-        o.y = fmaf(x.y, w, o.y);
-        o.z = fmaf(x.z, w, o.z);
-        o.w = fmaf(x.w, w, o.w);
-      }
-      if (whole) {
-        finish(sg, r, ch, M, L, o);
-      } else {
-        *reinterpret_cast<float4*>(slot + r * D + ch) = o;
-        if (ch == 0) {
-          slot[RG * D + 2 * r] = M;
-          slot[RG * D + 2 * r + 1] = L;
+      for (uint32_t left = members; left;) {
+        float4 x[4];
+        float ws[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {  // up to four loads on their way
+          const int src = left ? __ffs(left) - 1 : lead;
+          const float* at = reinterpret_cast<const float*>(
+              __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(mine), src));
+          ws[i] = __shfl_sync(0xffffffffu, w, src);
+          x[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (left) x[i] = *reinterpret_cast<const float4*>(at + r * D + ch);
+          else ws[i] = 0.f;
+          left &= left - 1;
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          o.x = fmaf(x[i].x, ws[i], o.x);
+          o.y = fmaf(x[i].y, ws[i], o.y);
+          o.z = fmaf(x[i].z, ws[i], o.z);
+          o.w = fmaf(x[i].w, ws[i], o.w);
         }
       }
+      put(r, M, L, o);
     }
-    if (!whole) {
-      // CTAs that hold units of the item: its first unit's to its last unit's
-      auto owner = [&](int u) {
-        return static_cast<int>(((static_cast<long long>(u) + 1) * W - 1) / U) / NW;
-      };
+  }
+  if (open) {
+    // At most two groups of a CTA are shared, its first and its last.  The
+    // CTAs of an item are those of its first to its last unit; the one that
+    // draws the last ticket joins them, in their order.
+    auto owner = [&](int u) {
+      return static_cast<int>(((static_cast<long long>(u) + 1) * W - 1) / U) / NW;
+    };
+    __threadfence();
+    __syncthreads();
+    if (warp == 0 && ((open >> lane) & 1)) {
       const int ca = owner(sg.u0), cb = owner(sg.u1 - 1);
-      __threadfence();
-      __syncthreads();
-      if (tid == 0) {
-        const int seen = atomicAdd(&p.tickets[ca], 1);
-        flags[31] = seen == cb - ca;
-        if (seen == cb - ca) p.tickets[ca] = 0;  // nobody else comes: ready for the next launch
-      }
-      __syncthreads();
-      if (flags[31]) {
-        __threadfence();
-        for (int e = tid; e < RG * D / 4; e += NW * 32) {
-          const int r = e / (D / 4), ch = e % (D / 4) * 4;
-          auto part = [&](int c) { return p.cta_part + static_cast<size_t>(2 * c + (c == ca ? 1 : 0)) * PART; };
-          float M = -INFINITY;
-          for (int c = ca; c <= cb; ++c) M = fmaxf(M, __ldcg(part(c) + RG * D + 2 * r));
-          const float mb = M == -INFINITY ? 0.f : M;
-          float L = 0.f;
-          float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-          for (int c = ca; c <= cb; ++c) {
-            const float* s = part(c);
-            const float2 ml = __ldcg(reinterpret_cast<const float2*>(s + RG * D + 2 * r));
-            const float4 x = __ldcg(reinterpret_cast<const float4*>(s + r * D + ch));
-            const float w = fast_exp2(ml.x - mb);
-            L = fmaf(ml.y, w, L);
-            o.x = fmaf(x.x, w, o.x);
-            o.y = fmaf(x.y, w, o.y);
-            o.z = fmaf(x.z, w, o.z);
-            o.w = fmaf(x.w, w, o.w);
-          }
-          finish(sg, r, ch, M, L, o);
-        }
-      }
-      __syncthreads();
+      const int seen = atomicAdd(&p.tickets[ca], 1);
+      const bool all = seen == cb - ca;
+      if (all) p.tickets[ca] = 0;  // nobody else comes: ready for the next launch
+      flags[lane] = all;
     }
-    i0 = i1;
+    __syncthreads();
+    for (uint32_t todo = open; todo; todo &= todo - 1) {
+      const int lead = __ffs(todo) - 1;
+      if (!flags[lead]) continue;
+      __threadfence();
+      const int u0 = __shfl_sync(0xffffffffu, sg.u0, lead), u1 = __shfl_sync(0xffffffffu, sg.u1, lead);
+      const int h = __shfl_sync(0xffffffffu, sg.h, lead), grp = __shfl_sync(0xffffffffu, sg.grp, lead);
+      const int q0 = __shfl_sync(0xffffffffu, sg.q0, lead), rows = __shfl_sync(0xffffffffu, sg.rows, lead);
+      const int ca = owner(u0), cb = owner(u1 - 1);
+      auto part = [&](int c) {
+        return p.cta_part + static_cast<size_t>(2 * c + (c == ca ? 1 : 0)) * PART;
+      };
+      for (int r = warp; r < rows; r += NW) {
+        float M = -INFINITY;
+        for (int c = ca + lane; c <= cb; c += 32) M = fmaxf(M, __ldcg(part(c) + RG * D + 2 * r));
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+        const float mb = M == -INFINITY ? 0.f : M;
+        float L = 0.f;
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int c = ca; c <= cb; c += 8) {
+          float4 x[8];
+          float2 ml[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const float* at = part(min(c + i, cb));
+            ml[i] = __ldcg(reinterpret_cast<const float2*>(at + RG * D + 2 * r));
+            x[i] = __ldcg(reinterpret_cast<const float4*>(at + r * D + ch));
+          }
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            if (c + i > cb) continue;
+            const float w = fast_exp2(ml[i].x - mb);
+            L = fmaf(ml[i].y, w, L);
+            o.x = fmaf(x[i].x, w, o.x);
+            o.y = fmaf(x[i].y, w, o.y);
+            o.z = fmaf(x[i].z, w, o.z);
+            o.w = fmaf(x[i].w, w, o.w);
+          }
+        }
+        finish(h, grp, q0, r, L, o);
+      }
+    }
   }
 }
 

@@ -219,104 +219,142 @@ __global__ void __launch_bounds__(kRowWarps * 32) paged_store_rows_kernel(const 
 
 // ---- prompts: a CTA looks at a chunk of tokens and one head -----------------
 //
-// The run's vectors stay in registers between the maximum and the codes, so
-// every input byte is read once: 128 threads a side, 128 / (D / 8) rows a
-// step, at most kMaxSteps steps (a whole 128-row page).
-constexpr int kChunkThreads = 256;
-constexpr int kChunk = 32;  // tokens a CTA looks for leaders in
+// A team of TEAM = page_size * D / 64 threads stores one side of a run: eight
+// 16-byte vectors a thread cover a whole page, stay in registers between the
+// maximum and the codes, and are all on their way at once.  A CTA holds as
+// many teams as fit 256 threads (512 for the largest page) and looks for
+// leaders in as many tokens as its teams store at a time.
+template <int TEAM>
+__host__ __device__ constexpr int chunk_threads() {
+  return TEAM == 256 ? 512 : 256;
+}
+constexpr int kSteps = 8;
 
-template <int D, bool BF16>
-__global__ void __launch_bounds__(kChunkThreads) paged_store_chunk_kernel(const PagedStoreParams p) {
-  constexpr int VPR = D / 8, RPS = 128 / VPR, STEPS = 128 / RPS;
-  __shared__ uint32_t s_lead;
-  __shared__ int s_len;
-  __shared__ uint32_t s_max[2][2][4];  // [pass][side][warp]
+template <int D, bool BF16, int TEAM>
+__global__ void __launch_bounds__(chunk_threads<TEAM>())
+    paged_store_chunk_kernel(const PagedStoreParams p) {
+  constexpr int THREADS = chunk_threads<TEAM>(), TEAMS = THREADS / (2 * TEAM);
+  constexpr int VPR = D / 8, RPS = TEAM / VPR, CHUNK = TEAM * 64 / D * TEAMS;
+  constexpr int WPT = TEAM > 32 ? TEAM / 32 : 1;  // warps of a team's side
+  __shared__ int s_list[CHUNK];
+  __shared__ int s_count;
+  __shared__ uint32_t s_max[TEAMS][2][2][WPT];  // [team][pass][side][warp]
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int side = tid / TEAM & 1, team = tid / (2 * TEAM), l = tid % TEAM;
+  const int sub = l / VPR, vec = l % VPR;
+  const int tb = blockIdx.x * CHUNK, h = blockIdx.y;
+  const int ps = 1 << p.lg_ps;
+  if (tid == 0) s_count = 0;
   grid_dep_wait();
   grid_dep_launch();
-  const int tid = threadIdx.x, lane = tid & 31;
-  const int side = tid >> 7, l = tid & 127, sub = l / VPR, vec = l % VPR;
-  const int tb = blockIdx.x * kChunk, h = blockIdx.y;
-  const int ps = 1 << p.lg_ps;
-  if (tid < 32) {
-    const int t = tb + lane;
-    bool lead = false;
-    if (t < p.n_tokens) lead = leads(p, t, p.slots[t], t > 0 ? p.slots[t - 1] : -1);
-    const uint32_t m = __ballot_sync(0xffffffffu, lead);
-    if (lane == 0) s_lead = m;
+  __syncthreads();
+  if (tid < CHUNK) {
+    const int t = tb + tid;
+    if (t < p.n_tokens && leads(p, t, p.slots[t], t > 0 ? p.slots[t - 1] : -1))
+      s_list[atomicAdd(&s_count, 1)] = t;
   }
   __syncthreads();
-  uint32_t todo = s_lead;
-  while (todo) {
-    const int t = tb + __ffs(todo) - 1;
-    todo &= todo - 1;
-    const int slot = p.slots[t];
+  const int count = s_count;
+  // Threads of a run's two sides wait for one another (whole warps when a
+  // side is 16 or 32 threads).
+  auto team_sync = [&]() {
+    if constexpr (TEAM > 32)
+      asm volatile("bar.sync %0, %1;" ::"r"(1 + team), "n"(2 * TEAM) : "memory");
+    else __syncwarp();
+  };
+  // The side's largest value of x; *both: the larger one of the two sides.
+  auto side_max = [&](int pass, uint32_t x, uint32_t* both) {
+    if constexpr (TEAM > 32) {
+      x = __reduce_max_sync(0xffffffffu, x);
+      if (lane == 0) s_max[team][pass][side][l >> 5] = x;
+      team_sync();
+      uint32_t m[2] = {0, 0};
+#pragma unroll
+      for (int w = 0; w < WPT; ++w) {
+        m[0] = max(m[0], s_max[team][pass][0][w]);
+        m[1] = max(m[1], s_max[team][pass][1][w]);
+      }
+      *both = max(m[0], m[1]);
+      return side ? m[1] : m[0];
+    } else {
+#pragma unroll
+      for (int o = 1; o < TEAM; o <<= 1) x = max(x, __shfl_xor_sync(0xffffffffu, x, o));
+      *both = __reduce_max_sync(0xffffffffu, x);  // the warp's: it decides for its lanes
+      return x;
+    }
+  };
+  // (all lanes of a warp make the same number of rounds)
+  const int rounds = TEAM >= 32 ? (count - team + TEAMS - 1) / TEAMS : (count + TEAMS - 1) / TEAMS;
+  for (int k = 0; k < rounds; ++k) {
+    const int i_run = k * TEAMS + team;
+    const bool has = i_run < count;
+    const int t = has ? s_list[i_run] : 0;
+    const int slot = has ? p.slots[t] : 0;
     const int page = slot >> p.lg_ps, row0 = slot & (ps - 1);
-    if (page >= p.n_pages) {
-      if (tid == 0) set_err(p.err, KVQ_PAGED_ERR_BAD_PAGE);
-      continue;
-    }
-    // rows of the run: the first token that does not follow
-    const int most = min(ps - row0, p.n_tokens - t);
-    if (tid == 0) s_len = most;
-    __syncthreads();
-    if (tid < most && p.slots[t + tid] != slot + tid) atomicMin(&s_len, tid);
-    float* scale = (side ? p.scale[1] : p.scale[0]) + static_cast<size_t>(page) * p.H + h;
-    const float was = *scale;
-    __syncthreads();
-    const int n = s_len;
-    uint4 x[STEPS];
-    uint32_t m2 = 0;
+    const bool good = has && page < p.n_pages;
+    if (has && !good && l == 0 && side == 0) set_err(p.err, KVQ_PAGED_ERR_BAD_PAGE);
+    // rows that follow the leader: token t + i in row row0 + i of the page
+    const int most = good ? min(ps - row0, p.n_tokens - t) : 0;
+    float* scale = (side ? p.scale[1] : p.scale[0]) + static_cast<size_t>(good ? page : 0) * p.H + h;
+    uint4 x[kSteps];
+    uint32_t rows = 0;  // bit s: this thread holds a vector of step s
 #pragma unroll
-    for (int s = 0; s < STEPS; ++s) {
+    for (int s = 0; s < kSteps; ++s) {
       const int i = s * RPS + sub;
-      x[s] = make_uint4(0, 0, 0, 0);
-      if (i < n) x[s] = __ldg(vec_ptr(p, side, t + i, h, D, vec));
+      if (i < most && (i == 0 || p.slots[t + i] == slot + i)) rows |= 1u << s;
     }
 #pragma unroll
-    for (int s = 0; s < STEPS; ++s) m2 = vec_max(x[s], m2);
-    uint32_t mag = __reduce_max_sync(0xffffffffu, fold2(m2));
-    if (lane == 0) s_max[0][side][(tid >> 5) & 3] = mag;
-    __syncthreads();
-    mag = 0;
+    for (int s = 0; s < kSteps; ++s) {
+      x[s] = make_uint4(0, 0, 0, 0);
+      if ((rows >> s) & 1) x[s] = __ldg(vec_ptr(p, side, t + s * RPS + sub, h, D, vec));
+    }
+    const float was = good && row0 > 0 ? *scale : 0.f;
+    uint32_t m2 = 0, both;
 #pragma unroll
-    for (int w = 0; w < 4; ++w) mag = max(mag, s_max[0][side][w]);
-    const bool odd = mag >= inf_bits<BF16>();
-    if (__syncthreads_or(odd)) {
+    for (int s = 0; s < kSteps; ++s) m2 = vec_max(x[s], m2);
+    uint32_t mag = side_max(0, fold2(m2), &both);
+    const bool odd = mag >= inf_bits<BF16>();  // the side holds a NaN or an infinity
+    if (both >= inf_bits<BF16>()) {
       m2 = 0;
 #pragma unroll
-      for (int s = 0; s < STEPS; ++s) m2 = vec_max_finite<BF16>(x[s], m2);
-      const uint32_t mw = __reduce_max_sync(0xffffffffu, fold2(m2));
-      if (lane == 0) s_max[1][side][(tid >> 5) & 3] = mw;
-      __syncthreads();
-      mag = 0;
-#pragma unroll
-      for (int w = 0; w < 4; ++w) mag = max(mag, s_max[1][side][w]);
+      for (int s = 0; s < kSteps; ++s) m2 = vec_max_finite<BF16>(x[s], m2);
+      mag = side_max(1, fold2(m2), &both);
       if (odd && l == 0) set_err(p.err, KVQ_PAGED_ERR_NONFINITE);
     }
     int e = exp_for_bits<BF16>(mag);
-    uint8_t* base = (side ? p.pages[1] : p.pages[0]) + ((static_cast<size_t>(page) * p.H + h) << p.lg_ps) * D + vec * 8;
-    if (row0 > 0) {
-      e = max(e, exp_of_scale(was));
-      const float now = exp2i(e);
-      if (was != now && was > 0.f) {
-        const float f = was / now;
-        for (int i = sub; i < row0; i += RPS) {
-          uint2* c = reinterpret_cast<uint2*>(base + static_cast<size_t>(i) * D);
-          *c = rescale8(*c, f);
+    if (good) {
+      uint8_t* base = (side ? p.pages[1] : p.pages[0]) +
+                      ((static_cast<size_t>(page) * p.H + h) << p.lg_ps) * D + vec * 8;
+      if (row0 > 0) {
+        e = max(e, exp_of_scale(was));
+        const float now = exp2i(e);
+        if (was != now && was > 0.f) {
+          const float f = was / now;
+          for (int i = sub; i < row0; i += RPS) {
+            uint2* c = reinterpret_cast<uint2*>(base + static_cast<size_t>(i) * D);
+            *c = rescale8(*c, f);
+          }
         }
       }
-    }
-    const float inv = exp2i(-e);
+      const float inv = exp2i(-e);
 #pragma unroll
-    for (int s = 0; s < STEPS; ++s) {
-      const int i = s * RPS + sub;
-      if (i < n)
-        *reinterpret_cast<uint2*>(base + static_cast<size_t>(row0 + i) * D) =
-            codes8<BF16>(x[s], inv, odd);
+      for (int s = 0; s < kSteps; ++s) {
+        if ((rows >> s) & 1)
+          *reinterpret_cast<uint2*>(base + static_cast<size_t>(row0 + s * RPS + sub) * D) =
+              codes8<BF16>(x[s], inv, odd);
+      }
     }
-    if (l == 0) *scale = exp2i(e);
-    __syncthreads();  // s_len, s_max and `was` of the next run
+    team_sync();  // s_max and `was` are read
+    if (good && l == 0) *scale = exp2i(e);
   }
+}
+
+template <int D, bool BF16, int TEAM>
+cudaError_t launch_chunks(const PagedStoreParams& p, cudaLaunchConfig_t& cfg) {
+  constexpr int CHUNK = TEAM * 64 / D * (chunk_threads<TEAM>() / (2 * TEAM));
+  cfg.gridDim = dim3((p.n_tokens + CHUNK - 1) / CHUNK, p.H);
+  cfg.blockDim = dim3(chunk_threads<TEAM>());
+  return cudaLaunchKernelEx(&cfg, paged_store_chunk_kernel<D, BF16, TEAM>, p);
 }
 
 template <int D, bool BF16>
@@ -334,9 +372,18 @@ cudaError_t launch(const PagedStoreParams& p, cudaStream_t st) {
     cfg.blockDim = dim3(kRowWarps * 32);
     return cudaLaunchKernelEx(&cfg, paged_store_rows_kernel<D, BF16>, p);
   }
-  cfg.gridDim = dim3((p.n_tokens + kChunk - 1) / kChunk, p.H);
-  cfg.blockDim = dim3(kChunkThreads);
-  return cudaLaunchKernelEx(&cfg, paged_store_chunk_kernel<D, BF16>, p);
+  switch ((D << p.lg_ps) / 64) {
+    case 16:
+      if constexpr (D == 64) return launch_chunks<D, BF16, 16>(p, cfg);
+      break;
+    case 32: return launch_chunks<D, BF16, 32>(p, cfg);
+    case 64: return launch_chunks<D, BF16, 64>(p, cfg);
+    case 128: return launch_chunks<D, BF16, 128>(p, cfg);
+    case 256:
+      if constexpr (D == 128) return launch_chunks<D, BF16, 256>(p, cfg);
+      break;
+  }
+  return cudaErrorInvalidValue;
 }
 
 }  // namespace
