@@ -14,7 +14,7 @@
 //   converters (4 warps)  raw codes -> fp16 tiles in shared memory, 128-byte
 //                         swizzle; the same layout serves keys (K-major
 //                         operand) and values (N-major operand)
-//   issuer     (1 thread) S_w = Q_w K^T, O_w += P_w V   (w = 0, 1)
+//   issuer     (1 warp)   S_w = Q_w K^T, O_w += P_w V   (w = 0, 1)
 //   softmax    (2 x 4 warps) a thread owns a row: maximum, weights, P into
 //                         tensor memory over S, rescaling of O when its
 //                         maximum moved by more than kLazy
@@ -39,6 +39,8 @@ struct PagedPromptParams {
   int items_max;  // row-tile pairs of all requests, at most
 };
 
+__host__ __device__ constexpr int round_up128(int x) { return (x + 127) / 128 * 128; }
+
 template <int D>
 struct PromptCfg {
   static constexpr int N = 128;                   // tokens of a tile
@@ -56,19 +58,26 @@ struct PromptCfg {
   static constexpr int OFF_REC = OFF_RAW + NRAW * RAW;
   static constexpr int OFF_BAR = OFF_REC + NREC * REC * 16;
   static constexpr int NBAR = 2 * NRAW + 2 * NT + NREC + 2 + 2 + 2 + 2 + 1;
-  static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
+  static constexpr int OFF_MISC = round_up128(OFF_BAR + NBAR * 8);
   static constexpr int SMEM = OFF_MISC + 128 + 1024;  // 1024 for the base's alignment
-  static constexpr int THREADS = 448;
-  static constexpr uint32_t S_COL = 0, O_COL = 256;
+  static constexpr int THREADS = 512;
+  // Registers of a thread: 128 at launch, then by role (two softmax groups,
+  // the converters, the rest); the sum stays the launch's 512 * 128.
+  static constexpr int R_SOFTMAX = 176, R_CONVERT = 96, R_REST = 64;
+  static_assert(256 * R_SOFTMAX + 128 * R_CONVERT + 128 * R_REST == 512 * 128, "register split");
+  static constexpr uint32_t S_COL = 0, O_COL = 256, P_OFF = 64;  // P: upper half of S
 };
 
 // ---- tcgen05 -------------------------------------------------------------
 
-__device__ __forceinline__ uint64_t umma_desc(uint32_t addr, uint32_t lbo, uint32_t sbo) {
-  // start, leading and stride byte offsets in 16-byte units; version 1;
-  // 128-byte swizzle
-  return static_cast<uint64_t>((addr >> 4) & 0x3fffu) | (static_cast<uint64_t>(lbo >> 4) << 16) |
-         (static_cast<uint64_t>(sbo >> 4) << 32) | (1ull << 46) | (2ull << 61);
+// Shared-memory operand descriptor.  High word: stride byte offset in 16-byte
+// units, version 1, 128-byte swizzle; low word: start address and leading byte
+// offset in 16-byte units.  Operands of one tile differ in the low word alone.
+__host__ __device__ constexpr uint32_t umma_desc_hi(uint32_t sbo) {
+  return (sbo >> 4) | (1u << 14) | (2u << 29);
+}
+__device__ __forceinline__ uint32_t umma_desc_lo(uint32_t addr, uint32_t lbo) {
+  return ((addr >> 4) & 0x3fffu) | ((lbo >> 4) << 16);
 }
 
 // Instruction descriptor: fp32 accumulator, fp16 operands, M = 128.
@@ -77,27 +86,33 @@ __host__ __device__ constexpr uint32_t umma_idesc(int n, bool b_n_major) {
          (static_cast<uint32_t>(128 / 16) << 24);
 }
 
-__device__ __forceinline__ void umma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
-                                        bool accumulate) {
+// The products are issued by one lane (`one`) of a warp that runs converged, so
+// the operands' words stay warp-uniform values.
+__device__ __forceinline__ void umma_ss(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t hi,
+                                        uint32_t idesc, uint32_t accumulate, uint32_t one) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(accumulate))
+      "{\n\t.reg .pred p, q;\n\t.reg .b64 a, b;\n\tsetp.ne.b32 p, %5, 0;\n\t"
+      "setp.ne.b32 q, %6, 0;\n\tmov.b64 a, {%1, %3};\n\tmov.b64 b, {%2, %3};\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, p;\n\t}" ::"r"(d),
+      "r"(a_lo), "r"(b_lo), "r"(hi), "r"(idesc), "r"(accumulate), "r"(one)
       : "memory");
 }
-__device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
-                                        bool accumulate) {
+__device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a, uint32_t b_lo, uint32_t hi,
+                                        uint32_t idesc, uint32_t accumulate, uint32_t one) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(accumulate))
+      "{\n\t.reg .pred p, q;\n\t.reg .b64 b;\n\tsetp.ne.b32 p, %5, 0;\n\t"
+      "setp.ne.b32 q, %6, 0;\n\tmov.b64 b, {%2, %3};\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b_lo), "r"(hi), "r"(idesc), "r"(accumulate), "r"(one)
       : "memory");
 }
 // Arrives on `bar` when the products issued so far are complete.
-__device__ __forceinline__ void umma_commit(uint64_t* bar) {
+__device__ __forceinline__ void umma_commit(uint64_t* bar, uint32_t one) {
   asm volatile(
-      "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
-          smem_addr(bar))
+      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(
+          smem_addr(bar)),
+      "r"(one)
       : "memory");
 }
 __device__ __forceinline__ void tmem_fence_before() {
@@ -126,17 +141,14 @@ __device__ __forceinline__ void tmem_ld32(uint32_t addr, uint32_t (&r)[32]) {
         "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
       : "r"(addr));
 }
-__device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t (&r)[32]) {
+__device__ __forceinline__ void tmem_ld16(uint32_t addr, uint32_t (&r)[16]) {
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], "
-      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};" ::"r"(r[0]),
-      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
-      "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]),
-      "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]),
-      "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]),
-      "r"(r[30]), "r"(r[31]), "r"(addr)
-      : "memory");
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
+      : "r"(addr));
 }
 __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t (&r)[16]) {
   asm volatile(
@@ -163,6 +175,22 @@ __device__ __forceinline__ float lg2(float x) {
   float y;
   asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;"
+      : "=l"(reinterpret_cast<unsigned long long&>(d))
+      : "l"(reinterpret_cast<unsigned long long&>(a)), "l"(reinterpret_cast<unsigned long long&>(b)),
+        "l"(reinterpret_cast<unsigned long long&>(c)));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("add.rn.f32x2 %0, %1, %2;"
+      : "=l"(reinterpret_cast<unsigned long long&>(d))
+      : "l"(reinterpret_cast<unsigned long long&>(a)), "l"(reinterpret_cast<unsigned long long&>(b)));
+  return d;
 }
 __device__ __forceinline__ uint32_t half2_bits(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
@@ -207,6 +235,7 @@ __global__ void __launch_bounds__(PromptCfg<D>::THREADS, 1)
   uint64_t* q_full = o_done + 2;
   uint64_t* drain = q_full + 2;
   float4* recs = reinterpret_cast<float4*>(smem + C::OFF_REC);
+  int* whole = reinterpret_cast<int*>(smem + C::OFF_MISC + 64);  // [NREC] every granule is there
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_MISC);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC + 4);
   PromptItem* found = reinterpret_cast<PromptItem*>(smem + C::OFF_MISC + 16);
@@ -288,6 +317,24 @@ __global__ void __launch_bounds__(PromptCfg<D>::THREADS, 1)
       }
     }
   }
+  __syncthreads();
+  grid_dep_launch();
+  const PromptItem it = *found;
+  if (it.b < 0) return;
+  const int nt = it.nt;
+  if (nt == 0) {
+    // no token is seen: zero rows
+    for (int e = tid; e < C::ROWS * (D / 8); e += C::THREADS) {
+      const int row = it.row0 + e / (D / 8);
+      if (row >= it.rows) break;
+      const int j = row / p.R;
+      reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) +
+                               static_cast<long long>(it.q0 + j) * p.out_stride +
+                               (static_cast<long long>(it.h) * p.R + (row - j * p.R)) * D)[e % (D / 8)] =
+          make_uint4(0, 0, 0, 0);
+    }
+    return;
+  }
   if (warp == 13) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
                      smem_addr(tmem_slot))
@@ -297,11 +344,8 @@ __global__ void __launch_bounds__(PromptCfg<D>::THREADS, 1)
   tmem_fence_before();
   __syncthreads();
   tmem_fence_after();
-  grid_dep_launch();
   const uint32_t tmem = *tmem_slot;
-  const PromptItem it = *found;
   const int halves = it.rows - it.row0 > 128 ? 2 : 1;
-  const int nt = it.b < 0 ? 0 : it.nt;
 
   // Bounded wait; false when it ran out or another role gave up.
   auto wait = [&](uint64_t* bar, uint32_t parity) {
@@ -314,71 +358,129 @@ __global__ void __launch_bounds__(PromptCfg<D>::THREADS, 1)
     return false;
   };
 
-  if (nt > 0 && warp == 12) {
-    // ================================================================ loader
-    const int box = p.box_rows, nbox = N / box;
-    const uint32_t box_bytes = static_cast<uint32_t>(box) * D;
-    int raw = 0;  // raw tiles requested so far
-    int pend = 0;
-    // lane l holds granule l % 8 of tile l / 8 of a batch of four tiles
-    auto granule_page = [&](int i) {
-      const int tile = i + lane / 8;
-      const int tok = it.t0 + tile * N + lane % 8 * 16;
-      const int bx = tok & ~(box - 1), rep = max(bx, it.lo);
-      if (tile >= nt || rep >= it.hi || bx + box <= it.lo) return -1;
-      const int page = p.table[static_cast<size_t>(it.b) * p.max_pages + (rep >> p.lg_ps)];
-      if (page >= 0 && page < p.n_pages) return page;
-      set_err(p.err, KVQ_PAGED_ERR_BAD_PAGE);
-      return -1;
-    };
-    int page = -1, next = granule_page(0);
-    bool ok = true;
-    for (int i = 0; i < nt && ok; ++i) {
-      if (i % 4 == 0) {
-        page = next;
-        next = granule_page(i + 4);
-      }
-      // the tile's records
-      if (lane / 8 == i % 4) {
-        const int tok = it.t0 + i * N + lane % 8 * 16;
-        float ks = 0.f, vs = 1.f;
-        if (page >= 0) {
-          const size_t at = static_cast<size_t>(page) * p.H + it.h;
-          ks = p.k_scale[at];
-          vs = p.v_scale[at];
+  if (warp >= 12) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::R_REST));
+    if (warp == 12) {
+      // ================================================================ loader
+      const int box = p.box_rows, nbox = N / box;
+      const uint32_t box_bytes = static_cast<uint32_t>(box) * D;
+      int raw = 0;  // raw tiles requested so far
+      int pend = 0;
+      // lane l holds granule l % 8 of tile l / 8 of a batch of four tiles
+      auto granule_page = [&](int i) {
+        const int tile = i + lane / 8;
+        const int tok = it.t0 + tile * N + lane % 8 * 16;
+        const int bx = tok & ~(box - 1), rep = max(bx, it.lo);
+        if (tile >= nt || rep >= it.hi || bx + box <= it.lo) return -1;
+        const int page = p.table[static_cast<size_t>(it.b) * p.max_pages + (rep >> p.lg_ps)];
+        if (page >= 0 && page < p.n_pages) return page;
+        set_err(p.err, KVQ_PAGED_ERR_BAD_PAGE);
+        return -1;
+      };
+      int page = -1, next = granule_page(0);
+      bool ok = true;
+      for (int i = 0; i < nt && ok; ++i) {
+        if (i % 4 == 0) {
+          page = next;
+          next = granule_page(i + 4);
         }
-        const bool seen = page >= 0 && tok < it.hi && tok + 16 > it.lo;
-        recs[i % C::NREC * C::REC + lane % 8] =
-            make_float4(ks, lg2(vs), 1.f / vs, seen ? 1.f : 0.f);
-      }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&rec_full[i % C::NREC]);
-      // lane l < nbox copies box l of the tile
-      const int src = (i % 4) * 8 + (lane < nbox ? lane : 0) * (box / 16);
-      const int pg = __shfl_sync(0xffffffffu, page, src);
-      const bool mine = lane < nbox && pg >= 0;
-      const int count = __popc(__ballot_sync(0xffffffffu, mine));
-      const int tok = it.t0 + i * N + lane * box;
-      const int row = mine ? ((pg * p.H + it.h) << p.lg_ps) + (tok & ((1 << p.lg_ps) - 1)) : 0;
-#pragma unroll
-      for (int side = 0; side < 2; ++side, ++raw) {
-        const int s = raw % NRAW;
-        if (raw >= NRAW && !wait(&raw_empty[s], raw / NRAW - 1)) {
-          ok = false;
-          break;
+        // the tile's records
+        if (lane / 8 == i % 4) {
+          const int tok = it.t0 + i * N + lane % 8 * 16;
+          float ks = 0.f, vs = 1.f;
+          if (page >= 0) {
+            const size_t at = static_cast<size_t>(page) * p.H + it.h;
+            ks = p.k_scale[at];
+            vs = p.v_scale[at];
+          }
+          const bool seen = page >= 0 && tok < it.hi && tok + 16 > it.lo;
+          recs[i % C::NREC * C::REC + lane % 8] =
+              make_float4(ks, lg2(vs), 1.f / vs, seen ? 1.f : 0.f);
+          const uint32_t m = 0xffu << (lane & 24);
+          const uint32_t all = __ballot_sync(m, seen);
+          if (lane % 8 == 0) whole[i % C::NREC] = all == m;
         }
-        if (lane == 0) mbar_arrive_expect_tx(&raw_full[s], count * box_bytes);
         __syncwarp();
-        if (mine)
-          tma_load_2d(smem + C::OFF_RAW + s * C::RAW + lane * box_bytes, side ? &vmap : &kmap, 0,
-                      row, &raw_full[s]);
-        pend = raw + 1;
+        if (lane == 0) mbar_arrive(&rec_full[i % C::NREC]);
+        // lane l < nbox copies box l of the tile
+        const int src = (i % 4) * 8 + (lane < nbox ? lane : 0) * (box / 16);
+        const int pg = __shfl_sync(0xffffffffu, page, src);
+        const bool mine = lane < nbox && pg >= 0;
+        const int count = __popc(__ballot_sync(0xffffffffu, mine));
+        const int tok = it.t0 + i * N + lane * box;
+        const int row = mine ? ((pg * p.H + it.h) << p.lg_ps) + (tok & ((1 << p.lg_ps) - 1)) : 0;
+#pragma unroll
+        for (int side = 0; side < 2; ++side, ++raw) {
+          const int s = raw % NRAW;
+          if (raw >= NRAW && !wait(&raw_empty[s], raw / NRAW - 1)) {
+            ok = false;
+            break;
+          }
+          if (lane == 0) mbar_arrive_expect_tx(&raw_full[s], count * box_bytes);
+          __syncwarp();
+          if (mine)
+            tma_load_2d(smem + C::OFF_RAW + s * C::RAW + lane * box_bytes, side ? &vmap : &kmap, 0,
+                        row, &raw_full[s]);
+          pend = raw + 1;
+        }
       }
+      // no copy may be in flight when the CTA leaves: the last NRAW of them
+      for (int r = max(0, pend - NRAW); r < pend; ++r)
+        mbar_wait_bounded(&raw_full[r % NRAW], (r / NRAW) & 1, kRoleWait);
+    } else if (warp == 13) {
+      // ================================================================ issuer
+      constexpr uint32_t id_s = umma_idesc(N, false), id_o = umma_idesc(D, true);
+      constexpr uint32_t hi = umma_desc_hi(1024);
+      const uint32_t one = lane == 0;
+      const uint32_t q_lo = umma_desc_lo(base + C::OFF_Q, 16);
+      const uint32_t k_lo = umma_desc_lo(base + C::OFF_T, 16);
+      const uint32_t v_lo = umma_desc_lo(base + C::OFF_T, N * 128);
+      auto scores = [&](int w, int i) {
+        const uint32_t q = q_lo + w * (C::QT >> 4), k = k_lo + (2 * i) % NT * (C::TILE >> 4);
+        const uint32_t d = tmem + C::S_COL + w * 128;
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks) {
+          const uint32_t off = ((ks >> 2) * (128 * 128) + (ks & 3) * 32) >> 4;
+          umma_ss(d, q + off, k + off, hi, id_s, ks > 0, one);
+        }
+        umma_commit(&s_full[w], one);
+      };
+      auto outputs = [&](int w, int i) {
+        const uint32_t v = v_lo + (2 * i + 1) % NT * (C::TILE >> 4);
+        const uint32_t d = tmem + C::O_COL + w * D, a = tmem + C::S_COL + w * 128 + C::P_OFF;
+#pragma unroll
+        for (int ks = 0; ks < N / 16; ++ks)
+          umma_ts(d, a + ks * 8, v + ks * (2048 >> 4), hi, id_o, i > 0 || ks > 0, one);
+        umma_commit(&o_done[w], one);
+      };
+      auto tile_ready = [&](int x) { return wait(&t_full[x % NT], x / NT); };
+      bool ok = tile_ready(0);
+      for (int w = 0; w < halves && ok; ++w) {
+        ok = wait(&q_full[w], 0);
+        if (!ok) break;
+        tmem_fence_after();
+        scores(w, 0);
+      }
+      if (ok) umma_commit(&t_empty[0], one);
+      for (int i = 0; i < nt && ok; ++i) {
+        ok = tile_ready(2 * i + 1) && (i + 1 >= nt || tile_ready(2 * i + 2));
+        for (int w = 0; w < halves && ok; ++w) {
+          ok = wait(&p_full[w], i);
+          if (!ok) break;
+          tmem_fence_after();
+          outputs(w, i);
+          if (i + 1 < nt) scores(w, i + 1);
+        }
+        if (!ok) break;
+        umma_commit(&t_empty[(2 * i + 1) % NT], one);
+        if (i + 1 < nt) umma_commit(&t_empty[(2 * i + 2) % NT], one);
+      }
+      // no product and no arrival may be in flight when the CTA leaves
+      umma_commit(drain, one);
+      mbar_wait_bounded(drain, 0, kRoleWait);
     }
-    // no copy may be in flight when the CTA leaves: the last NRAW of them
-    for (int r = max(0, pend - NRAW); r < pend; ++r)
-      mbar_wait_bounded(&raw_full[r % NRAW], (r / NRAW) & 1, kRoleWait);
-  } else if (nt > 0 && warp >= 8 && warp < 12) {
+  } else if (warp >= 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::R_CONVERT));
     // ============================================================ converters
     const int ct = tid - 256;  // 0 .. 127
     constexpr int CH = D / 16;             // 16-byte chunks of a raw row
@@ -391,11 +493,7 @@ __global__ void __launch_bounds__(PromptCfg<D>::THREADS, 1)
       uint8_t* dst = smem + C::OFF_T + d * C::TILE;
       const int tok = it.t0 + i * N;
       // rows of no page or no token may hold anything: they become zeros
-      bool edge = tok < it.lo || tok + N > it.hi;
-      if (!edge) {
-#pragma unroll
-        for (int g = 0; g < C::REC; ++g) edge |= recs[i % C::NREC * C::REC + g].w == 0.f;
-      }
+      const bool edge = tok < it.lo || tok + N > it.hi || !whole[i % C::NREC];
 #pragma unroll 4
       for (int k = 0; k < PASS; ++k) {
         int row, j;
@@ -434,245 +532,201 @@ __global__ void __launch_bounds__(PromptCfg<D>::THREADS, 1)
         mbar_arrive(&raw_empty[s]);
       }
     }
-  } else if (nt > 0 && warp == 13 && lane == 0) {
-    // ================================================================ issuer
-    constexpr uint32_t id_s = umma_idesc(N, false), id_o = umma_idesc(D, true);
-    const uint32_t tiles = base + C::OFF_T;
-    auto scores = [&](int w, int i) {
-      const uint32_t q = base + C::OFF_Q + w * C::QT, k = tiles + (2 * i) % NT * C::TILE;
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::R_SOFTMAX));
+    if ((warp >> 2) < halves) {
+      // =============================================================== softmax
+      const int w = warp >> 2;
+      const int lrow = (warp & 3) * 32 + lane;
+      const int row = it.row0 + w * 128 + lrow;
+      const bool live = row < it.rows;
+      const int tokj = min(row, it.rows - 1) / p.R;
+      const int pos = it.seq - it.n + tokj;
+      const int first = p.window == 0 ? 0 : max(0, pos - p.window + 1);
+      const uint32_t s_at = tmem + C::S_COL + w * 128 + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+      const uint32_t o_at = tmem + C::O_COL + w * D + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+      float cq = fabsf(p.qscale);  // the sign goes into the queries
+      {
+        // this row's query, as fp16, into its operand tile
+        const uint4* src = reinterpret_cast<const uint4*>(
+            static_cast<const uint16_t*>(p.q) + static_cast<long long>(it.q0 + tokj) * p.q_stride +
+            (static_cast<long long>(it.h) * p.R + (min(row, it.rows - 1) - tokj * p.R)) * D);
+        uint8_t* dst = smem + C::OFF_Q + w * C::QT;
+        float up = 1.f;
+        if constexpr (BF16) {
+          // the row times a power of two: its largest element to [2^14, 2^15)
+          uint32_t mg = 0;
 #pragma unroll
-      for (int ks = 0; ks < D / 16; ++ks) {
-        const uint32_t off = (ks >> 2) * (128 * 128) + (ks & 3) * 32;
-        umma_ss(tmem + C::S_COL + w * 128, umma_desc(q + off, 16, 1024),
-                umma_desc(k + off, 16, 1024), id_s, ks > 0);
+          for (int i = 0; i < D / 8; ++i) {
+            const uint4 v = src[i];
+            mg = __vmaxu2(mg, v.x & 0x7fff7fffu);
+            mg = __vmaxu2(mg, v.y & 0x7fff7fffu);
+            mg = __vmaxu2(mg, v.z & 0x7fff7fffu);
+            mg = __vmaxu2(mg, v.w & 0x7fff7fffu);
+          }
+          const int e = max(static_cast<int>(max(mg & 0xffffu, mg >> 16) >> 7) - 127, -100);
+          up = __uint_as_float(static_cast<uint32_t>(127 + 14 - e) << 23);
+          cq *= __uint_as_float(static_cast<uint32_t>(127 - 14 + e) << 23);
+        }
+        const uint32_t flip = p.qscale < 0.f ? 0x80008000u : 0u;
+#pragma unroll 4
+        for (int i = 0; i < D / 8; ++i) {
+          uint4 v = make_uint4(0, 0, 0, 0);
+          if (live) v = src[i];
+          if constexpr (BF16) {
+            auto cv = [&](uint32_t x) {
+              return half2_bits(__uint_as_float(x << 16) * up, __uint_as_float(x & 0xffff0000u) * up);
+            };
+            v = make_uint4(cv(v.x), cv(v.y), cv(v.z), cv(v.w));
+          }
+          v.x ^= flip;
+          v.y ^= flip;
+          v.z ^= flip;
+          v.w ^= flip;
+          *reinterpret_cast<uint4*>(dst + (i >> 3) * (128 * 128) + lrow * 128 +
+                                    (((i & 7) ^ (lrow & 7)) << 4)) = v;
+        }
+        fence_async_shared();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&q_full[w]);
       }
-      umma_commit(&s_full[w]);
-    };
-    auto outputs = [&](int w, int i) {
-      const uint32_t v = tiles + (2 * i + 1) % NT * C::TILE;
-#pragma unroll
-      for (int ks = 0; ks < N / 16; ++ks)
-        umma_ts(tmem + C::O_COL + w * D, tmem + C::S_COL + w * 128 + ks * 8,
-                umma_desc(v + ks * 2048, N * 128, 1024), id_o, i > 0 || ks > 0);
-      umma_commit(&o_done[w]);
-    };
-    auto tile_ready = [&](int x) { return wait(&t_full[x % NT], x / NT); };
-    bool ok = tile_ready(0);
-    for (int w = 0; w < halves && ok; ++w) {
-      ok = wait(&q_full[w], 0);
-      if (!ok) break;
-      tmem_fence_after();
-      scores(w, 0);
-    }
-    if (ok) umma_commit(&t_empty[0]);
-    for (int i = 0; i < nt && ok; ++i) {
-      ok = tile_ready(2 * i + 1) && (i + 1 >= nt || tile_ready(2 * i + 2));
-      for (int w = 0; w < halves && ok; ++w) {
-        ok = wait(&p_full[w], i);
+      float m = -INFINITY, l = 0.f;
+      bool ok = true;
+      // tokens every row of this half sees
+      const int r0 = it.row0 + w * 128, r1 = min(r0 + 128, it.rows) - 1;
+      const int all_hi = it.seq - it.n + r0 / p.R + 1;
+      const int all_lo = p.window == 0 ? 0 : max(0, it.seq - it.n + r1 / p.R + 1 - p.window);
+      for (int i = 0; i < nt; ++i) {
+        ok = wait(&rec_full[i % C::NREC], i / C::NREC) && wait(&s_full[w], i);
         if (!ok) break;
         tmem_fence_after();
-        outputs(w, i);
-        if (i + 1 < nt) scores(w, i + 1);
-      }
-      if (!ok) break;
-      umma_commit(&t_empty[(2 * i + 1) % NT]);
-      if (i + 1 < nt) umma_commit(&t_empty[(2 * i + 2) % NT]);
-    }
-    // no product and no arrival may be in flight when the CTA leaves
-    umma_commit(drain);
-    mbar_wait_bounded(drain, 0, kRoleWait);
-  } else if (nt > 0 && warp < 8 && (warp >> 2) < halves) {
-    // =============================================================== softmax
-    const int w = warp >> 2;
-    const int lrow = (warp & 3) * 32 + lane;
-    const int row = it.row0 + w * 128 + lrow;
-    const bool live = row < it.rows;
-    const int tokj = min(row, it.rows - 1) / p.R;
-    const int pos = it.seq - it.n + tokj;
-    const int first = p.window == 0 ? 0 : max(0, pos - p.window + 1);
-    const uint32_t s_at = tmem + C::S_COL + w * 128 + (static_cast<uint32_t>((warp & 3) * 32) << 16);
-    const uint32_t o_at = tmem + C::O_COL + w * D + (static_cast<uint32_t>((warp & 3) * 32) << 16);
-    float cq = fabsf(p.qscale);  // the sign goes into the queries
-    {
-      // this row's query, as fp16, into its operand tile
-      const uint4* src = reinterpret_cast<const uint4*>(
-          static_cast<const uint16_t*>(p.q) + static_cast<long long>(it.q0 + tokj) * p.q_stride +
-          (static_cast<long long>(it.h) * p.R + (min(row, it.rows - 1) - tokj * p.R)) * D);
-      uint8_t* dst = smem + C::OFF_Q + w * C::QT;
-      float up = 1.f;
-      if constexpr (BF16) {
-        // the row times a power of two: its largest element to [2^14, 2^15)
-        uint32_t mg = 0;
+        const int tok = it.t0 + i * N;
+        const float4* rec = recs + i % C::NREC * C::REC;
+        const bool edge = tok < all_lo || tok + N > all_hi || !whole[i % C::NREC];
+        auto tile = [&](auto masked) {
+          constexpr bool MASK = decltype(masked)::value;
+          // Chunks of 32 columns, the next one loading while one is worked on:
+          // first the maximum of chunks 0 .. 3, then the weights of 3 .. 0, so
+          // the last chunk stays in registers and P (over the upper half of S)
+          // overwrites only columns that are done with.
+          uint32_t r[2][32];
+          auto hide = [&](uint32_t (&x)[32], int c) {
+            if constexpr (MASK) {
+              // bit k: token tok + 32 c + k is seen
+              const int up = pos - (tok + 32 * c), dn = first - (tok + 32 * c);
+              uint32_t see = up >= 31 ? 0xffffffffu : up < 0 ? 0u : (2u << up) - 1;
+              see &= dn <= 0 ? 0xffffffffu : dn > 31 ? 0u : 0xffffffffu << dn;
+              if (rec[2 * c].w == 0.f) see &= 0xffff0000u;
+              if (rec[2 * c + 1].w == 0.f) see &= 0x0000ffffu;
 #pragma unroll
-        for (int i = 0; i < D / 8; ++i) {
-          const uint4 v = src[i];
-          mg = __vmaxu2(mg, v.x & 0x7fff7fffu);
-          mg = __vmaxu2(mg, v.y & 0x7fff7fffu);
-          mg = __vmaxu2(mg, v.z & 0x7fff7fffu);
-          mg = __vmaxu2(mg, v.w & 0x7fff7fffu);
-        }
-        const int e = max(static_cast<int>(max(mg & 0xffffu, mg >> 16) >> 7) - 127, -100);
-        up = __uint_as_float(static_cast<uint32_t>(127 + 14 - e) << 23);
-        cq *= __uint_as_float(static_cast<uint32_t>(127 - 14 + e) << 23);
-      }
-      const uint32_t flip = p.qscale < 0.f ? 0x80008000u : 0u;
-#pragma unroll 4
-      for (int i = 0; i < D / 8; ++i) {
-        uint4 v = make_uint4(0, 0, 0, 0);
-        if (live) v = src[i];
-        if constexpr (BF16) {
-          auto cv = [&](uint32_t x) {
-            return half2_bits(__uint_as_float(x << 16) * up, __uint_as_float(x & 0xffff0000u) * up);
+              for (int k = 0; k < 32; ++k)  // (the exponential of -inf is the weight 0)
+                x[k] = (see >> k) & 1 ? x[k] : 0xff800000u;
+            }
           };
-          v = make_uint4(cv(v.x), cv(v.y), cv(v.z), cv(v.w));
-        }
-        v.x ^= flip;
-        v.y ^= flip;
-        v.z ^= flip;
-        v.w ^= flip;
-        *reinterpret_cast<uint4*>(dst + (i >> 3) * (128 * 128) + lrow * 128 +
-                                  (((i & 7) ^ (lrow & 7)) << 4)) = v;
-      }
-      fence_async_shared();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&q_full[w]);
-    }
-    float m = -INFINITY, l = 0.f;
-    bool ok = true;
-    // tokens every row of this half sees
-    const int r0 = it.row0 + w * 128, r1 = min(r0 + 128, it.rows) - 1;
-    const int all_hi = it.seq - it.n + r0 / p.R + 1;
-    const int all_lo = p.window == 0 ? 0 : max(0, it.seq - it.n + r1 / p.R + 1 - p.window);
-    for (int i = 0; i < nt; ++i) {
-      ok = wait(&rec_full[i % C::NREC], i / C::NREC) && wait(&s_full[w], i);
-      if (!ok) break;
-      tmem_fence_after();
-      const int tok = it.t0 + i * N;
-      const float4* rec = recs + i % C::NREC * C::REC;
-      bool edge = tok < all_lo || tok + N > all_hi;
+          float mx = -INFINITY;
+          tmem_ld32(s_at, r[0]);
 #pragma unroll
-      for (int g = 0; g < C::REC; ++g) edge |= rec[g].w == 0.f;
-      auto tile = [&](auto masked) {
-        constexpr bool MASK = decltype(masked)::value;
-        // the row's maximum: raw maximum of each granule, then its scales
-        float mx = -INFINITY;
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          uint32_t r[32];
-          tmem_ld32(s_at + 32 * c, r);
-          tmem_wait_ld();
-#pragma unroll
-          for (int g = 0; g < 2; ++g) {
-            const float4 rc = rec[2 * c + g];
-            float gm = -INFINITY;
-            bool any = !MASK;
-#pragma unroll
-            for (int k = 0; k < 16; ++k) {
-              float x = __uint_as_float(r[16 * g + k]);
-              if constexpr (MASK) {
-                const int t = tok + 32 * c + 16 * g + k;
-                const bool see = t <= pos && t >= first && rc.w != 0.f;
-                any |= see;
-                x = see ? x : -INFINITY;
-              }
-              gm = fmaxf(gm, x);
-            }
-            if (any) mx = fmaxf(mx, fmaf(gm, rc.x * cq, rc.y));
-          }
-        }
-        const float mn = mx > m + kLazy || m == -INFINITY ? mx : m;
-        const float mb = mn == -INFINITY ? 0.f : mn;
-        const bool move = mn != m && m != -INFINITY;  // O holds sums at the old reference
-        const float al = move ? ex2(m - mn) : 1.f;
-        m = mn;
-        l *= al;
-        if (__any_sync(0xffffffffu, move)) {
-          if (!wait(&o_done[w], i - 1)) return false;
-          tmem_fence_after();
-#pragma unroll
-          for (int c = 0; c < D / 32; ++c) {
-            uint32_t r[32];
-            tmem_ld32(o_at + 32 * c, r);
+          for (int c = 0; c < 4; ++c) {
             tmem_wait_ld();
+            if (c < 3) tmem_ld32(s_at + 32 * (c + 1), r[(c + 1) & 1]);
+            uint32_t(&x)[32] = r[c & 1];
+            hide(x, c);
+            // the raw maximum of each granule, then its scales
 #pragma unroll
-            for (int k = 0; k < 32; ++k) r[k] = __float_as_uint(__uint_as_float(r[k]) * al);
-            tmem_st32(o_at + 32 * c, r);
+            for (int g = 0; g < 2; ++g) {
+              const float4 rc = rec[2 * c + g];
+              float gm = -INFINITY;
+#pragma unroll
+              for (int k = 0; k < 16; ++k) gm = fmaxf(gm, __uint_as_float(x[16 * g + k]));
+              const float f = MASK ? fmaxf(rc.x * cq, 1.17549435e-38f) : rc.x * cq;
+              mx = fmaxf(mx, fmaf(gm, f, rc.y));
+            }
           }
-        }
+          const float mn = mx > m + kLazy || m == -INFINITY ? mx : m;
+          const float mb = mn == -INFINITY ? 0.f : mn;
+          const bool move = mn != m && m != -INFINITY;  // O holds sums at the old reference
+          const float al = move ? ex2(m - mn) : 1.f;
+          m = mn;
+          l *= al;
+          if (__any_sync(0xffffffffu, move)) {
+            if (!wait(&o_done[w], i - 1)) return false;
+            tmem_fence_after();
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          uint32_t r[32], h[16];
-          tmem_ld32(s_at + 32 * c, r);
+            for (int c = 0; c < D / 16; ++c) {  // (few registers: S waits in 128)
+              uint32_t o[16];
+              tmem_ld16(o_at + 16 * c, o);
+              tmem_wait_ld();
+#pragma unroll
+              for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * al);
+              tmem_st16(o_at + 16 * c, o);
+            }
+          }
+#pragma unroll
+          for (int c = 3; c >= 0; --c) {
+            uint32_t h[16];
+            uint32_t(&x)[32] = r[c & 1];
+            if (c < 3) {
+              tmem_wait_ld();
+              hide(x, c);
+            }
+            if (c > 0) tmem_ld32(s_at + 32 * (c - 1), r[(c - 1) & 1]);
+#pragma unroll
+            for (int g = 0; g < 2; ++g) {
+              const float4 rc = rec[2 * c + g];
+              float f = rc.x * cq, y = rc.y - mb;
+              if constexpr (MASK) f = fmaxf(f, 1.17549435e-38f);  // -inf times it stays -inf
+              const float2 f2 = make_float2(f, f), y2 = make_float2(y, y);
+              float2 sum = make_float2(0.f, 0.f);
+#pragma unroll
+              for (int k = 0; k < 16; k += 2) {
+                const float2 z = fma2(make_float2(__uint_as_float(x[16 * g + k]),
+                                                  __uint_as_float(x[16 * g + k + 1])), f2, y2);
+                const float2 w = make_float2(ex2(z.x), ex2(z.y));
+                sum = add2(sum, w);
+                h[8 * g + k / 2] = half2_bits(w.x, w.y);
+              }
+              l = fmaf(sum.x + sum.y, rc.z, l);
+            }
+            tmem_st16(s_at + C::P_OFF + 16 * c, h);
+          }
+          tmem_wait_st();
+          return true;
+        };
+        ok = edge ? tile(std::true_type{}) : tile(std::false_type{});
+        if (!ok) break;
+        tmem_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_full[w]);
+      }
+      if (ok && wait(&o_done[w], nt - 1)) {
+        tmem_fence_after();
+        const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
+        uint4* dst = reinterpret_cast<uint4*>(
+            static_cast<uint16_t*>(p.out) + static_cast<long long>(it.q0 + tokj) * p.out_stride +
+            (static_cast<long long>(it.h) * p.R + (row - tokj * p.R)) * D);
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t r[32], o[16];
+          tmem_ld32(o_at + 32 * c, r);
           tmem_wait_ld();
 #pragma unroll
-          for (int g = 0; g < 2; ++g) {
-            const float4 rc = rec[2 * c + g];
-            const float f = rc.x * cq, y = rc.y - mb;
-            float sum = 0.f;
-#pragma unroll
-            for (int k = 0; k < 16; k += 2) {
-              float a = ex2(fmaf(__uint_as_float(r[16 * g + k]), f, y));
-              float b = ex2(fmaf(__uint_as_float(r[16 * g + k + 1]), f, y));
-              if constexpr (MASK) {
-                const int t = tok + 32 * c + 16 * g + k;
-                if (!(t <= pos && t >= first && rc.w != 0.f)) a = 0.f;
-                if (!(t + 1 <= pos && t + 1 >= first && rc.w != 0.f)) b = 0.f;
-              }
-              sum += a + b;
-              h[8 * g + k / 2] = half2_bits(a, b);
+          for (int k = 0; k < 16; ++k) {
+            const float x = __uint_as_float(r[2 * k]) * inv, y = __uint_as_float(r[2 * k + 1]) * inv;
+            if constexpr (BF16) {
+              const __nv_bfloat162 b = __floats2bfloat162_rn(x, y);
+              o[k] = *reinterpret_cast<const uint32_t*>(&b);
+            } else {
+              o[k] = half2_bits(x, y);
             }
-            l = fmaf(sum, rc.z, l);
           }
-          tmem_st16(s_at + 16 * c, h);
-        }
-        tmem_wait_st();
-        return true;
-      };
-      ok = edge ? tile(std::true_type{}) : tile(std::false_type{});
-      if (!ok) break;
-      tmem_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&p_full[w]);
-    }
-    if (ok && wait(&o_done[w], nt - 1)) {
-      tmem_fence_after();
-      const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
-      uint4* dst = reinterpret_cast<uint4*>(
-          static_cast<uint16_t*>(p.out) + static_cast<long long>(it.q0 + tokj) * p.out_stride +
-          (static_cast<long long>(it.h) * p.R + (row - tokj * p.R)) * D);
+          if (live) {
 #pragma unroll
-      for (int c = 0; c < D / 32; ++c) {
-        uint32_t r[32], o[16];
-        tmem_ld32(o_at + 32 * c, r);
-        tmem_wait_ld();
-#pragma unroll
-        for (int k = 0; k < 16; ++k) {
-          const float x = __uint_as_float(r[2 * k]) * inv, y = __uint_as_float(r[2 * k + 1]) * inv;
-          if constexpr (BF16) {
-            const __nv_bfloat162 b = __floats2bfloat162_rn(x, y);
-            o[k] = *reinterpret_cast<const uint32_t*>(&b);
-          } else {
-            o[k] = half2_bits(x, y);
+            for (int k = 0; k < 4; ++k)
+              dst[4 * c + k] = make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
           }
         }
-        if (live) {
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            dst[4 * c + k] = make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
-        }
+        tmem_fence_before();
       }
-      tmem_fence_before();
-    }
-  } else if (it.b >= 0 && nt == 0) {
-    // no token is seen: zero rows
-    for (int e = tid; e < C::ROWS * (D / 8); e += C::THREADS) {
-      const int row = it.row0 + e / (D / 8);
-      if (row >= it.rows) break;
-      const int j = row / p.R;
-      reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) +
-                               static_cast<long long>(it.q0 + j) * p.out_stride +
-                               (static_cast<long long>(it.h) * p.R + (row - j * p.R)) * D)[e % (D / 8)] =
-          make_uint4(0, 0, 0, 0);
     }
   }
   __syncwarp();
