@@ -63,6 +63,7 @@ struct PagedAttnParams {
   const int* seq_len;
   int batch, n_tokens, max_new;
   int H, R, lg_ps, n_pages, box_rows;
+  uint32_t r_magic;  // ceil(2^32 / R): row / R by one high product (R > 1)
   const float* k_scale;
   const float* v_scale;
   float qscale;  // softmax scale * log2(e)
@@ -107,6 +108,12 @@ __device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* map, i
 // Brings a tensor map of the kernel's parameters into the descriptor cache.
 __device__ __forceinline__ void tensormap_prefetch(const CUtensorMap* map) {
   asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
+}
+
+// row / R for row < 2^28: row * ceil(2^32 / R) overshoots row / R * 2^32 by less
+// than row * (R - 1) / R < 2^32 / R.
+__device__ __forceinline__ int row_token(const PagedAttnParams& p, int row) {
+  return p.R == 1 ? row : static_cast<int>(__umulhi(static_cast<uint32_t>(row), p.r_magic));
 }
 
 // Lengths of request b as the attention uses them: new tokens, first new

@@ -242,6 +242,7 @@ kvq_status kvq_paged_attention(const kvq_paged_pool* pool, const void* q, int dt
   const int ut = paged_unit_tokens(D);
   const long long span = static_cast<long long>(max_pages) * pool->page_size;
   const long long rows_all = static_cast<long long>(n_tokens) * R;
+  if (rows_all >= 1 << 28) return KVQ_ERR_UNSUPPORTED;  // row_token's range
   const long long groups = std::min<long long>(static_cast<long long>(batch) * (kDecodeRows / (8 * nt)),
                                                rows_all / (8 * nt) + batch);
   if (static_cast<double>(H) * groups * (static_cast<double>(span) / ut + 2) >= 2147483647.0)
@@ -271,6 +272,7 @@ kvq_status kvq_paged_attention(const kvq_paged_pool* pool, const void* q, int dt
   p.max_new = max_new;
   p.H = H;
   p.R = R;
+  p.r_magic = static_cast<uint32_t>(((1ull << 32) + R - 1) / R);
   p.lg_ps = log2_of(pool->page_size);
   p.n_pages = pool->n_pages;
   p.k_scale = pool->k_scale;

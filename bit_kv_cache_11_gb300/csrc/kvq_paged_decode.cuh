@@ -214,11 +214,11 @@ __global__ void __launch_bounds__(PagedCfg<D, NT>::NW * 32, 1)
   // Tokens [lo, hi) that any row of the group sees.
   auto seen_lo = [&](const PagedItem& it) {
     if (p.window == 0) return 0;
-    const int lo = it.seq - it.n + it.grp * RG / p.R + 1 - p.window;
+    const int lo = it.seq - it.n + row_token(p, it.grp * RG) + 1 - p.window;
     return lo > 0 ? lo : 0;
   };
   auto seen_hi = [&](const PagedItem& it) {
-    return max(0, it.seq - it.n + (it.grp * RG + it.rows - 1) / p.R + 1);
+    return max(0, it.seq - it.n + row_token(p, it.grp * RG + it.rows - 1) + 1);
   };
 
   // ---- the load cursor, NS units ahead -------------------------------------
@@ -332,7 +332,7 @@ __global__ void __launch_bounds__(PagedCfg<D, NT>::NW * 32, 1)
     lo = seen_lo(it);
     hi = seen_hi(it);
     // tokens [full_lo, full_hi) are seen by every row of the group
-    full_hi = it.seq - it.n + it.grp * RG / p.R + 1;
+    full_hi = it.seq - it.n + row_token(p, it.grp * RG) + 1;
     full_lo = p.window == 0 ? 0 : hi - p.window;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
@@ -343,7 +343,7 @@ __global__ void __launch_bounds__(PagedCfg<D, NT>::NW * 32, 1)
       for (int i = 0; i < KS * 2; ++i) w[i] = 0;
       if (r < it.rows) {
         const int row = it.grp * RG + r;
-        const int j = row / p.R;
+        const int j = row_token(p, row);
         const uint4* src = reinterpret_cast<const uint4*>(
             static_cast<const uint16_t*>(p.q) + static_cast<long long>(it.q0 + j) * p.q_stride +
             (static_cast<long long>(it.h) * p.R + (row - j * p.R)) * D + t * (D / 4));
@@ -450,7 +450,7 @@ __global__ void __launch_bounds__(PagedCfg<D, NT>::NW * 32, 1)
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
             const int row = it.grp * RG + nt * 8 + 2 * t + c;
-            const int pos = it.seq - it.n + row / p.R;
+            const int pos = it.seq - it.n + row_token(p, row);
             const int first = p.window == 0 ? 0 : pos - p.window + 1;
             const int ta = tok + mt * 16 + g, tb = ta + 8;
             const bool there = rec[mt].w != 0.f;
@@ -561,7 +561,7 @@ __global__ void __launch_bounds__(PagedCfg<D, NT>::NW * 32, 1)
         for (int c = 0; c < 2; ++c) {
           const int r = nt * 8 + 2 * t + c;
           if (r >= it.rows) continue;
-          const int row = it.grp * RG + r, j = row / p.R;
+          const int row = it.grp * RG + r, j = row_token(p, row);
           const float inv = l[nt][c] > 0.f ? 1.f / l[nt][c] : (l[nt][c] == 0.f ? 0.f : l[nt][c]);
           uint32_t w[D / 16];
 #pragma unroll
@@ -679,7 +679,7 @@ __global__ void __launch_bounds__(PagedCfg<D, NT>::NW * 32, 1)
 
   // Row r of a finished item.
   auto finish = [&](int h, int grp, int q0, int r, float L, float4 o) {
-    const int row = grp * RG + r, j = row / p.R;
+    const int row = grp * RG + r, j = row_token(p, row);
     const float inv = L > 0.f ? 1.f / L : (L == 0.f ? 0.f : L);
     uint2 w;
     if constexpr (BF16) {

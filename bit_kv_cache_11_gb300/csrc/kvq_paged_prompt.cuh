@@ -306,8 +306,8 @@ __global__ void __launch_bounds__(PromptCfg<D>::THREADS, 1)
           it.seq = r.seq;
           it.n = r.n;
           const int last = min(it.row0 + C::ROWS, it.rows) - 1;
-          it.hi = max(0, r.seq - r.n + last / p.R + 1);
-          it.lo = p.window == 0 ? 0 : max(0, r.seq - r.n + it.row0 / p.R + 1 - p.window);
+          it.hi = max(0, r.seq - r.n + row_token(p, last) + 1);
+          it.lo = p.window == 0 ? 0 : max(0, r.seq - r.n + row_token(p, it.row0) + 1 - p.window);
           it.t0 = it.lo / N * N;
           it.nt = it.hi > it.t0 ? (it.hi - it.t0 + N - 1) / N : 0;
           *found = it;
@@ -327,7 +327,7 @@ __global__ void __launch_bounds__(PromptCfg<D>::THREADS, 1)
     for (int e = tid; e < C::ROWS * (D / 8); e += C::THREADS) {
       const int row = it.row0 + e / (D / 8);
       if (row >= it.rows) break;
-      const int j = row / p.R;
+      const int j = row_token(p, row);
       reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) +
                                static_cast<long long>(it.q0 + j) * p.out_stride +
                                (static_cast<long long>(it.h) * p.R + (row - j * p.R)) * D)[e % (D / 8)] =
@@ -539,52 +539,71 @@ __global__ void __launch_bounds__(PromptCfg<D>::THREADS, 1)
       const int w = warp >> 2;
       const int lrow = (warp & 3) * 32 + lane;
       const int row = it.row0 + w * 128 + lrow;
-      const bool live = row < it.rows;
-      const int tokj = min(row, it.rows - 1) / p.R;
+      const int tokj = row_token(p, min(row, it.rows - 1));
       const int pos = it.seq - it.n + tokj;
       const int first = p.window == 0 ? 0 : max(0, pos - p.window + 1);
       const uint32_t s_at = tmem + C::S_COL + w * 128 + (static_cast<uint32_t>((warp & 3) * 32) << 16);
       const uint32_t o_at = tmem + C::O_COL + w * D + (static_cast<uint32_t>((warp & 3) * 32) << 16);
       float cq = fabsf(p.qscale);  // the sign goes into the queries
       {
-        // this row's query, as fp16, into its operand tile
-        const uint4* src = reinterpret_cast<const uint4*>(
-            static_cast<const uint16_t*>(p.q) + static_cast<long long>(it.q0 + tokj) * p.q_stride +
-            (static_cast<long long>(it.h) * p.R + (min(row, it.rows - 1) - tokj * p.R)) * D);
-        uint8_t* dst = smem + C::OFF_Q + w * C::QT;
-        float up = 1.f;
-        if constexpr (BF16) {
-          // the row times a power of two: its largest element to [2^14, 2^15)
-          uint32_t mg = 0;
-#pragma unroll
-          for (int i = 0; i < D / 8; ++i) {
-            const uint4 v = src[i];
-            mg = __vmaxu2(mg, v.x & 0x7fff7fffu);
-            mg = __vmaxu2(mg, v.y & 0x7fff7fffu);
-            mg = __vmaxu2(mg, v.z & 0x7fff7fffu);
-            mg = __vmaxu2(mg, v.w & 0x7fff7fffu);
-          }
-          const int e = max(static_cast<int>(max(mg & 0xffffu, mg >> 16) >> 7) - 127, -100);
-          up = __uint_as_float(static_cast<uint32_t>(127 + 14 - e) << 23);
-          cq *= __uint_as_float(static_cast<uint32_t>(127 - 14 + e) << 23);
+        // This warp's 32 query rows into their operand tile: a row is D / 8
+        // lanes wide, so a copy moves whole rows, and all copies are on their
+        // way at once.  (Loops that run once an item stay rolled: their code is
+        // fetched as it runs, and fetching costs more than looping.)
+        constexpr int LPR = D / 8, RPL = 32 / LPR;  // lanes of a row, rows of a copy
+        const int sub = lane / LPR, vec = lane % LPR;
+        const uint32_t tile = base + C::OFF_Q + w * C::QT;
+#pragma unroll 1
+        for (int i = 0; i < 32 / RPL; ++i) {
+          const int tr = (warp & 3) * 32 + i * RPL + sub;
+          const int gr = min(it.row0 + w * 128 + tr, it.rows - 1), j = row_token(p, gr);
+          const void* src = reinterpret_cast<const uint4*>(
+                                static_cast<const uint16_t*>(p.q) +
+                                static_cast<long long>(it.q0 + j) * p.q_stride +
+                                (static_cast<long long>(it.h) * p.R + (gr - j * p.R)) * D) + vec;
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                           tile + (vec >> 3) * (128 * 128) + tr * 128 + (((vec & 7) ^ (tr & 7)) << 4)),
+                       "l"(src)
+                       : "memory");
         }
-        const uint32_t flip = p.qscale < 0.f ? 0x80008000u : 0u;
-#pragma unroll 4
-        for (int i = 0; i < D / 8; ++i) {
-          uint4 v = make_uint4(0, 0, 0, 0);
-          if (live) v = src[i];
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        __syncwarp();
+        if (BF16 || p.qscale < 0.f) {
+          // a thread's own row: as fp16, with the sign of the softmax scale
+          uint8_t* own = smem + C::OFF_Q + w * C::QT + lrow * 128;
+          float up = 1.f;
           if constexpr (BF16) {
+            // the row times a power of two: its largest element to [2^14, 2^15)
+            uint32_t mg = 0;
+#pragma unroll 2
+            for (int i = 0; i < D / 8; ++i) {
+              const uint4 v = *reinterpret_cast<const uint4*>(
+                  own + (i >> 3) * (128 * 128) + (((i & 7) ^ (lrow & 7)) << 4));
+              mg = __vmaxu2(mg, __vmaxu2(__vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu),
+                                         __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu)));
+            }
+            const int e = max(static_cast<int>(max(mg & 0xffffu, mg >> 16) >> 7) - 127, -100);
+            up = __uint_as_float(static_cast<uint32_t>(127 + 14 - e) << 23);
+            cq *= __uint_as_float(static_cast<uint32_t>(127 - 14 + e) << 23);
+          }
+          if (p.qscale < 0.f) up = -up;
+#pragma unroll 2
+          for (int i = 0; i < D / 8; ++i) {
+            uint4* at = reinterpret_cast<uint4*>(own + (i >> 3) * (128 * 128) +
+                                                 (((i & 7) ^ (lrow & 7)) << 4));
+            uint4 v = *at;
             auto cv = [&](uint32_t x) {
-              return half2_bits(__uint_as_float(x << 16) * up, __uint_as_float(x & 0xffff0000u) * up);
+              float2 f;
+              if constexpr (BF16) {
+                f = make_float2(__uint_as_float(x << 16), __uint_as_float(x & 0xffff0000u));
+              } else {
+                f = __half22float2(*reinterpret_cast<const __half2*>(&x));
+              }
+              return half2_bits(f.x * up, f.y * up);
             };
             v = make_uint4(cv(v.x), cv(v.y), cv(v.z), cv(v.w));
+            *at = v;
           }
-          v.x ^= flip;
-          v.y ^= flip;
-          v.z ^= flip;
-          v.w ^= flip;
-          *reinterpret_cast<uint4*>(dst + (i >> 3) * (128 * 128) + lrow * 128 +
-                                    (((i & 7) ^ (lrow & 7)) << 4)) = v;
         }
         fence_async_shared();
         __syncwarp();
@@ -594,8 +613,8 @@ __global__ void __launch_bounds__(PromptCfg<D>::THREADS, 1)
       bool ok = true;
       // tokens every row of this half sees
       const int r0 = it.row0 + w * 128, r1 = min(r0 + 128, it.rows) - 1;
-      const int all_hi = it.seq - it.n + r0 / p.R + 1;
-      const int all_lo = p.window == 0 ? 0 : max(0, it.seq - it.n + r1 / p.R + 1 - p.window);
+      const int all_hi = it.seq - it.n + row_token(p, r0) + 1;
+      const int all_lo = p.window == 0 ? 0 : max(0, it.seq - it.n + row_token(p, r1) + 1 - p.window);
       for (int i = 0; i < nt; ++i) {
         ok = wait(&rec_full[i % C::NREC], i / C::NREC) && wait(&s_full[w], i);
         if (!ok) break;
@@ -701,9 +720,9 @@ __global__ void __launch_bounds__(PromptCfg<D>::THREADS, 1)
       if (ok && wait(&o_done[w], nt - 1)) {
         tmem_fence_after();
         const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
-        uint4* dst = reinterpret_cast<uint4*>(
-            static_cast<uint16_t*>(p.out) + static_cast<long long>(it.q0 + tokj) * p.out_stride +
-            (static_cast<long long>(it.h) * p.R + (row - tokj * p.R)) * D);
+// through the query tile (its products are complete), so that whole rows
+        // are written: this warp's rows, chunks swizzled as the queries were
+        uint8_t* tile = smem + C::OFF_Q + w * C::QT;
 #pragma unroll
         for (int c = 0; c < D / 32; ++c) {
           uint32_t r[32], o[16];
@@ -719,11 +738,28 @@ __global__ void __launch_bounds__(PromptCfg<D>::THREADS, 1)
               o[k] = half2_bits(x, y);
             }
           }
-          if (live) {
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-              dst[4 * c + k] = make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+          for (int k = 0; k < 4; ++k) {
+            const int ch = 4 * c + k;
+            *reinterpret_cast<uint4*>(tile + (ch >> 3) * (128 * 128) + lrow * 128 +
+                                      (((ch & 7) ^ (lrow & 7)) << 4)) =
+                make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
           }
+        }
+        __syncwarp();
+        constexpr int LPR = D / 8, RPL = 32 / LPR;
+        const int sub = lane / LPR, vec = lane % LPR;
+#pragma unroll 2
+        for (int i = 0; i < 32 / RPL; ++i) {
+          const int tr = (warp & 3) * 32 + i * RPL + sub;
+          const int gr = it.row0 + w * 128 + tr, j = row_token(p, gr);
+          const uint4 v = *reinterpret_cast<const uint4*>(tile + (vec >> 3) * (128 * 128) + tr * 128 +
+                                                          (((vec & 7) ^ (tr & 7)) << 4));
+          if (gr < it.rows)
+            *(reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) +
+                                       static_cast<long long>(it.q0 + j) * p.out_stride +
+                                       (static_cast<long long>(it.h) * p.R + (gr - j * p.R)) * D) +
+              vec) = v;
         }
         tmem_fence_before();
       }
