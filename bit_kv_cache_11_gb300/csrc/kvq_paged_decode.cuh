@@ -29,8 +29,6 @@
 // weights' B fragment by an 8x8 transpose (movmatrix).
 #pragma once
 
-#include <atomic>
-#include <type_traits>
 
 #include "kvq_decode_mma.cuh"
 #include "kvq_paged.cuh"
@@ -115,7 +113,8 @@ __global__ void __launch_bounds__(PagedCfg<D, NT>::NW * 32, 1)
   constexpr int KC = D / 64;   // 16-byte chunks of a key row a lane reads
   constexpr int KS = D / 16;   // k-steps of the scores
   constexpr int MT = D / 16;   // m-tiles of the values
-  extern __shared__ __align__(1024) uint8_t smem[];
+  extern __shared__ __align__(1024) uint8_t smem_paged[];
+  uint8_t* const smem = smem_paged;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = lane >> 2, t = lane & 3;
   uint8_t* stages = smem + warp * NS * C::STAGE;
@@ -406,11 +405,10 @@ __global__ void __launch_bounds__(PagedCfg<D, NT>::NW * 32, 1)
                                : (2 * t + i) * 64 + (((g >> 1) ^ t) << 4) + 8 * (g & 1));
   const uint32_t stages_s = smem_addr(stages);
 
-  // One unit from stage memory.  MASK: some of its tokens are hidden from
-  // some rows (or not there at all).
+  // One unit from stage memory.  edge: some of its tokens are hidden from some
+  // rows (or not there at all).
   float4 rec[GR];  // the unit's granule records
-  auto compute = [&](uint32_t st, int tok, auto masked) {
-    constexpr bool MASK = decltype(masked)::value;
+  auto compute = [&](uint32_t st, int tok, bool edge) {
     uint32_t pw[GR][NT][2];
     float s[GR][NT][4];
 #pragma unroll
@@ -446,7 +444,7 @@ __global__ void __launch_bounds__(PagedCfg<D, NT>::NW * 32, 1)
         x[1] = fmaf(x[1], f1, rec[mt].y);
         x[2] = fmaf(x[2], f0, rec[mt].y);
         x[3] = fmaf(x[3], f1, rec[mt].y);
-        if constexpr (MASK) {
+        if (edge) {
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
             const int row = it.grp * RG + nt * 8 + 2 * t + c;
@@ -515,7 +513,7 @@ __global__ void __launch_bounds__(PagedCfg<D, NT>::NW * 32, 1)
           v[i][0] = x.x;
           v[i][1] = x.y;
         }
-        if constexpr (MASK) {
+        if (edge) {
           // what lies in hidden rows may decode to NaN, which a weight of 0
           // would not cancel
           const int tk = tok + mt * 16 + 2 * t + (i & 1) + 8 * (i >> 1);
@@ -631,8 +629,7 @@ __global__ void __launch_bounds__(PagedCfg<D, NT>::NW * 32, 1)
         rec[i] = ring[(crec + i) & (C::RING - 1)];
         there &= rec[i].w != 0.f;
       }
-      if (there && tok >= full_lo && tok + UT <= full_hi) compute(sp, tok, std::false_type{});
-      else compute(sp, tok, std::true_type{});
+      compute(sp, tok, !there || tok < full_lo || tok + UT > full_hi);
     }
     crec += GR;
     __syncwarp();
@@ -736,16 +733,24 @@ __global__ void __launch_bounds__(PagedCfg<D, NT>::NW * 32, 1)
       const float w = lane < 16 || two ? fast_exp2(ml.x - (M == -INFINITY ? 0.f : M)) : 0.f;
       float L = ml.y * w;
       L += __shfl_xor_sync(0xffffffffu, L, 16);
-#pragma unroll
-      for (int r0 = 0; r0 < RG; r0 += 4) {
-        if (r0 >= rows) break;
-        float4 a[4], b[4];
+      float4 a[4], b[4], na[4], nb[4];
+      auto fetch = [&](int r0, float4(&xa)[4], float4(&xb)[4]) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          a[i] = *reinterpret_cast<const float4*>(pa + (r0 + i) * D + ch);
-          b[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-          if (two) b[i] = *reinterpret_cast<const float4*>(pb + (r0 + i) * D + ch);
+          xa[i] = *reinterpret_cast<const float4*>(pa + (r0 + i) * D + ch);
+          xb[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (two) xb[i] = *reinterpret_cast<const float4*>(pb + (r0 + i) * D + ch);
         }
+      };
+      fetch(0, na, nb);
+#pragma unroll 1
+      for (int r0 = 0; r0 < rows; r0 += 4) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          a[i] = na[i];
+          b[i] = nb[i];
+        }
+        if (r0 + 4 < rows) fetch(r0 + 4, na, nb);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int r = r0 + i;
@@ -822,6 +827,31 @@ __global__ void __launch_bounds__(PagedCfg<D, NT>::NW * 32, 1)
       auto part = [&](int c) {
         return p.cta_part + static_cast<size_t>(2 * c + (c == ca ? 1 : 0)) * PART;
       };
+      if (cb == ca + 1) {
+        // two shares (many items): all rows of a warp on their way at once
+        const float *pa = part(ca), *pb = part(cb);
+        float2 ma[RG / NW], mb_[RG / NW];
+        float4 xa[RG / NW], xb[RG / NW];
+#pragma unroll
+        for (int i = 0; i < RG / NW; ++i) {
+          const int r = warp + i * NW;
+          ma[i] = __ldcg(reinterpret_cast<const float2*>(pa + RG * D + 2 * r));
+          mb_[i] = __ldcg(reinterpret_cast<const float2*>(pb + RG * D + 2 * r));
+          xa[i] = __ldcg(reinterpret_cast<const float4*>(pa + r * D + ch));
+          xb[i] = __ldcg(reinterpret_cast<const float4*>(pb + r * D + ch));
+        }
+#pragma unroll
+        for (int i = 0; i < RG / NW; ++i) {
+          const int r = warp + i * NW;
+          if (r >= rows) continue;  // (its floats were never written)
+          const float M = fmaxf(ma[i].x, mb_[i].x), mz = M == -INFINITY ? 0.f : M;
+          const float wa = fast_exp2(ma[i].x - mz), wb = fast_exp2(mb_[i].x - mz);
+          finish(h, grp, q0, r, fmaf(ma[i].y, wa, mb_[i].y * wb),
+                 make_float4(fmaf(xa[i].x, wa, xb[i].x * wb), fmaf(xa[i].y, wa, xb[i].y * wb),
+                             fmaf(xa[i].z, wa, xb[i].z * wb), fmaf(xa[i].w, wa, xb[i].w * wb)));
+        }
+        continue;
+      }
       for (int r = warp; r < rows; r += NW) {
         float M = -INFINITY;
         for (int c = ca + lane; c <= cb; c += 32) M = fmaxf(M, __ldcg(part(c) + RG * D + 2 * r));
