@@ -13,6 +13,7 @@
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <cmath>
 #include <map>
 #include <mutex>
 #include <string>
@@ -256,11 +257,6 @@ PyObject* plan(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int64_t tokens = number(call, "n_tokens", a[6], 0, kIntMax);
     if (batch > kIntMax || tab.size(1) > kIntMax || fp.numel() > kIntMax)
       throw Refusal{KVQ_ERR_UNSUPPORTED, call};
-    place.add("ctx_len", ctx);
-    place.add("new_len", nw);
-    place.add("block_table", tab);
-    place.add("free_pages", fp);
-    place.add("n_free", nf);
     const char* names[4] = {"cu_new", "seq_len", "slots", "n_left"};
     const int64_t sizes[4] = {batch + 1, batch, tokens, 1};
     at::Tensor out[4];
@@ -268,8 +264,14 @@ PyObject* plan(PyObject*, PyObject* const* a, Py_ssize_t n) {
     for (int i = 0; i < 4; ++i) {
       if (a[7 + i] == Py_None) continue;
       out[i] = ints(call, names[i], a[7 + i], sizes[i]);
-      place.add(names[i], out[i]);
     }
+    place.add("ctx_len", ctx);
+    place.add("new_len", nw);
+    place.add("block_table", tab);
+    place.add("free_pages", fp);
+    place.add("n_free", nf);
+    for (int i = 0; i < 4; ++i)
+      if (out[i].defined()) place.add(names[i], out[i]);
     int* err = error_ptr(place, a[11]);
     const c10::cuda::CUDAGuard guard(static_cast<c10::DeviceIndex>(place.index));
     const cudaStream_t st = stream_of(call, a[12], place.index);

@@ -300,6 +300,13 @@ MULTI = [
     (128, 128, 1, 3, "fp16", [120, 0, 250], [20, 1, 64], 0),
     (64, 64, 2, 2, "fp16", [0, 10], [150, 0], 0),
     (64, 128, 1, 5, "bf16", [0, 77], [130, 70], 65),
+    # over 256 rows of 128 channels: two CTAs share an item
+    (16, 128, 2, 1, "fp16", [0, 300], [520, 270], 0),
+    (128, 128, 1, 8, "bf16", [100, 3], [65, 9], 0),
+    (32, 128, 1, 2, "fp16", [50, 0, 7], [129, 1, 300], 100),
+    (64, 128, 3, 1, "bf16", [1000], [257], 0),
+    (64, 64, 1, 1, "fp16", [3], [600], 0),
+    (128, 64, 1, 4, "bf16", [300, 0], [70, 140], 50),
 ]
 
 
@@ -311,3 +318,374 @@ def test_decode(kvq, case):
 @pytest.mark.parametrize("case", MULTI, ids=str)
 def test_several_new_tokens(kvq, case):
     check_attention(kvq, case)
+
+
+def test_a_mixed_batch(kvq):
+    """Decodes, drafted tokens, a short and a long prompt in one call."""
+    for ps, D, dtype in ((64, 128, "bf16"), (16, 64, "fp16"), (128, 128, "fp16")):
+        check_attention(kvq, (ps, D, 2, 4, dtype, [900, 37, 0, 200, 0, 3], [1, 4, 300, 17, 33, 0], 0))
+        check_attention(kvq, (ps, D, 2, 4, dtype, [900, 37, 0, 200], [1, 4, 300, 17], 50))
+
+
+def test_max_new_may_be_a_loose_bound(kvq):
+    check_attention(kvq, (32, 128, 1, 2, "fp16", [50, 7], [3, 1], 0), max_new=5000)
+    check_attention(kvq, (32, 64, 1, 1, "bf16", [50, 7], [1, 1], 0), max_new=4)
+
+
+@pytest.mark.parametrize("scale", [0.0, -0.3, 1e-30])
+def test_any_softmax_scale(kvq, scale):
+    """A scale of 0 averages the values; a negative one turns the order."""
+    for n, R in ((1, 2), (150, 1)):
+        rng = np.random.default_rng(n)
+        ps, D, T0 = 16, 64, 60
+        c, s, pages, sc = make_pool(rng, 20, 1, ps, D)
+        for i in range(2):
+            c[i] = ref.e4m3_code(rng.standard_normal(c[i].shape) / s[i][..., None, None] / 8)
+            pages[i] = torch.from_numpy(c[i]).cuda().view(torch.float8_e4m3fn)
+        q = torch.from_numpy(rng.standard_normal((n, R, D))).half()
+        table, cu, seq = np.arange(20)[None], np.array([0, n]), np.array([T0 + n])
+        got = kvq.kvq_paged_attention(q.cuda(), *pages, *sc, ints(table), ints(cu), ints(seq),
+                                      max_new=n, softmax_scale=scale)
+        want, size, reach = ref.attention(f64(q), c[0], c[1], s[0], s[1], table, cu, seq, ps, scale)
+        tol = ref.tolerance(want, size, reach, HALF["fp16"], T0 + n, (448 * s[1]).max())
+        worst = float((np.abs(f64(got) - want) / tol).max())
+        assert worst <= 1.0, worst
+
+
+def simple(rng, n_pages=12, H=1, ps=16, D=64, seq=(100, 40), new=(1, 1), R=2, dtype=torch.float16):
+    """A small call's arguments."""
+    c, s, pages, sc = make_pool(rng, n_pages, H, ps, D)
+    need = [-(-x // ps) for x in seq]
+    table = np.full((len(seq), max(need)), -1)
+    at = 0
+    for b, n in enumerate(need):
+        table[b, :n] = np.arange(at, at + n)
+        at += n
+    q = torch.from_numpy(rng.standard_normal((sum(new), H * R, D))).to(dtype).cuda()
+    cu = np.concatenate([[0], np.cumsum(new)])
+    return [q, *pages, *sc, ints(table), ints(cu), ints(seq)]
+
+
+@pytest.mark.parametrize("new", [(1, 1), (70, 33)])
+def test_bad_pages_are_flagged_and_skipped(kvq, new):
+    """A page id outside the pool hides its tokens, whatever lies around."""
+    for bad in (-1, 12, 1 << 30, -(1 << 31)):
+        args = simple(np.random.default_rng(2), new=new, seq=(100, 48))
+        whole = kvq.kvq_paged_attention(*args, max_new=max(new))
+        err = ints([0])
+        args[5][0, 2] = bad  # tokens 32 .. 47 of request 0
+        got = kvq.kvq_paged_attention(*args, max_new=max(new), error=err)
+        assert err.item() == kvq.KVQ_PAGED_ERR_BAD_PAGE
+        assert torch.equal(got[new[0]:], whole[new[0]:]) and torch.isfinite(got).all()
+        # the others of request 0 are as if those tokens had no weight: with a
+        # window that leaves them out, nothing is flagged and nothing changes
+        err.zero_()
+        args[5][0, 2] = 2
+        want = kvq.kvq_paged_attention(*args, max_new=max(new), window=20)
+        args[5][0, 0] = bad
+        if new[0] == 1:
+            again = kvq.kvq_paged_attention(*args, max_new=1, window=20, error=err)
+            assert err.item() == 0 and torch.equal(again, want)
+
+
+def test_store_flags_bad_slots(kvq):
+    c, s, pages, sc = make_pool(np.random.default_rng(0), 4, 2, 16, 64)
+    before = [p.view(torch.uint8).clone() for p in pages]
+    for T in (3, 1200):
+        k = torch.ones(T, 2, 64, dtype=torch.float16, device="cuda")
+        slots = np.full(T, -1)
+        slots[1] = 4 * 16 + 3
+        slots[2] = (1 << 31) - 5
+        err = ints([0])
+        kvq.kvq_paged_store(k, k, ints(slots), *pages, *sc, error=err)
+        assert err.item() == kvq.KVQ_PAGED_ERR_BAD_PAGE
+        assert all(torch.equal(p.view(torch.uint8), b) for p, b in zip(pages, before))
+
+
+def test_lengths_that_break_the_contract_are_skipped(kvq):
+    rng = np.random.default_rng(4)
+    for new in ((2, 3), (90, 80)):
+        args = simple(rng, seq=(100, 90), n_pages=16, new=new)
+        n = sum(new)
+        for seq, cu, ok in (((113, 90), None, 1), ((-5, 90), None, 1), ((100, 1 << 30), None, 0),
+                            (None, (0, new[0], n + 1), 0), (None, (-1, new[0], n), 1),
+                            (None, (new[0], 0, n), None)):
+            a = list(args)
+            if seq:
+                a[7] = ints(seq)
+            if cu:
+                a[6] = ints(cu)
+            out = torch.full_like(args[0], 5.0)
+            err = ints([0])
+            kvq.kvq_paged_attention(*a, max_new=max(new), out=out, error=err)
+            assert err.item() == kvq.KVQ_PAGED_ERR_LENGTH
+            rows = [slice(0, new[0]), slice(new[0], n)]
+            for b in range(2):
+                if ok is not None:
+                    assert bool((out[rows[b]] == 5.0).all()) == (b != ok)
+        # more new tokens than max_new
+        out, err = torch.full_like(args[0], 5.0), ints([0])
+        kvq.kvq_paged_attention(*args, max_new=min(new), out=out, error=err)
+        assert err.item() == kvq.KVQ_PAGED_ERR_LENGTH
+
+
+@pytest.mark.parametrize("new", [(1, 1), (100, 5)])
+def test_nan_queries_stay_in_their_rows(kvq, new):
+    for dtype in (torch.float16, torch.bfloat16):
+        args = simple(np.random.default_rng(6), H=2, n_pages=16, seq=(100, 48), new=new, dtype=dtype)
+        want = kvq.kvq_paged_attention(*args, max_new=max(new))
+        args[0][0, 1, 3] = float("nan")
+        got = kvq.kvq_paged_attention(*args, max_new=max(new))
+        assert got[0, 1].isnan().all()
+        rest = torch.ones(got.shape[:2], dtype=torch.bool, device="cuda")
+        rest[0, 1] = False
+        assert torch.equal(got[rest], want[rest])
+
+
+def test_a_query_that_sees_nothing_gives_zeros(kvq):
+    for new in ((3, 2), (90, 70)):
+        args = simple(np.random.default_rng(8), seq=(0, 40), new=new)
+        err = ints([0])
+        out = kvq.kvq_paged_attention(*args, max_new=max(new), error=err)
+        # request 0 holds nothing; request 1's first queries lie before token 0
+        assert (out[:new[0]] == 0).all() and err.item() == 0
+        early = max(0, new[1] - 40)
+        assert (out[new[0]:new[0] + early] == 0).all()
+        assert torch.isfinite(out).all() and (out[new[0] + early:] != 0).any()
+
+
+def test_values_of_very_different_pages(kvq):
+    """Pages whose scales differ by 2^50: a page of huge values with little
+    weight does not drown the others, a page of zeros still takes its share."""
+    for n in (1, 80):
+        ps, D = 16, 64
+        rng = np.random.default_rng(n)
+        c, s, pages, sc = make_pool(rng, 8, 1, ps, D)
+        for i in range(2):
+            c[i] = ref.e4m3_code(rng.standard_normal(c[i].shape))
+        s[0][:] = 1.0
+        s[1][:] = 1.0
+        s[1][1], s[1][2], s[1][3] = 2.0 ** 35, 2.0 ** -15, 2.0 ** 10
+        c[1][4] = 0
+        c[0][1] = ref.e4m3_code(-8 * np.ones((1, ps, D)))  # page 1: scores near -64 sigma
+        pages = [torch.from_numpy(x).cuda().view(torch.float8_e4m3fn) for x in c]
+        sc = [torch.from_numpy(x.astype(np.float32)).cuda() for x in s]
+        q = torch.from_numpy(np.abs(rng.standard_normal((n, 1, D)))).half()
+        table, cu, seq = np.arange(8)[None], np.array([0, n]), np.array([ps * 8])
+        got = kvq.kvq_paged_attention(q.cuda(), *pages, *sc, ints(table), ints(cu), ints(seq),
+                                      max_new=n, softmax_scale=0.25)
+        want, size, reach = ref.attention(f64(q), c[0], c[1], s[0], s[1], table, cu, seq, ps, 0.25)
+        # the floor of a weight is 2^-25 of the largest p * scale of its row
+        tol = ref.tolerance(want, size, reach, HALF["fp16"], 1, 0.0)
+        tol += size.max(axis=-1, keepdims=True) * ps * 8 * 2.0 ** -25
+        worst = float((np.abs(f64(got) - want) / tol).max())
+        assert worst <= 1.0, worst
+
+
+def test_a_pool_beyond_four_gigabytes(kvq):
+    """Pages at the end of a pool of 4.6 GB (K and V each)."""
+    ps, D, H = 128, 128, 8
+    n_pages = 35000
+    pages = [torch.zeros(n_pages, H, ps, D, dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn)
+             for _ in range(2)]
+    scale = [torch.ones(n_pages, H, device="cuda") for _ in range(2)]
+    T = 300
+    ids = np.array([n_pages - 1, n_pages - 2, 32768])
+    pos = np.arange(T)
+    slots = ids[pos // ps] * ps + pos % ps
+    k = torch.randn(T, H, D, device="cuda").half()
+    v = torch.randn(T, H, D, device="cuda").half()
+    kvq.kvq_paged_store(k, v, ints(slots), *pages, *scale)
+    small = [torch.zeros(3, H, ps, D, dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn)
+             for _ in range(2)]
+    small_scale = [torch.ones(3, H, device="cuda") for _ in range(2)]
+    kvq.kvq_paged_store(k, v, ints(pos), *small, *small_scale)
+    for n in (1, 100):
+        q = torch.randn(n, 2 * H, D, device="cuda").half()
+        rest = (ints([0, n]), ints([T]))
+        a = kvq.kvq_paged_attention(q, *pages, *scale, ints(ids[None]), *rest, max_new=n)
+        b = kvq.kvq_paged_attention(q, *small, *small_scale, ints([[0, 1, 2]]), *rest, max_new=n)
+        assert torch.equal(a, b) and a.abs().max() > 0
+
+
+# ---------------------------------------------------------------- together
+
+def serving_state(kvq, rng, H=2, R=4, D=128, ps=16, batch=5, n_pages=80):
+    cache = kvq.PagedCache(n_pages=n_pages, page_size=ps, n_q_heads=H * R, n_kv_heads=H, head_dim=D)
+    return dict(cache=cache, ctx=ints([0] * batch), table=ints(np.full((batch, 24), -1)),
+                free=ints(rng.permutation(n_pages)), n_free=ints([n_pages]), H=H, R=R, D=D, ps=ps,
+                batch=batch)
+
+
+def step(kvq, st, rng, new, dtype=torch.float16, log=None):
+    """plan, store and attend for one step; advances the lengths."""
+    n = int(sum(new))
+    k, v = (torch.from_numpy(rng.standard_normal((n + 2, st["H"], st["D"]))).to(dtype).cuda() for _ in range(2))
+    q = torch.from_numpy(rng.standard_normal((n + 2, st["H"] * st["R"], st["D"]))).to(dtype).cuda()
+    c = st["cache"]
+    cu, seq, slots, left = c.plan(st["ctx"], ints(new), st["table"], st["free"], st["n_free"], n + 2)
+    c.store(k, v, slots)
+    out = c.attention(q, st["table"], cu, seq, max_new=int(max(new)))
+    st["ctx"], st["n_free"] = seq, left
+    if log is not None:
+        log.append((k[:n], v[:n], q[:n], out[:n], np.concatenate([[0], np.cumsum(new)])))
+    return out
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+def test_serving_steps(kvq, dtype):
+    """Prompts, decode steps, drafted tokens and a chunk over shared pages:
+    every output against attention over the exact keys and values, whose codes
+    err by half a step of E4M3 (2^-4 of a value, twice where a scale grew)."""
+    rng = np.random.default_rng(11)
+    st = serving_state(kvq, rng)
+    log = []
+    plans = [[40, 3, 0, 17, 70], [1, 1, 1, 1, 1], [1, 0, 5, 1, 2]] + [[1] * 5] * 14 + [[30, 4, 0, 1, 33]]
+    hist = [[np.zeros((0, st["H"], st["D"]))] * 2 for _ in range(5)]
+    for new in plans:
+        step(kvq, st, rng, new, dtype, log)
+        k, v, q, out, cu = log[-1]
+        for b in range(5):
+            if new[b] == 0:
+                continue
+            hist[b] = [np.concatenate([h, f64(x[cu[b]:cu[b + 1]])]) for h, x in zip(hist[b], (k, v))]
+            K, V = hist[b]
+            for j in (0, new[b] - 1):
+                p = len(K) - new[b] + j
+                for hq in range(st["H"] * st["R"]):
+                    z = K[:p + 1, hq // st["R"]] @ f64(q[cu[b] + j, hq]) * st["D"] ** -0.5
+                    w = np.exp(z - z.max())
+                    want = (w / w.sum()) @ V[:p + 1, hq // st["R"]]
+                    d = f64(out[cu[b] + j, hq]) - want
+                    # values of size 1: codes err by 2^-4 at most, scores by
+                    # about sqrt(D) * 2^-5 * 0.09 rms: a bound on the rms
+                    assert np.sqrt((d * d).mean()) < 0.1 + 0.1 * np.abs(want).max()
+    st["cache"].check()
+    used = {int(x) for x in st["table"].flatten().tolist() if x >= 0}
+    assert len(used) == 80 - st["n_free"].item()
+
+
+def test_a_step_in_a_graph(kvq):
+    """A captured decode step replayed with other lengths gives what the eager
+    calls give, and eager calls in between do not disturb it."""
+    rng = np.random.default_rng(12)
+    st = serving_state(kvq, rng)
+    step(kvq, st, rng, [40, 3, 9, 17, 70])
+    c, B = st["cache"], 5
+    k, v = (torch.randn(B, st["H"], st["D"], device="cuda").half() for _ in range(2))
+    q = torch.randn(B, st["H"] * st["R"], st["D"], device="cuda").half()
+    ctx, new, n_free = st["ctx"].clone(), ints([1] * B), st["n_free"].clone()
+
+    def one():
+        cu, seq, slots, left = c.plan(ctx, new, st["table"], st["free"], n_free, B)
+        c.store(k, v, slots)
+        out = c.attention(q, st["table"], cu, seq, max_new=1)
+        ctx.copy_(seq)
+        n_free.copy_(left)
+        return out
+
+    save = [t.clone() for t in (c.k_pages.view(torch.uint8), c.v_pages.view(torch.uint8), c.k_scale,
+                                c.v_scale, st["table"], ctx, n_free)]
+
+    def restore():
+        for t, s in zip((c.k_pages.view(torch.uint8), c.v_pages.view(torch.uint8), c.k_scale, c.v_scale,
+                         st["table"], ctx, n_free), save):
+            t.copy_(s)
+
+    want = []
+    for _ in range(20):
+        want.append(one().clone())
+    restore()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=side):
+        out = one()
+    restore()
+    other = simple(rng, n_pages=64, seq=(900, 40), new=(1, 1))
+    plain = kvq.kvq_paged_attention(*other)
+    for i in range(20):
+        g.replay()
+        assert torch.equal(out, want[i]), i
+        assert torch.equal(kvq.kvq_paged_attention(*other), plain)
+    c.check()
+
+
+def test_two_graphs_at_the_same_time(kvq):
+    """Graphs captured from one cache replay on two streams at once: they share
+    no workspace."""
+    rng = np.random.default_rng(13)
+    calls = [simple(rng, n_pages=700, H=2, seq=(5000, 3000), new=(1, 1), R=4),
+             simple(rng, n_pages=700, H=2, seq=(2000, 6000), new=(2, 1), R=4)]
+    want = [kvq.kvq_paged_attention(*a, max_new=2) for a in calls]
+    streams, graphs, outs = [torch.cuda.Stream() for _ in range(2)], [], []
+    torch.cuda.synchronize()
+    for a, s in zip(calls, streams):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s):
+            for _ in range(3):
+                o = kvq.kvq_paged_attention(*a, max_new=2)
+        graphs.append(g)
+        outs.append(o)
+    for _ in range(30):
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+    torch.cuda.synchronize()
+    for o, w in zip(outs, want):
+        assert torch.equal(o, w)
+
+
+def test_streams_of_the_callers_choice(kvq):
+    """Another stream than the current one, by object and by address, eager
+    calls on two streams at once, and a workspace of the caller's."""
+    rng = np.random.default_rng(14)
+    a = simple(rng, n_pages=700, H=2, seq=(5000, 3000), new=(1, 1), R=4)
+    want = kvq.kvq_paged_attention(*a)
+    torch.cuda.synchronize()
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    outs = []
+    for _ in range(20):
+        for s in (s1, s2.cuda_stream):
+            o = torch.empty_like(want)
+            kvq.kvq_paged_attention(*a, out=o, stream=s)
+            outs.append(o)
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, want) for o in outs)
+    n = kvq.kvq_paged_workspace_bytes(700, 2, 16, 64)
+    ws = torch.zeros(n, dtype=torch.uint8, device="cuda")
+    assert torch.equal(kvq.kvq_paged_attention(*a, workspace=ws), want)
+    assert (ws[:1024] == 0).all()
+    with pytest.raises(kvq.KvqError):
+        kvq.kvq_paged_attention(*a, workspace=ws[:-16])
+    with pytest.raises(kvq.KvqError, match="stream"):
+        kvq.kvq_paged_attention(*a, stream="x")
+
+
+def test_cache_reports_what_was_flagged(kvq):
+    c = kvq.PagedCache(n_pages=4, page_size=16, n_q_heads=4, n_kv_heads=2, head_dim=64)
+    table = ints(np.full((1, 8), -1))
+    c.plan(ints([0]), ints([100]), table, ints([0, 1, 2, 3]), ints([4]), 100)
+    with pytest.raises(kvq.KvqError, match="free stack"):
+        c.check()
+    c.check()  # told once
+    x = torch.full((1, 2, 64), float("inf"), dtype=torch.float16, device="cuda")
+    c.store(x, x, ints([3]))
+    with pytest.raises(kvq.KvqError, match="non-finite"):
+        c.check()
+    with pytest.raises(kvq.KvqError, match="4 heads"):
+        c.attention(torch.zeros(1, 2, 64, dtype=torch.float16, device="cuda"), table, ints([0, 1]), ints([1]))
+    with pytest.raises(kvq.KvqError):
+        kvq.PagedCache(n_pages=4, page_size=16, n_q_heads=5, n_kv_heads=2, head_dim=64)
+    before = kvq.kvq_launch_count()
+    c.plan(ints([0]), ints([1]), table, ints([0, 1, 2, 3]), ints([4]), 1)
+    assert kvq.kvq_launch_count() == before + 1
+
+
+def test_nothing_to_do(kvq):
+    c, s, pages, sc = make_pool(np.random.default_rng(0), 4, 2, 16, 64)
+    e = torch.empty(0, 2, 64, dtype=torch.float16, device="cuda")
+    kvq.kvq_paged_store(e, e, ints([]), *pages, *sc)
+    out = kvq.kvq_paged_attention(torch.empty(0, 4, 64, dtype=torch.float16, device="cuda"), *pages,
+                                  *sc, ints([[0]]), ints([0, 0]), ints([5]))
+    assert out.shape == (0, 4, 64)
