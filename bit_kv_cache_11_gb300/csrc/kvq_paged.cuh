@@ -46,6 +46,7 @@ struct PagedStoreParams {
   const int* slots;
   int n_tokens;
   int n_pages, H, lg_ps;
+  int chunk;  // tokens a CTA looks at
   int* err;
 };
 
@@ -162,9 +163,21 @@ cudaError_t allow_smem(const void* fn, int bytes);
 constexpr int paged_warps(int) { return 8; }
 constexpr int kPagedMaxCtas = 152;
 // A request with at most this many query rows per kv head (new tokens * R) is
-// served by the decode kernel, which splits its tokens over the SMs and reads
-// them once per 16 rows; one with more rows by the prompt kernel.
-constexpr int kDecodeRows = 64;
+// served by the decode kernel, which splits its tokens over all SMs and reads
+// them once per 16 rows; one with more rows by the prompt kernel, which reads
+// them once per 256 rows but gives each of the call's batch * H (request,
+// head) items at most one SM.  Measured (us, decode / prompt kernel; R = 4):
+//   8 items of 32768 tokens, D = 128: 32 rows 43 / 411, 128 rows 110 / 412
+//                            D = 64:  32 rows 31 / 365, 128 rows 69 / 365
+//   128 items of 4000 tokens, D = 128: 32 rows 66 / 72, 64 rows 115 / 72
+//                             D = 64:  32 rows 45 / 57, 64 rows 73 / 57
+//   512 items of 1000 tokens, D = 128: 64 rows 115 / 89; D = 64: 74 / 73
+// so the turn lies near 32 rows (48 of the narrower ones) where the items fill
+// the SMs, and moves up in proportion where they do not.
+constexpr int decode_rows(long long items, int D) {
+  const int full = D == 64 ? 48 : 32;
+  return items >= 133 ? full : static_cast<int>(full * 133 / items);
+}
 constexpr int paged_unit_tokens(int D) { return 4096 / D; }
 // Requests a call may have: the prefix sums of the batch live in shared memory.
 constexpr int kPagedMaxBatch = 4096;

@@ -243,13 +243,14 @@ kvq_status kvq_paged_attention(const kvq_paged_pool* pool, const void* q, int dt
   const long long span = static_cast<long long>(max_pages) * pool->page_size;
   const long long rows_all = static_cast<long long>(n_tokens) * R;
   if (rows_all >= 1 << 28) return KVQ_ERR_UNSUPPORTED;  // row_token's range
-  const long long groups = std::min<long long>(static_cast<long long>(batch) * (kDecodeRows / (8 * nt)),
+  const int turn = decode_rows(static_cast<long long>(batch) * H, D);
+  const long long groups = std::min<long long>(static_cast<long long>(batch) * ((turn + 8 * nt - 1) / (8 * nt)),
                                                rows_all / (8 * nt) + batch);
   if (static_cast<double>(H) * groups * (static_cast<double>(span) / ut + 2) >= 2147483647.0)
     return KVQ_ERR_UNSUPPORTED;
   // row-tile pairs of the prompt kernel, at most
-  const bool prompts = static_cast<long long>(max_new) * R > kDecodeRows;
-  const long long pairs = rows_all / 256 + std::min<long long>(batch, rows_all / (kDecodeRows + 1));
+  const bool prompts = static_cast<long long>(max_new) * R > turn;
+  const long long pairs = rows_all / 256 + std::min<long long>(batch, rows_all / (turn + 1));
   if (prompts && pairs * H > INT_MAX) return KVQ_ERR_UNSUPPORTED;
 
   int dev = 0, sms = 0;
@@ -280,7 +281,7 @@ kvq_status kvq_paged_attention(const kvq_paged_pool* pool, const void* q, int dt
   p.qscale = softmax_scale * 1.4426950408889634f;
   p.window = window;
   p.row_min = 1;
-  p.row_max = kDecodeRows;
+  p.row_max = turn;
   p.n_warps = std::min(sms, kPagedMaxCtas) * paged_warps(nt);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   p.tickets = reinterpret_cast<int*>(ws);
@@ -292,7 +293,7 @@ kvq_status kvq_paged_attention(const kvq_paged_pool* pool, const void* q, int dt
   CUtensorMap km, vm;
   if (prompts && pairs > 0) {
     PagedAttnParams a = p;
-    a.row_min = kDecodeRows + 1;
+    a.row_min = turn + 1;
     a.row_max = INT_MAX;
     a.box_rows = pool->page_size;
     if (!row_map(&km, pool->k_pages, pool, a.box_rows) ||

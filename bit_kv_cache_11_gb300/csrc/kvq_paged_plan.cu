@@ -9,7 +9,8 @@
 // position ctx_b + t - cu_new[b], whose page is an old table entry or one of
 // the fresh ones.
 //
-// Bound: latency.  A step moves a few KB (a large admission 0.6 MB), so the
+// Bound: latency (4.0 us for 256 prompts and 140791 tokens, 0.6 MB; 5.5 us for
+// 64 requests).  A step moves a few KB (a large admission 0.6 MB), so the
 // kernel is one launch, and no CTA waits for another: every CTA reads all
 // lengths (at most 4096) and redoes the prefix sum, then fills its share of
 // the slots and table rows.  A fresh page's id comes from the stack itself,

@@ -22,10 +22,21 @@
 // over S_w.  The issuer alternates the two row tiles, so one tile's softmax
 // runs beside the other's products.
 //
-// Bound: the tensor pipe and shared memory together.  A key tile costs 4
-// products of 128 x 128 x 128 (512 cycles each at the dense rate), whose
-// operands are 192 KB of shared-memory reads, and the conversion moves 128 KB
-// more through it.
+// Bound: the chain of a row tile.  A key tile costs 4 products of 128 x 128 x
+// 128 (512 cycles each, the tensor pipe's 2048), but a row tile's softmax
+// (about 1900 cycles) and the hand-overs to it and back lie between its scores
+// and its output product, and only one other row tile's products fit beside
+// them: 3400 cycles a key tile, the tensor pipe 58 % active.  Measured: 2048
+// new tokens behind 32768 (32 heads, D = 128) 965 us, 1.17 PFLOP/s, 61 % of the
+// measured bf16 rate (two rounds of CTAs over 152 SMs: 84 % of a full one);
+// without the softmax 803 us, without the conversion 925 us, without either
+// 749 us.  Three prompts of up to 4001 tokens (40 heads) 263 us, where the
+// causal half and 9 us a CTA of start and end weigh more.
+// Measured and not kept: two CTAs sharing each key tile (cta_group::2, half of
+// the conversion each): 939 and 296 us; every CTA an equal share of the tiles,
+// items joined from shares: 958 us, and prompts need a cost for each item;
+// two threads a row: 1053 and 280 us; S read from tensor memory once, into 128
+// registers: 1037 and 261 us.
 #pragma once
 
 #include <type_traits>
@@ -658,7 +669,7 @@ __global__ void __launch_bounds__(PromptCfg<D>::THREADS, 1)
 #pragma unroll
               for (int k = 0; k < 16; ++k) gm = fmaxf(gm, __uint_as_float(x[16 * g + k]));
               // (never 0: -inf times it stays -inf)
-            const float f = fmaxf(rc.x * cq, 1.17549435e-38f);
+              const float f = fmaxf(rc.x * cq, 1.17549435e-38f);
               mx = fmaxf(mx, fmaf(gm, f, rc.y));
             }
           }
@@ -721,8 +732,8 @@ __global__ void __launch_bounds__(PromptCfg<D>::THREADS, 1)
       if (ok && wait(&o_done[w], nt - 1)) {
         tmem_fence_after();
         const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
-// through the query tile (its products are complete), so that whole rows
-        // are written: this warp's rows, chunks swizzled as the queries were
+        // Through the query tile (its products are complete), so that whole rows
+        // are written: this warp's rows, chunks swizzled as the queries were.
         uint8_t* tile = smem + C::OFF_Q + w * C::QT;
 #pragma unroll 1
         for (int c = 0; c < D / 32; ++c) {

@@ -15,8 +15,11 @@
 // one page; its first token leads it and whoever finds a leader stores the
 // whole run, so no two CTAs touch the same page and head.
 //
-// Bound: HBM for prompts (6 bytes a value: 2 read and 1 written, K and V),
-// latency for single tokens.
+// Bound: HBM for prompts (3 bytes a value: 2 read, 1 written), latency for
+// single tokens.  Measured: 26298 tokens x 8 heads x 128, 162 MB, 31 us (77 % of
+// the measured copy rate); 4861 tokens x 32 heads x 64 in 16-row pages, 60 MB,
+// 16 us (56 %, with 10 us of it the launch's and the last CTAs'); 256 single
+// tokens 2.2 us.
 #include "kvq_paged.cuh"
 
 namespace kvq {
@@ -138,24 +141,14 @@ __device__ __forceinline__ const uint4* vec_ptr(const PagedStoreParams& p, int s
                                         t * (side ? p.stride[1] : p.stride[0]) + h * D) + vec;
 }
 
-// ---- single tokens: a warp looks at one token and one head ------------------
+// ---- short runs: a warp stores a whole run of one head ------------------------
 //
 // Lanes [0, 16) serve K and [16, 32) V; a side's lanes hold a row as 16-byte
 // vectors (D / 8 of them, 16 / (D / 8) rows at a time).
-constexpr int kRowWarps = 4;
-
 template <int D, bool BF16>
-__global__ void __launch_bounds__(kRowWarps * 32) paged_store_rows_kernel(const PagedStoreParams p) {
+__device__ __forceinline__ void store_run(const PagedStoreParams& p, int t, int h, int lane) {
   constexpr int VPR = D / 8, RPS = 16 / VPR;  // vectors of a row, rows a step
-  grid_dep_wait();
-  grid_dep_launch();
-  const int lane = threadIdx.x & 31;
-  const long long gw = static_cast<long long>(blockIdx.x) * kRowWarps + (threadIdx.x >> 5);
-  const int t = static_cast<int>(gw / p.H), h = static_cast<int>(gw % p.H);
-  if (t >= p.n_tokens) return;
   const int slot = p.slots[t];
-  const int prev = t > 0 ? p.slots[t - 1] : -1;
-  if (!leads(p, t, slot, prev)) return;
   const int page = slot >> p.lg_ps, row0 = slot & ((1 << p.lg_ps) - 1);
   if (page >= p.n_pages) {
     if (lane == 0) set_err(p.err, KVQ_PAGED_ERR_BAD_PAGE);
@@ -217,13 +210,20 @@ __global__ void __launch_bounds__(kRowWarps * 32) paged_store_rows_kernel(const 
   if (l == 0) *scale = exp2i(e);
 }
 
-// ---- prompts: a CTA looks at a chunk of tokens and one head -----------------
+// ---- the kernel: a CTA looks at a chunk of tokens and one head ----------------
 //
-// A team of TEAM = page_size * D / 64 threads stores one side of a run: eight
-// 16-byte vectors a thread cover a whole page, stay in registers between the
-// maximum and the codes, and are all on their way at once.  A CTA holds as
-// many teams as fit 256 threads (512 for the largest page) and looks for
-// leaders in as many tokens as its teams store at a time.
+// It lists the chunk's leaders.  Where runs are short (more than an eighth of
+// the tokens lead), each warp stores whole runs.  Where they are long, a team
+// of TEAM = page_size * D / 64 threads stores one side of a run: eight 16-byte
+// vectors a thread cover a whole page, stay in registers between the maximum
+// and the codes, and are all on their way at once; a CTA holds as many teams
+// as fit 256 threads (512 for the largest page).
+//
+// Measured with either way alone (8 heads of 128, pages of 64, us): 256 single
+// tokens 2.5 by warps and 75 by teams, 2048 single tokens 6.8 and 94; four
+// prompts of 256 tokens 20 and 5.0, of 1024 tokens 29 and 7.6.  Chunks of 8
+// tokens: 2048 single tokens 8.3, four prompts of 512 tokens 7.0 (whole chunks
+// 6.0), of 1024 tokens 10.1 (7.6): short chunks up to 16384 token heads.
 template <int TEAM>
 __host__ __device__ constexpr int chunk_threads() {
   return TEAM == 256 ? 512 : 256;
@@ -231,10 +231,10 @@ __host__ __device__ constexpr int chunk_threads() {
 constexpr int kSteps = 8;
 
 template <int D, bool BF16, int TEAM>
-__global__ void __launch_bounds__(chunk_threads<TEAM>())
-    paged_store_chunk_kernel(const PagedStoreParams p) {
+__global__ void __launch_bounds__(chunk_threads<TEAM>(), 1024 / chunk_threads<TEAM>())
+    paged_store_kernel(const PagedStoreParams p) {
   constexpr int THREADS = chunk_threads<TEAM>(), TEAMS = THREADS / (2 * TEAM);
-  constexpr int VPR = D / 8, RPS = TEAM / VPR, CHUNK = TEAM * 64 / D * TEAMS;
+  constexpr int VPR = D / 8, RPS = TEAM / VPR, CHUNK = TEAM * 64 / D * TEAMS;  // the most
   constexpr int WPT = TEAM > 32 ? TEAM / 32 : 1;  // warps of a team's side
   __shared__ int s_list[CHUNK];
   __shared__ int s_count;
@@ -242,19 +242,23 @@ __global__ void __launch_bounds__(chunk_threads<TEAM>())
   const int tid = threadIdx.x, lane = tid & 31;
   const int side = tid / TEAM & 1, team = tid / (2 * TEAM), l = tid % TEAM;
   const int sub = l / VPR, vec = l % VPR;
-  const int tb = blockIdx.x * CHUNK, h = blockIdx.y;
+  const int tb = blockIdx.x * p.chunk, h = blockIdx.y;
   const int ps = 1 << p.lg_ps;
   if (tid == 0) s_count = 0;
   grid_dep_wait();
   grid_dep_launch();
   __syncthreads();
-  if (tid < CHUNK) {
+  if (tid < p.chunk) {
     const int t = tb + tid;
     if (t < p.n_tokens && leads(p, t, p.slots[t], t > 0 ? p.slots[t - 1] : -1))
       s_list[atomicAdd(&s_count, 1)] = t;
   }
   __syncthreads();
   const int count = s_count;
+  if (count * 8 > p.chunk) {
+    for (int i = tid >> 5; i < count; i += THREADS / 32) store_run<D, BF16>(p, s_list[i], h, lane);
+    return;
+  }
   // Threads of a run's two sides wait for one another (whole warps when a
   // side is 16 or 32 threads).
   auto team_sync = [&]() {
@@ -350,37 +354,34 @@ __global__ void __launch_bounds__(chunk_threads<TEAM>())
 }
 
 template <int D, bool BF16, int TEAM>
-cudaError_t launch_chunks(const PagedStoreParams& p, cudaLaunchConfig_t& cfg) {
-  constexpr int CHUNK = TEAM * 64 / D * (chunk_threads<TEAM>() / (2 * TEAM));
-  cfg.gridDim = dim3((p.n_tokens + CHUNK - 1) / CHUNK, p.H);
-  cfg.blockDim = dim3(chunk_threads<TEAM>());
-  return cudaLaunchKernelEx(&cfg, paged_store_chunk_kernel<D, BF16, TEAM>, p);
-}
-
-template <int D, bool BF16>
-cudaError_t launch(const PagedStoreParams& p, cudaStream_t st) {
+cudaError_t launch_team(PagedStoreParams p, cudaStream_t st) {
+  constexpr int THREADS = chunk_threads<TEAM>();
+  // Small calls take short chunks: their few runs spread over the SMs.
+  const int most = TEAM * 64 / D * (THREADS / (2 * TEAM));
+  p.chunk = static_cast<long long>(p.n_tokens) * p.H <= 16384 ? 8 : most;
   cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((p.n_tokens + p.chunk - 1) / p.chunk, p.H);
+  cfg.blockDim = dim3(THREADS);
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if (p.n_tokens <= 1024) {
-    const long long warps = static_cast<long long>(p.n_tokens) * p.H;
-    cfg.gridDim = dim3(static_cast<unsigned>((warps + kRowWarps - 1) / kRowWarps));
-    cfg.blockDim = dim3(kRowWarps * 32);
-    return cudaLaunchKernelEx(&cfg, paged_store_rows_kernel<D, BF16>, p);
-  }
+  return cudaLaunchKernelEx(&cfg, paged_store_kernel<D, BF16, TEAM>, p);
+}
+
+template <int D, bool BF16>
+cudaError_t launch(const PagedStoreParams& p, cudaStream_t st) {
   switch ((D << p.lg_ps) / 64) {
     case 16:
-      if constexpr (D == 64) return launch_chunks<D, BF16, 16>(p, cfg);
+      if constexpr (D == 64) return launch_team<D, BF16, 16>(p, st);
       break;
-    case 32: return launch_chunks<D, BF16, 32>(p, cfg);
-    case 64: return launch_chunks<D, BF16, 64>(p, cfg);
-    case 128: return launch_chunks<D, BF16, 128>(p, cfg);
+    case 32: return launch_team<D, BF16, 32>(p, st);
+    case 64: return launch_team<D, BF16, 64>(p, st);
+    case 128: return launch_team<D, BF16, 128>(p, st);
     case 256:
-      if constexpr (D == 128) return launch_chunks<D, BF16, 256>(p, cfg);
+      if constexpr (D == 128) return launch_team<D, BF16, 256>(p, st);
       break;
   }
   return cudaErrorInvalidValue;

@@ -157,6 +157,8 @@ def slots_of(rng, runs, ps, n_pages, pad=0):
     (64, 128, 2, [(10, 700), (0, 1), (0, 500), (63, 130)], 0),
     (16, 64, 3, [(1, 600), (15, 1), (9, 1), (0, 1), (0, 550)], 3),
     (128, 64, 1, [(127, 1000), (64, 64), (5, 9), (0, 128)], 0),
+    (128, 128, 1, [(3, 300), (127, 2), (0, 128)], 0),
+    (32, 128, 1, [(i % 32, 1 + i % 3) for i in range(90)] + [(0, 200)], 0),
 ])
 def test_store(kvq, dtype, ps, D, H, runs, pad):
     rng = np.random.default_rng(ps + D + len(runs))
@@ -166,6 +168,19 @@ def test_store(kvq, dtype, ps, D, H, runs, pad):
     # token sizes vary over 2^12, so scales grow, stay, and reach the subnormal codes
     x = [rng.standard_normal((T, H, D)) * 2.0 ** rng.integers(-8, 4, (T, H, 1)) for _ in range(2)]
     check_store(kvq, rng, x, slots, ps, D, H, n_pages, dtype, fused=D == 128)
+
+
+@pytest.mark.parametrize("ps,D,dtype", [(16, 64, "fp16"), (16, 128, "bf16"), (32, 128, "fp16"),
+                                        (64, 64, "bf16"), (64, 128, "fp16"), (128, 128, "bf16")])
+def test_store_large_calls(kvq, ps, D, dtype):
+    """Over 16384 token heads: whole chunks, of long runs and of single tokens."""
+    rng = np.random.default_rng(ps + D)
+    H, n_pages = 24, 1500 + 3000 // ps
+    runs = [(5 % ps, 700), (0, 1)] + [(int(r), 1) for r in rng.integers(0, ps, 500)] + [(ps - 1, 600)]
+    slots = slots_of(rng, runs, ps, n_pages)
+    x = [rng.standard_normal((len(slots), H, D)) * 2.0 ** rng.integers(-8, 4, (len(slots), H, 1))
+         for _ in range(2)]
+    check_store(kvq, rng, x, slots, ps, D, H, n_pages, dtype)
 
 
 @pytest.mark.parametrize("T", [3, 1100])
@@ -226,6 +241,10 @@ def test_store_page_by_page_equals_at_once(kvq):
 
 def check_attention(kvq, case, seed=0, **over):
     ps, D, H, R, dtype, ctx, new, window = case
+    # requests without tokens behind the others: with many of them the call
+    # counts as a large batch, whose many-row requests the prompt kernel serves
+    idle = over.get("idle", 0)
+    ctx, new = list(ctx) + [0] * idle, list(new) + [0] * idle
     rng = np.random.default_rng(seed + ps + D + H + R + sum(ctx) + sum(new) + window)
     B, T = len(ctx), sum(new)
     seq = np.array(ctx) + np.array(new)
@@ -300,7 +319,7 @@ MULTI = [
     (128, 128, 1, 3, "fp16", [120, 0, 250], [20, 1, 64], 0),
     (64, 64, 2, 2, "fp16", [0, 10], [150, 0], 0),
     (64, 128, 1, 5, "bf16", [0, 77], [130, 70], 65),
-    # over 256 rows of 128 channels: two CTAs share an item
+    # several row tiles of a request, a last one of few rows
     (16, 128, 2, 1, "fp16", [0, 300], [520, 270], 0),
     (128, 128, 1, 8, "bf16", [100, 3], [65, 9], 0),
     (32, 128, 1, 2, "fp16", [50, 0, 7], [129, 1, 300], 100),
@@ -315,16 +334,27 @@ def test_decode(kvq, case):
     check_attention(kvq, case)
 
 
+@pytest.mark.parametrize("idle", [0, 140])
 @pytest.mark.parametrize("case", MULTI, ids=str)
-def test_several_new_tokens(kvq, case):
-    check_attention(kvq, case)
+def test_several_new_tokens(kvq, case, idle):
+    check_attention(kvq, case, idle=idle)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_around_the_turn_to_the_prompt_kernel(kvq, D):
+    """Rows just below, at and above what one kernel leaves to the other."""
+    for new in (31, 32, 33, 48, 49):
+        check_attention(kvq, (32, D, 1, 1, "fp16", [200, 9], [new, 3], 0), idle=140)
+    for new in (265, 266, 267, 400):
+        check_attention(kvq, (64, D, 4, 1, "bf16", [30], [new], 0), idle=3)
 
 
 def test_a_mixed_batch(kvq):
     """Decodes, drafted tokens, a short and a long prompt in one call."""
     for ps, D, dtype in ((64, 128, "bf16"), (16, 64, "fp16"), (128, 128, "fp16")):
-        check_attention(kvq, (ps, D, 2, 4, dtype, [900, 37, 0, 200, 0, 3], [1, 4, 300, 17, 33, 0], 0))
-        check_attention(kvq, (ps, D, 2, 4, dtype, [900, 37, 0, 200], [1, 4, 300, 17], 50))
+        for idle in (0, 80):
+            check_attention(kvq, (ps, D, 2, 4, dtype, [900, 37, 0, 200, 0, 3], [1, 4, 300, 17, 33, 0], 0), idle=idle)
+            check_attention(kvq, (ps, D, 2, 4, dtype, [900, 37, 0, 200], [1, 4, 300, 17], 50), idle=idle)
 
 
 def test_max_new_may_be_a_loose_bound(kvq):
@@ -343,7 +373,9 @@ def test_any_softmax_scale(kvq, scale):
             c[i] = ref.e4m3_code(rng.standard_normal(c[i].shape) / s[i][..., None, None] / 8)
             pages[i] = torch.from_numpy(c[i]).cuda().view(torch.float8_e4m3fn)
         q = torch.from_numpy(rng.standard_normal((n, R, D))).half()
-        table, cu, seq = np.arange(20)[None], np.array([0, n]), np.array([T0 + n])
+        idle = 150 if n > 1 else 0  # (a large batch: the prompt kernel)
+        table = np.concatenate([np.arange(20)[None], np.full((idle, 20), -1)])
+        cu, seq = np.array([0] + [n] * (idle + 1)), np.array([T0 + n] + [0] * idle)
         got = kvq.kvq_paged_attention(q.cuda(), *pages, *sc, ints(table), ints(cu), ints(seq),
                                       max_new=n, softmax_scale=scale)
         want, size, reach = ref.attention(f64(q), c[0], c[1], s[0], s[1], table, cu, seq, ps, scale)
@@ -353,7 +385,10 @@ def test_any_softmax_scale(kvq, scale):
 
 
 def simple(rng, n_pages=12, H=1, ps=16, D=64, seq=(100, 40), new=(1, 1), R=2, dtype=torch.float16):
-    """A small call's arguments."""
+    """A small call's arguments.  Calls of many rows get requests without
+    tokens behind, so that the prompt kernel serves them."""
+    idle = 150 if max(new) > 60 else 0
+    seq, new = tuple(seq) + (0,) * idle, tuple(new) + (0,) * idle
     c, s, pages, sc = make_pool(rng, n_pages, H, ps, D)
     need = [-(-x // ps) for x in seq]
     table = np.full((len(seq), max(need)), -1)
@@ -411,10 +446,11 @@ def test_lengths_that_break_the_contract_are_skipped(kvq):
                             (None, (0, new[0], n + 1), 0), (None, (-1, new[0], n), 1),
                             (None, (new[0], 0, n), None)):
             a = list(args)
+            idle = a[7].numel() - 2
             if seq:
-                a[7] = ints(seq)
+                a[7] = ints(list(seq) + [0] * idle)
             if cu:
-                a[6] = ints(cu)
+                a[6] = ints(list(cu) + [cu[-1]] * idle)
             out = torch.full_like(args[0], 5.0)
             err = ints([0])
             kvq.kvq_paged_attention(*a, max_new=max(new), out=out, error=err)
@@ -471,7 +507,9 @@ def test_values_of_very_different_pages(kvq):
         pages = [torch.from_numpy(x).cuda().view(torch.float8_e4m3fn) for x in c]
         sc = [torch.from_numpy(x.astype(np.float32)).cuda() for x in s]
         q = torch.from_numpy(np.abs(rng.standard_normal((n, 1, D)))).half()
-        table, cu, seq = np.arange(8)[None], np.array([0, n]), np.array([ps * 8])
+        idle = 150 if n > 1 else 0  # (a large batch: the prompt kernel)
+        table = np.concatenate([np.arange(8)[None], np.full((idle, 8), -1)])
+        cu, seq = np.array([0] + [n] * (idle + 1)), np.array([ps * 8] + [0] * idle)
         got = kvq.kvq_paged_attention(q.cuda(), *pages, *sc, ints(table), ints(cu), ints(seq),
                                       max_new=n, softmax_scale=0.25)
         want, size, reach = ref.attention(f64(q), c[0], c[1], s[0], s[1], table, cu, seq, ps, 0.25)
@@ -500,11 +538,12 @@ def test_a_pool_beyond_four_gigabytes(kvq):
              for _ in range(2)]
     small_scale = [torch.ones(3, H, device="cuda") for _ in range(2)]
     kvq.kvq_paged_store(k, v, ints(pos), *small, *small_scale)
-    for n in (1, 100):
+    for n, idle in ((1, 0), (100, 0), (100, 30)):
         q = torch.randn(n, 2 * H, D, device="cuda").half()
-        rest = (ints([0, n]), ints([T]))
-        a = kvq.kvq_paged_attention(q, *pages, *scale, ints(ids[None]), *rest, max_new=n)
-        b = kvq.kvq_paged_attention(q, *small, *small_scale, ints([[0, 1, 2]]), *rest, max_new=n)
+        rest = (ints([0] + [n] * (idle + 1)), ints([T] + [0] * idle))
+        wide = lambda t: ints(np.concatenate([[t], np.zeros((idle, 3))]))  # noqa: E731
+        a = kvq.kvq_paged_attention(q, *pages, *scale, wide(ids), *rest, max_new=n)
+        b = kvq.kvq_paged_attention(q, *small, *small_scale, wide([0, 1, 2]), *rest, max_new=n)
         assert torch.equal(a, b) and a.abs().max() > 0
 
 
