@@ -237,6 +237,9 @@ kvq_status kvq_paged_attention(const kvq_paged_pool* pool, const void* q, int dt
   if (R > 16 || batch > kPagedMaxBatch || max_pages > INT_MAX / pool->page_size)
     return KVQ_ERR_UNSUPPORTED;
   max_new = std::min(max_new, n_tokens);
+  // positions minus the window stay inside 32 bits
+  if (window >= static_cast<long long>(max_pages) * pool->page_size) window = 0;
+  if (window > INT_MAX - (1 << 28)) return KVQ_ERR_UNSUPPORTED;
   const int nt = static_cast<long long>(max_new) * R <= 8 ? 1 : 2;
   // units of the decode kernel's items are counted in 31 bits
   const int ut = paged_unit_tokens(D);

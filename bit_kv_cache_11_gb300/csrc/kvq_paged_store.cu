@@ -16,10 +16,11 @@
 // whole run, so no two CTAs touch the same page and head.
 //
 // Bound: HBM for prompts (3 bytes a value: 2 read, 1 written), latency for
-// single tokens.  Measured: 26298 tokens x 8 heads x 128, 162 MB, 31 us (77 % of
-// the measured copy rate); 4861 tokens x 32 heads x 64 in 16-row pages, 60 MB,
-// 16 us (56 %, with 10 us of it the launch's and the last CTAs'); 256 single
-// tokens 2.2 us.
+// single tokens.  Measured: 26298 tokens x 8 heads x 128, 162 MB, 28.9 us (84 %
+// of the measured copy rate); 4861 tokens x 32 heads x 64 in 16-row pages, 60 MB,
+// 14.5 us (62 %; the launch and the last CTAs take the rest); 256 single tokens
+// 2.5 us.  One test per side for NaN instead of two selects a value, and fp16
+// codes without a step through fp32, took 31.0 -> 28.9 and 16.0 -> 14.5 us.
 #include "kvq_paged.cuh"
 
 namespace kvq {
@@ -94,24 +95,55 @@ __device__ __forceinline__ uint32_t codes2(float2 x) {
   return __nv_cvt_float2_to_fp8x2(x, __NV_SATFINITE, __NV_E4M3);
 }
 
-// Eight values times `inv` (a power of two) as E4M3 codes.  `clean` replaces
-// NaN by 0 first (the conversion would keep it).
+// Two fp16 pairs -> four E4M3 codes, nearest even.
+__device__ __forceinline__ uint32_t codes4(uint32_t lo, uint32_t hi) {
+  uint32_t c;
+  asm("{\n\t.reg .b16 l, h;\n\tcvt.rn.satfinite.e4m3x2.f16x2 l, %1;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f16x2 h, %2;\n\tmov.b32 %0, {l, h};\n\t}"
+      : "=r"(c)
+      : "r"(lo), "r"(hi));
+  return c;
+}
+
+// Eight values times `inv` = 2^-e as E4M3 codes.  `plain` (see plain_codes)
+// values take the shorter way, others pass through fp32 with NaN replaced by 0
+// (the conversion would keep it).
+// fp16 stays fp16 on the shorter way: the product, at most 448, is exact where
+// it is at least 2^-14, and below, where it may round, it stays below 2^-10,
+// the tie between code 0 and E4M3's least value 2^-9.
 template <bool BF16>
-__device__ __forceinline__ uint2 codes8(uint4 v, float inv, bool clean) {
+__device__ __forceinline__ uint2 codes8(uint4 v, float inv, bool plain) {
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  if (!BF16 && plain) {
+    const __half2 s = __float2half2_rn(inv);
+    uint32_t x[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const __half2 h = __hmul2(*reinterpret_cast<const __half2*>(&w[i]), s);
+      x[i] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+    return make_uint2(codes4(x[0], x[1]), codes4(x[2], x[3]));
+  }
   uint32_t c[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     float2 f = to_float2<BF16>(w[i]);
     f.x *= inv;
     f.y *= inv;
-    if (clean) {
+    if (!plain) {
       f.x = f.x == f.x ? f.x : 0.f;
       f.y = f.y == f.y ? f.y : 0.f;
     }
     c[i] = codes2(f);
   }
   return make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
+}
+
+// No NaN or infinity among the values; for fp16, 2^-e is a number of that type
+// (a page's older rows can hold its exponent above fp16's own need of 8).
+template <bool BF16>
+__device__ __forceinline__ bool plain_codes(bool odd, int e) {
+  return !odd && (BF16 || e <= 24);
 }
 
 // Eight E4M3 codes times `f` (a power of two <= 1), rounded again.
@@ -203,10 +235,11 @@ __device__ __forceinline__ void store_run(const PagedStoreParams& p, int t, int 
     }
   }
   const float inv = exp2i(-e);
-  if (sub < n) *reinterpret_cast<uint2*>(base + static_cast<size_t>(row0 + sub) * D) = codes8<BF16>(first, inv, odd);
+  const bool plain = plain_codes<BF16>(odd, e);
+  if (sub < n) *reinterpret_cast<uint2*>(base + static_cast<size_t>(row0 + sub) * D) = codes8<BF16>(first, inv, plain);
   for (int i = sub + RPS; i < n; i += RPS)
     *reinterpret_cast<uint2*>(base + static_cast<size_t>(row0 + i) * D) =
-        codes8<BF16>(*vec_ptr(p, side, t + i, h, D, vec), inv, odd);
+        codes8<BF16>(*vec_ptr(p, side, t + i, h, D, vec), inv, plain);
   if (l == 0) *scale = exp2i(e);
 }
 
@@ -341,11 +374,20 @@ __global__ void __launch_bounds__(chunk_threads<TEAM>(), 1024 / chunk_threads<TE
         }
       }
       const float inv = exp2i(-e);
+      if (plain_codes<BF16>(odd, e)) {
 #pragma unroll
-      for (int s = 0; s < kSteps; ++s) {
-        if ((rows >> s) & 1)
-          *reinterpret_cast<uint2*>(base + static_cast<size_t>(row0 + s * RPS + sub) * D) =
-              codes8<BF16>(x[s], inv, odd);
+        for (int s = 0; s < kSteps; ++s) {
+          if ((rows >> s) & 1)
+            *reinterpret_cast<uint2*>(base + static_cast<size_t>(row0 + s * RPS + sub) * D) =
+                codes8<BF16>(x[s], inv, true);
+        }
+      } else {
+#pragma unroll
+        for (int s = 0; s < kSteps; ++s) {
+          if ((rows >> s) & 1)
+            *reinterpret_cast<uint2*>(base + static_cast<size_t>(row0 + s * RPS + sub) * D) =
+                codes8<BF16>(x[s], inv, false);
+        }
       }
     }
     team_sync();  // s_max and `was` are read

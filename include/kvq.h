@@ -372,7 +372,10 @@ KVQ_API kvq_status kvq_decode_attention_noalloc(const kvq_config* cfg, const voi
  * codes c become E4M3(c * s / s') (exact but for codes that become
  * subnormal).  Elements below 2^-25 in magnitude become 0, as 2^-15 * 2^-9 is
  * the smallest value a page can hold.  Infinities saturate, NaN is stored as
- * 0, and either sets KVQ_PAGED_ERR_NONFINITE.
+ * 0, and either sets KVQ_PAGED_ERR_NONFINITE.  The attention takes any positive
+ * finite scale (pages filled by other means); where such a page's scale is no
+ * power of two, the store first rounds it up to one, within [2^-15, 2^40].
+ * Pages hold no NaN codes in rows that a token can see.
  *
  * Conventions, besides those at the top of this header.
  *   - Sizes with an upper bound: head_dim 64 or 128; page_size 16, 32, 64 or
@@ -383,7 +386,9 @@ KVQ_API kvq_status kvq_decode_attention_noalloc(const kvq_config* cfg, const voi
  *     contiguous elements per token; `stride` is the distance between tokens
  *     in elements, a multiple of 8 (slices of a fused projection fit).
  *   - int arrays are 32-bit and 4-byte aligned (slots: 16).
- *   - The calls launch on the current device, which holds every buffer.
+ *   - The calls launch on the current device, which holds every buffer.  They
+ *     can be captured into graphs; the first call of each kind on a device
+ *     loads its kernels, so make that one before a capture.
  *   - device_error is an optional device int that kernels OR the
  *     KVQ_PAGED_ERR_* bits into; the caller clears it.  What a kernel flags it
  *     also skips: no call reads or writes outside its buffers, whatever the

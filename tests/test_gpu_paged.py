@@ -170,6 +170,30 @@ def test_store(kvq, dtype, ps, D, H, runs, pad):
     check_store(kvq, rng, x, slots, ps, D, H, n_pages, dtype, fused=D == 128)
 
 
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("n", [1, 50])
+def test_store_beside_rows_of_a_larger_scale(kvq, dtype, n):
+    """Rows behind older ones of scales up to 2^40: codes around E4M3's least
+    value and 0, for 2^-e above, at and below fp16's least number 2^-24."""
+    rng = np.random.default_rng(n)
+    ps, H = 64, 3
+    for D in (64, 128):
+        for e in (*range(20, 28), 40):
+            c, s, pages, scale = make_pool(rng, 2, H, ps, D)
+            for i in range(2):
+                s[i][:] = 2.0 ** e
+                scale[i].fill_(2.0 ** e)
+            slots = np.arange(n) + ps + 9
+            x = [torch.from_numpy(rng.uniform(-65504, 65504, (n, H, D))).to(DT[dtype]) for _ in range(2)]
+            kvq.kvq_paged_store(x[0].cuda(), x[1].cuda(), ints(slots), *pages, *scale)
+            for i in range(2):
+                codes, sc = ref.store(f64(x[i]), slots, c[i], s[i], ps)
+                assert np.array_equal(scale[i].cpu().numpy().astype(np.float64), sc)
+                got = pages[i].view(torch.uint8).cpu().numpy()
+                same = (got == codes) | ((got & 127) == 0) & ((codes & 127) == 0)
+                assert same.all(), (D, e, np.argwhere(~same)[:5])
+
+
 @pytest.mark.parametrize("ps,D,dtype", [(16, 64, "fp16"), (16, 128, "bf16"), (32, 128, "fp16"),
                                         (64, 64, "bf16"), (64, 128, "fp16"), (128, 128, "bf16")])
 def test_store_large_calls(kvq, ps, D, dtype):
@@ -357,6 +381,31 @@ def test_a_mixed_batch(kvq):
             check_attention(kvq, (ps, D, 2, 4, dtype, [900, 37, 0, 200], [1, 4, 300, 17], 50), idle=idle)
 
 
+def test_the_largest_batch(kvq):
+    """4096 requests, of no token to three pages, in both kernels' batches."""
+    rng = np.random.default_rng(1)
+    ctx = [int(x) for x in rng.integers(0, 40, 4096)]
+    check_attention(kvq, (16, 64, 1, 1, "fp16", ctx, [int(x) for x in rng.integers(0, 3, 4096)], 0))
+    new = [0] * 4096
+    new[17], new[4095], new[300] = 60, 70, 1
+    check_attention(kvq, (16, 128, 1, 1, "bf16", ctx, new, 0))
+    args = simple(rng)
+    big = [ints(np.zeros((4097, 2))), ints(np.zeros(4098)), ints(np.zeros(4097))]
+    with pytest.raises(kvq.KvqError) as e:
+        kvq.kvq_paged_attention(*args[:5], *big)
+    assert e.value.status == kvq.KVQ_ERR_UNSUPPORTED
+
+
+def test_new_tokens_behind_other_rows(kvq):
+    """The first request's rows need not be row 0; rows before it are left."""
+    args = simple(np.random.default_rng(3))
+    want = kvq.kvq_paged_attention(*args)
+    q = torch.cat([torch.full_like(args[0], 9.0), args[0]])
+    out = torch.full_like(q, 5.0)
+    kvq.kvq_paged_attention(q, *args[1:6], args[6] + 2, args[7], out=out)
+    assert torch.equal(out[2:], want) and (out[:2] == 5.0).all()
+
+
 def test_max_new_may_be_a_loose_bound(kvq):
     check_attention(kvq, (32, 128, 1, 2, "fp16", [50, 7], [3, 1], 0), max_new=5000)
     check_attention(kvq, (32, 64, 1, 1, "bf16", [50, 7], [1, 1], 0), max_new=4)
@@ -488,6 +537,41 @@ def test_a_query_that_sees_nothing_gives_zeros(kvq):
         early = max(0, new[1] - 40)
         assert (out[new[0]:new[0] + early] == 0).all()
         assert torch.isfinite(out).all() and (out[new[0] + early:] != 0).any()
+
+
+@pytest.mark.parametrize("new", [(1, 1), (90, 70)])
+def test_the_widest_window_is_none(kvq, new):
+    args = simple(np.random.default_rng(9), seq=(0, 40), new=new)
+    want = kvq.kvq_paged_attention(*args, max_new=max(new))
+    for window in (40, 112, 1 << 30, (1 << 31) - 1):
+        got = kvq.kvq_paged_attention(*args, max_new=max(new), window=window)
+        assert torch.equal(got, want), window
+
+
+def test_pages_with_any_scale(kvq):
+    """Scales that are no powers of two: attended as they are, rounded up by a
+    store that adds rows."""
+    rng = np.random.default_rng(21)
+    ps, D = 16, 64
+    c, s, pages, sc = make_pool(rng, 4, 1, ps, D)
+    for i in range(2):
+        c[i] = ref.e4m3_code(rng.standard_normal(c[i].shape) * 8)
+        s[i] = rng.uniform(0.01, 0.2, s[i].shape).astype(np.float32).astype(np.float64)
+    pages = [torch.from_numpy(x).cuda().view(torch.float8_e4m3fn) for x in c]
+    sc = [torch.from_numpy(x.astype(np.float32)).cuda() for x in s]
+    q = torch.from_numpy(rng.standard_normal((2, 2, D))).half()
+    table, cu, seq = np.arange(4)[None], np.array([0, 2]), np.array([55])
+    got = kvq.kvq_paged_attention(q.cuda(), *pages, *sc, ints(table), ints(cu), ints(seq), max_new=2)
+    want, size, reach = ref.attention(f64(q), c[0], c[1], s[0], s[1], table, cu, seq, ps, D ** -0.5)
+    tol = ref.tolerance(want, size, reach, HALF["fp16"], 55, (448 * s[1]).max())
+    assert float((np.abs(f64(got) - want) / tol).max()) <= 1.0
+    x = torch.full((1, 1, D), 1.0, dtype=torch.float16, device="cuda")
+    kvq.kvq_paged_store(x, x, ints([3 * ps + 7]), *pages, *sc)
+    for i in range(2):
+        now = 2.0 ** np.ceil(np.log2(s[i][3, 0]))
+        assert sc[i][3, 0].item() == now
+        codes = pages[i].view(torch.uint8).cpu().numpy()[3, 0, :7]
+        assert np.array_equal(ref.E4M3[codes], ref.E4M3[ref.e4m3_code(ref.E4M3[c[i][3, 0, :7]] * (s[i][3, 0] / now))])
 
 
 def test_values_of_very_different_pages(kvq):
