@@ -7,6 +7,7 @@
 
 #include <ATen/core/Tensor.h>
 #include <ATen/cuda/EmptyTensor.h>
+#include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <cuda_runtime_api.h>
@@ -157,6 +158,8 @@ cudaStream_t stream_of(const char* call, PyObject* o, int index) {
     PyErr_Clear();
     refuse(call, "stream must be a stream or its address");
   }
+  // (one name for as many streams as there are threads; memory is kept by name)
+  if (p == cudaStreamPerThread) refuse(call, "stream must not be the per-thread default stream");
   return static_cast<cudaStream_t>(p);
 }
 
@@ -170,6 +173,19 @@ int* error_ptr(Place& place, PyObject* o) {
 at::Tensor empty(at::IntArrayRef sizes, at::ScalarType t, int index) {
   return at::detail::empty_cuda(sizes, t, c10::Device(c10::kCUDA, static_cast<c10::DeviceIndex>(index)),
                                 std::nullopt);
+}
+
+// An output of a call on stream st: memory of st, as work still waiting on the
+// current stream may use what that stream's allocations get again; and freed
+// only behind the current stream's work, which reads it.
+at::Tensor empty_on(cudaStream_t st, at::IntArrayRef sizes, at::ScalarType t, int index) {
+  const c10::cuda::CUDAStream cur = c10::cuda::getCurrentCUDAStream(static_cast<c10::DeviceIndex>(index));
+  if (cur.stream() == st) return empty(sizes, t, index);
+  const c10::cuda::CUDAStreamGuard guard(
+      c10::cuda::getStreamFromExternal(st, static_cast<c10::DeviceIndex>(index)));
+  at::Tensor x = empty(sizes, t, index);
+  if (x.numel() > 0) c10::cuda::CUDACachingAllocator::recordStream(x.storage().data_ptr(), cur);
+  return x;
 }
 
 // ---- workspaces ---------------------------------------------------------------
@@ -276,7 +292,7 @@ PyObject* plan(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const c10::cuda::CUDAGuard guard(static_cast<c10::DeviceIndex>(place.index));
     const cudaStream_t st = stream_of(call, a[12], place.index);
     for (int i = 0; i < 4; ++i)
-      if (!out[i].defined()) out[i] = empty({sizes[i]}, at::kInt, place.index);
+      if (!out[i].defined()) out[i] = empty_on(st, {sizes[i]}, at::kInt, place.index);
     check(kvq_paged_plan(int_ptr(ctx), int_ptr(nw), static_cast<int>(batch), int_ptr(tab),
                          static_cast<int>(tab.size(1)), int_ptr(fp), static_cast<int>(fp.numel()),
                          int_ptr(nf), ps, static_cast<int>(tokens), int_ptr(out[0]),
@@ -369,7 +385,7 @@ PyObject* attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
     int* err = error_ptr(place, a[13]);
     const c10::cuda::CUDAGuard guard(static_cast<c10::DeviceIndex>(place.index));
     const cudaStream_t st = stream_of(call, a[14], place.index);
-    if (!out.defined()) out = empty(q.sizes(), q.scalar_type(), place.index);
+    if (!out.defined()) out = empty_on(st, q.sizes(), q.scalar_type(), place.index);
     void* ws = nullptr;
     size_t bytes = 0;
     if (a[12] == Py_None) {

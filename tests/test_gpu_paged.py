@@ -759,6 +759,32 @@ def test_two_graphs_at_the_same_time(kvq):
         assert torch.equal(o, w)
 
 
+def test_outputs_are_the_streams_memory(kvq):
+    """Memory freed on the current stream may still be in use there, so a call
+    on another stream does not get it for its outputs."""
+    a = simple(np.random.default_rng(13))
+    want = kvq.kvq_paged_attention(*a)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    freed = torch.empty_like(want)
+    at = freed.data_ptr()
+    del freed
+    out = kvq.kvq_paged_attention(*a, stream=side)
+    assert out.data_ptr() != at
+    side.synchronize()
+    assert torch.equal(out, want)
+    ctx, new = ints([3, 20]), ints([1, 5])
+    free, left = ints(range(9)), ints([9])
+    tables = [torch.full((2, 4), 0, dtype=torch.int32, device="cuda") for _ in range(2)]
+    here = kvq.kvq_paged_plan(ctx, new, tables[0], free, left, 16, 6)
+    torch.cuda.synchronize()
+    there = kvq.kvq_paged_plan(ctx, new, tables[1], free, left, 16, 6, stream=side)
+    side.synchronize()
+    assert all(torch.equal(x, y) for x, y in zip(here, there))
+    with pytest.raises(kvq.KvqError, match="stream"):
+        kvq.kvq_paged_attention(*a, stream=2)  # the per-thread default stream
+
+
 def test_streams_of_the_callers_choice(kvq):
     """Another stream than the current one, by object and by address, eager
     calls on two streams at once, and a workspace of the caller's."""
