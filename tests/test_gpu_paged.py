@@ -785,6 +785,27 @@ def test_outputs_are_the_streams_memory(kvq):
         kvq.kvq_paged_attention(*a, stream=2)  # the per-thread default stream
 
 
+def test_a_branch_of_a_captured_graph(kvq):
+    """A call on a stream that a capture forked to: its output and workspace
+    are the graph's, beside a call of the capture's own stream."""
+    rng = np.random.default_rng(15)
+    a = simple(rng, n_pages=700, H=2, seq=(5000, 3000), new=(1, 1), R=4)
+    b = simple(rng, n_pages=700, H=2, seq=(4000, 1), new=(1, 1), R=4)
+    want = [kvq.kvq_paged_attention(*x) for x in (a, b)]
+    main, branch = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=main):
+        branch.wait_stream(main)
+        got = [kvq.kvq_paged_attention(*a), kvq.kvq_paged_attention(*b, stream=branch)]
+        main.wait_stream(branch)
+    for _ in range(20):
+        for x in got:
+            x.fill_(7.0)
+        g.replay()
+        assert all(torch.equal(x, y) for x, y in zip(got, want))
+
+
 def test_streams_of_the_callers_choice(kvq):
     """Another stream than the current one, by object and by address, eager
     calls on two streams at once, and a workspace of the caller's."""
