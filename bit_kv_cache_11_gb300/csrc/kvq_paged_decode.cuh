@@ -4,13 +4,15 @@
 // Mathematics.  With key codes a_t, value codes c_t and the page scales sk,
 // sv of token t, in log2 units (kappa = softmax scale * log2 e):
 //   s_t = kappa * sk_t * (q . a_t) + log2(sv_t)
-//   m   = max s_t,  w_t = 2^(s_t - m) <= 1
+//   m   = max s_t,  w_t = 2^(s_t - m + 15) <= 2^15
 //   out = (sum_t w_t c_t) / (sum_t w_t / sv_t)
 // The value scale rides in the exponent, so it costs one FMA a score and the
-// codes themselves are the matrix operands: E4M3 converts to fp16 exactly,
-// and w_t in fp16 is full precision for the tokens that carry the result,
-// whatever their pages' scales are.  Weights, sums and outputs accumulate in
-// fp32; the fp16 rounding of w_t is the only one besides the output's.
+// codes themselves are the matrix operands: E4M3 converts to fp16 exactly.
+// Weights, sums and outputs accumulate in fp32; the fp16 rounding of the w_t
+// that multiply the codes is the only one besides the output's: half a step,
+// 2^-11, of a token's weight * scale down to 2^-29 of the row's largest, and
+// 2^-40 of that largest below (the factor 2^15 uses fp16's whole range, and
+// 1 / sv carries 2^-15 so that the sum below stays as it is).
 //
 // Split.  Every warp streams a contiguous, equal range of units of UT = 32
 // (D = 128) or 64 (D = 64) tokens: 4 KB of key and 4 KB of value codes that
@@ -74,6 +76,20 @@ __device__ __forceinline__ uint2 lds64(uint32_t a) {
   uint2 v;
   asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
   return v;
+}
+
+// Weights as fp16; one that the rounding of huge scores (over 2^22) lifts above
+// fp16's largest number stays finite.
+__device__ __forceinline__ uint32_t pack_weights(float lo, float hi) {
+  uint32_t x;
+  asm("cvt.rn.satfinite.f16x2.f32 %0, %1, %2;" : "=r"(x) : "f"(hi), "f"(lo));
+  return x;
+}
+constexpr float kWeightLog2 = 15.f, kWeightInv = 0x1p-15f;  // weights are 2^15 times
+
+// What a row's sum of codes is multiplied by, from its sum of weights.
+__device__ __forceinline__ float row_factor(float l) {
+  return l > 0.f ? kWeightInv / l : (l == 0.f ? 0.f : l);
 }
 
 // No page is needed (a table entry is never this: ids are below 2^31 - 1).
@@ -270,7 +286,7 @@ __global__ void __launch_bounds__(PagedCfg<D, NT>::NW * 32, 1)
   auto put_record = [&](int u0b, int rec0, float ks, float vs) {
     const int tok = li.tok0 + (u0b - li.u0) * UT + lane * 16;
     const bool seen = my_page >= 0 && tok < lhi && tok + 16 > llo;
-    ring[(rec0 + lane) & (C::RING - 1)] = make_float4(ks, fast_log2(vs), 1.f / vs, seen ? 1.f : 0.f);
+    ring[(rec0 + lane) & (C::RING - 1)] = make_float4(ks, fast_log2(vs), kWeightInv / vs, seen ? 1.f : 0.f);
   };
   const int nbox = UT / p.box_rows;  // boxes of a side
   // lane i < nbox copies key box i, lane nbox + i value box i
@@ -481,6 +497,7 @@ __global__ void __launch_bounds__(PagedCfg<D, NT>::NW * 32, 1)
         al[c] = fast_exp2(m[nt][c] - mb[c]);
         m[nt][c] = mn;
         l[nt][c] *= al[c];
+        mb[c] -= kWeightLog2;
       }
 #pragma unroll
       for (int mt = 0; mt < GR; ++mt) {
@@ -491,8 +508,8 @@ __global__ void __launch_bounds__(PagedCfg<D, NT>::NW * 32, 1)
         x[3] = fast_exp2(x[3] - mb[1]);
         l[nt][0] = fmaf(x[0] + x[2], rec[mt].z, l[nt][0]);
         l[nt][1] = fmaf(x[1] + x[3], rec[mt].z, l[nt][1]);
-        pw[mt][nt][0] = movmatrix(pack_half2(x[0], x[1]));
-        pw[mt][nt][1] = movmatrix(pack_half2(x[2], x[3]));
+        pw[mt][nt][0] = movmatrix(pack_weights(x[0], x[1]));
+        pw[mt][nt][1] = movmatrix(pack_weights(x[2], x[3]));
       }
       if (__any_sync(0xffffffffu, al[0] != 1.f || al[1] != 1.f)) {
 #pragma unroll
@@ -571,7 +588,7 @@ __global__ void __launch_bounds__(PagedCfg<D, NT>::NW * 32, 1)
           const int r = nt * 8 + 2 * t + c;
           if (r >= it.rows) continue;
           const int row = it.grp * RG + r, j = row_token(p, row);
-          const float inv = l[nt][c] > 0.f ? 1.f / l[nt][c] : (l[nt][c] == 0.f ? 0.f : l[nt][c]);
+          const float inv = row_factor(l[nt][c]);
           uint32_t w[D / 16];
 #pragma unroll
           for (int mt = 0; mt < MT; ++mt) {
@@ -688,7 +705,7 @@ __global__ void __launch_bounds__(PagedCfg<D, NT>::NW * 32, 1)
   // Row r of a finished item.
   auto finish = [&](int h, int grp, int q0, int r, float L, float4 o) {
     const int row = grp * RG + r, j = row_token(p, row);
-    const float inv = L > 0.f ? 1.f / L : (L == 0.f ? 0.f : L);
+    const float inv = row_factor(L);
     uint2 w;
     if constexpr (BF16) {
       const __nv_bfloat162 a = __floats2bfloat162_rn(o.x * inv, o.y * inv);

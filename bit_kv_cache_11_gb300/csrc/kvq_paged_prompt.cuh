@@ -3,9 +3,12 @@
 // memory.
 //
 // The mathematics is kvq_paged_decode.cuh's: s = kappa * sk * (q . a) +
-// log2(sv), w = 2^(s - m), out = sum w c / sum (w / sv).  Keys, values and
-// weights enter the tensor cores as fp16: codes exactly, weights rounded
-// (w <= 2^8, see kLazy), queries exactly (bf16 rows through a power of two).
+// log2(sv), w = 2^(s - m + 7), out = sum w c / sum (w / sv).  Keys, values and
+// weights enter the tensor cores as fp16: codes exactly, fp16 queries exactly,
+// bf16 rows through a power of two (elements below 2^-22 of their row's largest
+// lose bits, an error below 2^-40 of it), weights rounded: half a step, 2^-11,
+// of a token's weight * scale down to 2^-21 of the row's largest, and at most
+// 2^-32 of that largest below (see kLazy).
 //
 // A CTA owns 256 query rows of one kv head (two tiles of 128; row r is new
 // token r / R, head r % R of the group, so grouped heads share every key
@@ -208,12 +211,25 @@ __device__ __forceinline__ uint32_t half2_bits(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
+// Two weights as fp16, finite whatever their scores (NaN stays NaN).
+__device__ __forceinline__ uint32_t weight_bits(float lo, float hi) {
+  uint32_t x;
+  asm("cvt.rn.satfinite.f16x2.f32 %0, %1, %2;" : "=r"(x) : "f"(hi), "f"(lo));
+  return x;
+}
+
 // Rounds of a wait between two roles of the CTA (each may suspend for a
 // hardware-chosen time; a legitimate wait is microseconds).
 constexpr uint32_t kRoleWait = 1u << 20;
-// The reference maximum is raised only when a score exceeds it by this much
-// (log2), so most tiles skip the rescaling of O; weights reach 2^kLazy.
+// The reference maximum m is raised only when a score exceeds it by this much
+// (log2), so most tiles skip the rescaling of O.  Weights are 2^(s - reference(m)),
+// at most 2^(kLazy + kWeightLog2) = 2^15, which uses fp16's range.  A huge score's
+// maximum and exponent are rounded apart, so there fp16's range is left to that.
 constexpr float kLazy = 8.0f;
+constexpr float kWeightLog2 = 7.0f, kWeightInv = 0x1p-7f;
+__device__ __forceinline__ float reference(float m) {
+  return fabsf(m) < 0x1p18f ? m - kWeightLog2 : m == -INFINITY ? 0.f : m;
+}
 
 // The work of a CTA: rows [row0, row0 + 256) of request b, kv head h.
 struct PromptItem {
@@ -406,7 +422,7 @@ __global__ void __launch_bounds__(PromptCfg<D>::THREADS, 1)
           }
           const bool seen = page >= 0 && tok < it.hi && tok + 16 > it.lo;
           recs[i % C::NREC * C::REC + lane % 8] =
-              make_float4(ks, lg2(vs), 1.f / vs, seen ? 1.f : 0.f);
+              make_float4(ks, lg2(vs), kWeightInv / vs, seen ? 1.f : 0.f);
           const uint32_t m = 0xffu << (lane & 24);
           const uint32_t all = __ballot_sync(m, seen);
           if (lane % 8 == 0) whole[i % C::NREC] = all == m;
@@ -674,9 +690,9 @@ __global__ void __launch_bounds__(PromptCfg<D>::THREADS, 1)
             }
           }
           const float mn = mx > m + kLazy || m == -INFINITY ? mx : m;
-          const float mb = mn == -INFINITY ? 0.f : mn;
+          const float mb = reference(mn);
           const bool move = mn != m && m != -INFINITY;  // O holds sums at the old reference
-          const float al = move ? ex2(m - mn) : 1.f;
+          const float al = move ? ex2(reference(m) - mb) : 1.f;
           m = mn;
           l *= al;
           if (__any_sync(0xffffffffu, move)) {
@@ -713,7 +729,7 @@ __global__ void __launch_bounds__(PromptCfg<D>::THREADS, 1)
                                                   __uint_as_float(x[16 * g + k + 1])), f2, y2);
                 const float2 w = make_float2(ex2(z.x), ex2(z.y));
                 sum = add2(sum, w);
-                h[8 * g + k / 2] = half2_bits(w.x, w.y);
+                h[8 * g + k / 2] = weight_bits(w.x, w.y);
               }
               l = fmaf(sum.x + sum.y, rc.z, l);
             }
@@ -731,7 +747,7 @@ __global__ void __launch_bounds__(PromptCfg<D>::THREADS, 1)
       }
       if (ok && wait(&o_done[w], nt - 1)) {
         tmem_fence_after();
-        const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
+        const float inv = l > 0.f ? kWeightInv / l : (l == 0.f ? 0.f : l);
         // Through the query tile (its products are complete), so that whole rows
         // are written: this warp's rows, chunks swizzled as the queries were.
         uint8_t* tile = smem + C::OFF_Q + w * C::QT;

@@ -120,3 +120,105 @@ def tolerance(out, size, reach, half_step, n_tokens, vmax):
     err = size * (2.0 ** -11 + 2 * D * 2.0 ** -23 * reach[..., None] + 2.0 ** -18)
     err = err + n_tokens * 2.0 ** -25 * vmax
     return err + half_step * (np.abs(out) + err) + 2.0 ** -25
+
+
+# The kernels' weights are fp16 numbers 2^15 (decode) and 2^7 (prompt) times the
+# share p * scale of the row's largest: half a step of fp16 is 2^-11 of a number
+# of at least 2^-14 and 2^-25 below.
+WEIGHT_LOG2 = {"decode": 15, "prompt": 7}
+
+
+def row(q, k, v, sv, scale, log2, half_step):
+    """Attention of one query over the tokens it sees, k and v [n][D] with v's page
+    scales sv [n]: (out, bound, parts).  `bound` is the largest error of an
+    output of the kernel: weights rounded to fp16, scores whose D products are
+    summed in fp32 (D * 2^-23 of sum |q k|, a step each) and scaled, exponentials
+    and logarithms of 22 bits, sums in fp32 of 16 tokens at a time (a step each),
+    and the output's rounding.  An error d of a score moves a weight by d of it
+    in the numerator and in the sum below.  parts: every token's p * v."""
+    n, D = k.shape
+    z = k @ q * scale
+    p = np.exp(z - z.max())
+    p /= p.sum()
+    out = p @ v
+    w = p * sv
+    rounded = np.where(w >= 2.0 ** (-14 - log2) * w.max(), 2.0 ** -11 * w, 2.0 ** (-25 - log2) * w.max()) / sv
+    score = D * 2.0 ** -23 * (np.abs(k) @ np.abs(q)) * abs(scale) + (np.abs(z) + 64) * 2.0 ** -23
+    other = score + 2.0 ** -20 + (n / 16 + 32) * 2.0 ** -23
+    err = rounded @ np.abs(v) + (p * other) @ np.abs(v) + (p @ other) * np.abs(out)
+    return out, err + half_step * (np.abs(out) + err) + 2.0 ** -25, p[:, None] * v
+
+
+def rows(q, kc, vc, ks, vs, table, cu, seq, ps, scale, window, log2, half_step, each=None):
+    """(out, bound) of all new tokens; `each(b, j, hq, parts, out, bound)` sees every row."""
+    T, Hq, D = q.shape
+    R = Hq // kc.shape[1]
+    out, bound = np.zeros(q.shape), np.full(q.shape, 2.0 ** -25)
+    for b in range(len(seq)):
+        n = int(cu[b + 1] - cu[b])
+        t = np.arange(seq[b])
+        pg, r = table[b][t // ps], t % ps
+        for h in range(kc.shape[1] if n else 0):
+            k, v = E4M3[kc[pg, h, r]] * ks[pg, h][:, None], E4M3[vc[pg, h, r]] * vs[pg, h][:, None]
+            for j in range(n):
+                pos = int(seq[b]) - n + j
+                lo = max(0, pos - window + 1) if window else 0
+                if pos < lo:
+                    continue
+                s = slice(lo, pos + 1)
+                for hq in range(h * R, h * R + R):
+                    o, e, parts = row(q[cu[b] + j, hq], k[s], v[s], vs[pg[s], h], scale, log2, half_step)
+                    out[cu[b] + j, hq], bound[cu[b] + j, hq] = o, e
+                    if each:
+                        each(b, j, hq, parts, o, e)
+    return out, bound
+
+
+# page size, head_dim, kv heads, query heads a kv head, type, cached, new, window, kernel
+SHARES = [
+    (64, 128, 2, 4, "fp16", [5000], [1], 0, "decode"),         # an item over many CTAs
+    (16, 64, 1, 1, "bf16", [3000, 2, 90], [1] * 3, 0, "decode"),
+    (128, 128, 1, 2, "fp16", [5300], [1], 0, "decode"),
+    (16, 64, 1, 8, "fp16", [2500, 700], [5, 3], 0, "decode"),  # three groups of rows
+    (32, 128, 1, 2, "bf16", [3000, 40], [4, 9], 1500, "decode"),
+    (32, 64, 2, 2, "fp16", list(range(100, 900, 50)), [1] * 16, 0, "decode"),
+    (64, 128, 1, 1, "fp16", [2000, 5], [130, 40], 0, "prompt"),
+    (16, 64, 1, 2, "bf16", [700], [70], 0, "prompt"),
+    (128, 64, 1, 1, "fp16", [900, 0], [60, 100], 300, "prompt"),
+]
+
+
+def shares_case(case):
+    """Numbers of a case of SHARES: values of about 1, scales 2^-9 .. 2^-4; rows that
+    hold no token are NaN codes in `stale`.  Requests without tokens follow in the
+    prompt kernel's cases (a large batch: many rows go to that kernel)."""
+    import torch
+    ps, D, H, R, dtype, ctx, new, window, kernel = case
+    idle = 140 if kernel == "prompt" else 0
+    ctx, new = list(ctx) + [0] * idle, list(new) + [0] * idle
+    rng = np.random.default_rng(ps + D + H + R + sum(ctx) + sum(new) + window)
+    seq = np.array(ctx) + np.array(new)
+    need = -(-seq // ps)
+    n_pages = int(need.sum()) + 2
+    scale = [2.0 ** rng.integers(-9, -3, (n_pages, H)).astype(np.float64) for _ in range(2)]
+    codes = [e4m3_code(rng.standard_normal((n_pages, H, ps, D)) / s[..., None, None]) for s in scale]
+    table = np.full((len(seq), int(need.max()) + 1), -1, np.int32)
+    ids, at = rng.permutation(n_pages), 0
+    used = np.zeros((n_pages, ps), bool)
+    for b, n in enumerate(need):
+        table[b, :n] = ids[at:at + n]
+        for i in range(n):
+            used[ids[at + i], :max(0, min(ps, seq[b] - i * ps))] = True
+        at += n
+    stale = [c.copy() for c in codes]
+    for c in stale:
+        c.transpose(0, 2, 1, 3)[~used] = 0x7F
+    q = torch.from_numpy(rng.standard_normal((sum(new), H * R, D))).to({"fp16": torch.float16, "bf16": torch.bfloat16}[dtype])
+    return dict(ps=ps, codes=codes, stale=stale, scale=scale, table=table, cu=np.concatenate([[0], np.cumsum(new)]),
+                seq=seq, q=q, max_new=max(new), window=window, softmax_scale=D ** -0.5, kernel=kernel,
+                half_step={"fp16": 2.0 ** -11, "bf16": 2.0 ** -8}[dtype])
+
+
+def shares_want(s, each=None):
+    return rows(s["q"].double().numpy(), *s["codes"], *s["scale"], s["table"], s["cu"], s["seq"], s["ps"],
+                s["softmax_scale"], s["window"], WEIGHT_LOG2[s["kernel"]], s["half_step"], each)
