@@ -76,6 +76,7 @@ struct PagedAttnParams {
   int* tickets;   // [CTAs], zero between launches
   float* warp_part;  // [n_warps][RG * (D + 2)]
   float* cta_part;   // [2 * CTAs][RG * (D + 2)]
+  uint32_t wait_limit;  // try_wait rounds of a main-loop wait, when below the kernel's own limit
   int* err;
 };
 

@@ -1,8 +1,9 @@
 // kvq_paged_api.cu — the paged 8-bit cache's part of the C ABI (include/kvq.h):
 // validation, tensor maps, workspace layout and launches.  Nothing is kept
-// between calls but the driver entry point and each kernel's shared-memory
-// opt-in.
+// between calls but the driver entry point, each kernel's shared-memory opt-in
+// and the wait limit that a test may have set.
 #include <algorithm>
+#include <atomic>
 #include <climits>
 #include <cmath>
 #include <mutex>
@@ -36,6 +37,8 @@ cudaError_t allow_smem(const void* fn, int bytes) {
 using namespace kvq;
 
 namespace {
+
+std::atomic<uint32_t> g_wait_limit{UINT32_MAX};
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 bool dev_ptr(const void* p, uintptr_t a) { return p != nullptr && aligned(p, a); }
@@ -290,6 +293,7 @@ kvq_status kvq_paged_attention(const kvq_paged_pool* pool, const void* q, int dt
   p.tickets = reinterpret_cast<int*>(ws);
   p.warp_part = reinterpret_cast<float*>(ws + kTicketBytes);
   p.cta_part = p.warp_part + static_cast<size_t>(p.n_warps) * part_floats(8 * nt, D);
+  p.wait_limit = g_wait_limit.load(std::memory_order_relaxed);
   p.err = device_error;
   const bool bf = dtype == KVQ_DTYPE_BF16;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
@@ -319,6 +323,11 @@ kvq_status kvq_paged_attention(const kvq_paged_pool* pool, const void* q, int dt
     return KVQ_ERR_CUDA;
   }
   count_launches(1);
+  return KVQ_OK;
+}
+
+kvq_status kvq_debug_set_paged_wait_limit(int limit) {
+  g_wait_limit.store(limit < 0 ? UINT32_MAX : static_cast<uint32_t>(limit), std::memory_order_relaxed);
   return KVQ_OK;
 }
 

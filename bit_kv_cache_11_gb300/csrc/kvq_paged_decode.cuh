@@ -642,11 +642,33 @@ __global__ void __launch_bounds__(PagedCfg<D, NT>::NW * 32, 1)
   for (int u = ua; u < ub; ++u) {
     if (u == iend) {
       if (u > ua) leave(false);
+      if (failed) {
+        find_item(u, li);
+        if (lane == 0) items[k_items & 3] = li;
+        __syncwarp();
+      }
       enter();
     }
-    if (!mbar_wait_bounded(&bars[st], phase)) {
+    // (decided for the whole warp: its lanes stay together)
+    if (!failed && !__all_sync(0xffffffffu, mbar_wait_bounded(&bars[st], phase, min(p.wait_limit, kWaitLimit)))) {
+      // A copy did not arrive in time: record it and let the warp's copies land
+      // (bounded).  The warp goes on without data from item to item, so that the
+      // shares that it owes are there, every CTA of a shared item draws its
+      // ticket and the tickets return to zero.
       failed = true;
-      break;
+      set_err(p.err, KVQ_PAGED_ERR_WAIT);
+      for (int k = u; k < lu; ++k) {
+        mbar_wait_bounded(&bars[st], phase);
+        if (++st == NS) {
+          st = 0;
+          phase ^= 1;
+        }
+      }
+      __syncwarp();
+    }
+    if (failed) {
+      u = min(iend, ub) - 1;
+      continue;
     }
     const int tok = it.tok0 + (u - it.u0) * UT;
     if (tok < hi && tok + UT > lo) {
@@ -667,19 +689,7 @@ __global__ void __launch_bounds__(PagedCfg<D, NT>::NW * 32, 1)
       phase ^= 1;
     }
   }
-  if (failed) {
-    // a copy did not arrive in time: record it, let the others land (bounded)
-    set_err(p.err, KVQ_PAGED_ERR_WAIT);
-    for (int i = 0; i < NS; ++i) {
-      mbar_wait_bounded(&bars[st], phase);
-      if (++st == NS) {
-        st = 0;
-        phase ^= 1;
-      }
-    }
-  } else if (ua < ub) {
-    leave(true);
-  }
+  if (ua < ub) leave(true);
 
   // ---- the CTA's join ---------------------------------------------------------
   // Every warp lists the segments (two a warp: the partial it left on its way,

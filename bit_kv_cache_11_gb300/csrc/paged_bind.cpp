@@ -408,23 +408,6 @@ PyObject* attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
-// Clears the counters of a device's workspaces, after a call that did not
-// finish.
-PyObject* reset_workspaces(PyObject*, PyObject* index) {
-  return guarded([&]() -> PyObject* {
-    const int dev = static_cast<int>(number("reset_workspaces", "index", index, 0, kIntMax));
-    const c10::cuda::CUDAGuard guard(static_cast<c10::DeviceIndex>(dev));
-    std::lock_guard<std::mutex> lock(g_mu);
-    for (auto& [key, w] : workspaces())
-      if (std::get<0>(key) == dev && !std::get<3>(key) &&
-          cudaMemset(w.mem.data_ptr(), 0, 1024) != cudaSuccess) {
-        cudaGetLastError();
-        throw Refusal{KVQ_ERR_CUDA, "reset_workspaces"};
-      }
-    Py_RETURN_NONE;
-  });
-}
-
 PyObject* set_error_class(PyObject*, PyObject* c) {
   Py_XDECREF(g_error_class);
   g_error_class = Py_NewRef(c);
@@ -436,7 +419,6 @@ PyMethodDef g_methods[] = {
     {"store", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)(void)>(store)), METH_FASTCALL, nullptr},
     {"attention", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)(void)>(attention)),
      METH_FASTCALL, nullptr},
-    {"reset_workspaces", reset_workspaces, METH_O, nullptr},
     {"set_error_class", set_error_class, METH_O, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 

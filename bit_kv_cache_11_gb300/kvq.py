@@ -97,6 +97,7 @@ _sigs = {
     "kvq_debug_fail_allocations": (_S, [_I, _I]),
     "kvq_debug_set_device_error": (_S, [_P, _I]),
     "kvq_debug_set_wait_limit": (_S, [_P, _I]),
+    "kvq_debug_set_paged_wait_limit": (_S, [_I]),
     "kvq_status_string": (ctypes.c_char_p, [_S]),
     "kvq_paged_pool_check": (_S, [_POOL]),
     "kvq_paged_plan": (_S, [_P, _P, _I, _P, _I, _P, _I, _P, _I, _I, _P, _P, _P, _P, _P, _P]),
@@ -274,6 +275,10 @@ def kvq_debug_set_device_error(handle, value: int) -> None:
 
 def kvq_debug_set_wait_limit(handle, limit: int) -> None:
     _check(_lib.kvq_debug_set_wait_limit(handle, limit), "kvq_debug_set_wait_limit")
+
+
+def kvq_debug_set_paged_wait_limit(limit: int) -> None:
+    _check(_lib.kvq_debug_set_paged_wait_limit(limit), "kvq_debug_set_paged_wait_limit")
 
 
 # ---- the paged 8-bit cache ----------------------------------------------------

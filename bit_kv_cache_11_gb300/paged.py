@@ -146,8 +146,6 @@ class PagedCache:
         if not bits:
             return
         self.error.zero_()
-        if bits & KVQ_PAGED_ERR_WAIT:  # a split that did not finish leaves its counters
-            _paged_bind.reset_workspaces(self.error.get_device())
         names = ((KVQ_PAGED_ERR_WAIT, "a bounded wait ran out"),
                  (KVQ_PAGED_ERR_BAD_PAGE, "a page id outside the pool"),
                  (KVQ_PAGED_ERR_NO_PAGES, "the free stack ran out"),

@@ -400,9 +400,7 @@ KVQ_API kvq_status kvq_decode_attention_noalloc(const kvq_config* cfg, const voi
 
 typedef enum { KVQ_DTYPE_FP16 = 0, KVQ_DTYPE_BF16 = 1 } kvq_dtype;
 
-#define KVQ_PAGED_ERR_WAIT 1      /* a bounded wait ran out; the output is not complete
-                                     and the workspace's first 1024 bytes have to be
-                                     zeroed before its next use                         */
+#define KVQ_PAGED_ERR_WAIT 1      /* a bounded wait ran out; the output is not complete  */
 #define KVQ_PAGED_ERR_BAD_PAGE 2  /* a needed page id is outside the pool: its rows are
                                      not stored, its tokens not attended                */
 #define KVQ_PAGED_ERR_NO_PAGES 4  /* the free stack did not hold a request's pages       */
@@ -528,10 +526,13 @@ KVQ_API uint64_t kvq_launch_count(void);
  *   the error word, waits with the normal limit for its own copies in flight,
  *   and leaves the launch).  0 gives up at the first wait, so a decode
  *   records the error without writing `out`; limit < 0 restores the normal
- *   limit.  Applies to launches enqueued afterwards. */
+ *   limit.  Applies to launches enqueued afterwards.
+ * kvq_debug_set_paged_wait_limit: the same for the waits of
+ *   kvq_paged_attention (KVQ_PAGED_ERR_WAIT).  Process-wide. */
 KVQ_API kvq_status kvq_debug_fail_allocations(int after, int n);
 KVQ_API kvq_status kvq_debug_set_device_error(kvq_cache* cache, int value);
 KVQ_API kvq_status kvq_debug_set_wait_limit(kvq_cache* cache, int limit);
+KVQ_API kvq_status kvq_debug_set_paged_wait_limit(int limit);
 
 /* Static description of a status code. */
 KVQ_API const char* kvq_status_string(kvq_status s);

@@ -1,0 +1,81 @@
+"""Failure paths of the paged calls.  Nothing here faults, traps or hangs the GPU:
+kvq_debug_set_paged_wait_limit makes the attention's main-loop waits give up early
+(the copies in flight are waited for all the same)."""
+import numpy as np
+import pytest
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def kvq():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from bit_kv_cache_11_gb300 import kvq as k
+    return k
+
+
+def ints(x):
+    return torch.tensor(np.asarray(x, np.int32), device="cuda")
+
+
+def call_of(seq, new, H=2, R=4, D=64, ps=16, dtype=torch.float16, seed=0):
+    """Arguments of an attention over random pages."""
+    rng = np.random.default_rng(seed)
+    need = [-(-x // ps) for x in seq]
+    pages = [torch.randn(sum(need), H, ps, D, device="cuda").to(torch.float8_e4m3fn) for _ in range(2)]
+    scale = [torch.ones(sum(need), H, device="cuda") for _ in range(2)]
+    table = np.full((len(seq), max(need)), -1)
+    ids, at = rng.permutation(sum(need)), 0
+    for b, n in enumerate(need):
+        table[b, :n] = ids[at:at + n]
+        at += n
+    q = torch.randn(sum(new), H * R, D, device="cuda").to(dtype)
+    return [q, *pages, *scale, ints(table), ints(np.cumsum([0] + list(new))), ints(seq)]
+
+
+@pytest.fixture
+def limit(kvq):
+    yield kvq.kvq_debug_set_paged_wait_limit
+    kvq.kvq_debug_set_paged_wait_limit(-1)
+
+
+DECODE = [((20000,), (1,)), ((5000, 3000, 17, 800), (1, 1, 1, 1)), (tuple(range(100, 4000, 60)), (2,) * 65)]
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("seq,new", DECODE, ids=["one", "four", "many"])
+def test_a_decode_wait_that_runs_out(kvq, limit, seq, new, D):
+    """It is flagged, the tickets of the shared items return to zero whichever warps
+    gave up, and the next call with the same workspace is right."""
+    a = call_of(seq, new, D=D)
+    most = max(new)
+    want = kvq.kvq_paged_attention(*a, max_new=most)
+    ws = torch.zeros(kvq.kvq_paged_workspace_bytes(a[1].shape[0], 2, 16, D), dtype=torch.uint8, device="cuda")
+    for rounds in (0, 1, 0, 2, 1, 3, 0):
+        err = ints([0])
+        limit(rounds)
+        for kw in (dict(workspace=ws), dict()):  # the caller's workspace, the stream's own
+            kvq.kvq_paged_attention(*a, max_new=most, error=err, **kw)
+        limit(-1)
+        assert err.item() == kvq.KVQ_PAGED_ERR_WAIT or (rounds > 0 and err.item() == 0)
+        assert (ws[:1024] == 0).all()
+        err.zero_()
+        for kw in (dict(workspace=ws), dict()):
+            assert torch.equal(kvq.kvq_paged_attention(*a, max_new=most, error=err, **kw), want)
+        assert err.item() == 0
+
+
+def test_the_cache_reports_a_wait_that_ran_out(kvq, limit):
+    c = kvq.PagedCache(n_pages=400, page_size=16, n_q_heads=8, n_kv_heads=2, head_dim=64)
+    a = call_of((5000,), (1,))
+    table = ints(np.arange(313)[None])
+    want = c.attention(a[0], table, a[6], a[7])
+    limit(0)
+    c.attention(a[0], table, a[6], a[7])
+    limit(-1)
+    with pytest.raises(kvq.KvqError, match="wait"):
+        c.check()
+    assert torch.equal(c.attention(a[0], table, a[6], a[7]), want)
+    c.check()
