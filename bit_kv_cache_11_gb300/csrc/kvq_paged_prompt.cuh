@@ -374,11 +374,15 @@ __global__ void __launch_bounds__(PromptCfg<D>::THREADS, 1)
   const uint32_t tmem = *tmem_slot;
   const int halves = it.rows - it.row0 > 128 ? 2 : 1;
 
-  // Bounded wait; false when it ran out or another role gave up.
+  // Bounded wait of a whole warp; false when it ran out or another role gave up.
+  // Lanes see the barrier and the flag at different times: they decide together,
+  // so that the warp stays converged for what it does next.  (A phase that one
+  // lane has seen lasts until all have: the warp's own arrival ends the next.)
+  const uint32_t rounds = min(p.wait_limit, kRoleWait);
   auto wait = [&](uint64_t* bar, uint32_t parity) {
-    for (uint32_t i = 0; i < kRoleWait; ++i) {
-      if (mbar_try_wait(bar, parity & 1)) return true;
-      if (*abort_flag) return false;
+    for (uint32_t i = 0; i < rounds; ++i) {
+      if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity & 1))) return true;
+      if (__any_sync(0xffffffffu, *abort_flag)) return false;
     }
     *abort_flag = 1;
     set_err(p.err, KVQ_PAGED_ERR_WAIT);

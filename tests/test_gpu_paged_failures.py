@@ -79,3 +79,22 @@ def test_the_cache_reports_a_wait_that_ran_out(kvq, limit):
         c.check()
     assert torch.equal(c.attention(a[0], table, a[6], a[7]), want)
     c.check()
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+def test_a_prompt_wait_that_runs_out(kvq, limit, dtype, D):
+    """Every role of the kernel leaves, whichever of them gave up; the next call is
+    right.  (140 requests without tokens: a large batch, whose many-row requests the
+    prompt kernel serves.)"""
+    a = call_of((900, 300, 40) + (1,) * 140, (200, 70, 5) + (0,) * 140, D=D, dtype=dtype)
+    want = kvq.kvq_paged_attention(*a, max_new=200)
+    for rounds in (0, 1, 0, 2, 1, 3, 8, 0):
+        err = ints([0])
+        limit(rounds)
+        kvq.kvq_paged_attention(*a, max_new=200, error=err)
+        limit(-1)
+        assert err.item() == kvq.KVQ_PAGED_ERR_WAIT or (rounds > 0 and err.item() == 0)
+        err.zero_()
+        assert torch.equal(kvq.kvq_paged_attention(*a, max_new=200, error=err), want)
+        assert err.item() == 0
