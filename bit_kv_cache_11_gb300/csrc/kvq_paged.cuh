@@ -118,6 +118,14 @@ __device__ __forceinline__ int row_token(const PagedAttnParams& p, int row) {
   return p.R == 1 ? row : static_cast<int>(__umulhi(static_cast<uint32_t>(row), p.r_magic));
 }
 
+// Sum of two counts, at most 2^31 - 1.  Offsets that decrease let requests share
+// rows, and their counts' sum pass any bound on the call's rows.
+constexpr int kCountMax = 0x7fffffff;
+__device__ __forceinline__ int add_counts(int a, int b) {
+  return static_cast<int>(min(static_cast<uint32_t>(a) + static_cast<uint32_t>(b),
+                              static_cast<uint32_t>(kCountMax)));
+}
+
 // Lengths of request b as the attention uses them: new tokens, first new
 // token's row of q, all tokens.  Values that break the contract of
 // include/kvq.h serve nothing (n = 0) and set the error word.

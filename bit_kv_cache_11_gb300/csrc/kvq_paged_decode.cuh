@@ -185,21 +185,21 @@ __global__ void __launch_bounds__(PagedCfg<D, NT>::NW * 32, 1)
       any_bad |= bad != 0;
       return r.n > 0 ? p.H * groups_of(r) * units_of(r) : 0;
     };
-    for (int b = b0; b < b1; ++b) mine += cost(b);
+    for (int b = b0; b < b1; ++b) mine = add_counts(mine, cost(b));
     int incl = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int x = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += x;
+      if (lane >= o) incl = add_counts(incl, x);
     }
     if (lane == 31) flags[warp] = incl;
+    int at = __shfl_up_sync(0xffffffffu, incl, 1);  // the lanes' before
+    if (lane == 0) at = 0;
     __syncthreads();
-    int base = 0;
-    for (int w = 0; w < warp; ++w) base += flags[w];
-    int at = base + incl - mine;
+    for (int w = 0; w < warp; ++w) at = add_counts(at, flags[w]);
     for (int b = b0; b < b1; ++b) {
       cum[b] = at;
-      at += per == 1 ? mine : cost(b);
+      at = add_counts(at, per == 1 ? mine : cost(b));
     }
     if (b1 == p.batch && b0 < b1) cum[p.batch] = at;
     if (any_bad && blockIdx.x == 0) set_err(p.err, KVQ_PAGED_ERR_LENGTH);
@@ -208,6 +208,10 @@ __global__ void __launch_bounds__(PagedCfg<D, NT>::NW * 32, 1)
   grid_dep_launch();
   const int U = cum[p.batch];
   if (U == 0) return;
+  if (U == kCountMax) {  // (the host refuses calls whose own rows could come to this)
+    if (blockIdx.x == 0 && tid == 0) set_err(p.err, KVQ_PAGED_ERR_LENGTH);
+    return;
+  }
   // warps in use: at least one unit each, packed into the first CTAs
   const int W = min(p.n_warps, U);
   const int gw = blockIdx.x * NW + warp;

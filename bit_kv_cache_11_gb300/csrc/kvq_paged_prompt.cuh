@@ -308,21 +308,22 @@ __global__ void __launch_bounds__(PromptCfg<D>::THREADS, 1)
     const int b0 = min(tid * per, p.batch), b1 = min(b0 + per, p.batch);
     int mine = 0;
     PagedReq r;
-    for (int b = b0; b < b1; ++b) mine += pairs_of(b, &r);
+    for (int b = b0; b < b1; ++b) mine = add_counts(mine, pairs_of(b, &r));
     int incl = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int x = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += x;
+      if (lane >= o) incl = add_counts(incl, x);
     }
     if (lane == 31) sums[warp] = incl;
+    int at = __shfl_up_sync(0xffffffffu, incl, 1);
+    if (lane == 0) at = 0;
     __syncthreads();
-    int at = incl - mine;
-    for (int w = 0; w < warp; ++w) at += sums[w];
-    if (item >= at && item < at + mine) {
+    for (int w = 0; w < warp; ++w) at = add_counts(at, sums[w]);
+    if (item >= at && item < add_counts(at, mine)) {
       for (int b = b0; b < b1; ++b) {
         const int c = pairs_of(b, &r);
-        if (item < at + c) {
+        if (item < add_counts(at, c)) {
           PromptItem it;
           it.b = b;
           it.h = h;
@@ -340,7 +341,7 @@ __global__ void __launch_bounds__(PromptCfg<D>::THREADS, 1)
           *found = it;
           break;
         }
-        at += c;
+        at = add_counts(at, c);
       }
     }
   }

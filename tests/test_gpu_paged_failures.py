@@ -98,3 +98,21 @@ def test_a_prompt_wait_that_runs_out(kvq, limit, dtype, D):
         err.zero_()
         assert torch.equal(kvq.kvq_paged_attention(*a, max_new=200, error=err), want)
         assert err.item() == 0
+
+
+def test_requests_that_share_rows_pass_no_bound(kvq):
+    """Offsets that decrease make several requests claim the same rows.  Their parts of
+    the work together may pass 31 bits (here 4 requests of 34 groups and 4e7 units
+    each, 2^32 and more together, over tables that nothing reads): the call is
+    flagged and skipped."""
+    n, batch, ps, D = 532, 8, 128, 128
+    width = 1_280_000_000 // ps
+    pages = [torch.zeros(4, 1, ps, D, dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn) for _ in range(2)]
+    scale = [torch.ones(4, 1, device="cuda") for _ in range(2)]
+    table = torch.zeros(batch, width, dtype=torch.int32, device="cuda")
+    q = torch.ones(n, 1, D, dtype=torch.float16, device="cuda")
+    out, err = torch.full_like(q, 5.0), ints([0])
+    kvq.kvq_paged_attention(q, *pages, *scale, table, ints([0, n] * 4 + [0]), ints([width * ps] * batch),
+                            max_new=n, out=out, error=err)
+    assert err.item() == kvq.KVQ_PAGED_ERR_LENGTH
+    assert (out == 5.0).all()
