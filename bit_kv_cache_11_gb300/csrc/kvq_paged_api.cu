@@ -237,7 +237,8 @@ kvq_status kvq_paged_attention(const kvq_paged_pool* pool, const void* q, int dt
       !stride_ok(out_stride, n_q_heads, D))
     return KVQ_ERR_INVALID_ARG;
   const int R = n_q_heads / H;
-  if (R > 16 || batch > kPagedMaxBatch || max_pages > INT_MAX / pool->page_size)
+  // (the kernels name positions of up to a batch of tiles behind the last token)
+  if (R > 16 || batch > kPagedMaxBatch || max_pages > (INT_MAX - 4096) / pool->page_size)
     return KVQ_ERR_UNSUPPORTED;
   max_new = std::min(max_new, n_tokens);
   // positions minus the window stay inside 32 bits

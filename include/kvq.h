@@ -380,8 +380,9 @@ KVQ_API kvq_status kvq_decode_attention_noalloc(const kvq_config* cfg, const voi
  * Conventions, besides those at the top of this header.
  *   - Sizes with an upper bound: head_dim 64 or 128; page_size 16, 32, 64 or
  *     128; batch <= 4096; n_q_heads a multiple of n_kv_heads, at most 16
- *     times; n_pages * n_kv_heads * page_size < 2^31 (KVQ_ERR_UNSUPPORTED
- *     beyond).  Buffers may be larger than 4 GB.
+ *     times; n_pages * n_kv_heads * page_size < 2^31; max_pages * page_size
+ *     < 2^31 - 4096 in the attention (KVQ_ERR_UNSUPPORTED beyond).  Buffers
+ *     may be larger than 4 GB.
  *   - 16-bit inputs are fp16 or bf16 (kvq_dtype), one row of heads x head_dim
  *     contiguous elements per token; `stride` is the distance between tokens
  *     in elements, a multiple of 8 (slices of a fused projection fit).
