@@ -19,6 +19,7 @@
 #include <mutex>
 #include <string>
 #include <tuple>
+#include <vector>
 
 #include "kvq.h"
 
@@ -193,9 +194,11 @@ at::Tensor empty_on(cudaStream_t st, at::IntArrayRef sizes, at::ScalarType t, in
 // Calls on one stream run one after the other and share a workspace; the calls
 // that a stream captures into one graph share another one, out of the
 // capture's memory, whose counters the graph clears before their first use.
-// So two graphs, or a graph and eager calls, never share.
+// So two graphs, or a graph and eager calls, never share.  A graph's workspace
+// is the graph's: it lives as long as the graph and what is instantiated of it.
 struct Workspace {
-  at::Tensor mem;
+  at::Tensor mem;  // eager calls'
+  void* at = nullptr;
   unsigned long long capture = 0;
 };
 using WorkKey = std::tuple<int, cudaStream_t, int, bool>;  // device, stream, head_dim, captured
@@ -205,30 +208,68 @@ std::map<WorkKey, Workspace>& workspaces() {
   return *m;
 }
 
+// Workspaces of graphs that are gone.  A graph is destroyed on a thread that may
+// not call CUDA, so the next call frees them.
+std::mutex g_gone_mu;
+std::vector<at::Tensor*>& gone() {
+  static auto* v = new std::vector<at::Tensor*>;
+  return *v;
+}
+void CUDART_CB graph_gone(void* mem) {
+  std::lock_guard<std::mutex> lock(g_gone_mu);
+  gone().push_back(static_cast<at::Tensor*>(mem));
+}
+void free_gone() {
+  std::vector<at::Tensor*> v;
+  {
+    std::lock_guard<std::mutex> lock(g_gone_mu);
+    v.swap(gone());
+  }
+  for (at::Tensor* t : v) delete t;
+}
+
+// Makes `graph` keep `mem`.
+bool keep_with_graph(cudaGraph_t graph, const at::Tensor& mem) {
+  auto* held = new at::Tensor(mem);
+  cudaUserObject_t object = nullptr;
+  if (cudaUserObjectCreate(&object, held, graph_gone, 1, cudaUserObjectNoDestructorSync) != cudaSuccess) {
+    delete held;
+    return false;
+  }
+  if (cudaGraphRetainUserObject(graph, object, 1, cudaGraphUserObjectMove) == cudaSuccess) return true;
+  cudaUserObjectRelease(object, 1);
+  return false;
+}
+
 void* workspace(const char* call, const kvq_paged_pool& pool, int index, cudaStream_t st,
                 size_t* bytes) {
   cudaStreamCaptureStatus status = cudaStreamCaptureStatusNone;
   unsigned long long id = 0;
-  if (cudaStreamGetCaptureInfo(st, &status, &id) != cudaSuccess) {
+  cudaGraph_t graph = nullptr;
+  if (cudaStreamGetCaptureInfo(st, &status, &id, &graph) != cudaSuccess) {
     cudaGetLastError();
     throw Refusal{KVQ_ERR_CUDA, call};
   }
   const bool captured = status == cudaStreamCaptureStatusActive;
   check(kvq_paged_workspace_bytes(&pool, bytes), call);
+  free_gone();
   std::lock_guard<std::mutex> lock(g_mu);
   Workspace& w = workspaces()[WorkKey(index, st, pool.head_dim, captured)];
-  if (!w.mem.defined() || (captured && w.capture != id)) {
+  if (w.at == nullptr || (captured && w.capture != id)) {
+    w.at = nullptr;
     const c10::cuda::CUDAStreamGuard guard(
         c10::cuda::getStreamFromExternal(st, static_cast<c10::DeviceIndex>(index)));
-    w.mem = empty({static_cast<int64_t>(*bytes)}, at::kByte, index);
-    w.capture = id;
-    if (cudaMemsetAsync(w.mem.data_ptr(), 0, 1024, st) != cudaSuccess) {
+    at::Tensor mem = empty({static_cast<int64_t>(*bytes)}, at::kByte, index);
+    if (cudaMemsetAsync(mem.data_ptr(), 0, 1024, st) != cudaSuccess ||
+        (captured && !keep_with_graph(graph, mem))) {
       cudaGetLastError();
-      w.mem.reset();
       throw Refusal{KVQ_ERR_CUDA, call};
     }
+    w.at = mem.data_ptr();
+    w.capture = id;
+    if (!captured) w.mem = std::move(mem);
   }
-  return w.mem.data_ptr();
+  return w.at;
 }
 
 // ---- the calls ------------------------------------------------------------------

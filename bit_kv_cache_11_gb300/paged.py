@@ -82,8 +82,9 @@ def kvq_paged_attention(q, k_pages, v_pages, k_scale, v_scale, block_table, cu_n
     max_new: the most new tokens of a request; softmax_scale: 1 / sqrt(head_dim)
     unless given; window: how many tokens back a token sees (0: all).
     `workspace`: a uint8 tensor of kvq_paged_workspace_bytes whose first 1024
-    bytes are zero.  Without it, the calls of a stream share one, and so do
-    the calls that a stream captures into one graph."""
+    bytes are zero.  Without it, the calls of a stream share one, which is kept
+    (12.6 MB for head_dim 128, 6.4 MB for 64), and the calls that a stream
+    captures into one graph share another, which goes when the graph does."""
     return _attention(q, k_pages, v_pages, k_scale, v_scale, block_table, cu_new, seq_len, max_new,
                       softmax_scale, window, out, workspace, error, stream)
 

@@ -116,3 +116,43 @@ def test_requests_that_share_rows_pass_no_bound(kvq):
                             max_new=n, out=out, error=err)
     assert err.item() == kvq.KVQ_PAGED_ERR_LENGTH
     assert (out == 5.0).all()
+
+
+def test_a_graphs_workspace_goes_with_the_graph(kvq):
+    """Captured calls leave no memory behind when their graphs are gone (the next call
+    frees it), and another capture of the same stream does not take it from a graph
+    that is still there."""
+    import gc
+    import time
+    a = call_of((5000, 3000), (1, 1), D=128)
+    want = kvq.kvq_paged_attention(*a)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+
+    def capture():
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=side):
+            out = kvq.kvq_paged_attention(*a)
+        return g, out
+
+    def allocated():
+        gc.collect()
+        kvq.kvq_paged_attention(*a)
+        torch.cuda.synchronize()
+        return torch.cuda.memory_allocated()
+
+    before = allocated()
+    graphs = [capture() for _ in range(3)]
+    assert allocated() - before >= 3 * kvq.kvq_paged_workspace_bytes(a[1].shape[0], 2, 16, 128)
+    for _ in range(3):
+        for g, out in graphs:
+            out.zero_()
+            g.replay()
+            assert torch.equal(out, want)
+    del g, out, graphs
+    for _ in range(100):  # (a graph is destroyed in its own time)
+        after = allocated()
+        if after == before:
+            break
+        time.sleep(0.05)
+    assert after == before, (before, after)
