@@ -59,7 +59,9 @@ def kvq_paged_plan(ctx_len, new_len, block_table, free_pages, n_free, page_size:
     block_table: int32 [batch][max_pages], written in place; free_pages: int32
     stack of free page ids of which n_free[0] are left.  Returns (cu_new
     [batch + 1], seq_len [batch], slots [n_tokens], n_left [1]); the stack's
-    new height is n_left[0]."""
+    new height is n_left[0].  A request that the stack cannot serve keeps
+    seq_len = ctx_len and gets slots -1: its rows of the attention's output
+    mean nothing, and its step can be made again when pages are free."""
     return _plan(ctx_len, new_len, block_table, free_pages, n_free, page_size, n_tokens, cu_new,
                  seq_len, slots, n_left, error, stream)
 

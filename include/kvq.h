@@ -436,7 +436,11 @@ KVQ_API kvq_status kvq_paged_pool_check(const kvq_paged_pool* pool);
  * (KVQ_PAGED_ERR_LENGTH), takes nothing: seq_len[b] = ctx_len[b], its tokens
  * keep their places in cu_new and get slot -1.  Requests behind one that the
  * stack could not serve get no fresh pages either (the order of admission is
- * kept).  *n_free above n_free_pages, or more new tokens than n_tokens, set
+ * kept).  A step goes on without them: the store writes nothing for them, the
+ * other requests' outputs are right, and the step can be made again for them
+ * when pages are free.  Their own rows of the attention's output mean nothing,
+ * as the attention takes the n rows for the last n of seq_len tokens.
+ * *n_free above n_free_pages, or more new tokens than n_tokens, set
  * KVQ_PAGED_ERR_LENGTH too; the stack is then read to n_free_pages, the slots
  * are written to n_tokens.
  * All arrays are device int32; seq_len, cu_new and n_left may not be the

@@ -156,3 +156,53 @@ def test_a_graphs_workspace_goes_with_the_graph(kvq):
             break
         time.sleep(0.05)
     assert after == before, (before, after)
+
+
+def test_a_step_that_the_free_stack_cannot_serve_in_full(kvq):
+    """The requests that fit are served, nothing of the others is stored, and their step
+    made again with pages gives what it would have given."""
+    # another batch is another split: each result is off by at most 2^-11 of the values'
+    # size (their weights' rounding) and of itself, and by a few fp32 steps
+    def same(x, y):
+        x, y = x.float(), y.float()
+        return bool(((x - y).abs() <= 2.1 * 2.0 ** -11 * (v.abs().max() + y.abs())).all())
+    H, R, D, ps = 2, 2, 64, 16
+    torch.manual_seed(7)
+    ctx, new = [20, 16, 30, 5], [3, 20, 5, 4]  # fresh pages: 0, 2, 1, 0
+    n_pages = 12
+
+    def state(free):
+        torch.manual_seed(8)
+        c = kvq.PagedCache(n_pages=n_pages, page_size=ps, n_q_heads=H * R, n_kv_heads=H, head_dim=D)
+        table, stack, n_free = ints(np.full((4, 6), -1)), ints(range(n_pages)), ints([n_pages])
+        z = ints([0] * 4)
+        cu, seq, slots, left = c.plan(z, ints(ctx), table, stack, n_free, sum(ctx))
+        c.store(*(torch.randn(sum(ctx), H, D, device="cuda").half() for _ in range(2)), slots)
+        assert left.item() == n_pages - 6
+        return c, table, stack, seq, ints([free])
+
+    torch.manual_seed(9)
+    k, v = (torch.randn(sum(new), H, D, device="cuda").half() for _ in range(2))
+    q = torch.randn(sum(new), H * R, D, device="cuda").half()
+    whole, table, stack, seq0, n_free = state(6)
+    cu, seq, slots, _ = whole.plan(seq0, ints(new), table, stack, n_free, sum(new))
+    whole.store(k, v, slots)
+    want = whole.attention(q, table, cu, seq, max_new=max(new))
+    whole.check()
+
+    c, table, stack, seq0, n_free = state(1)  # request 1 needs two pages
+    cu, seq, slots, left = c.plan(seq0, ints(new), table, stack, n_free, sum(new))
+    assert seq.tolist() == [23, 16, 30, 9] and left.item() == 1
+    c.store(k, v, slots)
+    out = c.attention(q, table, cu, seq, max_new=max(new))
+    with pytest.raises(kvq.KvqError, match="free stack"):
+        c.check()
+    for a, b in ((0, 3), (28, 32)):  # requests 0 and 3
+        assert same(out[a:b], want[a:b])
+    again = ints([0, 20, 5, 0])
+    cu, seq, slots, left = c.plan(seq, again, table, ints(range(n_pages)), ints([6]), 25)
+    assert seq.tolist() == [23, 36, 35, 9] and left.item() == 3
+    c.store(k[3:28], v[3:28], slots)
+    out = c.attention(q[3:28], table, cu, seq, max_new=20)
+    assert same(out, want[3:28])
+    c.check()
