@@ -94,3 +94,64 @@ def test_huge_scores(kvq, n, idle):
                                               max_new=n, softmax_scale=2.0 ** (e - 8))
                 want = np.broadcast_to(ref.E4M3[vc[at // ps, 0, at % ps]], (n, 1, D))
                 check(got, want, np.abs(want) * (2.0 ** -10 + 2.0 ** -11) + 2.0 ** -25)
+
+
+@pytest.mark.parametrize("case", ref.SHARES, ids=str)
+def test_every_share_counts(kvq, case):
+    s = ref.shares_case(case)
+    want, bound = ref.shares_want(s)
+    err = ints([0])
+    got = kvq.kvq_paged_attention(s["q"].cuda(), *map(e4m3, s["stale"]), *map(f32, s["scale"]), ints(s["table"]),
+                                  ints(s["cu"]), ints(s["seq"]), max_new=s["max_new"], window=s["window"],
+                                  softmax_scale=s["softmax_scale"], error=err)
+    assert err.item() == 0
+    check(got, want, bound)
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("n,kernel", [(1, "decode"), (70, "prompt")])
+def test_a_negative_softmax_scale(kvq, n, kernel, dtype):
+    s = ref.shares_case((16, 64, 2, 1, "bf16" if dtype == torch.bfloat16 else "fp16", [300, 9], [n, n], 0, kernel))
+    s["softmax_scale"] = -0.2
+    want, bound = ref.shares_want(s)
+    got = kvq.kvq_paged_attention(s["q"].cuda(), *map(e4m3, s["stale"]), *map(f32, s["scale"]), ints(s["table"]),
+                                  ints(s["cu"]), ints(s["seq"]), max_new=s["max_new"], softmax_scale=-0.2)
+    check(got, want, bound)
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+def test_a_serving_loop_against_its_own_pages(kvq, dtype):
+    """Prompts, decode steps, drafted tokens and a chunk: every output against the
+    attention over the codes and scales that the cache holds, and those against the
+    exact keys and values (half a step of E4M3, twice where a page's scale grew)."""
+    rng = np.random.default_rng(17)
+    H, R, D, ps, B = 2, 4, 128, 16, 5
+    c = kvq.PagedCache(n_pages=80, page_size=ps, n_q_heads=H * R, n_kv_heads=H, head_dim=D)
+    ctx, table = ints([0] * B), ints(np.full((B, 24), -1))
+    free, n_free = ints(rng.permutation(80)), ints([80])
+    hist = [[np.zeros((0, H, D))] * 2 for _ in range(B)]
+    half_step = 2.0 ** -11 if dtype == torch.float16 else 2.0 ** -8
+    for new in [[40, 3, 0, 17, 70], [1] * 5, [1, 0, 5, 1, 2]] + [[1] * 5] * 6 + [[30, 4, 0, 1, 33]]:
+        n = sum(new)
+        k, v = (torch.from_numpy(rng.standard_normal((n + 2, H, D))).to(dtype).cuda() for _ in range(2))
+        q = torch.from_numpy(rng.standard_normal((n + 2, H * R, D))).to(dtype).cuda()
+        cu, seq, slots, left = c.plan(ctx, ints(new), table, free, n_free, n + 2)
+        c.store(k, v, slots)
+        out = c.attention(q, table, cu, seq, max_new=max(new))
+        ctx, n_free = seq, left
+        codes = [p.view(torch.uint8).cpu().numpy() for p in (c.k_pages, c.v_pages)]
+        scale = [p.double().cpu().numpy() for p in (c.k_scale, c.v_scale)]
+        at, tab = np.concatenate([[0], np.cumsum(new)]), table.cpu().numpy()
+        want, bound = ref.rows(q[:n].double().cpu().numpy(), *codes, *scale, tab, at, seq.tolist(), ps, D ** -0.5, 0,
+                               ref.WEIGHT_LOG2["prompt"], half_step)
+        check(out[:n], want, bound)
+        for b in range(B):
+            for i, x in enumerate((k, v)):
+                hist[b][i] = np.concatenate([hist[b][i], x[at[b]:at[b + 1]].double().cpu().numpy()])
+                t = np.arange(len(hist[b][i]))
+                pg = tab[b][t // ps]
+                held = ref.E4M3[codes[i][pg, :, t % ps]] * scale[i][pg][..., None]
+                # 2^-4 of a value, or half a step of E4M3's subnormals, 2^-10 of the scale
+                assert (np.abs(held - hist[b][i]) <= 2 * np.maximum(2.0 ** -4 * np.abs(hist[b][i]),
+                                                                    2.0 ** -10 * scale[i][pg][..., None])).all()
+    c.check()
