@@ -254,14 +254,26 @@ __device__ __forceinline__ void store_run(const PagedStoreParams& p, int t, int 
 //
 // Measured with either way alone (8 heads of 128, pages of 64, us): 256 single
 // tokens 2.5 by warps and 75 by teams, 2048 single tokens 6.8 and 94; four
-// prompts of 256 tokens 20 and 5.0, of 1024 tokens 29 and 7.6.  Chunks of 8
-// tokens: 2048 single tokens 8.3, four prompts of 512 tokens 7.0 (whole chunks
-// 6.0), of 1024 tokens 10.1 (7.6): short chunks up to 16384 token heads.
+// prompts of 256 tokens 20 and 5.0, of 1024 tokens 29 and 7.6.
+//
+// A call of up to kShortChunks tokens x heads takes chunks of 8 tokens, so that
+// its runs spread over the SMs; a larger one takes chunks of as many rows as its
+// teams hold.  Measured (8 heads, short / whole chunks, us of a graph's call):
+//   tokens x heads                       2048       4096       8192      16384
+//   single tokens, 64 x 128          2.5/ 7.7   3.0/ 7.8   4.6/ 7.8   7.8/ 9.0
+//   single tokens, 16 x 64           2.5/13.8   3.0/13.9   4.6/14.2   7.9/14.7
+//   runs of 5, 64 x 128              3.2/ 4.5   3.9/ 4.6   6.0/ 4.6   9.5/ 5.4
+//   runs of 5, 16 x 64               3.0/ 7.6   3.5/ 7.8   5.5/ 8.1   8.4/ 8.5
+//   one prompt, 64 x 128             3.2/ 3.0   3.8/ 3.0   4.6/ 3.1   5.9/ 3.7
+//   one prompt, 16 x 64              3.0/ 2.8   3.6/ 2.8   4.6/ 2.9   7.1/ 2.9
+// The host does not know the runs: the turn lies where prompts lose by short
+// chunks what single tokens gain.
 template <int TEAM>
 __host__ __device__ constexpr int chunk_threads() {
   return TEAM == 256 ? 512 : 256;
 }
 constexpr int kSteps = 8;
+constexpr int kShortChunks = 8192;
 
 template <int D, bool BF16, int TEAM>
 __global__ void __launch_bounds__(chunk_threads<TEAM>(), 1024 / chunk_threads<TEAM>())
@@ -398,9 +410,8 @@ __global__ void __launch_bounds__(chunk_threads<TEAM>(), 1024 / chunk_threads<TE
 template <int D, bool BF16, int TEAM>
 cudaError_t launch_team(PagedStoreParams p, cudaStream_t st) {
   constexpr int THREADS = chunk_threads<TEAM>();
-  // Small calls take short chunks: their few runs spread over the SMs.
   const int most = TEAM * 64 / D * (THREADS / (2 * TEAM));
-  p.chunk = static_cast<long long>(p.n_tokens) * p.H <= 16384 ? 8 : most;
+  p.chunk = static_cast<long long>(p.n_tokens) * p.H <= kShortChunks ? 8 : most;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((p.n_tokens + p.chunk - 1) / p.chunk, p.H);
   cfg.blockDim = dim3(THREADS);
