@@ -396,7 +396,9 @@ KVQ_API kvq_status kvq_decode_attention_noalloc(const kvq_config* cfg, const voi
  *     tables and lengths hold.
  *   - Two calls that may overlap on the GPU must not write the same pages, nor
  *     share a workspace.  One call must not write a page from two places of
- *     the batch: the rows of a page that it writes are consecutive tokens.
+ *     the batch: the rows of a page that it writes are consecutive tokens in
+ *     consecutive rows, no row twice and none left out between.  The calls do
+ *     not look for that; such a page holds nothing that can be relied on.
  * ------------------------------------------------------------------------ */
 
 typedef enum { KVQ_DTYPE_FP16 = 0, KVQ_DTYPE_BF16 = 1 } kvq_dtype;
