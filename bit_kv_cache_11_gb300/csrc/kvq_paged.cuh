@@ -176,11 +176,11 @@ constexpr int kPagedMaxCtas = 152;
 // them once per 16 rows; one with more rows by the prompt kernel, which reads
 // them once per 256 rows but gives each of the call's batch * H (request,
 // head) items at most one SM.  Measured (us, decode / prompt kernel; R = 4):
-//   8 items of 32768 tokens, D = 128: 32 rows 43 / 411, 128 rows 110 / 412
-//                            D = 64:  32 rows 31 / 365, 128 rows 69 / 365
-//   128 items of 4000 tokens, D = 128: 32 rows 66 / 72, 64 rows 115 / 72
-//                             D = 64:  32 rows 45 / 57, 64 rows 73 / 57
-//   512 items of 1000 tokens, D = 128: 64 rows 115 / 89; D = 64: 74 / 73
+//   8 items of 32768 tokens, D = 128: 32 rows 43 / 409, 128 rows 110 / 410
+//                            D = 64:  32 rows 31 / 348, 128 rows 69 / 349
+//   128 items of 4000 tokens, D = 128: 32 rows 67 / 64, 64 rows 116 / 65
+//                             D = 64:  32 rows 45 / 53, 64 rows 74 / 53
+//   512 items of 1000 tokens, D = 128: 64 rows 116 / 85; D = 64: 74 / 71
 // so the turn lies near 32 rows (48 of the narrower ones) where the items fill
 // the SMs, and moves up in proportion where they do not.
 constexpr int decode_rows(long long items, int D) {

@@ -12,7 +12,10 @@
 // that multiply the codes is the only one besides the output's: half a step,
 // 2^-11, of a token's weight * scale down to 2^-29 of the row's largest, and
 // 2^-40 of that largest below (the factor 2^15 uses fp16's whole range, and
-// 1 / sv carries 2^-15 so that the sum below stays as it is).
+// 1 / sv carries 2^-15 so that the sum below stays as it is).  A second fp16
+// half for the rest of a weight would double the value products; outputs are
+// 16 bits, and their own rounding is as large: against 64 bits fp16 outputs are
+// 2.2 .. 2.4e-4 off (relative 2-norm; fp32 weights 1.9 .. 2.2e-4), bf16 1.7e-3 with either.
 //
 // Split.  Every warp streams a contiguous, equal range of units of UT = 32
 // (D = 128) or 64 (D = 64) tokens: 4 KB of key and 4 KB of value codes that
@@ -26,12 +29,12 @@
 // read 7.4 TB/s), latency around that: 4 us from the start of a launch to the
 // first data (lengths, table, page, copy, one after the other) and 3 .. 6 us of
 // joins.  Measured (us, and the share of the measured copy rate): 131072 tokens
-// 50 (80 %), 8 x 4113 tokens of 32 heads 54 (74 %), 64 ragged requests of up to
-// 2048 tokens 43 (57 %), five drafted tokens with a window 28.  Eight warps of
+// 49.5 (81 %), 8 x 4113 tokens of 32 heads 53.5 (75 %), 64 ragged requests of up to
+// 2048 tokens 43.6 (57 %), five drafted tokens with a window 28.  Eight warps of
 // three 8 KB stages were 3 % faster than twelve of two.  Code that runs once a
 // launch is fetched as it runs: the joins are small loops, and one body of the
-// unit serves edges too (separate bodies: 9.3 -> 7.9 us for the smallest call
-// together with the joins' loads in flight).
+// unit serves edges too (together with the joins' loads in flight that took 15 %
+// off the smallest call, now 8.6 us in a graph).
 //
 // Tensor-core operands (mma.sync m16n8k16, fp16 in, fp32 out).  Scores:
 // A = 16 tokens x 16 channels of codes, B = 8 query rows.  Lane (g, t) reads

@@ -29,17 +29,23 @@
 // 128 (512 cycles each, the tensor pipe's 2048), but a row tile's softmax
 // (about 1900 cycles) and the hand-overs to it and back lie between its scores
 // and its output product, and only one other row tile's products fit beside
-// them: 3400 cycles a key tile, the tensor pipe 58 % active.  Measured: 2048
-// new tokens behind 32768 (32 heads, D = 128) 965 us, 1.17 PFLOP/s, 61 % of the
+// them: about 3300 cycles a key tile, the tensor pipe 59 % active.  Measured: 2048
+// new tokens behind 32768 (32 heads, D = 128) 943 us, 1.20 PFLOP/s, 62 % of the
 // measured bf16 rate (two rounds of CTAs over 152 SMs: 84 % of a full one);
-// without the softmax 803 us, without the conversion 925 us, without either
-// 749 us.  Three prompts of up to 4001 tokens (40 heads) 263 us, where the
-// causal half and 9 us a CTA of start and end weigh more.
-// Measured and not kept: two CTAs sharing each key tile (cta_group::2, half of
-// the conversion each): 939 and 296 us; every CTA an equal share of the tiles,
-// items joined from shares: 958 us, and prompts need a cost for each item;
-// two threads a row: 1053 and 280 us; S read from tensor memory once, into 128
-// registers: 1037 and 261 us.
+// without the softmax 805 us, without the conversion 885 us, without either
+// 756 us.  Three prompts of up to 4001 tokens (40 heads) 254 us, where the
+// causal half and 9 us a CTA of start and end weigh more.  Lanes that wait by a
+// vote, so that the compiler knows a warp as converged, took 956 -> 943 and
+// 262 -> 254 us.
+// Measured and not kept, beside 957 and 265 us without the vote: two CTAs sharing
+// each key tile (cta_group::2, half of the conversion each): 939 and 296 us; every
+// CTA an equal share of the tiles, items joined from shares: 958 us, and prompts
+// need a cost for each item; two threads a row: 1053 and 280 us; S read from
+// tensor memory once, into 128 registers: 1037 and 261 us.
+// Weights as fp16: against 64 bits the chunk's outputs are 2.8e-4 off (relative
+// 2-norm; with fp32 weights 2.1e-4, the output's own rounding), bf16 prompts'
+// 1.6e-3 with either.  A second half of a weight would need 128 more columns of
+// tensor memory, which is full, and half as many products again.
 #pragma once
 
 #include <type_traits>
