@@ -369,7 +369,7 @@ def _append4(s):
     page, row = slots // ps, slots % ps
     out = {"q": _rotate(s, s["q"])}
     for n, x in (("k", _rotate(s, s["k"])), ("v", s["v"])):
-        codes, meta = _packed(x.clamp(-65504.0, 65504.0).half(), n == "k")
+        codes, meta = _packed(x.clamp(-65408.0, 65408.0).half(), n == "k")
         s[n + "_codes"][page, :, row] = codes
         s[n + "_meta"][page, :, row] = meta
         out[n] = _values(s[n + "_codes"][page, :, row], s[n + "_meta"][page, :, row], n == "k")
