@@ -34,6 +34,7 @@ struct PagedPlanParams {
   int* cu_new;
   int* seq_len;
   int* slots;
+  int* positions;  // may be null
   int* n_left;
   int* err;
 };
@@ -48,6 +49,10 @@ struct PagedStoreParams {
   int n_pages, H, lg_ps;
   int chunk;  // tokens a CTA looks at
   int* err;
+  // kvq_paged_append: keys turn by their tokens' angles [n_tokens][rot / 2]
+  // (rot 0: they are stored as they are)
+  const float2* angles;
+  int rot, interleaved;
 };
 
 // Attention over the pages.  Work is a flat sequence of units: request b's
@@ -67,6 +72,9 @@ struct PagedAttnParams {
   uint32_t r_magic;  // ceil(2^32 / R): row / R by one high product (R > 1)
   const float* k_scale;
   const float* v_scale;
+  // the 4-bit pages' (kvq_paged4_attention); scales are null then
+  const uint8_t* codes[2];
+  const uint32_t* meta[2];
   float qscale;  // softmax scale * log2(e)
   int window;    // 0: none
   // rows (new tokens * R) of the requests this launch serves: those with

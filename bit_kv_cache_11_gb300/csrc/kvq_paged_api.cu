@@ -1,4 +1,4 @@
-// kvq_paged_api.cu — the paged 8-bit cache's part of the C ABI (include/kvq.h):
+// kvq_paged_api.cu — the paged caches' part of the C ABI (include/kvq.h):
 // validation, tensor maps, workspace layout and launches.  Nothing is kept
 // between calls but the driver entry point, each kernel's shared-memory opt-in
 // and the wait limit that a test may have set.
@@ -9,7 +9,7 @@
 #include <mutex>
 
 #include "kvq.h"
-#include "kvq_paged.cuh"
+#include "kvq_paged4.cuh"
 
 namespace kvq {
 void count_launches(uint64_t n);
@@ -67,6 +67,9 @@ bool pool_pointers(const kvq_paged_pool* c) {
          dev_ptr(c->v_scale, 4);
 }
 
+// A 4-bit pool's metadata is copied in bulk.
+bool meta_pointers(const kvq_paged_pool* c) { return dev_ptr(c->k_scale, 16) && dev_ptr(c->v_scale, 16); }
+
 bool dtype_ok(int dtype) { return dtype == KVQ_DTYPE_FP16 || dtype == KVQ_DTYPE_BF16; }
 
 // Rows of `heads` heads at a stride: the stride holds them and keeps rows
@@ -122,109 +125,17 @@ size_t workspace_bytes(int D) {
 }
 static_assert(kPagedMaxCtas * sizeof(int) <= kTicketBytes, "a ticket per CTA");
 
-}  // namespace
-
-extern "C" {
-
-kvq_status kvq_paged_pool_check(const kvq_paged_pool* pool) { return check_pool(pool); }
-
-kvq_status kvq_paged_plan(const int* ctx_len, const int* new_len, int batch, int* block_table,
-                          int max_pages, const int* free_pages, int n_free_pages,
-                          const int* n_free, int page_size, int n_tokens, int* cu_new,
-                          int* seq_len, int* slots, int* n_left, int* device_error, void* stream) {
-  if (batch < 1 || max_pages < 1 || n_free_pages < 0 || n_tokens < 0 || page_size < 1)
-    return KVQ_ERR_INVALID_ARG;
-  if (!dev_ptr(ctx_len, 4) || !dev_ptr(new_len, 4) || !dev_ptr(block_table, 4) ||
-      !dev_ptr(n_free, 4) || !dev_ptr(cu_new, 4) || !dev_ptr(seq_len, 4) || !dev_ptr(n_left, 4) ||
-      !aligned(device_error, 4))
-    return KVQ_ERR_INVALID_ARG;
-  if (n_free_pages > 0 && !dev_ptr(free_pages, 4)) return KVQ_ERR_INVALID_ARG;
-  if (n_tokens > 0 && !dev_ptr(slots, 16)) return KVQ_ERR_INVALID_ARG;
-  // several CTAs read the inputs while the first writes these
-  if (seq_len == ctx_len || seq_len == new_len || n_left == n_free || cu_new == ctx_len ||
-      cu_new == new_len)
-    return KVQ_ERR_INVALID_ARG;
-  if (!page_size_ok(page_size) || batch > kPagedMaxBatch || max_pages > INT_MAX / page_size)
-    return KVQ_ERR_UNSUPPORTED;
-  PagedPlanParams p;
-  p.ctx_len = ctx_len;
-  p.new_len = new_len;
-  p.batch = batch;
-  p.table = block_table;
-  p.max_pages = max_pages;
-  p.free_pages = free_pages;
-  p.free_cap = n_free_pages;
-  p.n_free = n_free;
-  p.lg_ps = log2_of(page_size);
-  p.n_tokens = n_tokens;
-  p.cu_new = cu_new;
-  p.seq_len = seq_len;
-  p.slots = slots;
-  p.n_left = n_left;
-  p.err = device_error;
-  if (launch_paged_plan(p, static_cast<cudaStream_t>(stream)) != cudaSuccess) {
-    cudaGetLastError();
-    return KVQ_ERR_CUDA;
-  }
-  count_launches(1);
-  return KVQ_OK;
-}
-
-kvq_status kvq_paged_store(const kvq_paged_pool* pool, const void* k, const void* v, int dtype,
-                           long long k_stride, long long v_stride, const int* slots, int n_tokens,
-                           int* device_error, void* stream) {
-  kvq_status s = check_pool(pool);
-  if (s != KVQ_OK) return s;
-  if (!pool_pointers(pool) || n_tokens < 0 || !dtype_ok(dtype) || !aligned(device_error, 4))
-    return KVQ_ERR_INVALID_ARG;
-  if (n_tokens == 0) return KVQ_OK;
-  if (!dev_ptr(k, 16) || !dev_ptr(v, 16) || !dev_ptr(slots, 4) ||
-      !stride_ok(k_stride, pool->n_kv_heads, pool->head_dim) ||
-      !stride_ok(v_stride, pool->n_kv_heads, pool->head_dim))
-    return KVQ_ERR_INVALID_ARG;
-  if (pool->n_kv_heads > 65535) return KVQ_ERR_UNSUPPORTED;  // grid.y
-  PagedStoreParams p;
-  p.pages[0] = static_cast<uint8_t*>(pool->k_pages);
-  p.pages[1] = static_cast<uint8_t*>(pool->v_pages);
-  p.scale[0] = pool->k_scale;
-  p.scale[1] = pool->v_scale;
-  p.x[0] = k;
-  p.x[1] = v;
-  p.stride[0] = k_stride;
-  p.stride[1] = v_stride;
-  p.slots = slots;
-  p.n_tokens = n_tokens;
-  p.n_pages = pool->n_pages;
-  p.H = pool->n_kv_heads;
-  p.lg_ps = log2_of(pool->page_size);
-  p.err = device_error;
-  if (launch_paged_store(p, pool->head_dim, dtype, static_cast<cudaStream_t>(stream)) !=
-      cudaSuccess) {
-    cudaGetLastError();
-    return KVQ_ERR_CUDA;
-  }
-  count_launches(1);
-  return KVQ_OK;
-}
-
-kvq_status kvq_paged_workspace_bytes(const kvq_paged_pool* pool, size_t* bytes) {
-  if (bytes == nullptr) return KVQ_ERR_INVALID_ARG;
-  const kvq_status s = check_pool(pool);
-  if (s != KVQ_OK) return s;
-  *bytes = workspace_bytes(pool->head_dim);
-  return KVQ_OK;
-}
-
-kvq_status kvq_paged_attention(const kvq_paged_pool* pool, const void* q, int dtype,
-                               long long q_stride, void* out, long long out_stride, int n_tokens,
-                               int n_q_heads, const int* block_table, int max_pages,
-                               const int* cu_new, const int* seq_len, int batch, int max_new,
-                               float softmax_scale, int window, void* workspace,
-                               size_t n_workspace, int* device_error, void* stream) {
+// The attention over either kind of pages; `four`: *pool holds a 4-bit pool's
+// buffers (codes as pages, metadata as scales).
+kvq_status attention(const kvq_paged_pool* pool, bool four, const void* q, int dtype,
+                     long long q_stride, void* out, long long out_stride, int n_tokens,
+                     int n_q_heads, const int* block_table, int max_pages, const int* cu_new,
+                     const int* seq_len, int batch, int max_new, float softmax_scale, int window,
+                     void* workspace, size_t n_workspace, int* device_error, void* stream) {
   kvq_status s = check_pool(pool);
   if (s != KVQ_OK) return s;
   const int H = pool->n_kv_heads, D = pool->head_dim;
-  if (!pool_pointers(pool) || !dtype_ok(dtype) || n_tokens < 0 || batch < 1 || max_pages < 1 ||
+  if (!pool_pointers(pool) || (four && !meta_pointers(pool)) || !dtype_ok(dtype) || n_tokens < 0 || batch < 1 || max_pages < 1 ||
       max_new < 1 || window < 0 || n_q_heads < 1 || !std::isfinite(softmax_scale) ||
       !aligned(device_error, 4))
     return KVQ_ERR_INVALID_ARG;
@@ -283,8 +194,12 @@ kvq_status kvq_paged_attention(const kvq_paged_pool* pool, const void* q, int dt
   p.r_magic = static_cast<uint32_t>(((1ull << 32) + R - 1) / R);
   p.lg_ps = log2_of(pool->page_size);
   p.n_pages = pool->n_pages;
-  p.k_scale = pool->k_scale;
-  p.v_scale = pool->v_scale;
+  p.k_scale = four ? nullptr : pool->k_scale;
+  p.v_scale = four ? nullptr : pool->v_scale;
+  p.codes[0] = static_cast<const uint8_t*>(pool->k_pages);
+  p.codes[1] = static_cast<const uint8_t*>(pool->v_pages);
+  p.meta[0] = reinterpret_cast<const uint32_t*>(pool->k_scale);
+  p.meta[1] = reinterpret_cast<const uint32_t*>(pool->v_scale);
   p.qscale = softmax_scale * 1.4426950408889634f;
   p.window = window;
   p.row_min = 1;
@@ -298,6 +213,14 @@ kvq_status kvq_paged_attention(const kvq_paged_pool* pool, const void* q, int dt
   p.err = device_error;
   const bool bf = dtype == KVQ_DTYPE_BF16;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (four) {
+    if (launch_paged4_attention(p, D, bf, st) != cudaSuccess) {
+      cudaGetLastError();
+      return KVQ_ERR_CUDA;
+    }
+    count_launches(1);
+    return KVQ_OK;
+  }
   CUtensorMap km, vm;
   if (prompts && pairs > 0) {
     PagedAttnParams a = p;
@@ -325,6 +248,273 @@ kvq_status kvq_paged_attention(const kvq_paged_pool* pool, const void* q, int dt
   }
   count_launches(1);
   return KVQ_OK;
+}
+
+// A 4-bit pool's buffers and sizes as the calls of both kinds of pages pass them
+// on: codes as pages, metadata as scales.
+kvq_paged_pool as_pool(const kvq_paged4_pool* p) {
+  if (p == nullptr) return {};
+  return {p->k_codes, p->v_codes, static_cast<float*>(p->k_meta), static_cast<float*>(p->v_meta),
+          p->n_pages, p->n_kv_heads, p->page_size, p->head_dim};
+}
+
+kvq_status store_params(PagedStoreParams* p, const kvq_paged_pool* pool, const void* k, const void* v, int dtype,
+                        long long k_stride, long long v_stride, const int* slots, int n_tokens, int* device_error) {
+  const kvq_status s = check_pool(pool);
+  if (s != KVQ_OK) return s;
+  if (!pool_pointers(pool) || n_tokens < 0 || !dtype_ok(dtype) || !aligned(device_error, 4))
+    return KVQ_ERR_INVALID_ARG;
+  if (n_tokens == 0) return KVQ_OK;
+  if (!dev_ptr(k, 16) || !dev_ptr(v, 16) || !dev_ptr(slots, 4) ||
+      !stride_ok(k_stride, pool->n_kv_heads, pool->head_dim) ||
+      !stride_ok(v_stride, pool->n_kv_heads, pool->head_dim))
+    return KVQ_ERR_INVALID_ARG;
+  if (pool->n_kv_heads > 65535) return KVQ_ERR_UNSUPPORTED;  // grid.y
+  p->pages[0] = static_cast<uint8_t*>(pool->k_pages);
+  p->pages[1] = static_cast<uint8_t*>(pool->v_pages);
+  p->scale[0] = pool->k_scale;
+  p->scale[1] = pool->v_scale;
+  p->x[0] = k;
+  p->x[1] = v;
+  p->stride[0] = k_stride;
+  p->stride[1] = v_stride;
+  p->slots = slots;
+  p->n_tokens = n_tokens;
+  p->n_pages = pool->n_pages;
+  p->H = pool->n_kv_heads;
+  p->lg_ps = log2_of(pool->page_size);
+  p->err = device_error;
+  p->angles = nullptr;
+  p->rot = p->interleaved = 0;
+  return KVQ_OK;
+}
+
+kvq_status store(const PagedStoreParams& p, int D, int dtype, void* stream) {
+  if (launch_paged_store(p, D, dtype, static_cast<cudaStream_t>(stream)) != cudaSuccess) {
+    cudaGetLastError();
+    return KVQ_ERR_CUDA;
+  }
+  count_launches(1);
+  return KVQ_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+kvq_status kvq_paged_pool_check(const kvq_paged_pool* pool) { return check_pool(pool); }
+
+kvq_status kvq_paged_plan(const int* ctx_len, const int* new_len, int batch, int* block_table,
+                          int max_pages, const int* free_pages, int n_free_pages,
+                          const int* n_free, int page_size, int n_tokens, int* cu_new,
+                          int* seq_len, int* slots, int* n_left, int* device_error, void* stream) {
+  return kvq_paged_plan_positions(ctx_len, new_len, batch, block_table, max_pages, free_pages, n_free_pages,
+                                  n_free, page_size, n_tokens, cu_new, seq_len, slots, nullptr, n_left,
+                                  device_error, stream);
+}
+
+kvq_status kvq_paged_plan_positions(const int* ctx_len, const int* new_len, int batch,
+                                    int* block_table, int max_pages, const int* free_pages,
+                                    int n_free_pages, const int* n_free, int page_size,
+                                    int n_tokens, int* cu_new, int* seq_len, int* slots,
+                                    int* positions, int* n_left, int* device_error, void* stream) {
+  if (batch < 1 || max_pages < 1 || n_free_pages < 0 || n_tokens < 0 || page_size < 1)
+    return KVQ_ERR_INVALID_ARG;
+  if (!dev_ptr(ctx_len, 4) || !dev_ptr(new_len, 4) || !dev_ptr(block_table, 4) ||
+      !dev_ptr(n_free, 4) || !dev_ptr(cu_new, 4) || !dev_ptr(seq_len, 4) || !dev_ptr(n_left, 4) ||
+      !aligned(device_error, 4))
+    return KVQ_ERR_INVALID_ARG;
+  if (n_free_pages > 0 && !dev_ptr(free_pages, 4)) return KVQ_ERR_INVALID_ARG;
+  if (n_tokens > 0 && !dev_ptr(slots, 16)) return KVQ_ERR_INVALID_ARG;
+  if (!aligned(positions, 16) || (positions != nullptr && (positions == ctx_len || positions == new_len)))
+    return KVQ_ERR_INVALID_ARG;
+  // several CTAs read the inputs while the first writes these
+  if (seq_len == ctx_len || seq_len == new_len || n_left == n_free || cu_new == ctx_len ||
+      cu_new == new_len)
+    return KVQ_ERR_INVALID_ARG;
+  if (!page_size_ok(page_size) || batch > kPagedMaxBatch || max_pages > INT_MAX / page_size)
+    return KVQ_ERR_UNSUPPORTED;
+  PagedPlanParams p;
+  p.ctx_len = ctx_len;
+  p.new_len = new_len;
+  p.batch = batch;
+  p.table = block_table;
+  p.max_pages = max_pages;
+  p.free_pages = free_pages;
+  p.free_cap = n_free_pages;
+  p.n_free = n_free;
+  p.lg_ps = log2_of(page_size);
+  p.n_tokens = n_tokens;
+  p.cu_new = cu_new;
+  p.seq_len = seq_len;
+  p.slots = slots;
+  p.positions = positions;
+  p.n_left = n_left;
+  p.err = device_error;
+  if (launch_paged_plan(p, static_cast<cudaStream_t>(stream)) != cudaSuccess) {
+    cudaGetLastError();
+    return KVQ_ERR_CUDA;
+  }
+  count_launches(1);
+  return KVQ_OK;
+}
+
+kvq_status kvq_paged_store(const kvq_paged_pool* pool, const void* k, const void* v, int dtype,
+                           long long k_stride, long long v_stride, const int* slots, int n_tokens,
+                           int* device_error, void* stream) {
+  PagedStoreParams p;
+  const kvq_status s = store_params(&p, pool, k, v, dtype, k_stride, v_stride, slots, n_tokens, device_error);
+  if (s != KVQ_OK || n_tokens == 0) return s;
+  return store(p, pool->head_dim, dtype, stream);
+}
+
+kvq_status kvq_paged_append(const kvq_paged_pool* pool, const kvq_rotary* rotary, const void* k,
+                            const void* v, int dtype, long long k_stride, long long v_stride,
+                            const int* slots, int n_tokens, const void* q, long long q_stride,
+                            void* q_out, long long q_out_stride, int n_q_heads, int* device_error,
+                            void* stream) {
+  PagedStoreParams p;
+  kvq_status s = store_params(&p, pool, k, v, dtype, k_stride, v_stride, slots, n_tokens, device_error);
+  if (s != KVQ_OK) return s;
+  s = check_rotary(rotary, pool->head_dim, n_tokens);
+  if (s != KVQ_OK) return s;
+  RotateParams r;
+  const bool queries = q != nullptr || q_out != nullptr || n_q_heads != 0;
+  if (queries) {
+    if (n_q_heads < 1) return KVQ_ERR_INVALID_ARG;
+    s = rotate_params(&r, rotary, q, dtype, q_stride, q_out, q_out_stride, n_tokens, n_q_heads, pool->head_dim);
+    if (s != KVQ_OK) return s;
+  }
+  if (n_tokens == 0) return KVQ_OK;
+  p.angles = reinterpret_cast<const float2*>(rotary->angles);
+  p.rot = rotary->rotary_dim;
+  p.interleaved = rotary->interleaved;
+  s = store(p, pool->head_dim, dtype, stream);
+  if (s != KVQ_OK || !queries) return s;
+  if (launch_rotate(r, dtype, static_cast<cudaStream_t>(stream)) != cudaSuccess) {
+    cudaGetLastError();
+    return KVQ_ERR_CUDA;
+  }
+  count_launches(1);
+  return KVQ_OK;
+}
+
+kvq_status kvq_paged_workspace_bytes(const kvq_paged_pool* pool, size_t* bytes) {
+  if (bytes == nullptr) return KVQ_ERR_INVALID_ARG;
+  const kvq_status s = check_pool(pool);
+  if (s != KVQ_OK) return s;
+  *bytes = workspace_bytes(pool->head_dim);
+  return KVQ_OK;
+}
+
+kvq_status kvq_paged_attention(const kvq_paged_pool* pool, const void* q, int dtype,
+                               long long q_stride, void* out, long long out_stride, int n_tokens,
+                               int n_q_heads, const int* block_table, int max_pages,
+                               const int* cu_new, const int* seq_len, int batch, int max_new,
+                               float softmax_scale, int window, void* workspace,
+                               size_t n_workspace, int* device_error, void* stream) {
+  return attention(pool, false, q, dtype, q_stride, out, out_stride, n_tokens, n_q_heads, block_table, max_pages, cu_new,
+                   seq_len, batch, max_new, softmax_scale, window, workspace, n_workspace, device_error, stream);
+}
+
+kvq_status kvq_paged4_pool_check(const kvq_paged4_pool* pool) {
+  const kvq_paged_pool c = as_pool(pool);
+  return check_pool(pool ? &c : nullptr);
+}
+
+kvq_status kvq_paged4_append(const kvq_paged4_pool* pool, const kvq_rotary* rotary, const void* k,
+                             const void* v, int dtype, long long k_stride, long long v_stride,
+                             const int* slots, int n_tokens, const void* q, long long q_stride,
+                             void* q_out, long long q_out_stride, int n_q_heads, int* device_error,
+                             void* stream) {
+  const kvq_paged_pool c = as_pool(pool);
+  PagedStoreParams w;
+  kvq_status s = store_params(&w, pool ? &c : nullptr, k, v, dtype, k_stride, v_stride, slots, n_tokens,
+                              device_error);
+  if (s != KVQ_OK) return s;
+  if (!meta_pointers(&c)) return KVQ_ERR_INVALID_ARG;
+  Paged4StoreParams p = {};
+  const bool queries = q != nullptr || q_out != nullptr || n_q_heads != 0;
+  if (rotary != nullptr) {
+    s = check_rotary(rotary, c.head_dim, n_tokens);
+    if (s != KVQ_OK) return s;
+  }
+  if (queries) {
+    if (rotary == nullptr || n_q_heads < 1) return KVQ_ERR_INVALID_ARG;
+    s = rotate_params(&p.q, rotary, q, dtype, q_stride, q_out, q_out_stride, n_tokens, n_q_heads, c.head_dim);
+    if (s != KVQ_OK) return s;
+  }
+  if (n_tokens == 0) return KVQ_OK;
+  for (int i = 0; i < 2; ++i) {
+    p.codes[i] = w.pages[i];
+    p.meta[i] = reinterpret_cast<uint32_t*>(w.scale[i]);
+    p.x[i] = w.x[i];
+    p.stride[i] = w.stride[i];
+  }
+  p.slots = slots;
+  p.n_tokens = n_tokens;
+  p.n_pages = c.n_pages;
+  p.H = c.n_kv_heads;
+  p.lg_ps = w.lg_ps;
+  p.err = device_error;
+  if (rotary != nullptr) {
+    p.angles = reinterpret_cast<const float2*>(rotary->angles);
+    p.rot = rotary->rotary_dim;
+    p.interleaved = rotary->interleaved;
+  }
+  if (launch_paged4_append(p, c.head_dim, dtype, static_cast<cudaStream_t>(stream)) != cudaSuccess) {
+    cudaGetLastError();
+    return KVQ_ERR_CUDA;
+  }
+  count_launches(1);
+  return KVQ_OK;
+}
+
+kvq_status kvq_paged4_read(const kvq_paged4_pool* pool, const int* slots, int n_tokens, void* k_out,
+                           void* v_out, int* device_error, void* stream) {
+  const kvq_paged_pool c = as_pool(pool);
+  const kvq_status s = check_pool(pool ? &c : nullptr);
+  if (s != KVQ_OK) return s;
+  if (!pool_pointers(&c) || !meta_pointers(&c) || n_tokens < 0 || !aligned(device_error, 4) ||
+      !aligned(k_out, 16) || !aligned(v_out, 16))
+    return KVQ_ERR_INVALID_ARG;
+  if (n_tokens == 0 || (k_out == nullptr && v_out == nullptr)) return KVQ_OK;
+  if (!dev_ptr(slots, 4)) return KVQ_ERR_INVALID_ARG;
+  Paged4ReadParams p;
+  p.codes[0] = static_cast<const uint8_t*>(c.k_pages);
+  p.codes[1] = static_cast<const uint8_t*>(c.v_pages);
+  p.meta[0] = reinterpret_cast<const uint32_t*>(c.k_scale);
+  p.meta[1] = reinterpret_cast<const uint32_t*>(c.v_scale);
+  p.out[0] = static_cast<uint16_t*>(k_out);
+  p.out[1] = static_cast<uint16_t*>(v_out);
+  p.slots = slots;
+  p.n_tokens = n_tokens;
+  p.n_pages = c.n_pages;
+  p.H = c.n_kv_heads;
+  p.lg_ps = log2_of(c.page_size);
+  p.err = device_error;
+  if (launch_paged4_read(p, c.head_dim, static_cast<cudaStream_t>(stream)) != cudaSuccess) {
+    cudaGetLastError();
+    return KVQ_ERR_CUDA;
+  }
+  count_launches(1);
+  return KVQ_OK;
+}
+
+kvq_status kvq_paged4_workspace_bytes(const kvq_paged4_pool* pool, size_t* bytes) {
+  const kvq_paged_pool c = as_pool(pool);
+  return kvq_paged_workspace_bytes(pool ? &c : nullptr, bytes);
+}
+
+kvq_status kvq_paged4_attention(const kvq_paged4_pool* pool, const void* q, int dtype,
+                                long long q_stride, void* out, long long out_stride, int n_tokens,
+                                int n_q_heads, const int* block_table, int max_pages,
+                                const int* cu_new, const int* seq_len, int batch, int max_new,
+                                float softmax_scale, int window, void* workspace,
+                                size_t n_workspace, int* device_error, void* stream) {
+  const kvq_paged_pool c = as_pool(pool);
+  return attention(pool ? &c : nullptr, true, q, dtype, q_stride, out, out_stride, n_tokens, n_q_heads, block_table, max_pages, cu_new,
+                   seq_len, batch, max_new, softmax_scale, window, workspace, n_workspace, device_error, stream);
 }
 
 kvq_status kvq_debug_set_paged_wait_limit(int limit) {

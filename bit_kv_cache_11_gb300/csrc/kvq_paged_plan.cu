@@ -152,18 +152,21 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const PagedPla
     }
     int b = lo;
     int last_pg = -1, page = 0;  // page index of the cached table entry
-    int s[kTokensPerThread];
+    int s[kTokensPerThread], at[kTokensPerThread];
 #pragma unroll
     for (int i = 0; i < kTokensPerThread; ++i) {
       const long long t = t0 + i;
       s[i] = -1;
+      at[i] = 0;
       if (t >= total) continue;
       while (cu[b + 1] <= t) {
         ++b;
         last_pg = -1;
       }
+      // (unsigned: a request whose length breaks the contract may pass 31 bits)
+      const int pos = static_cast<int>(static_cast<uint32_t>(p.ctx_len[b]) + static_cast<uint32_t>(t) - cu[b]);
+      at[i] = pos;
       if (depth[b] < 0) continue;
-      const int pos = p.ctx_len[b] + static_cast<int>(t) - cu[b];
       const int have = (p.ctx_len[b] + ps1) >> p.lg_ps;
       const int pg = pos >> p.lg_ps;
       if (pg != last_pg) {
@@ -176,8 +179,12 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const PagedPla
     }
     if (t0 + kTokensPerThread <= p.n_tokens) {
       *reinterpret_cast<int4*>(p.slots + t0) = make_int4(s[0], s[1], s[2], s[3]);
+      if (p.positions) *reinterpret_cast<int4*>(p.positions + t0) = make_int4(at[0], at[1], at[2], at[3]);
     } else {
-      for (int i = 0; i < kTokensPerThread && t0 + i < p.n_tokens; ++i) p.slots[t0 + i] = s[i];
+      for (int i = 0; i < kTokensPerThread && t0 + i < p.n_tokens; ++i) {
+        p.slots[t0 + i] = s[i];
+        if (p.positions) p.positions[t0 + i] = at[i];
+      }
     }
   }
 }

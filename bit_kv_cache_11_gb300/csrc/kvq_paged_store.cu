@@ -21,7 +21,7 @@
 // 14.5 us (62 %; the launch and the last CTAs take the rest); 256 single tokens
 // 2.5 us.  One test per side for NaN instead of two selects a value, and fp16
 // codes without a step through fp32, took 31.0 -> 28.9 and 16.0 -> 14.5 us.
-#include "kvq_paged.cuh"
+#include "kvq_rotary.cuh"
 
 namespace kvq {
 namespace {
@@ -173,11 +173,23 @@ __device__ __forceinline__ const uint4* vec_ptr(const PagedStoreParams& p, int s
                                         t * (side ? p.stride[1] : p.stride[0]) + h * D) + vec;
 }
 
+// Vector `vec` of token t's key (side 0, turned by its angles when ROT) or value.
+template <int D, bool BF16, bool ROT>
+__device__ __forceinline__ uint4 load_vec(const PagedStoreParams& p, int side, long long t, int h, int vec) {
+  const uint4 v = __ldg(vec_ptr(p, side, t, h, D, vec));
+  if constexpr (ROT) {
+    if (side == 0)
+      return turned_chunk<BF16>(v, static_cast<const uint16_t*>(p.x[0]) + t * p.stride[0] + h * D, vec,
+                                p.angles + t * (p.rot >> 1), p.rot, p.interleaved);
+  }
+  return v;
+}
+
 // ---- short runs: a warp stores a whole run of one head ------------------------
 //
 // Lanes [0, 16) serve K and [16, 32) V; a side's lanes hold a row as 16-byte
 // vectors (D / 8 of them, 16 / (D / 8) rows at a time).
-template <int D, bool BF16>
+template <int D, bool BF16, bool ROT>
 __device__ __forceinline__ void store_run(const PagedStoreParams& p, int t, int h, int lane) {
   constexpr int VPR = D / 8, RPS = 16 / VPR;  // vectors of a row, rows a step
   const int slot = p.slots[t];
@@ -203,9 +215,9 @@ __device__ __forceinline__ void store_run(const PagedStoreParams& p, int t, int 
   float* scale = (side ? p.scale[1] : p.scale[0]) + static_cast<size_t>(page) * p.H + h;
   const float was = *scale;
   const uint4 zero = make_uint4(0, 0, 0, 0);
-  const uint4 first = sub < n ? *vec_ptr(p, side, t + sub, h, D, vec) : zero;
+  const uint4 first = sub < n ? load_vec<D, BF16, ROT>(p, side, t + sub, h, vec) : zero;
   uint32_t m2 = vec_max(first, 0);
-  for (int i = sub + RPS; i < n; i += RPS) m2 = vec_max(*vec_ptr(p, side, t + i, h, D, vec), m2);
+  for (int i = sub + RPS; i < n; i += RPS) m2 = vec_max(load_vec<D, BF16, ROT>(p, side, t + i, h, vec), m2);
   auto side_max = [](uint32_t x) {  // over the side's sixteen lanes
 #pragma unroll
     for (int o = 1; o < 16; o <<= 1) x = max(x, __shfl_xor_sync(0xffffffffu, x, o));
@@ -216,7 +228,7 @@ __device__ __forceinline__ void store_run(const PagedStoreParams& p, int t, int 
   if (__any_sync(0xffffffffu, odd)) {
     m2 = 0;
     for (int i = sub; i < n; i += RPS)
-      m2 = vec_max_finite<BF16>(*vec_ptr(p, side, t + i, h, D, vec), m2);
+      m2 = vec_max_finite<BF16>(load_vec<D, BF16, ROT>(p, side, t + i, h, vec), m2);
     mag = side_max(fold2(m2));
     if (odd && l == 0) set_err(p.err, KVQ_PAGED_ERR_NONFINITE);
   }
@@ -239,7 +251,7 @@ __device__ __forceinline__ void store_run(const PagedStoreParams& p, int t, int 
   if (sub < n) *reinterpret_cast<uint2*>(base + static_cast<size_t>(row0 + sub) * D) = codes8<BF16>(first, inv, plain);
   for (int i = sub + RPS; i < n; i += RPS)
     *reinterpret_cast<uint2*>(base + static_cast<size_t>(row0 + i) * D) =
-        codes8<BF16>(*vec_ptr(p, side, t + i, h, D, vec), inv, plain);
+        codes8<BF16>(load_vec<D, BF16, ROT>(p, side, t + i, h, vec), inv, plain);
   if (l == 0) *scale = exp2i(e);
 }
 
@@ -275,7 +287,7 @@ __host__ __device__ constexpr int chunk_threads() {
 constexpr int kSteps = 8;
 constexpr int kShortChunks = 8192;
 
-template <int D, bool BF16, int TEAM>
+template <int D, bool BF16, bool ROT, int TEAM>
 __global__ void __launch_bounds__(chunk_threads<TEAM>(), 1024 / chunk_threads<TEAM>())
     paged_store_kernel(const PagedStoreParams p) {
   constexpr int THREADS = chunk_threads<TEAM>(), TEAMS = THREADS / (2 * TEAM);
@@ -301,7 +313,7 @@ __global__ void __launch_bounds__(chunk_threads<TEAM>(), 1024 / chunk_threads<TE
   __syncthreads();
   const int count = s_count;
   if (count * 8 > p.chunk) {
-    for (int i = tid >> 5; i < count; i += THREADS / 32) store_run<D, BF16>(p, s_list[i], h, lane);
+    for (int i = tid >> 5; i < count; i += THREADS / 32) store_run<D, BF16, ROT>(p, s_list[i], h, lane);
     return;
   }
   // Threads of a run's two sides wait for one another (whole warps when a
@@ -355,7 +367,7 @@ __global__ void __launch_bounds__(chunk_threads<TEAM>(), 1024 / chunk_threads<TE
 #pragma unroll
     for (int s = 0; s < kSteps; ++s) {
       x[s] = make_uint4(0, 0, 0, 0);
-      if ((rows >> s) & 1) x[s] = __ldg(vec_ptr(p, side, t + s * RPS + sub, h, D, vec));
+      if ((rows >> s) & 1) x[s] = load_vec<D, BF16, ROT>(p, side, t + s * RPS + sub, h, vec);
     }
     const float was = good && row0 > 0 ? *scale : 0.f;
     uint32_t m2 = 0, both;
@@ -407,7 +419,7 @@ __global__ void __launch_bounds__(chunk_threads<TEAM>(), 1024 / chunk_threads<TE
   }
 }
 
-template <int D, bool BF16, int TEAM>
+template <int D, bool BF16, bool ROT, int TEAM>
 cudaError_t launch_team(PagedStoreParams p, cudaStream_t st) {
   constexpr int THREADS = chunk_threads<TEAM>();
   const int most = TEAM * 64 / D * (THREADS / (2 * TEAM));
@@ -421,20 +433,20 @@ cudaError_t launch_team(PagedStoreParams p, cudaStream_t st) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, paged_store_kernel<D, BF16, TEAM>, p);
+  return cudaLaunchKernelEx(&cfg, paged_store_kernel<D, BF16, ROT, TEAM>, p);
 }
 
-template <int D, bool BF16>
+template <int D, bool BF16, bool ROT>
 cudaError_t launch(const PagedStoreParams& p, cudaStream_t st) {
   switch ((D << p.lg_ps) / 64) {
     case 16:
-      if constexpr (D == 64) return launch_team<D, BF16, 16>(p, st);
+      if constexpr (D == 64) return launch_team<D, BF16, ROT, 16>(p, st);
       break;
-    case 32: return launch_team<D, BF16, 32>(p, st);
-    case 64: return launch_team<D, BF16, 64>(p, st);
-    case 128: return launch_team<D, BF16, 128>(p, st);
+    case 32: return launch_team<D, BF16, ROT, 32>(p, st);
+    case 64: return launch_team<D, BF16, ROT, 64>(p, st);
+    case 128: return launch_team<D, BF16, ROT, 128>(p, st);
     case 256:
-      if constexpr (D == 128) return launch_team<D, BF16, 256>(p, st);
+      if constexpr (D == 128) return launch_team<D, BF16, ROT, 256>(p, st);
       break;
   }
   return cudaErrorInvalidValue;
@@ -444,8 +456,15 @@ cudaError_t launch(const PagedStoreParams& p, cudaStream_t st) {
 
 cudaError_t launch_paged_store(const PagedStoreParams& p, int D, int dtype, cudaStream_t st) {
   const bool bf = dtype == KVQ_DTYPE_BF16;
-  if (D == 128) return bf ? launch<128, true>(p, st) : launch<128, false>(p, st);
-  if (D == 64) return bf ? launch<64, true>(p, st) : launch<64, false>(p, st);
+  const bool rot = p.rot > 0;
+  if (D == 128) {
+    if (rot) return bf ? launch<128, true, true>(p, st) : launch<128, false, true>(p, st);
+    return bf ? launch<128, true, false>(p, st) : launch<128, false, false>(p, st);
+  }
+  if (D == 64) {
+    if (rot) return bf ? launch<64, true, true>(p, st) : launch<64, false, true>(p, st);
+    return bf ? launch<64, true, false>(p, st) : launch<64, false, false>(p, st);
+  }
   return cudaErrorInvalidValue;
 }
 

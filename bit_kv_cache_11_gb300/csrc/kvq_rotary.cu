@@ -1,0 +1,180 @@
+// kvq_rotary.cu — rotary positions: frequencies (host), a step's angles, and
+// heads turned by them (include/kvq.h).
+#include <algorithm>
+#include <cmath>
+
+#include "kvq_rotary.cuh"
+
+namespace kvq {
+void count_launches(uint64_t n);
+
+namespace {
+
+constexpr int kThreads = 256;
+
+// ---- angles ---------------------------------------------------------------------
+//
+// position * turn modulo 2^64 is the exact part of a turn; the nearest quarter
+// comes off its top bits, the rest (at most an eighth of a turn) becomes an angle
+// within pi / 4, whose Taylor series to x^9 and x^10 leave 2^-29 and 2^-30.
+__device__ __forceinline__ float2 unit_of(uint64_t phase) {
+  const uint32_t quarter = static_cast<uint32_t>((phase + (1ull << 61)) >> 62);
+  // the 32 bits below the quarter's two, as a signed fraction of it
+  const float x = static_cast<float>(static_cast<int32_t>(phase >> 30)) * 3.65729521e-10f;  // 2 pi / 2^34
+  const float y = x * x;
+  const float s = fmaf(fmaf(fmaf(fmaf(2.7557319e-6f, y, -1.9841270e-4f), y, 8.3333333e-3f), y, -0.16666667f) * y, x, x);
+  const float c = fmaf(fmaf(fmaf(fmaf(fmaf(-2.7557319e-7f, y, 2.4801587e-5f), y, -1.3888889e-3f), y, 4.1666667e-2f), y,
+                            -0.5f), y, 1.0f);
+  const float a = quarter & 1 ? s : c, b = quarter & 1 ? c : s;
+  return make_float2(quarter == 1 || quarter == 2 ? -a : a, quarter & 2 ? -b : b);
+}
+
+__global__ void __launch_bounds__(kThreads) rotary_angles_kernel(const AnglesParams p) {
+  grid_dep_wait();
+  grid_dep_launch();
+  const long long n = static_cast<long long>(p.n_tokens) * p.half;
+  for (long long i = static_cast<long long>(blockIdx.x) * kThreads + threadIdx.x; i < n;
+       i += static_cast<long long>(gridDim.x) * kThreads) {
+    const int t = static_cast<int>(i / p.half), k = static_cast<int>(i - static_cast<long long>(t) * p.half);
+    const float2 u = unit_of(static_cast<uint64_t>(static_cast<int64_t>(p.positions[t])) *
+                             static_cast<uint64_t>(p.turns[k]));
+    p.angles[i] = make_float2(u.x * p.magnitude, u.y * p.magnitude);
+  }
+}
+
+// ---- rotate ---------------------------------------------------------------------
+
+template <bool BF16>
+__global__ void __launch_bounds__(kThreads) rotate_kernel(const RotateParams p) {
+  grid_dep_wait();
+  grid_dep_launch();
+  const long long per = static_cast<long long>(p.n_heads) * p.units;
+  const long long n = p.n_tokens * per;
+  for (long long i = static_cast<long long>(blockIdx.x) * kThreads + threadIdx.x; i < n;
+       i += static_cast<long long>(gridDim.x) * kThreads) {
+    const long long t = i / per;
+    const int r = static_cast<int>(i - t * per), h = r / p.units;
+    rotate_unit<BF16>(p, t, h, r - h * p.units);
+  }
+}
+
+template <typename P>
+cudaError_t launch(void (*fn)(P), const P& p, long long items, cudaStream_t st) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(std::min<long long>((items + kThreads - 1) / kThreads, 1 << 20)));
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, fn, p);
+}
+
+bool dev_ptr(const void* p, uintptr_t a) { return p != nullptr && (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+
+}  // namespace
+
+kvq_status check_rotary(const kvq_rotary* r, int head_dim, int n_tokens) {
+  if (r == nullptr || r->rotary_dim < 2 || r->rotary_dim % 2 != 0 || r->rotary_dim > head_dim ||
+      (r->interleaved != 0 && r->interleaved != 1))
+    return KVQ_ERR_INVALID_ARG;
+  return n_tokens == 0 || dev_ptr(r->angles, 16) ? KVQ_OK : KVQ_ERR_INVALID_ARG;
+}
+
+kvq_status rotate_params(RotateParams* p, const kvq_rotary* rotary, const void* x, int dtype, long long x_stride,
+                         void* out, long long out_stride, int n_tokens, int n_heads, int head_dim) {
+  if (head_dim < 1 || (dtype != KVQ_DTYPE_FP16 && dtype != KVQ_DTYPE_BF16)) return KVQ_ERR_INVALID_ARG;
+  const kvq_status s = check_rotary(rotary, head_dim, n_tokens);
+  if (s != KVQ_OK) return s;
+  if (head_dim % 8 != 0 || head_dim > 256) return KVQ_ERR_UNSUPPORTED;
+  const long long least = static_cast<long long>(n_heads) * head_dim;
+  if (n_tokens > 0 && (!dev_ptr(x, 16) || !dev_ptr(out, 16) || x_stride < least || out_stride < least ||
+                       x_stride % 8 != 0 || out_stride % 8 != 0 || (x == out && x_stride != out_stride)))
+    return KVQ_ERR_INVALID_ARG;
+  p->x = static_cast<const uint16_t*>(x);
+  p->out = static_cast<uint16_t*>(out);
+  p->x_stride = x_stride;
+  p->out_stride = out_stride;
+  p->angles = reinterpret_cast<const float2*>(rotary->angles);
+  p->n_tokens = n_tokens;
+  p->n_heads = n_heads;
+  p->D = head_dim;
+  p->rot = rotary->rotary_dim;
+  p->interleaved = rotary->interleaved;
+  p->units = rotate_units(head_dim, rotary->rotary_dim, rotary->interleaved);
+  return KVQ_OK;
+}
+
+cudaError_t launch_rotary_angles(const AnglesParams& p, cudaStream_t st) {
+  return launch(rotary_angles_kernel, p, static_cast<long long>(p.n_tokens) * p.half, st);
+}
+
+cudaError_t launch_rotate(const RotateParams& p, int dtype, cudaStream_t st) {
+  const long long items = static_cast<long long>(p.n_tokens) * p.n_heads * p.units;
+  return dtype == KVQ_DTYPE_BF16 ? launch(rotate_kernel<true>, p, items, st) : launch(rotate_kernel<false>, p, items, st);
+}
+
+}  // namespace kvq
+
+using namespace kvq;
+
+extern "C" {
+
+kvq_status kvq_rotary_turns(int64_t* turns, int rotary_dim, double base, double factor,
+                            double original_len, double low, double high) {
+  if (turns == nullptr || rotary_dim < 2 || rotary_dim % 2 != 0 || !std::isfinite(base) || base <= 1.0 ||
+      !std::isfinite(factor) || factor < 1.0 || !std::isfinite(original_len) || original_len < 0.0)
+    return KVQ_ERR_INVALID_ARG;
+  if (original_len > 0.0 && (!std::isfinite(low) || !std::isfinite(high) || low < 0.0 || high <= low))
+    return KVQ_ERR_INVALID_ARG;
+  if (rotary_dim > 256) return KVQ_ERR_UNSUPPORTED;
+  constexpr double two_pi = 6.283185307179586476925;
+  for (int i = 0; i < rotary_dim / 2; ++i) {
+    double f = std::pow(base, -2.0 * i / rotary_dim);
+    double keep = 0.0;
+    if (original_len > 0.0) keep = std::min(1.0, std::max(0.0, (original_len * f / two_pi - low) / (high - low)));
+    f = f * keep + f / factor * (1.0 - keep);
+    turns[i] = static_cast<int64_t>(std::llrint(f / two_pi * 0x1p64));  // f <= 1: below 2^62
+  }
+  return KVQ_OK;
+}
+
+kvq_status kvq_rotary_angles(const int* positions, int n_tokens, const int64_t* turns,
+                             int rotary_dim, float magnitude, float* angles, void* stream) {
+  if (n_tokens < 0 || rotary_dim < 2 || rotary_dim % 2 != 0 || !std::isfinite(magnitude)) return KVQ_ERR_INVALID_ARG;
+  if (rotary_dim > 256) return KVQ_ERR_UNSUPPORTED;
+  if (n_tokens == 0) return KVQ_OK;
+  if (!dev_ptr(positions, 4) || !dev_ptr(turns, 8) || !dev_ptr(angles, 16)) return KVQ_ERR_INVALID_ARG;
+  AnglesParams p;
+  p.positions = positions;
+  p.turns = turns;
+  p.angles = reinterpret_cast<float2*>(angles);
+  p.n_tokens = n_tokens;
+  p.half = rotary_dim / 2;
+  p.magnitude = magnitude;
+  if (launch_rotary_angles(p, static_cast<cudaStream_t>(stream)) != cudaSuccess) {
+    cudaGetLastError();
+    return KVQ_ERR_CUDA;
+  }
+  count_launches(1);
+  return KVQ_OK;
+}
+
+kvq_status kvq_rotate(const kvq_rotary* rotary, const void* x, int dtype, long long x_stride,
+                      void* out, long long out_stride, int n_tokens, int n_heads, int head_dim,
+                      void* stream) {
+  if (n_tokens < 0 || n_heads < 1) return KVQ_ERR_INVALID_ARG;
+  RotateParams p;
+  const kvq_status s = rotate_params(&p, rotary, x, dtype, x_stride, out, out_stride, n_tokens, n_heads, head_dim);
+  if (s != KVQ_OK || n_tokens == 0) return s;
+  if (launch_rotate(p, dtype, static_cast<cudaStream_t>(stream)) != cudaSuccess) {
+    cudaGetLastError();
+    return KVQ_ERR_CUDA;
+  }
+  count_launches(1);
+  return KVQ_OK;
+}
+
+}  // extern "C"

@@ -1,4 +1,4 @@
-// paged_bind.cpp — Python binding of the paged 8-bit cache's calls: checks the
+// paged_bind.cpp — Python binding of the paged caches' and the rotary calls: checks the
 // tensors, allocates what the caller left out and calls the C ABI (include/
 // kvq.h).  A call on a small batch takes a few microseconds on the GPU, less
 // than an interpreter needs to look at a dozen tensors, which is why these
@@ -19,6 +19,7 @@
 #include <mutex>
 #include <string>
 #include <tuple>
+#include <type_traits>
 #include <vector>
 
 #include "kvq.h"
@@ -127,6 +128,39 @@ struct Pool {
   }
 };
 
+struct Pool4 {
+  kvq_paged4_pool c;
+  Pool4(Place& place, PyObject* kc, PyObject* vc, PyObject* km, PyObject* vm) {
+    const char* call = place.call;
+    const at::Tensor &k = tensor(call, "k_codes", kc), &v = tensor(call, "v_codes", vc);
+    if (k.scalar_type() != at::kByte || v.scalar_type() != at::kByte || k.dim() != 4 ||
+        v.sizes() != k.sizes() || !k.is_contiguous() || !v.is_contiguous())
+      refuse(call, "k_codes and v_codes must be contiguous uint8 tensors "
+                   "[n_pages][n_kv_heads][page_size][head_dim / 2]");
+    const at::Tensor &mk = tensor(call, "k_meta", km), &mv = tensor(call, "v_meta", vm);
+    for (const at::Tensor* m : {&mk, &mv})
+      if (m->scalar_type() != at::kHalf || m->dim() != 5 || m->size(0) != k.size(0) ||
+          m->size(1) != k.size(1) || m->size(2) != k.size(2) || m->size(3) * 16 != k.size(3) ||
+          m->size(4) != 2 || !m->is_contiguous())
+        refuse(call, "k_meta and v_meta must be contiguous float16 tensors "
+                     "[n_pages][n_kv_heads][page_size][head_dim / 32][2]");
+    for (int i = 0; i < 4; ++i)
+      if (k.size(i) > kIntMax / 2) throw Refusal{KVQ_ERR_UNSUPPORTED, call};
+    c.k_codes = k.data_ptr();
+    c.v_codes = v.data_ptr();
+    c.k_meta = mk.data_ptr();
+    c.v_meta = mv.data_ptr();
+    c.n_pages = static_cast<int>(k.size(0));
+    c.n_kv_heads = static_cast<int>(k.size(1));
+    c.page_size = static_cast<int>(k.size(2));
+    c.head_dim = static_cast<int>(2 * k.size(3));
+    place.add("k_codes", k);
+    place.add("v_codes", v);
+    place.add("k_meta", mk);
+    place.add("v_meta", mv);
+  }
+};
+
 int dtype_of(const char* call, const char* name, const at::Tensor& x) {
   if (x.scalar_type() == at::kHalf) return KVQ_DTYPE_FP16;
   if (x.scalar_type() == at::kBFloat16) return KVQ_DTYPE_BF16;
@@ -189,9 +223,62 @@ at::Tensor empty_on(cudaStream_t st, at::IntArrayRef sizes, at::ScalarType t, in
   return x;
 }
 
+// angles: fp32 [tokens][rotary_dim / 2][2].
+const at::Tensor& angles_of(const char* call, PyObject* o, int64_t tokens, kvq_rotary* r, bool interleaved) {
+  const at::Tensor& x = tensor(call, "angles", o);
+  if (x.scalar_type() != at::kFloat || x.dim() != 3 || x.size(0) != tokens || x.size(2) != 2 ||
+      x.size(1) > 1 << 20 || !x.is_contiguous())
+    refuse(call, "angles must be a contiguous float32 tensor [" + std::to_string(tokens) + "][rotary_dim / 2][2]");
+  r->angles = static_cast<const float*>(x.data_ptr());
+  r->rotary_dim = static_cast<int>(2 * x.size(1));
+  r->interleaved = interleaved ? 1 : 0;
+  return x;
+}
+bool truth(const char* call, const char* name, PyObject* o) {
+  const int v = PyObject_IsTrue(o);
+  if (v < 0) {
+    PyErr_Clear();
+    refuse(call, std::string(name) + " must be true or false");
+  }
+  return v != 0;
+}
+
+// The heads that a call turns: x [tokens][heads][dim], and out of the same type
+// and shape (allocated at finish() when the caller gave none).
+struct Turned {
+  const at::Tensor* x = nullptr;
+  at::Tensor out;
+  long long xs = 0, os = 0;
+  int64_t heads = 0, dim = 0;
+  Turned() = default;
+  Turned(const char* call, const char* xn, PyObject* xo, const char* on, PyObject* oo) {
+    x = &tensor(call, xn, xo);
+    dtype_of(call, xn, *x);
+    if (x->dim() != 3) refuse(call, std::string(xn) + " must be [tokens][heads][head_dim]");
+    heads = x->size(1);
+    dim = x->size(2);
+    if (heads > kIntMax || dim > kIntMax) throw Refusal{KVQ_ERR_UNSUPPORTED, call};
+    xs = rows(call, xn, *x, heads, dim);
+    os = heads * dim;
+    if (oo != Py_None) {
+      out = tensor(call, on, oo);
+      if (out.scalar_type() != x->scalar_type() || out.sizes() != x->sizes())
+        refuse(call, std::string(on) + " must have " + xn + "'s type and shape");
+      os = rows(call, on, out, heads, dim);
+    }
+  }
+  void add(Place& place, const char* xn, const char* on) const {
+    place.add(xn, *x);
+    if (out.defined()) place.add(on, out);
+  }
+  void finish(cudaStream_t st, int index) {
+    if (!out.defined()) out = empty_on(st, x->sizes(), x->scalar_type(), index);
+  }
+};
+
 // ---- workspaces ---------------------------------------------------------------
 //
-// Calls on one stream run one after the other and share a workspace; the calls
+// Calls on one stream, over either kind of pages, run one after the other and share a workspace; the calls
 // that a stream captures into one graph share another one, out of the
 // capture's memory, whose counters the graph clears before their first use.
 // So two graphs, or a graph and eager calls, never share.  A graph's workspace
@@ -241,8 +328,7 @@ bool keep_with_graph(cudaGraph_t graph, const at::Tensor& mem) {
   return false;
 }
 
-void* workspace(const char* call, const kvq_paged_pool& pool, int index, cudaStream_t st,
-                size_t* bytes) {
+void* workspace(const char* call, int head_dim, int index, cudaStream_t st, size_t bytes) {
   cudaStreamCaptureStatus status = cudaStreamCaptureStatusNone;
   unsigned long long id = 0;
   cudaGraph_t graph = nullptr;
@@ -251,15 +337,14 @@ void* workspace(const char* call, const kvq_paged_pool& pool, int index, cudaStr
     throw Refusal{KVQ_ERR_CUDA, call};
   }
   const bool captured = status == cudaStreamCaptureStatusActive;
-  check(kvq_paged_workspace_bytes(&pool, bytes), call);
   free_gone();
   std::lock_guard<std::mutex> lock(g_mu);
-  Workspace& w = workspaces()[WorkKey(index, st, pool.head_dim, captured)];
+  Workspace& w = workspaces()[WorkKey(index, st, head_dim, captured)];
   if (w.at == nullptr || (captured && w.capture != id)) {
     w.at = nullptr;
     const c10::cuda::CUDAStreamGuard guard(
         c10::cuda::getStreamFromExternal(st, static_cast<c10::DeviceIndex>(index)));
-    at::Tensor mem = empty({static_cast<int64_t>(*bytes)}, at::kByte, index);
+    at::Tensor mem = empty({static_cast<int64_t>(bytes)}, at::kByte, index);
     if (cudaMemsetAsync(mem.data_ptr(), 0, 1024, st) != cudaSuccess ||
         (captured && !keep_with_graph(graph, mem))) {
       cudaGetLastError();
@@ -271,6 +356,18 @@ void* workspace(const char* call, const kvq_paged_pool& pool, int index, cudaStr
   }
   return w.at;
 }
+
+int workspace_bytes(const kvq_paged_pool& p, size_t* n) { return kvq_paged_workspace_bytes(&p, n); }
+int workspace_bytes(const kvq_paged4_pool& p, size_t* n) { return kvq_paged4_workspace_bytes(&p, n); }
+template <typename... A>
+int attend(const kvq_paged_pool* p, A... a) { return kvq_paged_attention(p, a...); }
+template <typename... A>
+int attend(const kvq_paged4_pool* p, A... a) { return kvq_paged4_attention(p, a...); }
+
+template <typename... A>
+int store_turned(const kvq_paged_pool* p, A... a) { return kvq_paged_append(p, a...); }
+template <typename... A>
+int store_turned(const kvq_paged4_pool* p, A... a) { return kvq_paged4_append(p, a...); }
 
 // ---- the calls ------------------------------------------------------------------
 
@@ -298,9 +395,9 @@ bool count_is(const char* call, Py_ssize_t n, Py_ssize_t want) {
 }
 
 // (ctx_len, new_len, block_table, free_pages, n_free, page_size, n_tokens,
-//  cu_new, seq_len, slots, n_left, error, stream)
+//  cu_new, seq_len, slots, n_left, error, stream, positions)
 PyObject* plan(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  if (!count_is("plan", n, 13)) return nullptr;
+  if (!count_is("plan", n, 14)) return nullptr;
   return guarded([&]() -> PyObject* {
     const char* call = "kvq_paged_plan";
     Place place{call};
@@ -322,6 +419,7 @@ PyObject* plan(PyObject*, PyObject* const* a, Py_ssize_t n) {
       if (a[7 + i] == Py_None) continue;
       out[i] = ints(call, names[i], a[7 + i], sizes[i]);
     }
+    const at::Tensor* positions = a[13] == Py_None ? nullptr : &ints(call, "positions", a[13], tokens);
     place.add("ctx_len", ctx);
     place.add("new_len", nw);
     place.add("block_table", tab);
@@ -329,15 +427,16 @@ PyObject* plan(PyObject*, PyObject* const* a, Py_ssize_t n) {
     place.add("n_free", nf);
     for (int i = 0; i < 4; ++i)
       if (out[i].defined()) place.add(names[i], out[i]);
+    if (positions) place.add("positions", *positions);
     int* err = error_ptr(place, a[11]);
     const c10::cuda::CUDAGuard guard(static_cast<c10::DeviceIndex>(place.index));
     const cudaStream_t st = stream_of(call, a[12], place.index);
     for (int i = 0; i < 4; ++i)
       if (!out[i].defined()) out[i] = empty_on(st, {sizes[i]}, at::kInt, place.index);
-    check(kvq_paged_plan(int_ptr(ctx), int_ptr(nw), static_cast<int>(batch), int_ptr(tab),
+    check(kvq_paged_plan_positions(int_ptr(ctx), int_ptr(nw), static_cast<int>(batch), int_ptr(tab),
                          static_cast<int>(tab.size(1)), int_ptr(fp), static_cast<int>(fp.numel()),
                          int_ptr(nf), ps, static_cast<int>(tokens), int_ptr(out[0]),
-                         int_ptr(out[1]), int_ptr(out[2]), int_ptr(out[3]), err, st),
+                         int_ptr(out[1]), int_ptr(out[2]), positions ? int_ptr(*positions) : nullptr, int_ptr(out[3]), err, st),
           call);
     for (int i = 0; i < 4; ++i)
       ret[i] = a[7 + i] != Py_None ? Py_NewRef(a[7 + i]) : THPVariable_Wrap(std::move(out[i]));
@@ -380,11 +479,14 @@ PyObject* store(PyObject*, PyObject* const* a, Py_ssize_t n) {
 }
 
 // (q, k_pages, v_pages, k_scale, v_scale, block_table, cu_new, seq_len,
-//  max_new, softmax_scale, window, out, workspace, error, stream)
+//  max_new, softmax_scale, window, out, workspace, error, stream); `P`: Pool, or
+// Pool4 with codes and metadata in the pages' and scales' places
+template <typename P>
 PyObject* attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  if (!count_is("attention", n, 15)) return nullptr;
+  constexpr bool four = std::is_same<P, Pool4>::value;
+  if (!count_is(four ? "attention4" : "attention", n, 15)) return nullptr;
   return guarded([&]() -> PyObject* {
-    const char* call = "kvq_paged_attention";
+    const char* call = four ? "kvq_paged4_attention" : "kvq_paged_attention";
     Place place{call};
     const at::Tensor& q = tensor(call, "q", a[0]);
     const int dt = dtype_of(call, "q", q);
@@ -405,8 +507,8 @@ PyObject* attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
       }
     }
     const int window = static_cast<int>(number(call, "window", a[10], 0, kIntMax));
-    const at::Tensor& kp = tensor(call, "k_pages", a[1]);
-    const long long qs = rows(call, "q", q, heads, kp.dim() == 4 ? kp.size(3) : dim);
+    const at::Tensor& kp = tensor(call, four ? "k_codes" : "k_pages", a[1]);
+    const long long qs = rows(call, "q", q, heads, kp.dim() == 4 ? kp.size(3) * (four ? 2 : 1) : dim);
     at::Tensor out;
     long long os = heads * dim;
     if (a[11] != Py_None) {
@@ -417,7 +519,7 @@ PyObject* attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
     }
     if (batch > kIntMax || tab.size(1) > kIntMax || heads > kIntMax)
       throw Refusal{KVQ_ERR_UNSUPPORTED, call};
-    const Pool pool(place, a[1], a[2], a[3], a[4]);
+    const P pool(place, a[1], a[2], a[3], a[4]);
     place.add("q", q);
     place.add("block_table", tab);
     place.add("cu_new", cu);
@@ -430,7 +532,8 @@ PyObject* attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
     void* ws = nullptr;
     size_t bytes = 0;
     if (a[12] == Py_None) {
-      ws = workspace(call, pool.c, place.index, st, &bytes);
+      check(workspace_bytes(pool.c, &bytes), call);
+      ws = workspace(call, pool.c.head_dim, place.index, st, bytes);
     } else {
       const at::Tensor& w = tensor(call, "workspace", a[12]);
       if (w.scalar_type() != at::kByte || !w.is_contiguous())
@@ -439,13 +542,175 @@ PyObject* attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
       ws = w.data_ptr();
       bytes = static_cast<size_t>(w.numel());
     }
-    check(kvq_paged_attention(&pool.c, q.data_ptr(), dt, qs, out.data_ptr(), os,
-                              static_cast<int>(tokens), static_cast<int>(heads), int_ptr(tab),
-                              static_cast<int>(tab.size(1)), int_ptr(cu), int_ptr(seq),
-                              static_cast<int>(batch), max_new, static_cast<float>(scale), window,
-                              ws, bytes, err, st),
+    check(attend(&pool.c, q.data_ptr(), dt, qs, out.data_ptr(), os, static_cast<int>(tokens),
+                 static_cast<int>(heads), int_ptr(tab), static_cast<int>(tab.size(1)), int_ptr(cu),
+                 int_ptr(seq), static_cast<int>(batch), max_new, static_cast<float>(scale), window, ws,
+                 bytes, err, st),
           call);
     return a[11] != Py_None ? Py_NewRef(a[11]) : THPVariable_Wrap(std::move(out));
+  });
+}
+
+// k and v of a store: types, shapes and strides.
+struct Tokens {
+  const at::Tensor *k, *v, *slots;
+  int dtype;
+  long long ks = 0, vs = 0;
+  Tokens(const char* call, PyObject* ko, PyObject* vo, PyObject* so, const at::Tensor& pages, int64_t per) {
+    k = &tensor(call, "k", ko);
+    v = &tensor(call, "v", vo);
+    dtype = dtype_of(call, "k", *k);
+    if (v->scalar_type() != k->scalar_type() || v->sizes() != k->sizes())
+      refuse(call, "k and v must have the same type and shape");
+    if (k->dim() != 3) refuse(call, "k must be [tokens][n_kv_heads][head_dim]");
+    slots = &ints(call, "slots", so, k->size(0));
+    if (pages.dim() == 4) {
+      ks = rows(call, "k", *k, pages.size(1), pages.size(3) * per);
+      vs = rows(call, "v", *v, pages.size(1), pages.size(3) * per);
+    }
+  }
+  void add(Place& place) const {
+    place.add("k", *k);
+    place.add("v", *v);
+    place.add("slots", *slots);
+  }
+};
+
+// (k, v, slots, k_pages, v_pages, k_scale, v_scale, angles, interleaved, q, q_out,
+//  error, stream); `P`: Pool, or Pool4 with codes and metadata in the pages' and
+// scales' places
+template <typename P>
+PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  constexpr bool four = std::is_same<P, Pool4>::value;
+  if (!count_is(four ? "append4" : "append", n, 13)) return nullptr;
+  return guarded([&]() -> PyObject* {
+    const char* call = four ? "kvq_paged4_append" : "kvq_paged_append";
+    const Tokens t(call, a[0], a[1], a[2], tensor(call, four ? "k_codes" : "k_pages", a[3]), four ? 2 : 1);
+    const int64_t tokens = t.k->size(0);
+    kvq_rotary rotary = {};
+    Place place{call};
+    const bool turns = a[7] != Py_None, queries = a[9] != Py_None;
+    if (!turns && !four) refuse(call, "angles must be a tensor");
+    if (!turns && queries) refuse(call, "angles must be given with q");
+    if (!queries && a[10] != Py_None) refuse(call, "q_out must be given with q");
+    const at::Tensor* angles = nullptr;
+    if (turns) angles = &angles_of(call, a[7], tokens, &rotary, truth(call, "interleaved", a[8]));
+    Turned q;
+    if (queries) {
+      q = Turned(call, "q", a[9], "q_out", a[10]);
+      if (q.x->scalar_type() != t.k->scalar_type() || q.x->size(0) != tokens || q.dim != t.k->size(2))
+        refuse(call, "q must have k's type, tokens and head_dim");
+    }
+    const P pool(place, a[3], a[4], a[5], a[6]);
+    t.add(place);
+    if (turns) place.add("angles", *angles);
+    if (queries) q.add(place, "q", "q_out");
+    int* err = error_ptr(place, a[11]);
+    const c10::cuda::CUDAGuard guard(static_cast<c10::DeviceIndex>(place.index));
+    const cudaStream_t st = stream_of(call, a[12], place.index);
+    if (queries) q.finish(st, place.index);
+    check(store_turned(&pool.c, turns ? &rotary : nullptr, t.k->data_ptr(), t.v->data_ptr(), t.dtype, t.ks,
+                       t.vs, int_ptr(*t.slots), static_cast<int>(tokens),
+                       queries ? q.x->data_ptr() : nullptr, q.xs, queries ? q.out.data_ptr() : nullptr,
+                       q.os, static_cast<int>(q.heads), err, st),
+          call);
+    if (!queries) Py_RETURN_NONE;
+    return a[10] != Py_None ? Py_NewRef(a[10]) : THPVariable_Wrap(std::move(q.out));
+  });
+}
+
+// (slots, k_codes, v_codes, k_meta, v_meta, k, v, error, stream)
+PyObject* read4(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  if (!count_is("read4", n, 9)) return nullptr;
+  return guarded([&]() -> PyObject* {
+    const char* call = "kvq_paged4_read";
+    Place place{call};
+    const at::Tensor& slots = ints(call, "slots", a[0], 0);
+    const Pool4 pool(place, a[1], a[2], a[3], a[4]);
+    const int64_t tokens = slots.numel();
+    if (tokens > kIntMax) throw Refusal{KVQ_ERR_UNSUPPORTED, call};
+    const int64_t sizes[3] = {tokens, pool.c.n_kv_heads, pool.c.head_dim};
+    at::Tensor out[2];
+    const char* names[2] = {"k", "v"};
+    for (int i = 0; i < 2; ++i) {
+      if (a[5 + i] == Py_None) continue;
+      out[i] = tensor(call, names[i], a[5 + i]);
+      if (out[i].scalar_type() != at::kHalf || out[i].sizes() != at::IntArrayRef(sizes, 3) ||
+          !out[i].is_contiguous())
+        refuse(call, std::string(names[i]) + " must be a contiguous float16 tensor [slots][n_kv_heads][head_dim]");
+      place.add(names[i], out[i]);
+    }
+    place.add("slots", slots);
+    int* err = error_ptr(place, a[7]);
+    const c10::cuda::CUDAGuard guard(static_cast<c10::DeviceIndex>(place.index));
+    const cudaStream_t st = stream_of(call, a[8], place.index);
+    for (int i = 0; i < 2; ++i)
+      if (!out[i].defined()) out[i] = empty_on(st, at::IntArrayRef(sizes, 3), at::kHalf, place.index);
+    check(kvq_paged4_read(&pool.c, int_ptr(slots), static_cast<int>(tokens), out[0].data_ptr(),
+                          out[1].data_ptr(), err, st),
+          call);
+    PyObject* t = PyTuple_New(2);
+    for (int i = 0; i < 2; ++i)
+      PyTuple_SET_ITEM(t, i, a[5 + i] != Py_None ? Py_NewRef(a[5 + i]) : THPVariable_Wrap(std::move(out[i])));
+    return t;
+  });
+}
+
+// (positions, turns, magnitude, out, stream)
+PyObject* angles(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  if (!count_is("angles", n, 5)) return nullptr;
+  return guarded([&]() -> PyObject* {
+    const char* call = "kvq_rotary_angles";
+    Place place{call};
+    const at::Tensor& pos = ints(call, "positions", a[0], 0);
+    const at::Tensor& turns = tensor(call, "turns", a[1]);
+    if (turns.scalar_type() != at::kLong || turns.dim() != 1 || !turns.is_contiguous() || turns.numel() < 1)
+      refuse(call, "turns must be a contiguous int64 tensor [rotary_dim / 2]");
+    const double magnitude = PyFloat_AsDouble(a[2]);
+    if (PyErr_Occurred()) {
+      PyErr_Clear();
+      refuse(call, "magnitude must be a number");
+    }
+    if (pos.numel() > kIntMax || turns.numel() > kIntMax / 2) throw Refusal{KVQ_ERR_UNSUPPORTED, call};
+    const int64_t sizes[3] = {pos.numel(), turns.numel(), 2};
+    at::Tensor out;
+    if (a[3] != Py_None) {
+      out = tensor(call, "out", a[3]);
+      if (out.scalar_type() != at::kFloat || out.sizes() != at::IntArrayRef(sizes, 3) || !out.is_contiguous())
+        refuse(call, "out must be a contiguous float32 tensor [tokens][rotary_dim / 2][2]");
+    }
+    place.add("positions", pos);
+    place.add("turns", turns);
+    if (out.defined()) place.add("out", out);
+    const c10::cuda::CUDAGuard guard(static_cast<c10::DeviceIndex>(place.index));
+    const cudaStream_t st = stream_of(call, a[4], place.index);
+    if (!out.defined()) out = empty_on(st, at::IntArrayRef(sizes, 3), at::kFloat, place.index);
+    check(kvq_rotary_angles(int_ptr(pos), static_cast<int>(pos.numel()),
+                            static_cast<const int64_t*>(turns.data_ptr()), static_cast<int>(2 * turns.numel()),
+                            static_cast<float>(magnitude), static_cast<float*>(out.data_ptr()), st),
+          call);
+    return a[3] != Py_None ? Py_NewRef(a[3]) : THPVariable_Wrap(std::move(out));
+  });
+}
+
+// (x, angles, interleaved, out, stream)
+PyObject* rotate(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  if (!count_is("rotate", n, 5)) return nullptr;
+  return guarded([&]() -> PyObject* {
+    const char* call = "kvq_rotate";
+    Place place{call};
+    Turned x(call, "x", a[0], "out", a[3]);
+    kvq_rotary rotary = {};
+    const at::Tensor& ang = angles_of(call, a[1], x.x->size(0), &rotary, truth(call, "interleaved", a[2]));
+    x.add(place, "x", "out");
+    place.add("angles", ang);
+    const c10::cuda::CUDAGuard guard(static_cast<c10::DeviceIndex>(place.index));
+    const cudaStream_t st = stream_of(call, a[4], place.index);
+    x.finish(st, place.index);
+    check(kvq_rotate(&rotary, x.x->data_ptr(), dtype_of(call, "x", *x.x), x.xs, x.out.data_ptr(), x.os,
+                     static_cast<int>(x.x->size(0)), static_cast<int>(x.heads), static_cast<int>(x.dim), st),
+          call);
+    return a[3] != Py_None ? Py_NewRef(a[3]) : THPVariable_Wrap(std::move(x.out));
   });
 }
 
@@ -455,13 +720,21 @@ PyObject* set_error_class(PyObject*, PyObject* c) {
   Py_RETURN_NONE;
 }
 
-PyMethodDef g_methods[] = {
-    {"plan", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)(void)>(plan)), METH_FASTCALL, nullptr},
-    {"store", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)(void)>(store)), METH_FASTCALL, nullptr},
-    {"attention", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)(void)>(attention)),
-     METH_FASTCALL, nullptr},
-    {"set_error_class", set_error_class, METH_O, nullptr},
-    {nullptr, nullptr, 0, nullptr}};
+using Fast = PyObject* (*)(PyObject*, PyObject* const*, Py_ssize_t);
+PyMethodDef fast(const char* name, Fast f) {
+  return {name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)(void)>(f)), METH_FASTCALL, nullptr};
+}
+PyMethodDef g_methods[] = {fast("plan", plan),
+                           fast("store", store),
+                           fast("attention", attention<Pool>),
+                           fast("append", append<Pool>),
+                           fast("append4", append<Pool4>),
+                           fast("read4", read4),
+                           fast("attention4", attention<Pool4>),
+                           fast("angles", angles),
+                           fast("rotate", rotate),
+                           {"set_error_class", set_error_class, METH_O, nullptr},
+                           {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_paged_bind", nullptr, -1, g_methods,
                         nullptr, nullptr, nullptr, nullptr};

@@ -69,12 +69,27 @@ class kvq_paged_pool(ctypes.Structure):
                 ("page_size", ctypes.c_int), ("head_dim", ctypes.c_int)]
 
 
+class kvq_paged4_pool(ctypes.Structure):
+    _fields_ = [("k_codes", ctypes.c_void_p), ("v_codes", ctypes.c_void_p),
+                ("k_meta", ctypes.c_void_p), ("v_meta", ctypes.c_void_p),
+                ("n_pages", ctypes.c_int), ("n_kv_heads", ctypes.c_int),
+                ("page_size", ctypes.c_int), ("head_dim", ctypes.c_int)]
+
+
+class kvq_rotary(ctypes.Structure):
+    _fields_ = [("angles", ctypes.c_void_p), ("rotary_dim", ctypes.c_int),
+                ("interleaved", ctypes.c_int)]
+
+
 _P = ctypes.c_void_p
 _I = ctypes.c_int
 _L = ctypes.c_longlong
 _S = ctypes.c_int  # kvq_status
 _CFG = ctypes.POINTER(kvq_config)
 _POOL = ctypes.POINTER(kvq_paged_pool)
+_POOL4 = ctypes.POINTER(kvq_paged4_pool)
+_ROT = ctypes.POINTER(kvq_rotary)
+_D = ctypes.c_double
 
 _sigs = {
     "kvq_config_check": (_S, [_CFG]),
@@ -105,6 +120,17 @@ _sigs = {
     "kvq_paged_workspace_bytes": (_S, [_POOL, ctypes.POINTER(ctypes.c_size_t)]),
     "kvq_paged_attention": (_S, [_POOL, _P, _I, _L, _P, _L, _I, _I, _P, _I, _P, _P, _I, _I,
                                  ctypes.c_float, _I, _P, ctypes.c_size_t, _P, _P]),
+    "kvq_paged_plan_positions": (_S, [_P, _P, _I, _P, _I, _P, _I, _P, _I, _I, _P, _P, _P, _P, _P, _P, _P]),
+    "kvq_paged_append": (_S, [_POOL, _ROT, _P, _P, _I, _L, _L, _P, _I, _P, _L, _P, _L, _I, _P, _P]),
+    "kvq_rotary_turns": (_S, [ctypes.POINTER(ctypes.c_int64), _I, _D, _D, _D, _D, _D]),
+    "kvq_rotary_angles": (_S, [_P, _I, _P, _I, ctypes.c_float, _P, _P]),
+    "kvq_rotate": (_S, [_ROT, _P, _I, _L, _P, _L, _I, _I, _I, _P]),
+    "kvq_paged4_pool_check": (_S, [_POOL4]),
+    "kvq_paged4_append": (_S, [_POOL4, _ROT, _P, _P, _I, _L, _L, _P, _I, _P, _L, _P, _L, _I, _P, _P]),
+    "kvq_paged4_read": (_S, [_POOL4, _P, _I, _P, _P, _P, _P]),
+    "kvq_paged4_workspace_bytes": (_S, [_POOL4, ctypes.POINTER(ctypes.c_size_t)]),
+    "kvq_paged4_attention": (_S, [_POOL4, _P, _I, _L, _P, _L, _I, _I, _P, _I, _P, _P, _I, _I,
+                                  ctypes.c_float, _I, _P, ctypes.c_size_t, _P, _P]),
 }
 for _name, (_res, _args) in _sigs.items():
     _fn = getattr(_lib, _name)
@@ -281,16 +307,22 @@ def kvq_debug_set_paged_wait_limit(limit: int) -> None:
     _check(_lib.kvq_debug_set_paged_wait_limit(limit), "kvq_debug_set_paged_wait_limit")
 
 
-# ---- the paged 8-bit cache ----------------------------------------------------
+# ---- the paged caches and the rotary positions ----------------------------------
 
 def __getattr__(name):
-    """kvq_paged_plan, kvq_paged_store, kvq_paged_attention and PagedCache live
-    in paged.py, which needs torch; it is imported at their first use."""
-    if name.startswith("kvq_paged_") or name == "PagedCache":
-        from . import paged
-        if hasattr(paged, name):
-            globals()[name] = getattr(paged, name)
-            return globals()[name]
+    """The paged caches' and the rotary calls live in paged.py, paged4.py and
+    rotary.py, which need torch; they are imported at their first use."""
+    if name.startswith(("kvq_paged4_", "PagedCache4")):
+        from . import paged4 as home
+    elif name.startswith("kvq_paged_") or name == "PagedCache":
+        from . import paged as home
+    elif name.startswith(("kvq_rotary_", "kvq_rotate")):
+        from . import rotary as home
+    else:
+        home = None
+    if hasattr(home, name):
+        globals()[name] = getattr(home, name)
+        return globals()[name]
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
 
 

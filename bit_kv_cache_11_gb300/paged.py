@@ -30,6 +30,7 @@ _paged_bind.set_error_class(KvqError)
 _plan = _paged_bind.plan
 _store = _paged_bind.store
 _attention = _paged_bind.attention
+_append = _paged_bind.append
 
 
 def kvq_paged_pool_check(n_pages: int, n_kv_heads: int, page_size: int, head_dim: int) -> int:
@@ -52,7 +53,7 @@ def kvq_paged_workspace_bytes(n_pages: int, n_kv_heads: int, page_size: int,
 
 def kvq_paged_plan(ctx_len, new_len, block_table, free_pages, n_free, page_size: int,
                    n_tokens: int, cu_new=None, seq_len=None, slots=None, n_left=None, error=None,
-                   stream=None):
+                   stream=None, positions=None):
     """Block tables and slots of a serving step.
 
     ctx_len, new_len: int32 [batch], cached and new tokens of each request;
@@ -61,9 +62,11 @@ def kvq_paged_plan(ctx_len, new_len, block_table, free_pages, n_free, page_size:
     [batch + 1], seq_len [batch], slots [n_tokens], n_left [1]); the stack's
     new height is n_left[0].  A request that the stack cannot serve keeps
     seq_len = ctx_len and gets slots -1: its rows of the attention's output
-    mean nothing, and its step can be made again when pages are free."""
+    mean nothing, and its step can be made again when pages are free.
+    `positions`, an int32 tensor [n_tokens], gets every new token's position
+    (0 behind the last one)."""
     return _plan(ctx_len, new_len, block_table, free_pages, n_free, page_size, n_tokens, cu_new,
-                 seq_len, slots, n_left, error, stream)
+                 seq_len, slots, n_left, error, stream, positions)
 
 
 def kvq_paged_store(k, v, slots, k_pages, v_pages, k_scale, v_scale, error=None,
@@ -72,6 +75,17 @@ def kvq_paged_store(k, v, slots, k_pages, v_pages, k_scale, v_scale, error=None,
     any token stride that is a multiple of 8) at their slots (int32 [tokens],
     negative: nowhere)."""
     _store(k, v, slots, k_pages, v_pages, k_scale, v_scale, error, stream)
+
+
+def kvq_paged_append(k, v, slots, k_pages, v_pages, k_scale, v_scale, angles, interleaved=False,
+                     q=None, q_out=None, error=None, stream=None):
+    """kvq_paged_store with the keys turned on the way by their tokens' angles
+    (kvq_rotary_angles: fp32 [tokens][rotary_dim / 2][2]); the step's queries q
+    [tokens][n_q_heads][head_dim], where given, are turned too.  Returns them
+    (q_out, which may be q itself, or a new tensor), or None.  The same bits as
+    kvq_rotate of k and q followed by kvq_paged_store."""
+    return _append(k, v, slots, k_pages, v_pages, k_scale, v_scale, angles, interleaved, q, q_out,
+                   error, stream)
 
 
 def kvq_paged_attention(q, k_pages, v_pages, k_scale, v_scale, block_table, cu_new, seq_len,
@@ -109,38 +123,52 @@ class PagedCache:
     stack that ran out, a non-finite key or value)."""
 
     def __init__(self, n_pages, page_size, n_q_heads, n_kv_heads, head_dim, device="cuda"):
-        kvq._check(kvq_paged_pool_check(n_pages, n_kv_heads, page_size, head_dim),
-                   "kvq_paged_pool_check")
+        self._make_pool(n_pages, n_kv_heads, page_size, head_dim, device)
         if n_q_heads < 1 or n_q_heads % n_kv_heads:
             raise KvqError(KVQ_ERR_INVALID_ARG,
-                           "PagedCache: n_q_heads must be a multiple of n_kv_heads")
+                           f"{type(self).__name__}: n_q_heads must be a multiple of n_kv_heads")
         self.n_q_heads = int(n_q_heads)
         self.page_size = int(page_size)
+        self.error = torch.zeros(1, dtype=torch.int32, device=device)
+
+    def _make_pool(self, n_pages, n_kv_heads, page_size, head_dim, device):
+        kvq._check(kvq_paged_pool_check(n_pages, n_kv_heads, page_size, head_dim),
+                   "kvq_paged_pool_check")
         shape = (n_pages, n_kv_heads, page_size, head_dim)
         zeros = lambda s, t: torch.zeros(s, dtype=t, device=device)  # noqa: E731
         self.k_pages = zeros(shape, torch.uint8).view(torch.float8_e4m3fn)
         self.v_pages = zeros(shape, torch.uint8).view(torch.float8_e4m3fn)
         self.k_scale = zeros(shape[:2], torch.float32).fill_(2.0 ** -15)
         self.v_scale = zeros(shape[:2], torch.float32).fill_(2.0 ** -15)
-        self.error = zeros(1, torch.int32)
 
-    def plan(self, ctx_len, new_len, block_table, free_pages, n_free, n_tokens, stream=None):
+    def _pool(self):
+        return self.k_pages, self.v_pages, self.k_scale, self.v_scale
+
+    _store_call = staticmethod(kvq_paged_store)
+    _append_call = staticmethod(kvq_paged_append)
+    _attention_call = staticmethod(kvq_paged_attention)
+
+    def plan(self, ctx_len, new_len, block_table, free_pages, n_free, n_tokens, stream=None,
+             positions=None):
         return kvq_paged_plan(ctx_len, new_len, block_table, free_pages, n_free, self.page_size,
-                              n_tokens, error=self.error, stream=stream)
+                              n_tokens, error=self.error, stream=stream, positions=positions)
 
     def store(self, k, v, slots, stream=None):
-        kvq_paged_store(k, v, slots, self.k_pages, self.v_pages, self.k_scale, self.v_scale,
-                        error=self.error, stream=stream)
+        self._store_call(k, v, slots, *self._pool(), error=self.error, stream=stream)
+
+    def append(self, k, v, slots, angles, interleaved=False, q=None, q_out=None, stream=None):
+        """store with the keys, and the queries q where given, turned by `angles`."""
+        return self._append_call(k, v, slots, *self._pool(), angles, interleaved=interleaved, q=q,
+                                 q_out=q_out, error=self.error, stream=stream)
 
     def attention(self, q, block_table, cu_new, seq_len, max_new=1, softmax_scale=None, window=0,
                   out=None, stream=None):
         if q.dim() == 3 and q.shape[1] != self.n_q_heads:
             raise KvqError(KVQ_ERR_INVALID_ARG,
-                           f"PagedCache.attention: q must have {self.n_q_heads} heads")
-        return kvq_paged_attention(q, self.k_pages, self.v_pages, self.k_scale, self.v_scale,
-                                   block_table, cu_new, seq_len, max_new=max_new,
-                                   softmax_scale=softmax_scale, window=window, out=out,
-                                   error=self.error, stream=stream)
+                           f"{type(self).__name__}.attention: q must have {self.n_q_heads} heads")
+        return self._attention_call(q, *self._pool(), block_table, cu_new, seq_len, max_new=max_new,
+                                    softmax_scale=softmax_scale, window=window, out=out,
+                                    error=self.error, stream=stream)
 
     def check(self) -> None:
         """Synchronizes the device; raises KvqError for what the kernels flagged."""

@@ -495,6 +495,155 @@ KVQ_API kvq_status kvq_paged_attention(const kvq_paged_pool* pool, const void* q
                                        void* workspace, size_t n_workspace, int* device_error,
                                        void* stream);
 
+/* kvq_paged_plan that also writes positions [n_tokens] (device, 16-byte
+ * aligned): the position of every new token within its request, 0 behind the
+ * last one.  A request that gets no pages still gets its positions. */
+KVQ_API kvq_status kvq_paged_plan_positions(const int* ctx_len, const int* new_len, int batch,
+                                            int* block_table, int max_pages, const int* free_pages,
+                                            int n_free_pages, const int* n_free, int page_size,
+                                            int n_tokens, int* cu_new, int* seq_len, int* slots,
+                                            int* positions, int* n_left, int* device_error,
+                                            void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Rotary positions.
+ *
+ * A head's first rotary_dim channels are pairs that turn with the token's
+ * position; the others stay as they are.  Pair i moves f_i radians a position:
+ *   f_i = base^(-2 i / rotary_dim), scaled for contexts longer than the model's
+ * (kvq_rotary_turns).  Its channels are (i, i + rotary_dim / 2), or (2 i,
+ * 2 i + 1) when interleaved.  A frequency is held as the whole number
+ * f_i / (2 pi) * 2^64, so that position * frequency modulo 2^64 is the exact
+ * part of a turn, however far the position.
+ *
+ * A step's cosines and sines are computed once for all layers
+ * (kvq_rotary_angles) and passed to the calls that turn queries and keys:
+ *   a' = a cos - b sin,  b' = b cos + a sin
+ * both products and their sum rounded to fp32, the result rounded to the
+ * input's type.
+ * ------------------------------------------------------------------------ */
+
+/* Frequencies (host): turns[rotary_dim / 2].  rotary_dim even, at most 256.
+ * factor > 1 slows the pairs down for contexts longer than those of the
+ * training: all of them (positions divided by factor) when original_len is 0;
+ * by parts otherwise: with r = original_len f / (2 pi), the turns of a pair in
+ * the original context, and keep = (r - low) / (high - low) within [0, 1],
+ *   f' = f keep + f / factor (1 - keep)
+ * so that pairs of many turns stay and pairs of few are slowed down.  A larger
+ * base serves contexts that are stretched by the base. */
+KVQ_API kvq_status kvq_rotary_turns(int64_t* turns, int rotary_dim, double base, double factor,
+                                    double original_len, double low, double high);
+
+/* Cosine and sine of every token's angles, times magnitude: angles fp32
+ * [n_tokens][rotary_dim / 2][2], 16-byte aligned.  positions: device int32
+ * [n_tokens], any values; turns: device int64 [rotary_dim / 2].  Errors are
+ * below 2^-22 of magnitude. */
+KVQ_API kvq_status kvq_rotary_angles(const int* positions, int n_tokens, const int64_t* turns,
+                                     int rotary_dim, float magnitude, float* angles, void* stream);
+
+/* How heads are turned: a step's angles (device, 16-byte aligned) and the
+ * layout of the pairs. */
+typedef struct {
+  const float* angles; /* [n_tokens][rotary_dim / 2][2] */
+  int rotary_dim;      /* even, 2 .. head_dim */
+  int interleaved;     /* 0 or 1 */
+} kvq_rotary;
+
+/* Turns the heads of every token: out = x turned by its token's angles.
+ *   x, out  device fp16 or bf16 (dtype) [n_tokens][n_heads][head_dim] at
+ *           x_stride / out_stride elements a token (multiples of 8), 16-byte
+ *           aligned; out may be x itself (with the same stride), but not
+ *           overlap it otherwise.
+ * head_dim is a multiple of 8, at most 256. */
+KVQ_API kvq_status kvq_rotate(const kvq_rotary* rotary, const void* x, int dtype,
+                              long long x_stride, void* out, long long out_stride, int n_tokens,
+                              int n_heads, int head_dim, void* stream);
+
+/* Stores new keys and values into the E4M3 pages as kvq_paged_store does, the
+ * keys turned on the way, and turns the step's queries: the same bits as
+ * kvq_rotate of k and of q followed by kvq_paged_store, without the turned
+ * keys' way through memory.
+ *   q, q_out  [n_tokens][n_q_heads][head_dim] as for kvq_rotate; both NULL
+ *             (and n_q_heads 0) when there are no queries to turn.  q_out may
+ *             be q itself, and overlaps nothing else. */
+KVQ_API kvq_status kvq_paged_append(const kvq_paged_pool* pool, const kvq_rotary* rotary,
+                                    const void* k, const void* v, int dtype, long long k_stride,
+                                    long long v_stride, const int* slots, int n_tokens,
+                                    const void* q, long long q_stride, void* q_out,
+                                    long long q_out_stride, int n_q_heads, int* device_error,
+                                    void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Paged 4-bit cache: the paged cache's calls over pages of the dense cache's
+ * 4-bit codes, 5 bits a value with their metadata (the E4M3 pages hold 8).
+ *
+ * Pool.  For K and for V, codes [n_pages][n_kv_heads][page_size][head_dim / 2]
+ * (bytes of two codes) and metadata [n_pages][n_kv_heads][page_size]
+ * [head_dim / 32][2] (fp16 step and minimum of each group of 32 channels).
+ * Keys and values are both grouped per token, so that tokens come one at a
+ * time and every page takes them in any order; tables, slots, sizes and
+ * conventions are those of the E4M3 pages.
+ *
+ * Arithmetic of the store, exactly, per token, kv head and group of 32
+ * channels (turned keys are first rounded to their own type):
+ *   x     = the value as fp16, within +-65408 (NaN: 0)
+ *   mn,mx = minimum and maximum of the group
+ *   step  = fp16((mx - mn) / 15), the divide in fp32
+ *   code  = round((x - mn) / step), half to even, within [0, 15]; 0 if step is 0
+ * and a value is fp16(code * step + mn), rounded once.  (The bound keeps the
+ * largest code of the widest group a finite number.)  Infinities and NaN set
+ * KVQ_PAGED_ERR_NONFINITE.
+ *
+ * Order of the codes.  The 32-bit word i of a row holds channels 8 i .. 8 i + 7:
+ *   keys    channel 8 i + 2 j + e at bits 4 j + 16 e   (j = 0 .. 3, e = 0, 1)
+ *   values  channel 8 i + j at bits 4 j                (j = 0 .. 7)
+ * A tensor-core operand pairs two channels of a key and two tokens of a value
+ * in the halves of a register; so both come out of a word by a mask.
+ * ------------------------------------------------------------------------ */
+
+typedef struct {
+  void* k_codes; /* [n_pages][n_kv_heads][page_size][head_dim / 2] bytes, 16-byte aligned */
+  void* v_codes;
+  void* k_meta;  /* fp16 [n_pages][n_kv_heads][page_size][head_dim / 32][2], 16-byte aligned */
+  void* v_meta;
+  int n_pages, n_kv_heads, page_size, head_dim;
+} kvq_paged4_pool;
+
+/* Validates a pool's sizes on the host (the pointers are not looked at). */
+KVQ_API kvq_status kvq_paged4_pool_check(const kvq_paged4_pool* pool);
+
+/* Stores n_tokens new keys and values: token t goes to slots[t] (negative:
+ * nowhere).  Arguments as for kvq_paged_append; rotary may be NULL: the keys
+ * are stored as they are (and there are no queries to turn).  Rows without a
+ * slot are left as they are; two tokens must not share a slot. */
+KVQ_API kvq_status kvq_paged4_append(const kvq_paged4_pool* pool, const kvq_rotary* rotary,
+                                     const void* k, const void* v, int dtype, long long k_stride,
+                                     long long v_stride, const int* slots, int n_tokens,
+                                     const void* q, long long q_stride, void* q_out,
+                                     long long q_out_stride, int n_q_heads, int* device_error,
+                                     void* stream);
+
+/* Reads tokens back: k_out, v_out fp16 [n_tokens][n_kv_heads][head_dim]
+ * contiguous, 16-byte aligned (either may be NULL); rows of negative slots
+ * become zeros. */
+KVQ_API kvq_status kvq_paged4_read(const kvq_paged4_pool* pool, const int* slots, int n_tokens,
+                                   void* k_out, void* v_out, int* device_error, void* stream);
+
+/* Bytes of kvq_paged4_attention's workspace for this pool (host only).  The
+ * first 1024 bytes must be zero before the first call with it; every call
+ * leaves them zero. */
+KVQ_API kvq_status kvq_paged4_workspace_bytes(const kvq_paged4_pool* pool, size_t* bytes);
+
+/* kvq_paged_attention over the 4-bit pages: the same arguments, rules and
+ * order of sums. */
+KVQ_API kvq_status kvq_paged4_attention(const kvq_paged4_pool* pool, const void* q, int dtype,
+                                        long long q_stride, void* out, long long out_stride,
+                                        int n_tokens, int n_q_heads, const int* block_table,
+                                        int max_pages, const int* cu_new, const int* seq_len,
+                                        int batch, int max_new, float softmax_scale, int window,
+                                        void* workspace, size_t n_workspace, int* device_error,
+                                        void* stream);
+
 /* Host-side lengths: quantized tokens and tail tokens per pair
  * (KVQ_ERR_UNSUPPORTED for a ragged cache). */
 KVQ_API kvq_status kvq_get_state(const kvq_cache* cache, int* T_q,
