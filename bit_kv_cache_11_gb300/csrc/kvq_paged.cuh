@@ -72,9 +72,7 @@ struct PagedAttnParams {
   uint32_t r_magic;  // ceil(2^32 / R): row / R by one high product (R > 1)
   const float* k_scale;
   const float* v_scale;
-  // the 4-bit pages' (kvq_paged4_attention); scales are null then
-  const uint8_t* codes[2];
-  const uint32_t* meta[2];
+  const uint32_t* meta[2];  // the 4-bit pages' metadata, whose calls have no scales
   float qscale;  // softmax scale * log2(e)
   int window;    // 0: none
   // rows (new tokens * R) of the requests this launch serves: those with
@@ -172,6 +170,13 @@ cudaError_t paged_decode_d128(const PagedAttnParams& p, const CUtensorMap& km,
                               const CUtensorMap& vm, bool bf16, int nt, cudaStream_t st);
 cudaError_t launch_paged_prompt(const PagedAttnParams& a, int items_max, const CUtensorMap& km,
                                 const CUtensorMap& vm, int D, bool bf16, cudaStream_t st);
+// The same over 4-bit pages.
+cudaError_t paged4_decode_d64(const PagedAttnParams& p, const CUtensorMap& km, const CUtensorMap& vm,
+                              bool bf16, int nt, cudaStream_t st);
+cudaError_t paged4_decode_d128(const PagedAttnParams& p, const CUtensorMap& km,
+                               const CUtensorMap& vm, bool bf16, int nt, cudaStream_t st);
+cudaError_t launch_paged4_prompt(const PagedAttnParams& a, int items_max, const CUtensorMap& km,
+                                 const CUtensorMap& vm, int D, bool bf16, cudaStream_t st);
 // Lets kernel `fn` use `bytes` of dynamic shared memory on the current device
 // (set once per kernel and device).
 cudaError_t allow_smem(const void* fn, int bytes);

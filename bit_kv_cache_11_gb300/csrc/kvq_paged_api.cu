@@ -98,19 +98,21 @@ EncodeFn encode_fn() {
   return fn;
 }
 
-// The pool's rows (one token of one page and head) as a 2-D tensor of bytes;
-// a box is `box_rows` whole rows, swizzled over its row's width.
-bool row_map(CUtensorMap* m, void* pages, const kvq_paged_pool* c, int box_rows) {
+// The pool's rows (one token of one page and head, `width` bytes) as a 2-D tensor
+// of bytes; a box is `box_rows` whole rows, swizzled over its row's width.
+bool row_map(CUtensorMap* m, void* pages, const kvq_paged_pool* c, int width, int box_rows) {
   EncodeFn fn = encode_fn();
   if (fn == nullptr) return false;
-  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(c->head_dim),
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(width),
                               static_cast<cuuint64_t>(c->n_pages) * c->n_kv_heads * c->page_size};
-  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(c->head_dim)};
-  const cuuint32_t box[2] = {static_cast<cuuint32_t>(c->head_dim), static_cast<cuuint32_t>(box_rows)};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(width)};
+  const cuuint32_t box[2] = {static_cast<cuuint32_t>(width), static_cast<cuuint32_t>(box_rows)};
   const cuuint32_t es[2] = {1, 1};
   return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, pages, dims, strides, box, es,
             CU_TENSOR_MAP_INTERLEAVE_NONE,
-            c->head_dim == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+            width == 128  ? CU_TENSOR_MAP_SWIZZLE_128B
+            : width == 64 ? CU_TENSOR_MAP_SWIZZLE_64B
+                          : CU_TENSOR_MAP_SWIZZLE_32B,
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -196,10 +198,8 @@ kvq_status attention(const kvq_paged_pool* pool, bool four, const void* q, int d
   p.n_pages = pool->n_pages;
   p.k_scale = four ? nullptr : pool->k_scale;
   p.v_scale = four ? nullptr : pool->v_scale;
-  p.codes[0] = static_cast<const uint8_t*>(pool->k_pages);
-  p.codes[1] = static_cast<const uint8_t*>(pool->v_pages);
-  p.meta[0] = reinterpret_cast<const uint32_t*>(pool->k_scale);
-  p.meta[1] = reinterpret_cast<const uint32_t*>(pool->v_scale);
+  p.meta[0] = four ? reinterpret_cast<const uint32_t*>(pool->k_scale) : nullptr;
+  p.meta[1] = four ? reinterpret_cast<const uint32_t*>(pool->v_scale) : nullptr;
   p.qscale = softmax_scale * 1.4426950408889634f;
   p.window = window;
   p.row_min = 1;
@@ -213,35 +213,30 @@ kvq_status attention(const kvq_paged_pool* pool, bool four, const void* q, int d
   p.err = device_error;
   const bool bf = dtype == KVQ_DTYPE_BF16;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (four) {
-    if (launch_paged4_attention(p, D, bf, st) != cudaSuccess) {
-      cudaGetLastError();
-      return KVQ_ERR_CUDA;
-    }
-    count_launches(1);
-    return KVQ_OK;
-  }
+  const int width = four ? D / 2 : D;
   CUtensorMap km, vm;
   if (prompts && pairs > 0) {
     PagedAttnParams a = p;
     a.row_min = turn + 1;
     a.row_max = INT_MAX;
     a.box_rows = pool->page_size;
-    if (!row_map(&km, pool->k_pages, pool, a.box_rows) ||
-        !row_map(&vm, pool->v_pages, pool, a.box_rows))
+    if (!row_map(&km, pool->k_pages, pool, width, a.box_rows) ||
+        !row_map(&vm, pool->v_pages, pool, width, a.box_rows))
       return KVQ_ERR_CUDA;
-    if (launch_paged_prompt(a, static_cast<int>(pairs), km, vm, D, bf, st) != cudaSuccess) {
+    if ((four ? launch_paged4_prompt : launch_paged_prompt)(a, static_cast<int>(pairs), km, vm, D, bf, st) !=
+        cudaSuccess) {
       cudaGetLastError();
       return KVQ_ERR_CUDA;
     }
     count_launches(1);
   }
   p.box_rows = std::min(pool->page_size, ut);
-  if (!row_map(&km, pool->k_pages, pool, p.box_rows) ||
-      !row_map(&vm, pool->v_pages, pool, p.box_rows))
+  if (!row_map(&km, pool->k_pages, pool, width, p.box_rows) ||
+      !row_map(&vm, pool->v_pages, pool, width, p.box_rows))
     return KVQ_ERR_CUDA;
-  const cudaError_t e = D == 128 ? paged_decode_d128(p, km, vm, bf, nt, st)
-                                 : paged_decode_d64(p, km, vm, bf, nt, st);
+  const auto decode = four ? (D == 128 ? paged4_decode_d128 : paged4_decode_d64)
+                           : (D == 128 ? paged_decode_d128 : paged_decode_d64);
+  const cudaError_t e = decode(p, km, vm, bf, nt, st);
   if (e != cudaSuccess) {
     cudaGetLastError();
     return KVQ_ERR_CUDA;

@@ -47,7 +47,7 @@
 
 
 #include "kvq_decode_mma.cuh"
-#include "kvq_paged.cuh"
+#include "kvq_paged4.cuh"
 
 namespace kvq {
 
@@ -81,6 +81,44 @@ __device__ __forceinline__ uint2 lds64(uint32_t a) {
   return v;
 }
 
+// Four 8 x 8 matrices of 16-bit units: lane (g, t) gets units 2t, 2t + 1 of row g, or
+// (trans) unit g of rows 2t and 2t + 1.  Lane l names row l % 8 of matrix l / 8.
+__device__ __forceinline__ void ldmatrix4(uint32_t a, uint32_t (&x)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3])
+               : "r"(a));
+}
+__device__ __forceinline__ void ldmatrix4_trans(uint32_t a, uint32_t (&x)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3])
+               : "r"(a));
+}
+
+// A token's {step, minimum} pairs of the 4-bit pages.
+template <int D>
+struct Meta4 {
+  uint32_t m[D / 32];
+  __device__ __forceinline__ void load(uint32_t a) {
+    if constexpr (D == 128) {
+      const uint4 v = lds128(a);
+      m[0] = v.x;
+      m[1] = v.y;
+      m[2] = v.z;
+      m[3] = v.w;
+    } else {
+      const uint2 v = lds64(a);
+      m[0] = v.x;
+      m[1] = v.y;
+    }
+  }
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) m[i] = 0;
+  }
+  __device__ __forceinline__ uint32_t step(int w) const { return __byte_perm(m[w], m[w], 0x1010); }
+  __device__ __forceinline__ uint32_t least(int w) const { return __byte_perm(m[w], m[w], 0x3232); }
+};
+
 // Weights as fp16; one that the rounding of huge scores (over 2^22) lifts above
 // fp16's largest number stays finite.
 __device__ __forceinline__ uint32_t pack_weights(float lo, float hi) {
@@ -98,14 +136,16 @@ __device__ __forceinline__ float row_factor(float l) {
 // No page is needed (a table entry is never this: ids are below 2^31 - 1).
 constexpr int kNoPage = 0x7fffffff;
 
-template <int D, int NT>
+template <int D, int NT, bool Q4>
 struct PagedCfg {
   static constexpr int NW = paged_warps(NT);
   static constexpr int UT = paged_unit_tokens(D);  // tokens of a unit
   static constexpr int GR = UT / 16;               // 16-token granules of a unit
-  static constexpr int NS = 3;                     // stages of a warp
+  static constexpr int NS = Q4 ? 4 : 3;            // stages of a warp
   static constexpr int RG = 8 * NT;                // query rows of a group
-  static constexpr int STAGE = 8192;
+  static constexpr int STAGE = Q4 ? 5120 : 8192;
+  // places in a stage: keys, values, and the 4-bit pages' metadata
+  static constexpr int OFF_V = Q4 ? 2048 : 4096, OFF_KM = 4096, OFF_VM = 4608;
   static constexpr int PART = RG * (D + 2);        // floats of a partial: O, then m, l
   static constexpr int RING = 64;                  // granule records of a warp
   static constexpr int OFF_BAR = NW * NS * STAGE;
@@ -133,12 +173,12 @@ struct PagedSeg {
   int h, grp, q0, rows;
 };
 
-template <int D, int NT, bool BF16>
-__global__ void __launch_bounds__(PagedCfg<D, NT>::NW * 32, 1)
+template <int D, int NT, bool BF16, bool Q4>
+__global__ void __launch_bounds__(PagedCfg<D, NT, Q4>::NW * 32, 1)
     paged_decode_kernel(const __grid_constant__ PagedAttnParams p,
                         const __grid_constant__ CUtensorMap kmap,
                         const __grid_constant__ CUtensorMap vmap) {
-  using C = PagedCfg<D, NT>;
+  using C = PagedCfg<D, NT, Q4>;
   constexpr int NW = C::NW, UT = C::UT, GR = C::GR, NS = C::NS, RG = C::RG, PART = C::PART;
   constexpr int KC = D / 64;   // 16-byte chunks of a key row a lane reads
   constexpr int KS = D / 16;   // k-steps of the scores
@@ -264,7 +304,7 @@ __global__ void __launch_bounds__(PagedCfg<D, NT>::NW * 32, 1)
   // next scales half way, so neither wait stops the stream.
   int my_page = -1;
   int nx_page = -1;
-  float nx_ks = 0.f, nx_vs = 1.f;
+  float nx_ks = 0.f, nx_vs = 1.f;  // (4-bit pages have none)
   // Page of the lane's granule when the batch starts at unit u (-1: none).
   auto granule_page = [&](int u) {
     const int tok = li.tok0 + (u - li.u0) * UT + lane * 16;
@@ -283,7 +323,7 @@ __global__ void __launch_bounds__(PagedCfg<D, NT>::NW * 32, 1)
     return -1;
   };
   auto granule_scales = [&](int page, float* ks, float* vs) {
-    if (page < 0) return;
+    if (Q4 || page < 0) return;
     const size_t at = static_cast<size_t>(page) * p.H + li.h;
     *ks = p.k_scale[at];
     *vs = p.v_scale[at];
@@ -293,13 +333,17 @@ __global__ void __launch_bounds__(PagedCfg<D, NT>::NW * 32, 1)
   auto put_record = [&](int u0b, int rec0, float ks, float vs) {
     const int tok = li.tok0 + (u0b - li.u0) * UT + lane * 16;
     const bool seen = my_page >= 0 && tok < lhi && tok + 16 > llo;
-    ring[(rec0 + lane) & (C::RING - 1)] = make_float4(ks, fast_log2(vs), kWeightInv / vs, seen ? 1.f : 0.f);
+    ring[(rec0 + lane) & (C::RING - 1)] =
+        Q4 ? make_float4(1.f, 0.f, kWeightInv, seen ? 1.f : 0.f)
+           : make_float4(ks, fast_log2(vs), kWeightInv / vs, seen ? 1.f : 0.f);
   };
   const int nbox = UT / p.box_rows;  // boxes of a side
-  // lane i < nbox copies key box i, lane nbox + i value box i
+  // lane i < nbox copies key box i, lane nbox + i value box i, and the next 2 nbox
+  // lanes their metadata
   const bool key = lane < nbox;
-  const int bx = key ? lane : lane - nbox;
-  const uint32_t box_bytes = static_cast<uint32_t>(p.box_rows) * D;
+  const int part = lane >> (31 - __clz(nbox)), bx = lane & (nbox - 1);
+  constexpr int ROW = Q4 ? D / 2 : D;  // bytes of a row of codes
+  const uint32_t box_bytes = static_cast<uint32_t>(p.box_rows) * ROW;
   const int box_g = bx * (p.box_rows / 16) & (GR - 1);  // first granule of the lane's box
   auto issue = [&](int s) {
     const int u_first = lu, rec_first = grec;
@@ -326,15 +370,23 @@ __global__ void __launch_bounds__(PagedCfg<D, NT>::NW * 32, 1)
       granule_scales(nx_page, &nx_ks, &nx_vs);
     }
     const int page = __shfl_sync(0xffffffffu, my_page, gbase + box_g);
-    const bool mine = lane < 2 * nbox && page >= 0;
-    const int n = __popc(__ballot_sync(0xffffffffu, mine));
-    if (lane == 0) mbar_arrive_expect_tx(&bars[s], n * box_bytes);
+    const bool mine = lane < (Q4 ? 4 : 2) * nbox && page >= 0;
+    const uint32_t who = __ballot_sync(0xffffffffu, mine);
+    if (lane == 0) {
+      const uint32_t n = Q4 ? __popc(who) / 4 * 2 * (box_bytes + box_bytes / 4) : __popc(who) * box_bytes;
+      mbar_arrive_expect_tx(&bars[s], n);
+    }
     __syncwarp();
     if (mine) {
       const int tok = li.tok0 + (lu - li.u0) * UT + bx * p.box_rows;
       const int row = ((page * p.H + li.h) << p.lg_ps) + (tok & ((1 << p.lg_ps) - 1));
-      tma_load_2d(stages + s * C::STAGE + (key ? 0 : 4096) + bx * box_bytes, key ? &kmap : &vmap,
-                  0, row, &bars[s]);
+      uint8_t* st = stages + s * C::STAGE;
+      if (!Q4 || part < 2) {
+        tma_load_2d(st + (key ? 0 : C::OFF_V) + bx * box_bytes, key ? &kmap : &vmap, 0, row, &bars[s]);
+      } else {
+        bulk_g2s(st + (part == 2 ? C::OFF_KM : C::OFF_VM) + bx * (box_bytes / 4),
+                 p.meta[part - 2] + static_cast<size_t>(row) * (D / kGroup4), box_bytes / 4, &bars[s]);
+      }
     }
     if (fresh) put_record(u_first, rec_first, ks, vs);
     if (gbase == 0) nx_page = granule_page(lu + 32 / GR);
@@ -379,10 +431,10 @@ __global__ void __launch_bounds__(PagedCfg<D, NT>::NW * 32, 1)
         const int j = row_token(p, row);
         const uint4* src = reinterpret_cast<const uint4*>(
             static_cast<const uint16_t*>(p.q) + static_cast<long long>(it.q0 + j) * p.q_stride +
-            (static_cast<long long>(it.h) * p.R + (row - j * p.R)) * D + t * (D / 4));
+            (static_cast<long long>(it.h) * p.R + (row - j * p.R)) * D + t * (Q4 ? 8 : D / 4));
 #pragma unroll
         for (int i = 0; i < KS / 2; ++i) {
-          const uint4 v = src[i];
+          const uint4 v = src[Q4 ? 4 * i : i];
           w[4 * i] = v.x;
           w[4 * i + 1] = v.y;
           w[4 * i + 2] = v.z;
@@ -435,8 +487,15 @@ __global__ void __launch_bounds__(PagedCfg<D, NT>::NW * 32, 1)
     koff[c] = D == 128 ? g * 128 + (((2 * t + c) ^ g) << 4) : g * 64 + ((t ^ (g >> 1)) << 4);
 #pragma unroll
   for (int i = 0; i < 2; ++i)
-    voff[i] = 4096 + (D == 128 ? (2 * t + i) * 128 + ((g ^ (2 * t + i)) << 4)
+    voff[i] = C::OFF_V + (D == 128 ? (2 * t + i) * 128 + ((g ^ (2 * t + i)) << 4)
                                : (2 * t + i) * 64 + (((g >> 1) ^ t) << 4) + 8 * (g & 1));
+  // 4-bit pages: the lane's row of a matrix pair that ldmatrix reads, tokens 0 .. 15
+  // of group 0 and 1 (the next two groups are 32 bytes on, under the swizzle).
+  uint32_t moff = 0;
+  if constexpr (Q4) {
+    const int row = (lane & 7) + (lane & 8), chunk = lane >> 4;
+    moff = D == 128 ? row * 64 + ((chunk ^ ((row >> 1) & 3)) << 4) : row * 32 + ((chunk ^ ((row >> 2) & 1)) << 4);
+  }
   const uint32_t stages_s = smem_addr(stages);
 
   // One unit from stage memory.  edge: some of its tokens are hidden from some
@@ -451,19 +510,44 @@ __global__ void __launch_bounds__(PagedCfg<D, NT>::NW * 32, 1)
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int i = 0; i < 4; ++i) s[mt][nt][i] = 0.f;
+      if constexpr (Q4) {
+        // words of channels 32 w + 8 t .. of tokens g and g + 8, and the tokens'
+        // steps and minima
+        Meta4<D> ma, mb;
+        ma.load(st + C::OFF_KM + (mt * 16 + g) * (D / 8));
+        mb.load(st + C::OFF_KM + (mt * 16 + g + 8) * (D / 8));
 #pragma unroll
-      for (int c = 0; c < KC; ++c) {
-        const uint4 a = lds128(st + koff[c] + mt * 16 * D);
-        const uint4 b = lds128(st + koff[c] + (mt * 16 + 8) * D);
-        const uint32_t aw[4] = {a.x, a.y, a.z, a.w}, bw[4] = {b.x, b.y, b.z, b.w};
+        for (int w = 0; w < D / 32; w += 2) {
+          uint32_t x[4];
+          ldmatrix4((st + mt * 8 * D + moff) ^ (16 * w), x);
 #pragma unroll
-        for (int w = 0; w < 4; ++w) {
-          uint32_t a0, a1, a2, a3;
-          e4m3x4_to_half2x2(aw[w], a0, a2);
-          e4m3x4_to_half2x2(bw[w], a1, a3);
+          for (int i = 0; i < 2; ++i) {
+            uint32_t a[4], b[4];
+            values4(x[2 * i], ma.step(w + i), ma.least(w + i), a);
+            values4(x[2 * i + 1], mb.step(w + i), mb.least(w + i), b);
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-            mma_16816(s[mt][nt], a0, a1, a2, a3, qf[nt][4 * c + w][0], qf[nt][4 * c + w][1]);
+            for (int nt = 0; nt < NT; ++nt) {
+              const int ks = 2 * (w + i);
+              mma_16816(s[mt][nt], a[0], b[0], a[1], b[1], qf[nt][ks][0], qf[nt][ks][1]);
+              mma_16816(s[mt][nt], a[2], b[2], a[3], b[3], qf[nt][ks + 1][0], qf[nt][ks + 1][1]);
+            }
+          }
+        }
+      } else {
+#pragma unroll
+        for (int c = 0; c < KC; ++c) {
+          const uint4 a = lds128(st + koff[c] + mt * 16 * D);
+          const uint4 b = lds128(st + koff[c] + (mt * 16 + 8) * D);
+          const uint32_t aw[4] = {a.x, a.y, a.z, a.w}, bw[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+          for (int w = 0; w < 4; ++w) {
+            uint32_t a0, a1, a2, a3;
+            e4m3x4_to_half2x2(aw[w], a0, a2);
+            e4m3x4_to_half2x2(bw[w], a1, a3);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+              mma_16816(s[mt][nt], a0, a1, a2, a3, qf[nt][4 * c + w][0], qf[nt][4 * c + w][1]);
+          }
         }
       }
     }
@@ -472,12 +556,13 @@ __global__ void __launch_bounds__(PagedCfg<D, NT>::NW * 32, 1)
       float mx[2] = {-INFINITY, -INFINITY};
 #pragma unroll
       for (int mt = 0; mt < GR; ++mt) {
-        const float f0 = rec[mt].x * cq[nt][0], f1 = rec[mt].x * cq[nt][1];
+        const float f0 = Q4 ? cq[nt][0] : rec[mt].x * cq[nt][0], f1 = Q4 ? cq[nt][1] : rec[mt].x * cq[nt][1];
+        const float lv = Q4 ? 0.f : rec[mt].y;
         float* x = s[mt][nt];
-        x[0] = fmaf(x[0], f0, rec[mt].y);
-        x[1] = fmaf(x[1], f1, rec[mt].y);
-        x[2] = fmaf(x[2], f0, rec[mt].y);
-        x[3] = fmaf(x[3], f1, rec[mt].y);
+        x[0] = fmaf(x[0], f0, lv);
+        x[1] = fmaf(x[1], f1, lv);
+        x[2] = fmaf(x[2], f0, lv);
+        x[3] = fmaf(x[3], f1, lv);
         if (edge) {
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
@@ -513,8 +598,9 @@ __global__ void __launch_bounds__(PagedCfg<D, NT>::NW * 32, 1)
         x[1] = fast_exp2(x[1] - mb[1]);
         x[2] = fast_exp2(x[2] - mb[0]);
         x[3] = fast_exp2(x[3] - mb[1]);
-        l[nt][0] = fmaf(x[0] + x[2], rec[mt].z, l[nt][0]);
-        l[nt][1] = fmaf(x[1] + x[3], rec[mt].z, l[nt][1]);
+        const float wi = Q4 ? kWeightInv : rec[mt].z;
+        l[nt][0] = fmaf(x[0] + x[2], wi, l[nt][0]);
+        l[nt][1] = fmaf(x[1] + x[3], wi, l[nt][1]);
         pw[mt][nt][0] = movmatrix(pack_weights(x[0], x[1]));
         pw[mt][nt][1] = movmatrix(pack_weights(x[2], x[3]));
       }
@@ -530,52 +616,83 @@ __global__ void __launch_bounds__(PagedCfg<D, NT>::NW * 32, 1)
     }
 #pragma unroll
     for (int mt = 0; mt < GR; ++mt) {
-      // value rows of tokens 2t, 2t + 1, 2t + 8, 2t + 9 of the granule:
-      // channels [D/8 * g, D/8 * (g + 1))
-      constexpr int VW = D / 32;  // words of a lane's row
-      uint32_t v[4][VW];
+      if constexpr (Q4) {
+        // Transposed matrices: channels 32 w + 4 g .. + 3 of tokens 2t and 2t + 1
+        // (2t + 8 and 2t + 9) in the halves of a word.
+        Meta4<D> mv[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint32_t at = st + voff[i & 1] + (mt * 16 + 8 * (i >> 1)) * D;
-        if constexpr (D == 128) {
-          const uint4 x = lds128(at);
-          v[i][0] = x.x;
-          v[i][1] = x.y;
-          v[i][2] = x.z;
-          v[i][3] = x.w;
-        } else {
-          const uint2 x = lds64(at);
-          v[i][0] = x.x;
-          v[i][1] = x.y;
+        for (int i = 0; i < 4; ++i) {
+          const int tr = mt * 16 + 2 * t + (i & 1) + 8 * (i >> 1);
+          mv[i].load(st + C::OFF_VM + tr * (D / 8));
+          // (what lies in hidden rows may be NaN, which a weight of 0 would not cancel)
+          if (edge && (tok + tr < lo || tok + tr >= hi || rec[mt].w == 0.f)) mv[i].clear();
         }
-        if (edge) {
-          // what lies in hidden rows may decode to NaN, which a weight of 0
-          // would not cancel
-          const int tk = tok + mt * 16 + 2 * t + (i & 1) + 8 * (i >> 1);
-          if (tk < lo || tk >= hi || rec[mt].w == 0.f) {
 #pragma unroll
-            for (int w = 0; w < VW; ++w) v[i][w] = 0;
+        for (int w = 0; w < D / 32; w += 2) {
+          uint32_t x[4];
+          ldmatrix4_trans((st + C::OFF_V + mt * 8 * D + moff) ^ (16 * w), x);
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            uint32_t a[4], b[4];
+            values4(x[2 * i], pair_lo(mv[0].m[w + i], mv[1].m[w + i]), pair_hi(mv[0].m[w + i], mv[1].m[w + i]), a);
+            values4(x[2 * i + 1], pair_lo(mv[2].m[w + i], mv[3].m[w + i]), pair_hi(mv[2].m[w + i], mv[3].m[w + i]), b);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              mma_16816(acc[2 * (w + i)][nt], a[0], a[1], b[0], b[1], pw[mt][nt][0], pw[mt][nt][1]);
+              mma_16816(acc[2 * (w + i) + 1][nt], a[2], a[3], b[2], b[3], pw[mt][nt][0], pw[mt][nt][1]);
+            }
           }
         }
-      }
+      } else {
+        // value rows of tokens 2t, 2t + 1, 2t + 8, 2t + 9 of the granule:
+        // channels [D/8 * g, D/8 * (g + 1))
+        constexpr int VW = D / 32;  // words of a lane's row
+        uint32_t v[4][VW];
 #pragma unroll
-      for (int w = 0; w < VW; ++w) {
-        const uint32_t x0 = __byte_perm(v[0][w], v[1][w], 0x5140), x1 = __byte_perm(v[0][w], v[1][w], 0x7362);
-        const uint32_t y0 = __byte_perm(v[2][w], v[3][w], 0x5140), y1 = __byte_perm(v[2][w], v[3][w], 0x7362);
-        uint32_t a0, a1, a2, a3, b0, b1, b2, b3;
-        e4m3x4_to_half2x2(x0, a0, a1);
-        e4m3x4_to_half2x2(y0, a2, a3);
-        e4m3x4_to_half2x2(x1, b0, b1);
-        e4m3x4_to_half2x2(y1, b2, b3);
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t at = st + voff[i & 1] + (mt * 16 + 8 * (i >> 1)) * D;
+          if constexpr (D == 128) {
+            const uint4 x = lds128(at);
+            v[i][0] = x.x;
+            v[i][1] = x.y;
+            v[i][2] = x.z;
+            v[i][3] = x.w;
+          } else {
+            const uint2 x = lds64(at);
+            v[i][0] = x.x;
+            v[i][1] = x.y;
+          }
+          if (edge) {
+            // what lies in hidden rows may decode to NaN, which a weight of 0
+            // would not cancel
+            const int tk = tok + mt * 16 + 2 * t + (i & 1) + 8 * (i >> 1);
+            if (tk < lo || tk >= hi || rec[mt].w == 0.f) {
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          mma_16816(acc[2 * w][nt], a0, a1, a2, a3, pw[mt][nt][0], pw[mt][nt][1]);
-          mma_16816(acc[2 * w + 1][nt], b0, b1, b2, b3, pw[mt][nt][0], pw[mt][nt][1]);
+              for (int w = 0; w < VW; ++w) v[i][w] = 0;
+            }
+          }
+        }
+#pragma unroll
+        for (int w = 0; w < VW; ++w) {
+          const uint32_t x0 = __byte_perm(v[0][w], v[1][w], 0x5140), x1 = __byte_perm(v[0][w], v[1][w], 0x7362);
+          const uint32_t y0 = __byte_perm(v[2][w], v[3][w], 0x5140), y1 = __byte_perm(v[2][w], v[3][w], 0x7362);
+          uint32_t a0, a1, a2, a3, b0, b1, b2, b3;
+          e4m3x4_to_half2x2(x0, a0, a1);
+          e4m3x4_to_half2x2(y0, a2, a3);
+          e4m3x4_to_half2x2(x1, b0, b1);
+          e4m3x4_to_half2x2(y1, b2, b3);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            mma_16816(acc[2 * w][nt], a0, a1, a2, a3, pw[mt][nt][0], pw[mt][nt][1]);
+            mma_16816(acc[2 * w + 1][nt], b0, b1, b2, b3, pw[mt][nt][0], pw[mt][nt][1]);
+          }
         }
       }
     }
   };
 
+  // The first of this lane's channels in m-tile mt.
+  auto channel = [&](int mt) { return Q4 ? mt / 2 * 32 + 4 * g + 2 * (mt & 1) : g * (D / 8) + 2 * mt; };
   // Leaves the current item after unit u - 1: a finished output, or a partial.
   auto leave = [&](bool last) {
 #pragma unroll
@@ -607,12 +724,18 @@ __global__ void __launch_bounds__(PagedCfg<D, NT>::NW * 32, 1)
               w[mt] = pack_half2(x, y);
             }
           }
-          uint4* dst = reinterpret_cast<uint4*>(
-              static_cast<uint16_t*>(p.out) + static_cast<long long>(it.q0 + j) * p.out_stride +
-              (static_cast<long long>(it.h) * p.R + (row - j * p.R)) * D + g * (D / 8));
+          uint16_t* head = static_cast<uint16_t*>(p.out) + static_cast<long long>(it.q0 + j) * p.out_stride +
+                           (static_cast<long long>(it.h) * p.R + (row - j * p.R)) * D;
+          if constexpr (Q4) {
 #pragma unroll
-          for (int i = 0; i < D / 64; ++i)
-            dst[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+            for (int i = 0; i < D / 32; ++i)
+              *reinterpret_cast<uint2*>(head + channel(2 * i)) = make_uint2(w[2 * i], w[2 * i + 1]);
+          } else {
+            uint4* dst = reinterpret_cast<uint4*>(head + channel(0));
+#pragma unroll
+            for (int i = 0; i < D / 64; ++i)
+              dst[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+          }
         }
       return;
     }
@@ -625,7 +748,7 @@ __global__ void __launch_bounds__(PagedCfg<D, NT>::NW * 32, 1)
         const int r = nt * 8 + 2 * t + c;
 #pragma unroll
         for (int mt = 0; mt < MT; mt += 2) {
-          *reinterpret_cast<float4*>(dst + r * D + g * (D / 8) + 2 * mt) =
+          *reinterpret_cast<float4*>(dst + r * D + channel(mt)) =
               make_float4(acc[mt][nt][c], acc[mt][nt][2 + c], acc[mt + 1][nt][c], acc[mt + 1][nt][2 + c]);
         }
         if (g == 0) {
@@ -931,11 +1054,11 @@ __global__ void __launch_bounds__(PagedCfg<D, NT>::NW * 32, 1)
   }
 }
 
-template <int D, int NT, bool BF16>
+template <int D, int NT, bool BF16, bool Q4>
 cudaError_t launch_paged_decode_t(const PagedAttnParams& p, const CUtensorMap& km,
                                   const CUtensorMap& vm, cudaStream_t st) {
-  using C = PagedCfg<D, NT>;
-  auto fn = paged_decode_kernel<D, NT, BF16>;
+  using C = PagedCfg<D, NT, Q4>;
+  auto fn = paged_decode_kernel<D, NT, BF16, Q4>;
   const int smem = C::smem(p.batch);
   const cudaError_t e = allow_smem(reinterpret_cast<const void*>(fn), C::smem(kPagedMaxBatch));
   if (e != cudaSuccess) return e;

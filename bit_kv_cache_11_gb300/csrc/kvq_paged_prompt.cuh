@@ -50,7 +50,7 @@
 
 #include <type_traits>
 
-#include "kvq_paged.cuh"
+#include "kvq_paged4.cuh"
 
 namespace kvq {
 
@@ -61,13 +61,14 @@ struct PagedPromptParams {
 
 __host__ __device__ constexpr int round_up128(int x) { return (x + 127) / 128 * 128; }
 
-template <int D>
+template <int D, bool Q4>
 struct PromptCfg {
   static constexpr int N = 128;                   // tokens of a tile
   static constexpr int ROWS = 256;                // query rows of a CTA
-  static constexpr int NRAW = 2;                  // raw tiles in flight
+  static constexpr int NRAW = Q4 ? 3 : 2;         // raw tiles in flight
   static constexpr int NT = 4;                    // fp16 tiles
-  static constexpr int RAW = N * D;               // bytes of a raw tile
+  static constexpr int ROW = Q4 ? D / 2 : D;      // bytes of a row of codes
+  static constexpr int RAW = Q4 ? N * (ROW + D / 8) : N * ROW;  // bytes of a raw tile: codes, metadata
   static constexpr int TILE = N * D * 2;          // bytes of an fp16 tile
   static constexpr int QT = 128 * D * 2;          // bytes of a query tile
   static constexpr int REC = 8;                   // granule records of a tile
@@ -245,12 +246,12 @@ struct PromptItem {
   int t0, nt;            // first tile's first token, tiles
 };
 
-template <int D, bool BF16>
-__global__ void __launch_bounds__(PromptCfg<D>::THREADS, 1)
+template <int D, bool BF16, bool Q4>
+__global__ void __launch_bounds__(PromptCfg<D, Q4>::THREADS, 1)
     paged_prompt_kernel(const __grid_constant__ PagedPromptParams pp,
                         const __grid_constant__ CUtensorMap kmap,
                         const __grid_constant__ CUtensorMap vmap) {
-  using C = PromptCfg<D>;
+  using C = PromptCfg<D, Q4>;
   constexpr int N = C::N, NRAW = C::NRAW, NT = C::NT;
   const PagedAttnParams& p = pp.a;
   extern __shared__ uint8_t smem_raw[];
@@ -401,7 +402,7 @@ __global__ void __launch_bounds__(PromptCfg<D>::THREADS, 1)
     if (warp == 12) {
       // ================================================================ loader
       const int box = p.box_rows, nbox = N / box;
-      const uint32_t box_bytes = static_cast<uint32_t>(box) * D;
+      const uint32_t box_bytes = static_cast<uint32_t>(box) * C::ROW;
       int raw = 0;  // raw tiles requested so far
       int pend = 0;
       // lane l holds granule l % 8 of tile l / 8 of a batch of four tiles
@@ -426,26 +427,28 @@ __global__ void __launch_bounds__(PromptCfg<D>::THREADS, 1)
         if (lane / 8 == i % 4) {
           const int tok = it.t0 + i * N + lane % 8 * 16;
           float ks = 0.f, vs = 1.f;
-          if (page >= 0) {
+          if (!Q4 && page >= 0) {
             const size_t at = static_cast<size_t>(page) * p.H + it.h;
             ks = p.k_scale[at];
             vs = p.v_scale[at];
           }
           const bool seen = page >= 0 && tok < it.hi && tok + 16 > it.lo;
           recs[i % C::NREC * C::REC + lane % 8] =
-              make_float4(ks, lg2(vs), kWeightInv / vs, seen ? 1.f : 0.f);
+              Q4 ? make_float4(1.f, 0.f, kWeightInv, seen ? 1.f : 0.f)
+                 : make_float4(ks, lg2(vs), kWeightInv / vs, seen ? 1.f : 0.f);
           const uint32_t m = 0xffu << (lane & 24);
           const uint32_t all = __ballot_sync(m, seen);
           if (lane % 8 == 0) whole[i % C::NREC] = all == m;
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&rec_full[i % C::NREC]);
-        // lane l < nbox copies box l of the tile
-        const int src = (i % 4) * 8 + (lane < nbox ? lane : 0) * (box / 16);
+        // lane l < nbox copies box l of the tile, lane 8 + l its metadata
+        const int bx = Q4 ? lane & 7 : lane;
+        const int src = (i % 4) * 8 + (bx < nbox ? bx : 0) * (box / 16);
         const int pg = __shfl_sync(0xffffffffu, page, src);
-        const bool mine = lane < nbox && pg >= 0;
+        const bool mine = bx < nbox && (!Q4 || lane < 16) && pg >= 0;
         const int count = __popc(__ballot_sync(0xffffffffu, mine));
-        const int tok = it.t0 + i * N + lane * box;
+        const int tok = it.t0 + i * N + bx * box;
         const int row = mine ? ((pg * p.H + it.h) << p.lg_ps) + (tok & ((1 << p.lg_ps) - 1)) : 0;
 #pragma unroll
         for (int side = 0; side < 2; ++side, ++raw) {
@@ -454,11 +457,16 @@ __global__ void __launch_bounds__(PromptCfg<D>::THREADS, 1)
             ok = false;
             break;
           }
-          if (lane == 0) mbar_arrive_expect_tx(&raw_full[s], count * box_bytes);
+          if (lane == 0)
+            mbar_arrive_expect_tx(&raw_full[s], Q4 ? count / 2 * (box_bytes + box_bytes / 4) : count * box_bytes);
           __syncwarp();
-          if (mine)
-            tma_load_2d(smem + C::OFF_RAW + s * C::RAW + lane * box_bytes, side ? &vmap : &kmap, 0,
-                        row, &raw_full[s]);
+          uint8_t* dst = smem + C::OFF_RAW + s * C::RAW;
+          if (mine && (!Q4 || lane < 8)) {
+            tma_load_2d(dst + bx * box_bytes, side ? &vmap : &kmap, 0, row, &raw_full[s]);
+          } else if (mine) {
+            bulk_g2s(dst + N * C::ROW + bx * (box_bytes / 4), p.meta[side] + static_cast<size_t>(row) * (D / kGroup4),
+                     box_bytes / 4, &raw_full[s]);
+          }
           pend = raw + 1;
         }
       }
@@ -532,36 +540,69 @@ __global__ void __launch_bounds__(PromptCfg<D>::THREADS, 1)
       const int tok = it.t0 + i * N;
       // rows of no page or no token may hold anything: they become zeros
       const bool edge = tok < it.lo || tok + N > it.hi || !whole[i % C::NREC];
-#pragma unroll 4
-      for (int k = 0; k < PASS; ++k) {
-        int row, j;
-        if constexpr (D == 128) {
-          // eight lanes read two half rows and write two half rows, all on
-          // different banks
-          const int u = k * 16 + (ct >> 3);  // (row pair, half) of the tile
-          const int pair = u >> 1, flip = u & 1;
-          row = pair * 2 + ((ct >> 2) & 1);
-          j = (ct & 3) + 4 * (((ct >> 2) & 1) ^ flip);
-        } else {
-          row = k * 32 + (ct >> 2);
-          j = ct & 3;
-        }
-        const int sw = D == 128 ? (j ^ (row & 7)) : (j ^ ((row >> 1) & 3));
-        uint4 v = *reinterpret_cast<const uint4*>(src + row * D + (sw << 4));
+      if constexpr (Q4) {
+        // A thread takes a row: eight lanes read eight chunks and write eight, all
+        // on different banks.  A word of a key is eight channels in order; a word
+        // of a value its channels j and j + 4 in pairs, an order that the output
+        // undoes.
+        const int row = ct;
+        uint32_t m[D / 32];
+#pragma unroll
+        for (int w = 0; w < D / 32; ++w) m[w] = reinterpret_cast<const uint32_t*>(src + N * C::ROW + row * (D / 8))[w];
         if (edge) {
           const int tk = tok + row;
-          if (tk < it.lo || tk >= it.hi || recs[i % C::NREC * C::REC + (row >> 4)].w == 0.f)
-            v = make_uint4(0, 0, 0, 0);
+          if (tk < it.lo || tk >= it.hi || recs[i % C::NREC * C::REC + (row >> 4)].w == 0.f) {
+#pragma unroll
+            for (int w = 0; w < D / 32; ++w) m[w] = 0;
+          }
         }
-        uint4 lo, hi;
-        e4m3x4_to_half2x2(v.x, lo.x, lo.y);
-        e4m3x4_to_half2x2(v.y, lo.z, lo.w);
-        e4m3x4_to_half2x2(v.z, hi.x, hi.y);
-        e4m3x4_to_half2x2(v.w, hi.z, hi.w);
-        uint8_t* o = dst + (j >> 2) * (N * 128) + row * 128;
-        const int c0 = (j & 3) * 2;
-        *reinterpret_cast<uint4*>(o + ((c0 ^ (row & 7)) << 4)) = lo;
-        *reinterpret_cast<uint4*>(o + (((c0 + 1) ^ (row & 7)) << 4)) = hi;
+#pragma unroll
+        for (int w = 0; w < D / 32; ++w) {
+          const int sw = D == 128 ? w ^ ((row >> 1) & 3) : w ^ ((row >> 2) & 1);
+          const uint4 v = *reinterpret_cast<const uint4*>(src + row * C::ROW + (sw << 4));
+          const uint32_t x[4] = {v.x, v.y, v.z, v.w};
+          const uint32_t step = __byte_perm(m[w], m[w], 0x1010), least = __byte_perm(m[w], m[w], 0x3232);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            uint32_t o[4];
+            values4(x[j], step, least, o);
+            const int ch = 4 * w + j;  // chunk of eight channels
+            *reinterpret_cast<uint4*>(dst + (ch >> 3) * (N * 128) + row * 128 + (((ch & 7) ^ (row & 7)) << 4)) =
+                make_uint4(o[0], o[1], o[2], o[3]);
+          }
+        }
+      } else {
+#pragma unroll 4
+        for (int k = 0; k < PASS; ++k) {
+          int row, j;
+          if constexpr (D == 128) {
+            // eight lanes read two half rows and write two half rows, all on
+            // different banks
+            const int u = k * 16 + (ct >> 3);  // (row pair, half) of the tile
+            const int pair = u >> 1, flip = u & 1;
+            row = pair * 2 + ((ct >> 2) & 1);
+            j = (ct & 3) + 4 * (((ct >> 2) & 1) ^ flip);
+          } else {
+            row = k * 32 + (ct >> 2);
+            j = ct & 3;
+          }
+          const int sw = D == 128 ? (j ^ (row & 7)) : (j ^ ((row >> 1) & 3));
+          uint4 v = *reinterpret_cast<const uint4*>(src + row * D + (sw << 4));
+          if (edge) {
+            const int tk = tok + row;
+            if (tk < it.lo || tk >= it.hi || recs[i % C::NREC * C::REC + (row >> 4)].w == 0.f)
+              v = make_uint4(0, 0, 0, 0);
+          }
+          uint4 lo, hi;
+          e4m3x4_to_half2x2(v.x, lo.x, lo.y);
+          e4m3x4_to_half2x2(v.y, lo.z, lo.w);
+          e4m3x4_to_half2x2(v.z, hi.x, hi.y);
+          e4m3x4_to_half2x2(v.w, hi.z, hi.w);
+          uint8_t* o = dst + (j >> 2) * (N * 128) + row * 128;
+          const int c0 = (j & 3) * 2;
+          *reinterpret_cast<uint4*>(o + ((c0 ^ (row & 7)) << 4)) = lo;
+          *reinterpret_cast<uint4*>(o + (((c0 + 1) ^ (row & 7)) << 4)) = hi;
+        }
       }
       fence_async_shared();
       __syncwarp();
@@ -769,7 +810,9 @@ __global__ void __launch_bounds__(PromptCfg<D>::THREADS, 1)
           tmem_wait_ld();
 #pragma unroll
           for (int k = 0; k < 16; ++k) {
-            const float x = __uint_as_float(r[2 * k]) * inv, y = __uint_as_float(r[2 * k + 1]) * inv;
+            // (4-bit values: columns 2j and 2j + 1 of eight are channels j and j + 4)
+            const int at = Q4 ? (k & ~3) * 2 + 4 * (k & 1) + (k >> 1 & 1) : 2 * k, next = at + (Q4 ? 2 : 1);
+            const float x = __uint_as_float(r[at]) * inv, y = __uint_as_float(r[next]) * inv;
             if constexpr (BF16) {
               const __nv_bfloat162 b = __floats2bfloat162_rn(x, y);
               o[k] = *reinterpret_cast<const uint32_t*>(&b);
@@ -813,11 +856,11 @@ __global__ void __launch_bounds__(PromptCfg<D>::THREADS, 1)
   }
 }
 
-template <int D, bool BF16>
+template <int D, bool BF16, bool Q4>
 cudaError_t launch_paged_prompt_t(const PagedPromptParams& p, const CUtensorMap& km,
                                   const CUtensorMap& vm, cudaStream_t st) {
-  using C = PromptCfg<D>;
-  auto fn = paged_prompt_kernel<D, BF16>;
+  using C = PromptCfg<D, Q4>;
+  auto fn = paged_prompt_kernel<D, BF16, Q4>;
   const cudaError_t e = allow_smem(reinterpret_cast<const void*>(fn), C::SMEM);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
