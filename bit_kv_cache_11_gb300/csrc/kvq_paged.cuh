@@ -182,7 +182,7 @@ cudaError_t launch_paged4_prompt(const PagedAttnParams& a, int items_max, const 
 cudaError_t allow_smem(const void* fn, int bytes);
 // Warps per CTA of the decode kernel, its most CTAs (one per SM of a GB300) and
 // the tokens of a unit.
-constexpr int paged_warps(int) { return 8; }
+constexpr int paged_warps(int nt, bool four) { return four && nt == 1 ? 12 : 8; }
 constexpr int kPagedMaxCtas = 152;
 // A request with at most this many query rows per kv head (new tokens * R) is
 // served by the decode kernel, which splits its tokens over all SMs and reads

@@ -44,15 +44,22 @@ __device__ __forceinline__ uint32_t pair_hi(uint32_t a, uint32_t b) { return __b
 __device__ __forceinline__ __half2 as_half2(uint32_t x) { return *reinterpret_cast<const __half2*>(&x); }
 __device__ __forceinline__ uint32_t as_word(__half2 x) { return *reinterpret_cast<const uint32_t*>(&x); }
 
+// (x & mask) | bits in one operation.
+__device__ __forceinline__ uint32_t and_or(uint32_t x, uint32_t mask, uint32_t bits) {
+  uint32_t y;
+  asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(y) : "r"(x), "r"(mask), "r"(bits));
+  return y;
+}
+
 // The four code pairs of a word, (bits 4j .., bits 4j + 16 ..), j = 0 .. 3, as values
-// code * step + least, rounded once.  A code below 16 in the mantissa of 1024 is
-// 1024 + code, four bits higher 1024 + 16 code: one operation on the pair gives
-// the code itself, exactly.
+// code * step + least, rounded once.  A code in the mantissa of 1024 is 1024 + code,
+// four bits higher 1024 + 16 code: one operation on the pair gives the code
+// itself, exactly.
 __device__ __forceinline__ void values4(uint32_t w, uint32_t step, uint32_t least, uint32_t (&v)[4]) {
   const __half2 minus = __float2half2_rn(-1024.f), sixteenth = __float2half2_rn(0.0625f), less = __float2half2_rn(-64.f);
 #pragma unroll
   for (int j = 0; j < 4; j += 2, w >>= 8) {
-    const uint32_t lo = (w & 0x000f000fu) | 0x64006400u, hi = (w & 0x00f000f0u) | 0x64006400u;
+    const uint32_t lo = and_or(w, 0x000f000fu, 0x64006400u), hi = and_or(w, 0x00f000f0u, 0x64006400u);
     v[j] = as_word(__hfma2(__hadd2(as_half2(lo), minus), as_half2(step), as_half2(least)));
     v[j + 1] = as_word(__hfma2(__hfma2(as_half2(hi), sixteenth, less), as_half2(step), as_half2(least)));
   }

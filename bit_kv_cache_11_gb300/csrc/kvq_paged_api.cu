@@ -122,7 +122,8 @@ constexpr size_t part_floats(int rg, int D) { return static_cast<size_t>(rg) * (
 size_t workspace_bytes(int D) {
   size_t most = 0;  // per CTA: a slot for each warp and two of its own
   for (int nt = 1; nt <= 2; ++nt)
-    most = std::max(most, (paged_warps(nt) + 2) * part_floats(8 * nt, D) * sizeof(float));
+    for (const bool four : {false, true})
+      most = std::max(most, (paged_warps(nt, four) + 2) * part_floats(8 * nt, D) * sizeof(float));
   return kTicketBytes + kPagedMaxCtas * most;
 }
 static_assert(kPagedMaxCtas * sizeof(int) <= kTicketBytes, "a ticket per CTA");
@@ -204,7 +205,7 @@ kvq_status attention(const kvq_paged_pool* pool, bool four, const void* q, int d
   p.window = window;
   p.row_min = 1;
   p.row_max = turn;
-  p.n_warps = std::min(sms, kPagedMaxCtas) * paged_warps(nt);
+  p.n_warps = std::min(sms, kPagedMaxCtas) * paged_warps(nt, four);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   p.tickets = reinterpret_cast<int*>(ws);
   p.warp_part = reinterpret_cast<float*>(ws + kTicketBytes);
