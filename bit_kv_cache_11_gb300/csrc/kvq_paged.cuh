@@ -39,22 +39,6 @@ struct PagedPlanParams {
   int* err;
 };
 
-struct PagedStoreParams {
-  uint8_t* pages[2];  // K, V: [n_pages][H][ps][D]
-  float* scale[2];    // [n_pages][H]
-  const void* x[2];   // k, v: token t, head h at t * stride + h * D
-  long long stride[2];
-  const int* slots;
-  int n_tokens;
-  int n_pages, H, lg_ps;
-  int chunk;  // tokens a CTA looks at
-  int* err;
-  // kvq_paged_append: keys turn by their tokens' angles [n_tokens][rot / 2]
-  // (rot 0: they are stored as they are)
-  const float2* angles;
-  int rot, interleaved;
-};
-
 // Attention over the pages.  Work is a flat sequence of units: request b's
 // query rows (row r = new token r / R, query head r % R of the kv head's
 // group) form groups of RG rows, and item (b, kv head, group) owns nu_b
@@ -163,7 +147,6 @@ __device__ __forceinline__ int first_seen(const PagedAttnParams& p, const PagedR
 }
 
 cudaError_t launch_paged_plan(const PagedPlanParams& p, cudaStream_t st);
-cudaError_t launch_paged_store(const PagedStoreParams& p, int D, int dtype, cudaStream_t st);
 cudaError_t paged_decode_d64(const PagedAttnParams& p, const CUtensorMap& km, const CUtensorMap& vm,
                              bool bf16, int nt, cudaStream_t st);
 cudaError_t paged_decode_d128(const PagedAttnParams& p, const CUtensorMap& km,

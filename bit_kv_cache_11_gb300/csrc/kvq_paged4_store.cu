@@ -4,7 +4,8 @@
 //
 // Per token, kv head and group of 32 channels, x fp16 within +-65408:
 //   step = fp16((mx - mn) / 15),  code = rint((x - mn) / step) in [0, 15]
-// A thread holds eight channels, four threads a group.
+// A thread holds eight channels (a word of codes), four threads a group, and
+// several words' loads are on their way at once.
 #include <algorithm>
 
 #include "kvq_paged4.cuh"
@@ -13,138 +14,194 @@ namespace kvq {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kWords = 2;  // of a thread at a time
 
-// A pair of 16-bit values as fp16 pair within +-kMost4, NaN as 0; *odd when one
-// of them is infinite or NaN.
+// A pair of 16-bit values as an fp16 pair within +-kMost4, NaN as 0.
 template <bool BF16>
-__device__ __forceinline__ uint32_t as_fp16(uint32_t w, bool* odd) {
+__device__ __forceinline__ uint32_t as_fp16(uint32_t w) {
   float2 f = pair_to_float2<BF16>(w);
-  *odd |= !isfinite(f.x) || !isfinite(f.y);
   f.x = f.x == f.x ? fminf(fmaxf(f.x, -kMost4), kMost4) : 0.f;
   f.y = f.y == f.y ? fminf(fmaxf(f.y, -kMost4), kMost4) : 0.f;
-  const __half2 h = __floats2half2_rn(f.x, f.y);
-  return *reinterpret_cast<const uint32_t*>(&h);
+  return as_word(__floats2half2_rn(f.x, f.y));
 }
 
 // rint(d / step) where the quotient is rounded to fp32 before.
-__device__ __forceinline__ int code_of(float d, float step) {
+__device__ __forceinline__ uint32_t code_of(float d, float step) {
   return step > 0.f ? min(max(__float2int_rn(__fdiv_rn(d, step)), 0), 15) : 0;
 }
 
-template <int D, bool BF16>
-__global__ void __launch_bounds__(kThreads) paged4_append_kernel(const Paged4StoreParams p, long long kv_items,
-                                                                 long long items) {
-  constexpr int VPR = D / 8;
-  grid_dep_wait();
-  grid_dep_launch();
-  const long long i = static_cast<long long>(blockIdx.x) * kThreads + threadIdx.x;
-  if (i >= items) return;
-  if (i >= kv_items) {
-    const long long k = i - kv_items;
-    const long long per = static_cast<long long>(p.q.n_heads) * p.q.units;
-    const long long t = k / per;
-    const int r = static_cast<int>(k - t * per), h = r / p.q.units;
-    rotate_unit<BF16>(p.q, t, h, r - h * p.q.units);
-    return;
-  }
-  // (kv_items is a multiple of 32: a warp is all here)
-  const long long per = 2LL * p.H * VPR;
-  const long long t = i / per;
-  const bool real = t < p.n_tokens;
-  const int r = static_cast<int>(i - t * per);
-  const int side = r >= p.H * VPR, rh = r - side * p.H * VPR, h = rh / VPR, vec = rh - h * VPR;
-  const int slot = real ? p.slots[t] : -1;
-  const int page = slot >> p.lg_ps, row = slot & ((1 << p.lg_ps) - 1);
-  const bool good = slot >= 0 && page < p.n_pages;
-  if (slot >= 0 && !good && r == 0) set_err(p.err, KVQ_PAGED_ERR_BAD_PAGE);
-  uint4 v = make_uint4(0, 0, 0, 0);
-  if (good) {
-    const uint16_t* head = static_cast<const uint16_t*>(side ? p.x[1] : p.x[0]) +
-                           t * (side ? p.stride[1] : p.stride[0]) + h * D;
-    v = __ldg(reinterpret_cast<const uint4*>(head) + vec);
-    if (side == 0 && p.rot > 0)
-      v = turned_chunk<BF16>(v, head, vec, p.angles + t * (p.rot >> 1), p.rot, p.interleaved);
-  }
-  bool odd = false;
-  const uint32_t w[4] = {as_fp16<BF16>(v.x, &odd), as_fp16<BF16>(v.y, &odd), as_fp16<BF16>(v.z, &odd),
-                         as_fp16<BF16>(v.w, &odd)};
-  if (odd) set_err(p.err, KVQ_PAGED_ERR_NONFINITE);
-  float x[8];
+// The word of codes and the {step, minimum} pair of eight channels v, whose group
+// is the four lanes of a quad.  *odd: a value is infinite or NaN.
+template <bool BF16, bool KEY>
+__device__ __forceinline__ uint32_t quantize8(uint4 v, uint32_t quad, uint32_t* meta, bool* odd) {
+  uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  // largest magnitudes: beyond kMost4 (bf16: its largest number below) the
+  // values need a look each
+  uint32_t m2 = 0;
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const float2 f = pair_to_float2<false>(w[j]);
-    x[2 * j] = f.x;
-    x[2 * j + 1] = f.y;
-  }
-  float mn = x[0], mx = x[0];
+  for (int j = 0; j < 4; ++j) m2 = __vmaxu2(m2, w[j] & 0x7fff7fffu);
+  const uint32_t mag = max(m2 & 0xffffu, m2 >> 16);
+  *odd = mag >= (BF16 ? 0x7f80u : 0x7c00u);
+  if (mag > (BF16 ? 0x477fu : 0x7bfcu)) {
 #pragma unroll
-  for (int j = 1; j < 8; ++j) {
-    mn = fminf(mn, x[j]);
-    mx = fmaxf(mx, x[j]);
-  }
+    for (int j = 0; j < 4; ++j) w[j] = as_fp16<BF16>(w[j]);
+  } else if constexpr (BF16) {
 #pragma unroll
-  for (int o = 1; o < 4; o <<= 1) {
-    mn = fminf(mn, __shfl_xor_sync(0xffffffffu, mn, o));
-    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+    for (int j = 0; j < 4; ++j) {
+      const float2 f = pair_to_float2<true>(w[j]);
+      w[j] = as_word(__floats2half2_rn(f.x, f.y));
+    }
   }
-  if (!good) return;
-  mn += 0.f;  // (a minimum or a range of -0 is stored as 0)
-  const __half sh = __float2half_rn(__fdiv_rn(mx - mn + 0.f, 15.f));
+  const __half2 lo2 = __hmin2(__hmin2(as_half2(w[0]), as_half2(w[1])), __hmin2(as_half2(w[2]), as_half2(w[3])));
+  const __half2 hi2 = __hmax2(__hmax2(as_half2(w[0]), as_half2(w[1])), __hmax2(as_half2(w[2]), as_half2(w[3])));
+  // (minimum, -maximum) in one word for the quad
+  __half2 both = __halves2half2(__hmin(__low2half(lo2), __high2half(lo2)), __hneg(__hmax(__low2half(hi2), __high2half(hi2))));
+#pragma unroll
+  for (int o = 1; o < 4; o <<= 1) both = __hmin2(both, as_half2(__shfl_xor_sync(quad, as_word(both), o)));
+  // (a minimum or a range of -0 is stored as 0)
+  const float mn = __low2float(both) + 0.f, range = -__high2float(both) - mn + 0.f;
+  const __half sh = __float2half_rn(__fdiv_rn(range, 15.f));
   const float step = __half2float(sh);
+  *meta = as_word(__halves2half2(sh, __float2half_rn(mn)));
+  // rint by the fp32 numbers around 1.5 * 2^23, whose last bit is 1; a quotient
+  // near a tie (the reciprocal errs by 2^-18 of a step at most) is divided out.
+  constexpr float kRint = 12582912.f;
+  const float inv = step > 0.f ? __frcp_rn(step) : 0.f;
+  float d[8], tie = 0.f;
   uint32_t word = 0;
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
-    const uint32_t c = code_of(x[j] - mn, step);
-    word |= c << (side ? 4 * j : 4 * (j >> 1) + 16 * (j & 1));
+    const float2 f = __half22float2(as_half2(w[j >> 1]));
+    d[j] = (j & 1 ? f.y : f.x) - mn;
+    const float r = fmaf(d[j], inv, kRint);
+    tie = fmaxf(tie, fabsf(fmaf(d[j], inv, kRint - r)));
+    const uint32_t c = __float_as_uint(fminf(r, kRint + 15.f)) & 15u;
+    word |= c << (KEY ? 4 * (j >> 1) + 16 * (j & 1) : 4 * j);
   }
-  const size_t at = (((static_cast<size_t>(page) * p.H + h) << p.lg_ps) + row);
-  *reinterpret_cast<uint32_t*>((side ? p.codes[1] : p.codes[0]) + at * (D / 2) + vec * 4) = word;
-  if ((vec & 3) == 0) {
-    const __half2 m = __halves2half2(sh, __float2half_rn(mn));
-    (side ? p.meta[1] : p.meta[0])[at * (D / kGroup4) + (vec >> 2)] = *reinterpret_cast<const uint32_t*>(&m);
+  if (tie > 0.5f - 0x1p-16f) {
+    word = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) word |= code_of(d[j], step) << (KEY ? 4 * (j >> 1) + 16 * (j & 1) : 4 * j);
+  }
+  return word;
+}
+
+struct Grid4 {
+  int tokens;         // of a CTA
+  Divisor per;  // words of a token and side
+  unsigned kv_ctas;
+};
+
+template <int D, bool BF16>
+__device__ __forceinline__ void append_tokens(const Paged4StoreParams& p, const Grid4& g, long long t0, int tid) {
+  constexpr int VPR = D / 8;
+  const int n = static_cast<int>(min(static_cast<long long>(g.tokens), p.n_tokens - t0));
+  const uint32_t per = 2 * g.per.d, total = static_cast<uint32_t>(n) * per;
+  const uint32_t quad = 0xfu << (tid & 28);
+  for (uint32_t i0 = 0; i0 < total; i0 += kWords * kThreads) {
+    uint4 v[kWords];
+    size_t at[kWords];  // row of the pool
+    int vec[kWords];
+    bool good[kWords], key[kWords];
+#pragma unroll
+    for (int k = 0; k < kWords; ++k) {
+      const uint32_t i = i0 + k * kThreads + tid;
+      good[k] = false;
+      if (i >= total) continue;  // (whole quads)
+      const uint32_t st = i / g.per, r = i - st * g.per.d, t = st >> 1, side = st & 1;
+      const uint32_t h = r / VPR;
+      vec[k] = r - h * VPR;
+      key[k] = side == 0;
+      const int slot = p.slots[t0 + t];
+      const int page = slot >> p.lg_ps;
+      good[k] = slot >= 0 && page < p.n_pages;
+      if (slot >= 0 && !good[k] && r == 0) set_err(p.err, KVQ_PAGED_ERR_BAD_PAGE);
+      if (!good[k]) continue;
+      at[k] = ((static_cast<size_t>(page) * p.H + h) << p.lg_ps) + (slot & ((1 << p.lg_ps) - 1));
+      const uint16_t* head = static_cast<const uint16_t*>(side ? p.x[1] : p.x[0]) +
+                             (t0 + t) * (side ? p.stride[1] : p.stride[0]) + h * D;
+      v[k] = __ldg(reinterpret_cast<const uint4*>(head) + vec[k]);
+      if (key[k] && p.rot > 0)
+        v[k] = turned_chunk<BF16>(v[k], head, vec[k], p.angles + (t0 + t) * (p.rot >> 1), p.rot, p.interleaved);
+    }
+#pragma unroll
+    for (int k = 0; k < kWords; ++k) {
+      if (!good[k]) continue;
+      bool odd;
+      uint32_t meta;
+      const uint32_t word = key[k] ? quantize8<BF16, true>(v[k], quad, &meta, &odd)
+                                   : quantize8<BF16, false>(v[k], quad, &meta, &odd);
+      if (odd) set_err(p.err, KVQ_PAGED_ERR_NONFINITE);
+      const int side = key[k] ? 0 : 1;
+      *reinterpret_cast<uint32_t*>(p.codes[side] + at[k] * (D / 2) + vec[k] * 4) = word;
+      if ((vec[k] & 3) == 0) p.meta[side][at[k] * (D / kGroup4) + (vec[k] >> 2)] = meta;
+    }
+  }
+}
+
+template <int D, bool BF16, RotateKind KIND>
+__global__ void __launch_bounds__(kThreads) paged4_append_kernel(const Paged4StoreParams p, const Grid4 g) {
+  grid_dep_wait();
+  grid_dep_launch();
+  if (blockIdx.x < g.kv_ctas) {
+    append_tokens<D, BF16>(p, g, static_cast<long long>(blockIdx.x) * g.tokens, threadIdx.x);
+  } else {
+    rotate_tokens<BF16, KIND, kThreads>(p.q, static_cast<long long>(blockIdx.x - g.kv_ctas) * p.q.tokens, threadIdx.x);
   }
 }
 
 template <int D>
-__global__ void __launch_bounds__(kThreads) paged4_read_kernel(const Paged4ReadParams p, long long items) {
-  constexpr int VPR = D / 8;
+__global__ void __launch_bounds__(kThreads) paged4_read_kernel(const Paged4ReadParams p, const Grid4 g) {
+  constexpr int VPR = D / 8, U = 4;
   grid_dep_wait();
   grid_dep_launch();
-  const long long i = static_cast<long long>(blockIdx.x) * kThreads + threadIdx.x;
-  if (i >= items) return;
-  const long long per = 2LL * p.H * VPR;
-  const long long t = i / per;
-  const int r = static_cast<int>(i - t * per);
-  const int side = r >= p.H * VPR, rh = r - side * p.H * VPR, h = rh / VPR, vec = rh - h * VPR;
-  uint16_t* out = side ? p.out[1] : p.out[0];
-  if (out == nullptr) return;
-  const int slot = p.slots[t];
-  const int page = slot >> p.lg_ps, row = slot & ((1 << p.lg_ps) - 1);
-  uint32_t o[4] = {0, 0, 0, 0};
-  if (slot >= 0 && page >= p.n_pages) {
-    if (r == 0 || (p.out[0] == nullptr && rh == 0)) set_err(p.err, KVQ_PAGED_ERR_BAD_PAGE);
-  } else if (slot >= 0) {
-    const size_t at = (((static_cast<size_t>(page) * p.H + h) << p.lg_ps) + row);
-    const uint32_t word = *reinterpret_cast<const uint32_t*>((side ? p.codes[1] : p.codes[0]) + at * (D / 2) + vec * 4);
-    const uint32_t m = (side ? p.meta[1] : p.meta[0])[at * (D / kGroup4) + (vec >> 2)];
-    const __half2 sm = *reinterpret_cast<const __half2*>(&m);
-    const __half2 s2 = __low2half2(sm), m2 = __high2half2(sm);
+  const long long t0 = static_cast<long long>(blockIdx.x) * g.tokens;
+  const int n = static_cast<int>(min(static_cast<long long>(g.tokens), p.n_tokens - t0));
+  const uint32_t total = static_cast<uint32_t>(n) * 2 * g.per.d;
+  for (uint32_t i0 = threadIdx.x; i0 < total; i0 += U * kThreads) {
+    uint32_t word[U], meta[U];
+    uint4* out[U];
+    bool key[U];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      // codes of channels 2j, 2j + 1 in the halves' low bits
-      const uint32_t w = side ? (word >> (8 * j) & 0xfu) | (word >> (8 * j + 4) & 0xfu) << 16 : word >> (4 * j);
-      const __half2 x = __hfma2(codes_to_half2(w), s2, m2);
-      o[j] = *reinterpret_cast<const uint32_t*>(&x);
+    for (int k = 0; k < U; ++k) {
+      const uint32_t i = i0 + k * kThreads;
+      out[k] = nullptr;
+      word[k] = meta[k] = 0;
+      if (i >= total) continue;
+      const uint32_t st = i / g.per, r = i - st * g.per.d, t = st >> 1, side = st & 1;
+      uint16_t* to = side ? p.out[1] : p.out[0];
+      if (to == nullptr) continue;
+      const uint32_t h = r / VPR, vec = r - h * VPR;
+      out[k] = reinterpret_cast<uint4*>(to + ((t0 + t) * p.H + h) * D) + vec;
+      key[k] = side == 0;
+      const int slot = p.slots[t0 + t];
+      const int page = slot >> p.lg_ps;
+      if (slot < 0) continue;
+      if (page >= p.n_pages) {
+        if (r == 0) set_err(p.err, KVQ_PAGED_ERR_BAD_PAGE);
+        continue;
+      }
+      const size_t at = ((static_cast<size_t>(page) * p.H + h) << p.lg_ps) + (slot & ((1 << p.lg_ps) - 1));
+      word[k] = __ldg(reinterpret_cast<const uint32_t*>((side ? p.codes[1] : p.codes[0]) + at * (D / 2)) + vec);
+      meta[k] = __ldg((side ? p.meta[1] : p.meta[0]) + at * (D / kGroup4) + (vec >> 2));
+    }
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+      if (out[k] == nullptr) continue;
+      uint32_t o[4];
+      values4(word[k], pair_lo(meta[k], meta[k]), pair_hi(meta[k], meta[k]), o);
+      // a key's pairs are neighbours, a value's are channels j and j + 4
+      *out[k] = key[k] ? make_uint4(o[0], o[1], o[2], o[3])
+                       : make_uint4(pair_lo(o[0], o[1]), pair_lo(o[2], o[3]), pair_hi(o[0], o[1]), pair_hi(o[2], o[3]));
     }
   }
-  *(reinterpret_cast<uint4*>(out + (static_cast<size_t>(t) * p.H + h) * D) + vec) = make_uint4(o[0], o[1], o[2], o[3]);
 }
 
 template <typename... K, typename... A>
-cudaError_t launch(void (*fn)(K...), long long items, cudaStream_t st, A... args) {
-  if (items > static_cast<long long>(kThreads) * 0x7fffffff) return cudaErrorInvalidValue;
+cudaError_t launch(void (*fn)(K...), long long ctas, cudaStream_t st, A... args) {
+  if (ctas > 0x7fffffff) return cudaErrorInvalidValue;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>((items + kThreads - 1) / kThreads));
+  cfg.gridDim = dim3(static_cast<unsigned>(ctas));
   cfg.blockDim = dim3(kThreads);
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
@@ -155,23 +212,41 @@ cudaError_t launch(void (*fn)(K...), long long items, cudaStream_t st, A... args
   return cudaLaunchKernelEx(&cfg, fn, args...);
 }
 
+// CTAs that take the tokens' words: a few rounds each, fewer while that leaves
+// SMs idle.
+Grid4 grid_of(int n_tokens, int H, int D, int rounds) {
+  const long long per = 2LL * H * (D / 8), all = per * n_tokens;
+  const long long want = std::min<long long>(static_cast<long long>(rounds) * kThreads, std::max<long long>(kThreads, all / (152 * 4)));
+  Grid4 g = {};
+  g.tokens = static_cast<int>(std::max<long long>(1, std::min<long long>(want / per, n_tokens)));
+  g.per = divisor(static_cast<uint32_t>(per / 2), per * g.tokens);
+  g.kv_ctas = static_cast<unsigned>((n_tokens + g.tokens - 1) / g.tokens);
+  return g;
+}
+
+template <int D, bool BF16>
+cudaError_t append(Paged4StoreParams p, cudaStream_t st) {
+  const Grid4 g = grid_of(p.n_tokens, p.H, D, 4 * kWords);
+  const long long ctas = g.kv_ctas + (p.q.n_heads ? rotate_ctas(&p.q, kThreads) : 0);
+  switch (p.q.n_heads ? rotate_kind(p.q.rot, p.q.interleaved) : kInterleaved) {
+    case kInterleaved: return launch(paged4_append_kernel<D, BF16, kInterleaved>, ctas, st, p, g);
+    case kHalves: return launch(paged4_append_kernel<D, BF16, kHalves>, ctas, st, p, g);
+    default: return launch(paged4_append_kernel<D, BF16, kSingle>, ctas, st, p, g);
+  }
+}
+
 }  // namespace
 
 cudaError_t launch_paged4_append(const Paged4StoreParams& p, int D, int dtype, cudaStream_t st) {
-  const long long kv = (static_cast<long long>(p.n_tokens) * 2 * p.H * (D / 8) + 31) / 32 * 32;
-  const long long items = kv + static_cast<long long>(p.n_tokens) * p.q.n_heads * p.q.units;
   const bool bf = dtype == KVQ_DTYPE_BF16;
-  if (D == 128)
-    return bf ? launch(paged4_append_kernel<128, true>, items, st, p, kv, items)
-              : launch(paged4_append_kernel<128, false>, items, st, p, kv, items);
-  return bf ? launch(paged4_append_kernel<64, true>, items, st, p, kv, items)
-            : launch(paged4_append_kernel<64, false>, items, st, p, kv, items);
+  if (D == 128) return bf ? append<128, true>(p, st) : append<128, false>(p, st);
+  return bf ? append<64, true>(p, st) : append<64, false>(p, st);
 }
 
 cudaError_t launch_paged4_read(const Paged4ReadParams& p, int D, cudaStream_t st) {
-  const long long items = static_cast<long long>(p.n_tokens) * 2 * p.H * (D / 8);
-  return D == 128 ? launch(paged4_read_kernel<128>, items, st, p, items)
-                  : launch(paged4_read_kernel<64>, items, st, p, items);
+  const Grid4 g = grid_of(p.n_tokens, p.H, D, 16);
+  return D == 128 ? launch(paged4_read_kernel<128>, g.kv_ctas, st, p, g)
+                  : launch(paged4_read_kernel<64>, g.kv_ctas, st, p, g);
 }
 
 }  // namespace kvq

@@ -282,6 +282,7 @@ kvq_status store_params(PagedStoreParams* p, const kvq_paged_pool* pool, const v
   p->err = device_error;
   p->angles = nullptr;
   p->rot = p->interleaved = 0;
+  p->q.n_heads = 0;
   return KVQ_OK;
 }
 
@@ -374,25 +375,16 @@ kvq_status kvq_paged_append(const kvq_paged_pool* pool, const kvq_rotary* rotary
   if (s != KVQ_OK) return s;
   s = check_rotary(rotary, pool->head_dim, n_tokens);
   if (s != KVQ_OK) return s;
-  RotateParams r;
-  const bool queries = q != nullptr || q_out != nullptr || n_q_heads != 0;
-  if (queries) {
+  if (q != nullptr || q_out != nullptr || n_q_heads != 0) {
     if (n_q_heads < 1) return KVQ_ERR_INVALID_ARG;
-    s = rotate_params(&r, rotary, q, dtype, q_stride, q_out, q_out_stride, n_tokens, n_q_heads, pool->head_dim);
+    s = rotate_params(&p.q, rotary, q, dtype, q_stride, q_out, q_out_stride, n_tokens, n_q_heads, pool->head_dim);
     if (s != KVQ_OK) return s;
   }
   if (n_tokens == 0) return KVQ_OK;
   p.angles = reinterpret_cast<const float2*>(rotary->angles);
   p.rot = rotary->rotary_dim;
   p.interleaved = rotary->interleaved;
-  s = store(p, pool->head_dim, dtype, stream);
-  if (s != KVQ_OK || !queries) return s;
-  if (launch_rotate(r, dtype, static_cast<cudaStream_t>(stream)) != cudaSuccess) {
-    cudaGetLastError();
-    return KVQ_ERR_CUDA;
-  }
-  count_launches(1);
-  return KVQ_OK;
+  return store(p, pool->head_dim, dtype, stream);
 }
 
 kvq_status kvq_paged_workspace_bytes(const kvq_paged_pool* pool, size_t* bytes) {

@@ -288,7 +288,7 @@ constexpr int kSteps = 8;
 constexpr int kShortChunks = 8192;
 
 template <int D, bool BF16, bool ROT, int TEAM>
-__global__ void __launch_bounds__(chunk_threads<TEAM>(), 1024 / chunk_threads<TEAM>())
+__global__ void __launch_bounds__(chunk_threads<TEAM>(), (ROT ? 768 : 1024) / chunk_threads<TEAM>())
     paged_store_kernel(const PagedStoreParams p) {
   constexpr int THREADS = chunk_threads<TEAM>(), TEAMS = THREADS / (2 * TEAM);
   constexpr int VPR = D / 8, RPS = TEAM / VPR, CHUNK = TEAM * 64 / D * TEAMS;  // the most
@@ -304,6 +304,13 @@ __global__ void __launch_bounds__(chunk_threads<TEAM>(), 1024 / chunk_threads<TE
   if (tid == 0) s_count = 0;
   grid_dep_wait();
   grid_dep_launch();
+  if constexpr (ROT) {
+    if (h >= p.H) {  // the step's queries
+      const long long t0 = (static_cast<long long>(h - p.H) * gridDim.x + blockIdx.x) * p.q.tokens;
+      if (t0 < p.q.n_tokens) rotate_any<BF16, THREADS>(p.q, t0, tid);
+      return;
+    }
+  }
   __syncthreads();
   if (tid < p.chunk) {
     const int t = tb + tid;
@@ -426,6 +433,11 @@ cudaError_t launch_team(PagedStoreParams p, cudaStream_t st) {
   p.chunk = static_cast<long long>(p.n_tokens) * p.H <= kShortChunks ? 8 : most;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((p.n_tokens + p.chunk - 1) / p.chunk, p.H);
+  if (ROT && p.q.n_heads > 0) {
+    const long long ctas = rotate_ctas(&p.q, THREADS);
+    cfg.gridDim.y += static_cast<unsigned>((ctas + cfg.gridDim.x - 1) / cfg.gridDim.x);
+    if (cfg.gridDim.y > 65535) return cudaErrorInvalidValue;
+  }
   cfg.blockDim = dim3(THREADS);
   cfg.stream = st;
   cudaLaunchAttribute attr[1];

@@ -29,39 +29,48 @@ __device__ __forceinline__ float2 unit_of(uint64_t phase) {
   return make_float2(quarter == 1 || quarter == 2 ? -a : a, quarter & 2 ? -b : b);
 }
 
+// A thread takes V neighbouring pairs of a token and every gridDim.x * rows-th
+// token, so that the frequencies are read once.
+template <int V>
 __global__ void __launch_bounds__(kThreads) rotary_angles_kernel(const AnglesParams p) {
+  const uint32_t row = threadIdx.x / p.lanes, k = (threadIdx.x - row * p.lanes.d) * V;
+  const uint32_t rows = kThreads / p.lanes;
   grid_dep_wait();
   grid_dep_launch();
-  const long long n = static_cast<long long>(p.n_tokens) * p.half;
-  for (long long i = static_cast<long long>(blockIdx.x) * kThreads + threadIdx.x; i < n;
-       i += static_cast<long long>(gridDim.x) * kThreads) {
-    const int t = static_cast<int>(i / p.half), k = static_cast<int>(i - static_cast<long long>(t) * p.half);
-    const float2 u = unit_of(static_cast<uint64_t>(static_cast<int64_t>(p.positions[t])) *
-                             static_cast<uint64_t>(p.turns[k]));
-    p.angles[i] = make_float2(u.x * p.magnitude, u.y * p.magnitude);
+  if (row >= rows) return;
+  uint64_t turn[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) turn[i] = static_cast<uint64_t>(p.turns[k + i]);
+  const long long step = static_cast<long long>(gridDim.x) * rows;
+#pragma unroll 4
+  for (long long t = static_cast<long long>(blockIdx.x) * rows + row; t < p.n_tokens; t += step) {
+    const uint64_t pos = static_cast<uint64_t>(static_cast<int64_t>(p.positions[t]));
+    float2 u[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      u[i] = unit_of(pos * turn[i]);
+      u[i].x *= p.magnitude;
+      u[i].y *= p.magnitude;
+    }
+    float2* out = p.angles + t * p.half + k;
+    if constexpr (V == 2) *reinterpret_cast<float4*>(out) = make_float4(u[0].x, u[0].y, u[1].x, u[1].y);
+    else *out = u[0];
   }
 }
 
 // ---- rotate ---------------------------------------------------------------------
 
-template <bool BF16>
+template <bool BF16, RotateKind KIND>
 __global__ void __launch_bounds__(kThreads) rotate_kernel(const RotateParams p) {
   grid_dep_wait();
   grid_dep_launch();
-  const long long per = static_cast<long long>(p.n_heads) * p.units;
-  const long long n = p.n_tokens * per;
-  for (long long i = static_cast<long long>(blockIdx.x) * kThreads + threadIdx.x; i < n;
-       i += static_cast<long long>(gridDim.x) * kThreads) {
-    const long long t = i / per;
-    const int r = static_cast<int>(i - t * per), h = r / p.units;
-    rotate_unit<BF16>(p, t, h, r - h * p.units);
-  }
+  rotate_tokens<BF16, KIND, kThreads>(p, static_cast<long long>(blockIdx.x) * p.tokens, threadIdx.x);
 }
 
 template <typename P>
-cudaError_t launch(void (*fn)(P), const P& p, long long items, cudaStream_t st) {
+cudaError_t launch(void (*fn)(P), const P& p, long long ctas, cudaStream_t st) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(std::min<long long>((items + kThreads - 1) / kThreads, 1 << 20)));
+  cfg.gridDim = dim3(static_cast<unsigned>(ctas));
   cfg.blockDim = dim3(kThreads);
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
@@ -70,6 +79,16 @@ cudaError_t launch(void (*fn)(P), const P& p, long long items, cudaStream_t st) 
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, fn, p);
+}
+
+template <bool BF16>
+cudaError_t launch_kind(RotateParams p, cudaStream_t st) {
+  const long long ctas = rotate_ctas(&p, kThreads);
+  switch (rotate_kind(p.rot, p.interleaved)) {
+    case kInterleaved: return launch(rotate_kernel<BF16, kInterleaved>, p, ctas, st);
+    case kHalves: return launch(rotate_kernel<BF16, kHalves>, p, ctas, st);
+    default: return launch(rotate_kernel<BF16, kSingle>, p, ctas, st);
+  }
 }
 
 bool dev_ptr(const void* p, uintptr_t a) { return p != nullptr && (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
@@ -103,17 +122,24 @@ kvq_status rotate_params(RotateParams* p, const kvq_rotary* rotary, const void* 
   p->D = head_dim;
   p->rot = rotary->rotary_dim;
   p->interleaved = rotary->interleaved;
-  p->units = rotate_units(head_dim, rotary->rotary_dim, rotary->interleaved);
+  p->units.d = rotate_units(head_dim, rotary->rotary_dim, rotary->interleaved);
+  const long long per = static_cast<long long>(n_heads) * p->units.d;
+  if (per > 1 << 28) return KVQ_ERR_UNSUPPORTED;
+  p->per.d = static_cast<uint32_t>(per);
   return KVQ_OK;
 }
 
-cudaError_t launch_rotary_angles(const AnglesParams& p, cudaStream_t st) {
-  return launch(rotary_angles_kernel, p, static_cast<long long>(p.n_tokens) * p.half, st);
+cudaError_t launch_rotary_angles(AnglesParams p, cudaStream_t st) {
+  const int v = p.half % 2 == 0 ? 2 : 1, lanes = p.half / v;  // (at most 128 pairs: 256 threads hold a token)
+  p.lanes = divisor(lanes, kThreads + 1);
+  const int rows = kThreads / lanes;
+  // four tokens a thread where there are many
+  const long long ctas = std::min<long long>((p.n_tokens + rows - 1) / rows, std::max<long long>(152 * 8, (p.n_tokens + 4LL * rows - 1) / (4 * rows)));
+  return v == 2 ? launch(rotary_angles_kernel<2>, p, ctas, st) : launch(rotary_angles_kernel<1>, p, ctas, st);
 }
 
 cudaError_t launch_rotate(const RotateParams& p, int dtype, cudaStream_t st) {
-  const long long items = static_cast<long long>(p.n_tokens) * p.n_heads * p.units;
-  return dtype == KVQ_DTYPE_BF16 ? launch(rotate_kernel<true>, p, items, st) : launch(rotate_kernel<false>, p, items, st);
+  return dtype == KVQ_DTYPE_BF16 ? launch_kind<true>(p, st) : launch_kind<false>(p, st);
 }
 
 }  // namespace kvq

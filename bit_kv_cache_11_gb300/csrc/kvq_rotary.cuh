@@ -3,9 +3,23 @@
 // Internal to csrc/.
 #pragma once
 
+#include <algorithm>
+
 #include "kvq_paged.cuh"
 
 namespace kvq {
+
+// Quotients by one divisor: ceil(2^32 / d) overshoots n / d by less than n / 2^32,
+// below 1 / d while n * d < 2^32 (m = 0 beyond, or for d = 1: a plain division).
+struct Divisor {
+  uint32_t d, m;
+};
+inline Divisor divisor(uint32_t d, unsigned long long most) {
+  return {d, d > 1 && most * d < 1ull << 32 ? static_cast<uint32_t>(((1ull << 32) + d - 1) / d) : 0};
+}
+__device__ __forceinline__ uint32_t operator/(uint32_t n, const Divisor& v) {
+  return v.m ? __umulhi(n, v.m) : n / v.d;
+}
 
 // x -> out, heads of D channels whose first `rot` turn by angles
 // [token][rot / 2] (cos, sin).
@@ -17,19 +31,24 @@ struct RotateParams {
   int n_tokens, n_heads, D;
   int rot;          // even
   int interleaved;
-  int units;        // of a head, rotate_units()
+  int tokens;       // of a CTA
+  Divisor per, units;  // units of a token and of a head
 };
 
 // A unit of a head is what one thread turns: the channels of whole pairs, so
 // that out may be x itself.  Where the layout's chunks of eight channels are
-// aligned (rotate_aligned) a unit is
-//   interleaved   one chunk, its four pairs or (from rot on) its copy
-//   half          two chunks of eight pairs, or a chunk to copy
-// and else four pairs of single channels, or eight channels to copy.
+// aligned a unit is
+//   kInterleaved  one chunk, its four pairs or (from rot on) its copy
+//   kHalves       two chunks of eight pairs, or a chunk to copy
+// and else (kSingle) four pairs of single channels, or eight channels to copy.
+enum RotateKind { kInterleaved, kHalves, kSingle };
 inline __host__ __device__ bool rotate_aligned(int rot, int interleaved) {
   return rot % (interleaved ? 8 : 16) == 0;
 }
-inline __host__ __device__ int rotate_units(int D, int rot, int interleaved) {
+inline RotateKind rotate_kind(int rot, int interleaved) {
+  return !rotate_aligned(rot, interleaved) ? kSingle : interleaved ? kInterleaved : kHalves;
+}
+inline int rotate_units(int D, int rot, int interleaved) {
   if (!rotate_aligned(rot, interleaved)) return (rot / 2 + 3) / 4 + (D - rot + 7) / 8;
   return interleaved ? D / 8 : rot / 16 + (D - rot) / 8;
 }
@@ -147,49 +166,104 @@ __device__ __forceinline__ uint4 turned_chunk(uint4 own, const uint16_t* head, i
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// Unit u of head h of token t.
-template <bool BF16>
-__device__ __forceinline__ void rotate_unit(const RotateParams& p, long long t, int h, int u) {
-  const uint16_t* x = p.x + t * p.x_stride + static_cast<long long>(h) * p.D;
-  uint16_t* out = p.out + t * p.out_stride + static_cast<long long>(h) * p.D;
-  const float2* a = p.angles + t * (p.rot >> 1);
-  const bool aligned = rotate_aligned(p.rot, p.interleaved);
-  const bool copies = x != out;
-  if (aligned && p.interleaved) {
-    if (8 * u < p.rot || copies) {
-      uint4 v = *reinterpret_cast<const uint4*>(x + 8 * u);
-      if (8 * u < p.rot) v = turn_interleaved<BF16>(v, a + 4 * u);
-      *reinterpret_cast<uint4*>(out + 8 * u) = v;
-    }
-    return;
-  }
+// The units of tokens [t0, t0 + p.tokens) by a CTA's THREADS threads, U at a time
+// a thread so that as many loads are on their way.
+template <bool BF16, RotateKind KIND, int THREADS>
+__device__ __forceinline__ void rotate_tokens(const RotateParams& p, long long t0, int tid) {
+  constexpr int U = KIND == kSingle ? 1 : 4;
+  const int n = static_cast<int>(min(static_cast<long long>(p.tokens), p.n_tokens - t0));
+  const uint32_t total = static_cast<uint32_t>(n) * p.per.d;
   const int half = p.rot >> 1;
-  if (aligned) {
-    if (u < p.rot / 16) {
-      uint4 va = *reinterpret_cast<const uint4*>(x + 8 * u), vb = *reinterpret_cast<const uint4*>(x + half + 8 * u);
-      turn_halves<BF16>(va, vb, a + 8 * u);
-      *reinterpret_cast<uint4*>(out + 8 * u) = va;
-      *reinterpret_cast<uint4*>(out + half + 8 * u) = vb;
-    } else if (copies) {
-      const int c = p.rot + 8 * (u - p.rot / 16);
-      *reinterpret_cast<uint4*>(out + c) = *reinterpret_cast<const uint4*>(x + c);
+  const bool copies = p.x != p.out;
+  for (uint32_t i0 = tid; i0 < total; i0 += U * THREADS) {
+    const uint16_t* x[U];
+    uint16_t* out[U];
+    const float2* a[U];
+    int c[U];
+    uint4 va[U], vb[U];
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+      const uint32_t i = min(i0 + k * THREADS, total - 1);
+      const uint32_t t = i / p.per, r = i - t * p.per.d, h = r / p.units, u = r - h * p.units.d;
+      x[k] = p.x + (t0 + t) * p.x_stride + h * p.D;
+      out[k] = p.out + (t0 + t) * p.out_stride + h * p.D;
+      a[k] = p.angles + (t0 + t) * half;
+      c[k] = static_cast<int>(u);
+      if constexpr (KIND == kInterleaved) {
+        c[k] = 8 * c[k];
+        va[k] = *reinterpret_cast<const uint4*>(x[k] + c[k]);
+      } else if constexpr (KIND == kHalves) {
+        c[k] = c[k] < p.rot / 16 ? 8 * c[k] : p.rot + 8 * (c[k] - p.rot / 16);
+        va[k] = *reinterpret_cast<const uint4*>(x[k] + c[k]);
+        if (c[k] < half) vb[k] = *reinterpret_cast<const uint4*>(x[k] + c[k] + half);
+      }
     }
-    return;
-  }
-  const int turning = (half + 3) / 4;
-  if (u < turning) {
-    for (int i = 4 * u; i < min(4 * u + 4, half); ++i) {
-      const int ca = p.interleaved ? 2 * i : i, cb = p.interleaved ? 2 * i + 1 : i + half;
-      const float xa = one_to_float<BF16>(x[ca]), xb = one_to_float<BF16>(x[cb]);
-      const float2 cs = __ldg(a + i);
-      out[ca] = float_to_one<BF16>(turn_a(xa, xb, cs));
-      out[cb] = float_to_one<BF16>(turn_b(xa, xb, cs));
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+      if (i0 + k * THREADS >= total) break;
+      if constexpr (KIND == kSingle) {
+        const int turning = (half + 3) / 4;
+        if (c[k] < turning) {
+          for (int i = 4 * c[k]; i < min(4 * c[k] + 4, half); ++i) {
+            const int ca = p.interleaved ? 2 * i : i, cb = p.interleaved ? 2 * i + 1 : i + half;
+            const float xa = one_to_float<BF16>(x[k][ca]), xb = one_to_float<BF16>(x[k][cb]);
+            const float2 cs = __ldg(a[k] + i);
+            out[k][ca] = float_to_one<BF16>(turn_a(xa, xb, cs));
+            out[k][cb] = float_to_one<BF16>(turn_b(xa, xb, cs));
+          }
+        } else if (copies) {
+          const int c0 = p.rot + 8 * (c[k] - turning);
+          for (int j = c0; j < min(c0 + 8, p.D); ++j) out[k][j] = x[k][j];
+        }
+        continue;
+      }
+      const bool turns = c[k] < p.rot;
+      if constexpr (KIND == kInterleaved) {
+        if (turns) va[k] = turn_interleaved<BF16>(va[k], a[k] + (c[k] >> 1));
+      } else if (turns) {
+        turn_halves<BF16>(va[k], vb[k], a[k] + c[k]);
+        *reinterpret_cast<uint4*>(out[k] + c[k] + half) = vb[k];
+      }
+      if (turns || copies) *reinterpret_cast<uint4*>(out[k] + c[k]) = va[k];
     }
-  } else if (copies) {
-    const int c0 = p.rot + 8 * (u - turning);
-    for (int c = c0; c < min(c0 + 8, p.D); ++c) out[c] = x[c];
   }
 }
+
+// The same where the kind is known at run time only.
+template <bool BF16, int THREADS>
+__device__ __forceinline__ void rotate_any(const RotateParams& p, long long t0, int tid) {
+  if (!rotate_aligned(p.rot, p.interleaved)) rotate_tokens<BF16, kSingle, THREADS>(p, t0, tid);
+  else if (p.interleaved) rotate_tokens<BF16, kInterleaved, THREADS>(p, t0, tid);
+  else rotate_tokens<BF16, kHalves, THREADS>(p, t0, tid);
+}
+
+// CTAs of `threads` that turn p's heads: enough units a CTA for every thread's
+// loads in flight, fewer while that leaves SMs idle.
+inline long long rotate_ctas(RotateParams* p, int threads) {
+  const long long per = p->per.d, all = per * p->n_tokens;
+  const long long want = std::min<long long>(8 * threads, std::max<long long>(threads, all / (152 * 4)));
+  p->tokens = static_cast<int>(std::max<long long>(1, std::min<long long>(want / per, p->n_tokens)));
+  p->per = divisor(p->per.d, per * p->tokens);
+  p->units = divisor(p->units.d, per);
+  return (p->n_tokens + p->tokens - 1) / p->tokens;
+}
+
+struct PagedStoreParams {
+  uint8_t* pages[2];  // K, V: [n_pages][H][ps][D]
+  float* scale[2];    // [n_pages][H]
+  const void* x[2];   // k, v: token t, head h at t * stride + h * D
+  long long stride[2];
+  const int* slots;
+  int n_tokens;
+  int n_pages, H, lg_ps;
+  int chunk;  // tokens a CTA looks at
+  int* err;
+  // kvq_paged_append: keys turn by their tokens' angles [n_tokens][rot / 2]
+  // (rot 0: they are stored as they are)
+  const float2* angles;
+  int rot, interleaved;
+  RotateParams q;  // the step's queries; n_heads 0: none
+};
 
 struct AnglesParams {
   const int* positions;
@@ -197,6 +271,7 @@ struct AnglesParams {
   float2* angles;
   int n_tokens, half;
   float magnitude;
+  Divisor lanes;  // threads of a token
 };
 
 // Checks a rotary description against heads of head_dim (KVQ_ERR_INVALID_ARG).
@@ -204,7 +279,8 @@ kvq_status check_rotary(const kvq_rotary* r, int head_dim, int n_tokens);
 // Fills *p after checking the arguments of a call that turns heads.
 kvq_status rotate_params(RotateParams* p, const kvq_rotary* rotary, const void* x, int dtype, long long x_stride,
                          void* out, long long out_stride, int n_tokens, int n_heads, int head_dim);
-cudaError_t launch_rotary_angles(const AnglesParams& p, cudaStream_t st);
+cudaError_t launch_rotary_angles(AnglesParams p, cudaStream_t st);
+cudaError_t launch_paged_store(const PagedStoreParams& p, int D, int dtype, cudaStream_t st);
 cudaError_t launch_rotate(const RotateParams& p, int dtype, cudaStream_t st);
 
 }  // namespace kvq
