@@ -4,8 +4,7 @@
 //
 // Per token, kv head and group of 32 channels, x fp16 within +-65408:
 //   step = fp16((mx - mn) / 15),  code = rint((x - mn) / step) in [0, 15]
-// A thread holds eight channels (a word of codes), four threads a group, and
-// several words' loads are on their way at once.
+// A thread holds 16 channels, half a group.
 #include <algorithm>
 
 #include "kvq_paged4.cuh"
@@ -14,7 +13,6 @@ namespace kvq {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kWords = 2;  // of a thread at a time
 
 // A pair of 16-bit values as an fp16 pair within +-kMost4, NaN as 0.
 template <bool BF16>
@@ -25,117 +23,175 @@ __device__ __forceinline__ uint32_t as_fp16(uint32_t w) {
   return as_word(__floats2half2_rn(f.x, f.y));
 }
 
-// rint(d / step) where the quotient is rounded to fp32 before.
-__device__ __forceinline__ uint32_t code_of(float d, float step) {
-  return step > 0.f ? min(max(__float2int_rn(__fdiv_rn(d, step)), 0), 15) : 0;
+// range / 15 correctly rounded: with y = 1 / 15 rounded, q + (range - 15 q) y is
+// (Markstein's theorem; range is 0 or at least 2^-24, so nothing underflows).
+__device__ __forceinline__ float fifteenth(float range) {
+  constexpr float y = 1.f / 15.f;
+  const float q = range * y;
+  return fmaf(fmaf(-15.f, q, range), y, q);
+}
+__device__ __forceinline__ float about_inverse(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
 
-// The word of codes and the {step, minimum} pair of eight channels v, whose group
-// is the four lanes of a quad.  *odd: a value is infinite or NaN.
+__device__ __forceinline__ float2 twice(float x) { return make_float2(x, x); }
+
+// Smallest and largest of eight pairs; NaN where one of them is.
+template <bool BF16>
+__device__ __forceinline__ float2 bounds(const uint32_t (&w)[8]) {
+  if constexpr (BF16) {
+    auto b2 = [](uint32_t x) { return *reinterpret_cast<const __nv_bfloat162*>(&x); };
+    __nv_bfloat162 lo = b2(w[0]), hi = lo;
+#pragma unroll
+    for (int j = 1; j < 8; ++j) {
+      lo = __hmin2_nan(lo, b2(w[j]));
+      hi = __hmax2_nan(hi, b2(w[j]));
+    }
+    return make_float2(__bfloat162float(__hmin_nan(__low2bfloat16(lo), __high2bfloat16(lo))),
+                       __bfloat162float(__hmax_nan(__low2bfloat16(hi), __high2bfloat16(hi))));
+  } else {
+    __half2 lo = as_half2(w[0]), hi = lo;
+#pragma unroll
+    for (int j = 1; j < 8; ++j) {
+      lo = __hmin2_nan(lo, as_half2(w[j]));
+      hi = __hmax2_nan(hi, as_half2(w[j]));
+    }
+    return make_float2(__half2float(__hmin_nan(__low2half(lo), __high2half(lo))),
+                       __half2float(__hmax_nan(__low2half(hi), __high2half(hi))));
+  }
+}
+
+// The two words of codes of 16 channels w and the {step, minimum} pair of their
+// group, whose other half the lane's neighbour holds.  *odd: one of the 16 is
+// infinite or NaN.
 template <bool BF16, bool KEY>
-__device__ __forceinline__ uint32_t quantize8(uint4 v, uint32_t quad, uint32_t* meta, bool* odd) {
-  uint32_t w[4] = {v.x, v.y, v.z, v.w};
-  // largest magnitudes: beyond kMost4 (bf16: its largest number below) the
-  // values need a look each
-  uint32_t m2 = 0;
+__device__ __forceinline__ uint2 quantize16(uint32_t (&w)[8], uint32_t pair, uint32_t* meta, bool* odd) {
+  float2 b = bounds<BF16>(w);
+  *odd = false;
+  if (!(b.x >= -kMost4 && b.y <= kMost4)) {  // beyond the bounds, infinite or NaN
+    *odd = !isfinite(b.x) || !isfinite(b.y);
 #pragma unroll
-  for (int j = 0; j < 4; ++j) m2 = __vmaxu2(m2, w[j] & 0x7fff7fffu);
-  const uint32_t mag = max(m2 & 0xffffu, m2 >> 16);
-  *odd = mag >= (BF16 ? 0x7f80u : 0x7c00u);
-  if (mag > (BF16 ? 0x477fu : 0x7bfcu)) {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) w[j] = as_fp16<BF16>(w[j]);
+    for (int j = 0; j < 8; ++j) w[j] = as_fp16<BF16>(w[j]);
+    b = bounds<false>(w);
   } else if constexpr (BF16) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    for (int j = 0; j < 8; ++j) {
       const float2 f = pair_to_float2<true>(w[j]);
       w[j] = as_word(__floats2half2_rn(f.x, f.y));
     }
+    // (rounding keeps the order)
+    b = make_float2(__half2float(__float2half_rn(b.x)), __half2float(__float2half_rn(b.y)));
   }
-  const __half2 lo2 = __hmin2(__hmin2(as_half2(w[0]), as_half2(w[1])), __hmin2(as_half2(w[2]), as_half2(w[3])));
-  const __half2 hi2 = __hmax2(__hmax2(as_half2(w[0]), as_half2(w[1])), __hmax2(as_half2(w[2]), as_half2(w[3])));
-  // (minimum, -maximum) in one word for the quad
-  __half2 both = __halves2half2(__hmin(__low2half(lo2), __high2half(lo2)), __hneg(__hmax(__low2half(hi2), __high2half(hi2))));
-#pragma unroll
-  for (int o = 1; o < 4; o <<= 1) both = __hmin2(both, as_half2(__shfl_xor_sync(quad, as_word(both), o)));
   // (a minimum or a range of -0 is stored as 0)
-  const float mn = __low2float(both) + 0.f, range = -__high2float(both) - mn + 0.f;
-  const __half sh = __float2half_rn(__fdiv_rn(range, 15.f));
+  const float mn = fminf(b.x, __shfl_xor_sync(pair, b.x, 1)) + 0.f;
+  const float range = fmaxf(b.y, __shfl_xor_sync(pair, b.y, 1)) - mn + 0.f;
+  const __half sh = __float2half_rn(fifteenth(range));
   const float step = __half2float(sh);
   *meta = as_word(__halves2half2(sh, __float2half_rn(mn)));
-  // rint by the fp32 numbers around 1.5 * 2^23, whose last bit is 1; a quotient
-  // near a tie (the reciprocal errs by 2^-18 of a step at most) is divided out.
+  // rint by the fp32 numbers around 1.5 * 2^23, whose last bit is 1 and whose bits
+  // are this one's plus the code.  `far` is the largest distance of a difference
+  // from its code's multiple of the step (exact): up to half a step, less what the
+  // reciprocal errs by, the code is the nearest.  A tie, or a step that is no
+  // normal fp16 number and so may be far too small, needs another look.
   constexpr float kRint = 12582912.f;
-  const float inv = step > 0.f ? __frcp_rn(step) : 0.f;
-  float d[8], tie = 0.f;
-  uint32_t word = 0;
+  constexpr uint32_t kBits = 0x4b400000u, kAll = 0x11111111u;
+  const float inv = step > 0.f ? about_inverse(step) : 0.f;
+  float far = 0.f;
+  uint32_t o[2];
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const float2 f = __half22float2(as_half2(w[j >> 1]));
-    d[j] = (j & 1 ? f.y : f.x) - mn;
-    const float r = fmaf(d[j], inv, kRint);
-    tie = fmaxf(tie, fabsf(fmaf(d[j], inv, kRint - r)));
-    const uint32_t c = __float_as_uint(fminf(r, kRint + 15.f)) & 15u;
-    word |= c << (KEY ? 4 * (j >> 1) + 16 * (j & 1) : 4 * j);
-  }
-  if (tie > 0.5f - 0x1p-16f) {
-    word = 0;
+  for (int c = 0; c < 2; ++c) {
+    uint32_t word = 0u - kBits * kAll;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) word |= code_of(d[j], step) << (KEY ? 4 * (j >> 1) + 16 * (j & 1) : 4 * j);
+    for (int j = 0; j < 4; ++j) {
+      const float2 d = add2(__half22float2(as_half2(w[4 * c + j])), twice(-mn));
+      const float2 r = fma2(d, twice(inv), twice(kRint));
+      const float2 e = fma2(add2(r, twice(-kRint)), twice(-step), d);
+      far = fmaxf(far, fmaxf(fabsf(e.x), fabsf(e.y)));
+      word += __float_as_uint(r.x) << (KEY ? 4 * j : 8 * j);
+      word += __float_as_uint(r.y) << (KEY ? 4 * j + 16 : 8 * j + 4);
+    }
+    o[c] = word;
   }
-  return word;
+  if (step > 0.f && (far > 0.49999f * step || step < 0x1p-14f)) {
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      o[c] = 0;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float2 f = __half22float2(as_half2(w[4 * c + (j >> 1)]));
+        const float d = (j & 1 ? f.y : f.x) - mn;
+        float code = rintf(d * inv);
+        const float e = fmaf(-code, step, d);
+        // an exact tie goes to the even code; near one (or far off) divide
+        if (fabsf(e) == 0.5f * step && step >= 0x1p-14f) {
+          code += static_cast<int>(code) & 1 ? copysignf(1.f, e) : 0.f;
+        } else if (fabsf(e) > 0.49999f * step) {
+          code = rintf(__fdiv_rn(d, step));
+        }
+        o[c] |= static_cast<uint32_t>(min(static_cast<int>(code), 15)) << (KEY ? 4 * (j >> 1) + 16 * (j & 1) : 4 * j);
+      }
+    }
+  }
+  return make_uint2(o[0], o[1]);
 }
 
 struct Grid4 {
-  int tokens;         // of a CTA
-  Divisor per;  // words of a token and side
+  int tokens;  // of a CTA
+  Divisor per;  // threads of a token and side
   unsigned kv_ctas;
 };
 
+// Channels c .. c + 7 of a key at `head`, in `own`, after the turn by angles a.
+template <bool BF16>
+__device__ __forceinline__ uint4 turned(uint4 own, const uint16_t* head, int c, const float2* a, int rot, int interleaved) {
+  if (c >= rot) return own;
+  const int half = rot >> 1;
+  if (!rotate_aligned(rot, interleaved)) return turn_single<BF16>(own, head, c, a, rot, interleaved);
+  if (interleaved) return turn_interleaved<BF16>(own, a + (c >> 1));
+  const int oc = c < half ? c + half : c - half;
+  const float sign = c < oc ? -1.f : 1.f;
+  const uint4 other = __ldg(reinterpret_cast<const uint4*>(head + oc));
+  a += min(c, oc);
+  return make_uint4(turn_own<BF16>(own.x, other.x, angles2(a), sign), turn_own<BF16>(own.y, other.y, angles2(a + 2), sign),
+                    turn_own<BF16>(own.z, other.z, angles2(a + 4), sign), turn_own<BF16>(own.w, other.w, angles2(a + 6), sign));
+}
+
+// Tokens [t0, t0 + g.tokens): a thread takes 16 channels, half a group.
 template <int D, bool BF16>
 __device__ __forceinline__ void append_tokens(const Paged4StoreParams& p, const Grid4& g, long long t0, int tid) {
-  constexpr int VPR = D / 8;
+  constexpr int TPR = D / 16;  // threads of a row
   const int n = static_cast<int>(min(static_cast<long long>(g.tokens), p.n_tokens - t0));
-  const uint32_t per = 2 * g.per.d, total = static_cast<uint32_t>(n) * per;
-  const uint32_t quad = 0xfu << (tid & 28);
-  for (uint32_t i0 = 0; i0 < total; i0 += kWords * kThreads) {
-    uint4 v[kWords];
-    size_t at[kWords];  // row of the pool
-    int vec[kWords];
-    bool good[kWords], key[kWords];
+  const uint32_t total = static_cast<uint32_t>(n) * 2 * g.per.d;
+  const uint32_t pair = 3u << (tid & 30);
+  for (uint32_t i = tid; i < total; i += kThreads) {
+    const uint32_t st = i / g.per, r = i - st * g.per.d, t = st >> 1, side = st & 1;
+    const uint32_t h = r / TPR, c = 16 * (r - h * TPR);
+    const uint16_t* head = static_cast<const uint16_t*>(side ? p.x[1] : p.x[0]) +
+                           (t0 + t) * (side ? p.stride[1] : p.stride[0]) + h * D;
+    const int slot = p.slots[t0 + t];
+    uint4 v[2];
 #pragma unroll
-    for (int k = 0; k < kWords; ++k) {
-      const uint32_t i = i0 + k * kThreads + tid;
-      good[k] = false;
-      if (i >= total) continue;  // (whole quads)
-      const uint32_t st = i / g.per, r = i - st * g.per.d, t = st >> 1, side = st & 1;
-      const uint32_t h = r / VPR;
-      vec[k] = r - h * VPR;
-      key[k] = side == 0;
-      const int slot = p.slots[t0 + t];
-      const int page = slot >> p.lg_ps;
-      good[k] = slot >= 0 && page < p.n_pages;
-      if (slot >= 0 && !good[k] && r == 0) set_err(p.err, KVQ_PAGED_ERR_BAD_PAGE);
-      if (!good[k]) continue;
-      at[k] = ((static_cast<size_t>(page) * p.H + h) << p.lg_ps) + (slot & ((1 << p.lg_ps) - 1));
-      const uint16_t* head = static_cast<const uint16_t*>(side ? p.x[1] : p.x[0]) +
-                             (t0 + t) * (side ? p.stride[1] : p.stride[0]) + h * D;
-      v[k] = __ldg(reinterpret_cast<const uint4*>(head) + vec[k]);
-      if (key[k] && p.rot > 0)
-        v[k] = turned_chunk<BF16>(v[k], head, vec[k], p.angles + (t0 + t) * (p.rot >> 1), p.rot, p.interleaved);
-    }
+    for (int j = 0; j < 2; ++j) v[j] = __ldg(reinterpret_cast<const uint4*>(head + c + 8 * j));
+    if (side == 0 && p.rot > 0) {
+      const float2* a = p.angles + (t0 + t) * (p.rot >> 1);
 #pragma unroll
-    for (int k = 0; k < kWords; ++k) {
-      if (!good[k]) continue;
-      bool odd;
-      uint32_t meta;
-      const uint32_t word = key[k] ? quantize8<BF16, true>(v[k], quad, &meta, &odd)
-                                   : quantize8<BF16, false>(v[k], quad, &meta, &odd);
-      if (odd) set_err(p.err, KVQ_PAGED_ERR_NONFINITE);
-      const int side = key[k] ? 0 : 1;
-      *reinterpret_cast<uint32_t*>(p.codes[side] + at[k] * (D / 2) + vec[k] * 4) = word;
-      if ((vec[k] & 3) == 0) p.meta[side][at[k] * (D / kGroup4) + (vec[k] >> 2)] = meta;
+      for (int j = 0; j < 2; ++j) v[j] = turned<BF16>(v[j], head, c + 8 * j, a, p.rot, p.interleaved);
     }
+    const int page = slot >> p.lg_ps;
+    if (slot < 0) continue;
+    if (page >= p.n_pages) {
+      if (r == 0) set_err(p.err, KVQ_PAGED_ERR_BAD_PAGE);
+      continue;
+    }
+    uint32_t w[8] = {v[0].x, v[0].y, v[0].z, v[0].w, v[1].x, v[1].y, v[1].z, v[1].w}, meta;
+    bool odd;
+    const uint2 codes = side ? quantize16<BF16, false>(w, pair, &meta, &odd) : quantize16<BF16, true>(w, pair, &meta, &odd);
+    if (odd) set_err(p.err, KVQ_PAGED_ERR_NONFINITE);
+    const size_t at = (((static_cast<size_t>(page) * p.H + h) << p.lg_ps) + (slot & ((1 << p.lg_ps) - 1))) * (D / 2) + c / 2;
+    *reinterpret_cast<uint2*>((side ? p.codes[1] : p.codes[0]) + at) = codes;
+    if ((c & 16) == 0) (side ? p.meta[1] : p.meta[0])[at / 16] = meta;
   }
 }
 
@@ -143,10 +199,13 @@ template <int D, bool BF16, RotateKind KIND>
 __global__ void __launch_bounds__(kThreads) paged4_append_kernel(const Paged4StoreParams p, const Grid4 g) {
   grid_dep_wait();
   grid_dep_launch();
-  if (blockIdx.x < g.kv_ctas) {
-    append_tokens<D, BF16>(p, g, static_cast<long long>(blockIdx.x) * g.tokens, threadIdx.x);
+  // CTAs for keys and values lie evenly among those for the step's queries, so that
+  // the ones' arithmetic runs beside the others' traffic
+  const unsigned kv = static_cast<unsigned>(static_cast<unsigned long long>(blockIdx.x) * g.kv_ctas / gridDim.x);
+  if ((static_cast<unsigned long long>(blockIdx.x) + 1) * g.kv_ctas / gridDim.x != kv) {
+    append_tokens<D, BF16>(p, g, static_cast<long long>(kv) * g.tokens, threadIdx.x);
   } else {
-    rotate_tokens<BF16, KIND, kThreads>(p.q, static_cast<long long>(blockIdx.x - g.kv_ctas) * p.q.tokens, threadIdx.x);
+    rotate_tokens<BF16, KIND, kThreads, kAppendHeads>(p.q, static_cast<long long>(blockIdx.x - kv) * p.q.tokens, threadIdx.x);
   }
 }
 
@@ -212,10 +271,10 @@ cudaError_t launch(void (*fn)(K...), long long ctas, cudaStream_t st, A... args)
   return cudaLaunchKernelEx(&cfg, fn, args...);
 }
 
-// CTAs that take the tokens' words: a few rounds each, fewer while that leaves
-// SMs idle.
-Grid4 grid_of(int n_tokens, int H, int D, int rounds) {
-  const long long per = 2LL * H * (D / 8), all = per * n_tokens;
+// CTAs that take `per` threads' work a token: `rounds` of it each, fewer while that
+// leaves SMs idle.
+Grid4 grid_of(int n_tokens, long long per, int rounds) {
+  const long long all = per * n_tokens;
   const long long want = std::min<long long>(static_cast<long long>(rounds) * kThreads, std::max<long long>(kThreads, all / (152 * 4)));
   Grid4 g = {};
   g.tokens = static_cast<int>(std::max<long long>(1, std::min<long long>(want / per, n_tokens)));
@@ -226,8 +285,8 @@ Grid4 grid_of(int n_tokens, int H, int D, int rounds) {
 
 template <int D, bool BF16>
 cudaError_t append(Paged4StoreParams p, cudaStream_t st) {
-  const Grid4 g = grid_of(p.n_tokens, p.H, D, 4 * kWords);
-  const long long ctas = g.kv_ctas + (p.q.n_heads ? rotate_ctas(&p.q, kThreads) : 0);
+  const Grid4 g = grid_of(p.n_tokens, 2LL * p.H * (D / 16), 2);
+  const long long ctas = g.kv_ctas + (p.q.n_heads ? rotate_ctas(&p.q, kThreads, kAppendHeads) : 0);
   switch (p.q.n_heads ? rotate_kind(p.q.rot, p.q.interleaved) : kInterleaved) {
     case kInterleaved: return launch(paged4_append_kernel<D, BF16, kInterleaved>, ctas, st, p, g);
     case kHalves: return launch(paged4_append_kernel<D, BF16, kHalves>, ctas, st, p, g);
@@ -244,7 +303,7 @@ cudaError_t launch_paged4_append(const Paged4StoreParams& p, int D, int dtype, c
 }
 
 cudaError_t launch_paged4_read(const Paged4ReadParams& p, int D, cudaStream_t st) {
-  const Grid4 g = grid_of(p.n_tokens, p.H, D, 16);
+  const Grid4 g = grid_of(p.n_tokens, 2LL * p.H * (D / 8), 16);
   return D == 128 ? launch(paged4_read_kernel<128>, g.kv_ctas, st, p, g)
                   : launch(paged4_read_kernel<64>, g.kv_ctas, st, p, g);
 }

@@ -173,14 +173,17 @@ __device__ __forceinline__ const uint4* vec_ptr(const PagedStoreParams& p, int s
                                         t * (side ? p.stride[1] : p.stride[0]) + h * D) + vec;
 }
 
-// Vector `vec` of token t's key (side 0, turned by its angles when ROT) or value.
+// Vector `vec` of token t's key (side 0, turned by its angles when ROT) or value; a
+// row's vectors are in the consecutive lanes of `mask`.
 template <int D, bool BF16, bool ROT>
-__device__ __forceinline__ uint4 load_vec(const PagedStoreParams& p, int side, long long t, int h, int vec) {
+__device__ __forceinline__ uint4 load_vec(const PagedStoreParams& p, int side, long long t, int h, int vec, int lane,
+                                          uint32_t mask) {
   const uint4 v = __ldg(vec_ptr(p, side, t, h, D, vec));
   if constexpr (ROT) {
     if (side == 0)
-      return turned_chunk<BF16>(v, static_cast<const uint16_t*>(p.x[0]) + t * p.stride[0] + h * D, vec,
-                                p.angles + t * (p.rot >> 1), p.rot, p.interleaved);
+      return turn_chunk<BF16>(v, ChunkTurn(vec, lane, p.rot, p.interleaved),
+                              static_cast<const uint16_t*>(p.x[0]) + t * p.stride[0] + h * D, vec,
+                              p.angles + t * (p.rot >> 1), p.rot, p.interleaved, mask);
   }
   return v;
 }
@@ -199,6 +202,7 @@ __device__ __forceinline__ void store_run(const PagedStoreParams& p, int t, int 
     return;
   }
   const int side = lane >> 4, l = lane & 15, sub = l / VPR, vec = l % VPR;
+  const uint32_t mask = (VPR == 16 ? 0xffffu : 0xffu) << (lane & ~(VPR - 1));  // the lanes of a row
   // rows of the run: until the page ends or the slots stop following
   const int most = min((1 << p.lg_ps) - row0, p.n_tokens - t);
   int n = 1;
@@ -215,9 +219,9 @@ __device__ __forceinline__ void store_run(const PagedStoreParams& p, int t, int 
   float* scale = (side ? p.scale[1] : p.scale[0]) + static_cast<size_t>(page) * p.H + h;
   const float was = *scale;
   const uint4 zero = make_uint4(0, 0, 0, 0);
-  const uint4 first = sub < n ? load_vec<D, BF16, ROT>(p, side, t + sub, h, vec) : zero;
+  const uint4 first = sub < n ? load_vec<D, BF16, ROT>(p, side, t + sub, h, vec, lane, mask) : zero;
   uint32_t m2 = vec_max(first, 0);
-  for (int i = sub + RPS; i < n; i += RPS) m2 = vec_max(load_vec<D, BF16, ROT>(p, side, t + i, h, vec), m2);
+  for (int i = sub + RPS; i < n; i += RPS) m2 = vec_max(load_vec<D, BF16, ROT>(p, side, t + i, h, vec, lane, mask), m2);
   auto side_max = [](uint32_t x) {  // over the side's sixteen lanes
 #pragma unroll
     for (int o = 1; o < 16; o <<= 1) x = max(x, __shfl_xor_sync(0xffffffffu, x, o));
@@ -228,7 +232,7 @@ __device__ __forceinline__ void store_run(const PagedStoreParams& p, int t, int 
   if (__any_sync(0xffffffffu, odd)) {
     m2 = 0;
     for (int i = sub; i < n; i += RPS)
-      m2 = vec_max_finite<BF16>(load_vec<D, BF16, ROT>(p, side, t + i, h, vec), m2);
+      m2 = vec_max_finite<BF16>(load_vec<D, BF16, ROT>(p, side, t + i, h, vec, lane, mask), m2);
     mag = side_max(fold2(m2));
     if (odd && l == 0) set_err(p.err, KVQ_PAGED_ERR_NONFINITE);
   }
@@ -251,7 +255,7 @@ __device__ __forceinline__ void store_run(const PagedStoreParams& p, int t, int 
   if (sub < n) *reinterpret_cast<uint2*>(base + static_cast<size_t>(row0 + sub) * D) = codes8<BF16>(first, inv, plain);
   for (int i = sub + RPS; i < n; i += RPS)
     *reinterpret_cast<uint2*>(base + static_cast<size_t>(row0 + i) * D) =
-        codes8<BF16>(load_vec<D, BF16, ROT>(p, side, t + i, h, vec), inv, plain);
+        codes8<BF16>(load_vec<D, BF16, ROT>(p, side, t + i, h, vec, lane, mask), inv, plain);
   if (l == 0) *scale = exp2i(e);
 }
 
@@ -299,15 +303,19 @@ __global__ void __launch_bounds__(chunk_threads<TEAM>(), (ROT ? 768 : 1024) / ch
   const int tid = threadIdx.x, lane = tid & 31;
   const int side = tid / TEAM & 1, team = tid / (2 * TEAM), l = tid % TEAM;
   const int sub = l / VPR, vec = l % VPR;
-  const int tb = blockIdx.x * p.chunk, h = blockIdx.y;
+  const int tb = blockIdx.x * p.chunk;
+  int h = blockIdx.y;
   const int ps = 1 << p.lg_ps;
   if (tid == 0) s_count = 0;
   grid_dep_wait();
   grid_dep_launch();
   if constexpr (ROT) {
-    if (h >= p.H) {  // the step's queries
-      const long long t0 = (static_cast<long long>(h - p.H) * gridDim.x + blockIdx.x) * p.q.tokens;
-      if (t0 < p.q.n_tokens) rotate_any<BF16, THREADS>(p.q, t0, tid);
+    // rows of CTAs for the heads lie evenly among those for the step's queries, so
+    // that the ones' arithmetic runs beside the others' traffic
+    h = blockIdx.y * p.H / gridDim.y;
+    if (gridDim.y > p.H && (blockIdx.y + 1) * p.H / gridDim.y == h) {
+      const long long t0 = (static_cast<long long>(blockIdx.y - h) * gridDim.x + blockIdx.x) * p.q.tokens;
+      if (t0 < p.q.n_tokens) rotate_any<BF16, THREADS, kAppendHeads>(p.q, t0, tid);
       return;
     }
   }
@@ -374,7 +382,21 @@ __global__ void __launch_bounds__(chunk_threads<TEAM>(), (ROT ? 768 : 1024) / ch
 #pragma unroll
     for (int s = 0; s < kSteps; ++s) {
       x[s] = make_uint4(0, 0, 0, 0);
-      if ((rows >> s) & 1) x[s] = load_vec<D, BF16, ROT>(p, side, t + s * RPS + sub, h, vec);
+      if ((rows >> s) & 1) x[s] = __ldg(vec_ptr(p, side, t + s * RPS + sub, h, D, vec));
+    }
+    if constexpr (ROT) {
+      // (a row's lanes hold it together, or none of them)
+      const uint32_t mask = (VPR == 16 ? 0xffffu : 0xffu) << (lane & ~(VPR - 1));
+      const ChunkTurn ct(vec, lane, p.rot, p.interleaved);
+      if (side == 0) {
+#pragma unroll
+        for (int s = 0; s < kSteps; ++s) {
+          const long long tok = t + s * RPS + sub;
+          if ((rows >> s) & 1)
+            x[s] = turn_chunk<BF16>(x[s], ct, static_cast<const uint16_t*>(p.x[0]) + tok * p.stride[0] + h * D, vec,
+                                    p.angles + tok * (p.rot >> 1), p.rot, p.interleaved, mask);
+        }
+      }
     }
     const float was = good && row0 > 0 ? *scale : 0.f;
     uint32_t m2 = 0, both;
@@ -434,7 +456,7 @@ cudaError_t launch_team(PagedStoreParams p, cudaStream_t st) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((p.n_tokens + p.chunk - 1) / p.chunk, p.H);
   if (ROT && p.q.n_heads > 0) {
-    const long long ctas = rotate_ctas(&p.q, THREADS);
+    const long long ctas = rotate_ctas(&p.q, THREADS, kAppendHeads);
     cfg.gridDim.y += static_cast<unsigned>((ctas + cfg.gridDim.x - 1) / cfg.gridDim.x);
     if (cfg.gridDim.y > 65535) return cudaErrorInvalidValue;
   }

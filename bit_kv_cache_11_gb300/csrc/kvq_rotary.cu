@@ -64,7 +64,7 @@ template <bool BF16, RotateKind KIND>
 __global__ void __launch_bounds__(kThreads) rotate_kernel(const RotateParams p) {
   grid_dep_wait();
   grid_dep_launch();
-  rotate_tokens<BF16, KIND, kThreads>(p, static_cast<long long>(blockIdx.x) * p.tokens, threadIdx.x);
+  rotate_tokens<BF16, KIND, kThreads, kRotateHeads>(p, static_cast<long long>(blockIdx.x) * p.tokens, threadIdx.x);
 }
 
 template <typename P>
@@ -83,7 +83,7 @@ cudaError_t launch(void (*fn)(P), const P& p, long long ctas, cudaStream_t st) {
 
 template <bool BF16>
 cudaError_t launch_kind(RotateParams p, cudaStream_t st) {
-  const long long ctas = rotate_ctas(&p, kThreads);
+  const long long ctas = rotate_ctas(&p, kThreads, kRotateHeads);
   switch (rotate_kind(p.rot, p.interleaved)) {
     case kInterleaved: return launch(rotate_kernel<BF16, kInterleaved>, p, ctas, st);
     case kHalves: return launch(rotate_kernel<BF16, kHalves>, p, ctas, st);
@@ -123,9 +123,7 @@ kvq_status rotate_params(RotateParams* p, const kvq_rotary* rotary, const void* 
   p->rot = rotary->rotary_dim;
   p->interleaved = rotary->interleaved;
   p->units.d = rotate_units(head_dim, rotary->rotary_dim, rotary->interleaved);
-  const long long per = static_cast<long long>(n_heads) * p->units.d;
-  if (per > 1 << 28) return KVQ_ERR_UNSUPPORTED;
-  p->per.d = static_cast<uint32_t>(per);
+  if (static_cast<long long>(n_heads) * head_dim > 1 << 28) return KVQ_ERR_UNSUPPORTED;  // 32-bit places in a token
   return KVQ_OK;
 }
 

@@ -31,8 +31,9 @@ struct RotateParams {
   int n_tokens, n_heads, D;
   int rot;          // even
   int interleaved;
-  int tokens;       // of a CTA
-  Divisor per, units;  // units of a token and of a head
+  int step;            // a thread's heads are h, h + step, ..., below n_heads
+  int tokens;          // of a CTA
+  Divisor per, units;  // threads of a token, units of a head
 };
 
 // A unit of a head is what one thread turns: the channels of whole pairs, so
@@ -120,34 +121,20 @@ __device__ __forceinline__ void turn_words(uint32_t& va, uint32_t& vb, float4 cs
   vb = float2_to_pair<BF16>(turn_b(a.x, b.x, c0), turn_b(a.y, b.y, c1));
 }
 
-// Eight pairs: channels i .. i + 7 (va) and i + rot / 2 .. (vb), a = their angles.
+// A word of two channels, with the other channels of their pairs: own cos + (-)
+// other sin, the same roundings as turn_a (sign -1) and turn_b (1).
 template <bool BF16>
-__device__ __forceinline__ void turn_halves(uint4& va, uint4& vb, const float2* a) {
-  turn_words<BF16>(va.x, vb.x, angles2(a));
-  turn_words<BF16>(va.y, vb.y, angles2(a + 2));
-  turn_words<BF16>(va.z, vb.z, angles2(a + 4));
-  turn_words<BF16>(va.w, vb.w, angles2(a + 6));
+__device__ __forceinline__ uint32_t turn_own(uint32_t own, uint32_t other, float4 cs, float sign) {
+  const float2 x = pair_to_float2<BF16>(own), y = pair_to_float2<BF16>(other);
+  return float2_to_pair<BF16>(__fadd_rn(__fmul_rn(x.x, cs.x), sign * __fmul_rn(y.x, cs.y)),
+                              __fadd_rn(__fmul_rn(x.y, cs.z), sign * __fmul_rn(y.y, cs.w)));
 }
 
-// Channels [8 vec, 8 vec + 8) of a head after the turn; `own` holds them before,
-// `head` is the whole head in memory (the pairs' other channels are read there).
+// Channels [c0, c0 + 8) of `head`, in `own`, after the turn, channel by channel.
 template <bool BF16>
-__device__ __forceinline__ uint4 turned_chunk(uint4 own, const uint16_t* head, int vec, const float2* a,
-                                              int rot, int interleaved) {
-  const int c0 = vec * 8;
-  if (c0 >= rot) return own;
+__device__ __forceinline__ uint4 turn_single(uint4 own, const uint16_t* head, int c0, const float2* a, int rot,
+                                             int interleaved) {
   const int half = rot >> 1;
-  if (rotate_aligned(rot, interleaved)) {
-    if (interleaved) return turn_interleaved<BF16>(own, a + (c0 >> 1));
-    const bool second = c0 >= half;
-    uint4 other = __ldg(reinterpret_cast<const uint4*>(head + (second ? c0 - half : c0 + half)));
-    if (second) {
-      turn_halves<BF16>(other, own, a + (c0 - half));
-    } else {
-      turn_halves<BF16>(own, other, a + c0);
-    }
-    return own;
-  }
   uint32_t w[4] = {own.x, own.y, own.z, own.w};
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
@@ -166,84 +153,140 @@ __device__ __forceinline__ uint4 turned_chunk(uint4 own, const uint16_t* head, i
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// The units of tokens [t0, t0 + p.tokens) by a CTA's THREADS threads, U at a time
-// a thread so that as many loads are on their way.
-template <bool BF16, RotateKind KIND, int THREADS>
+// How a lane turns its chunk of a head, channels [8 vec, 8 vec + 8), where a head's
+// chunks lie in consecutive lanes: the other channels of its pairs come from
+// another lane, or (kSingle) from memory.
+struct ChunkTurn {
+  bool turns;   // the chunk has channels that turn
+  bool pairs;   // aligned halves: the partner is a lane's whole chunk
+  int src;      // that lane
+  int angle;    // first angle
+  float sign;
+  __device__ __forceinline__ ChunkTurn(int vec, int lane, int rot, int interleaved) {
+    const int c = vec * 8, half = rot >> 1;
+    turns = c < rot;
+    pairs = !interleaved && rotate_aligned(rot, interleaved);
+    const bool second = !interleaved && c >= half;
+    angle = interleaved ? c >> 1 : second ? c - half : c;
+    src = !turns || !pairs ? lane : second ? lane - (half >> 3) : lane + (half >> 3);
+    sign = second ? 1.f : -1.f;
+  }
+};
+
+// The chunk `own` of `head` after the turn by angles a [rot / 2].  Every lane of
+// `mask` takes part.
+template <bool BF16>
+__device__ __forceinline__ uint4 turn_chunk(uint4 own, const ChunkTurn& ct, const uint16_t* head, int vec,
+                                            const float2* a, int rot, int interleaved, uint32_t mask) {
+  if (ct.pairs) {
+    uint4 o;
+    o.x = __shfl_sync(mask, own.x, ct.src);
+    o.y = __shfl_sync(mask, own.y, ct.src);
+    o.z = __shfl_sync(mask, own.z, ct.src);
+    o.w = __shfl_sync(mask, own.w, ct.src);
+    if (!ct.turns) return own;
+    a += ct.angle;
+    return make_uint4(turn_own<BF16>(own.x, o.x, angles2(a), ct.sign), turn_own<BF16>(own.y, o.y, angles2(a + 2), ct.sign),
+                      turn_own<BF16>(own.z, o.z, angles2(a + 4), ct.sign), turn_own<BF16>(own.w, o.w, angles2(a + 6), ct.sign));
+  }
+  if (!ct.turns) return own;
+  if (rotate_aligned(rot, interleaved)) return turn_interleaved<BF16>(own, a + ct.angle);
+  return turn_single<BF16>(own, head, vec * 8, a, rot, interleaved);
+}
+
+// Tokens [t0, t0 + p.tokens) by a CTA's THREADS threads.  A thread turns one unit
+// of HEADS heads of a token: their angles are the same, and their loads are on
+// their way at once.
+template <bool BF16, RotateKind KIND, int THREADS, int HEADS>
 __device__ __forceinline__ void rotate_tokens(const RotateParams& p, long long t0, int tid) {
-  constexpr int U = KIND == kSingle ? 1 : 4;
   const int n = static_cast<int>(min(static_cast<long long>(p.tokens), p.n_tokens - t0));
   const uint32_t total = static_cast<uint32_t>(n) * p.per.d;
-  const int half = p.rot >> 1;
+  const int half = p.rot >> 1, step = p.step * p.D;
   const bool copies = p.x != p.out;
-  for (uint32_t i0 = tid; i0 < total; i0 += U * THREADS) {
-    const uint16_t* x[U];
-    uint16_t* out[U];
-    const float2* a[U];
-    int c[U];
-    uint4 va[U], vb[U];
-#pragma unroll
-    for (int k = 0; k < U; ++k) {
-      const uint32_t i = min(i0 + k * THREADS, total - 1);
-      const uint32_t t = i / p.per, r = i - t * p.per.d, h = r / p.units, u = r - h * p.units.d;
-      x[k] = p.x + (t0 + t) * p.x_stride + h * p.D;
-      out[k] = p.out + (t0 + t) * p.out_stride + h * p.D;
-      a[k] = p.angles + (t0 + t) * half;
-      c[k] = static_cast<int>(u);
-      if constexpr (KIND == kInterleaved) {
-        c[k] = 8 * c[k];
-        va[k] = *reinterpret_cast<const uint4*>(x[k] + c[k]);
-      } else if constexpr (KIND == kHalves) {
-        c[k] = c[k] < p.rot / 16 ? 8 * c[k] : p.rot + 8 * (c[k] - p.rot / 16);
-        va[k] = *reinterpret_cast<const uint4*>(x[k] + c[k]);
-        if (c[k] < half) vb[k] = *reinterpret_cast<const uint4*>(x[k] + c[k] + half);
-      }
-    }
-#pragma unroll
-    for (int k = 0; k < U; ++k) {
-      if (i0 + k * THREADS >= total) break;
-      if constexpr (KIND == kSingle) {
-        const int turning = (half + 3) / 4;
-        if (c[k] < turning) {
-          for (int i = 4 * c[k]; i < min(4 * c[k] + 4, half); ++i) {
-            const int ca = p.interleaved ? 2 * i : i, cb = p.interleaved ? 2 * i + 1 : i + half;
-            const float xa = one_to_float<BF16>(x[k][ca]), xb = one_to_float<BF16>(x[k][cb]);
-            const float2 cs = __ldg(a[k] + i);
-            out[k][ca] = float_to_one<BF16>(turn_a(xa, xb, cs));
-            out[k][cb] = float_to_one<BF16>(turn_b(xa, xb, cs));
+  for (uint32_t i = tid; i < total; i += THREADS) {
+    const uint32_t t = i / p.per, r = i - t * p.per.d, h0 = r / p.units, u = r - h0 * p.units.d;
+    const int heads = min(HEADS, static_cast<int>((p.n_heads - h0 + p.step - 1) / p.step));  // h0, h0 + step, ...
+    const uint16_t* x = p.x + (t0 + t) * p.x_stride + h0 * p.D;
+    uint16_t* out = p.out + (t0 + t) * p.out_stride + h0 * p.D;
+    const float2* a = p.angles + (t0 + t) * half;
+    if constexpr (KIND == kSingle) {
+      const int turning = (half + 3) / 4, v = static_cast<int>(u);
+      for (int k = 0; k < heads; ++k, x += step, out += step) {
+        if (v < turning) {
+          for (int j = 4 * v; j < min(4 * v + 4, half); ++j) {
+            const int ca = p.interleaved ? 2 * j : j, cb = p.interleaved ? 2 * j + 1 : j + half;
+            const float xa = one_to_float<BF16>(x[ca]), xb = one_to_float<BF16>(x[cb]);
+            const float2 cs = __ldg(a + j);
+            out[ca] = float_to_one<BF16>(turn_a(xa, xb, cs));
+            out[cb] = float_to_one<BF16>(turn_b(xa, xb, cs));
           }
         } else if (copies) {
-          const int c0 = p.rot + 8 * (c[k] - turning);
-          for (int j = c0; j < min(c0 + 8, p.D); ++j) out[k][j] = x[k][j];
+          const int c0 = p.rot + 8 * (v - turning);
+          for (int j = c0; j < min(c0 + 8, p.D); ++j) out[j] = x[j];
         }
-        continue;
       }
-      const bool turns = c[k] < p.rot;
-      if constexpr (KIND == kInterleaved) {
-        if (turns) va[k] = turn_interleaved<BF16>(va[k], a[k] + (c[k] >> 1));
-      } else if (turns) {
-        turn_halves<BF16>(va[k], vb[k], a[k] + c[k]);
-        *reinterpret_cast<uint4*>(out[k] + c[k] + half) = vb[k];
+    } else {
+      int c = 8 * static_cast<int>(u);
+      if (KIND == kHalves && c >= half) c += half;
+      const bool turns = c < p.rot;
+      if (!turns && !copies) continue;
+      uint4 va[HEADS], vb[HEADS];
+#pragma unroll
+      for (int k = 0; k < HEADS; ++k) {
+        if (k < heads) {
+          va[k] = *reinterpret_cast<const uint4*>(x + c + k * step);
+          if (KIND == kHalves && turns) vb[k] = *reinterpret_cast<const uint4*>(x + c + half + k * step);
+        }
       }
-      if (turns || copies) *reinterpret_cast<uint4*>(out[k] + c[k]) = va[k];
+      float4 cs[4];
+      if (turns) {
+        a += KIND == kHalves ? c : c >> 1;
+#pragma unroll
+        for (int j = 0; j < (KIND == kHalves ? 4 : 2); ++j) cs[j] = angles2(a + 2 * j);
+      }
+#pragma unroll
+      for (int k = 0; k < HEADS; ++k) {
+        if (k >= heads) break;
+        if (turns) {
+          if constexpr (KIND == kHalves) {
+            turn_words<BF16>(va[k].x, vb[k].x, cs[0]);
+            turn_words<BF16>(va[k].y, vb[k].y, cs[1]);
+            turn_words<BF16>(va[k].z, vb[k].z, cs[2]);
+            turn_words<BF16>(va[k].w, vb[k].w, cs[3]);
+            *reinterpret_cast<uint4*>(out + c + half + k * step) = vb[k];
+          } else {
+            va[k].x = turn_word<BF16>(va[k].x, make_float2(cs[0].x, cs[0].y));
+            va[k].y = turn_word<BF16>(va[k].y, make_float2(cs[0].z, cs[0].w));
+            va[k].z = turn_word<BF16>(va[k].z, make_float2(cs[1].x, cs[1].y));
+            va[k].w = turn_word<BF16>(va[k].w, make_float2(cs[1].z, cs[1].w));
+          }
+        }
+        *reinterpret_cast<uint4*>(out + c + k * step) = va[k];
+      }
     }
   }
 }
 
 // The same where the kind is known at run time only.
-template <bool BF16, int THREADS>
+template <bool BF16, int THREADS, int HEADS>
 __device__ __forceinline__ void rotate_any(const RotateParams& p, long long t0, int tid) {
-  if (!rotate_aligned(p.rot, p.interleaved)) rotate_tokens<BF16, kSingle, THREADS>(p, t0, tid);
-  else if (p.interleaved) rotate_tokens<BF16, kInterleaved, THREADS>(p, t0, tid);
-  else rotate_tokens<BF16, kHalves, THREADS>(p, t0, tid);
+  if (!rotate_aligned(p.rot, p.interleaved)) rotate_tokens<BF16, kSingle, THREADS, HEADS>(p, t0, tid);
+  else if (p.interleaved) rotate_tokens<BF16, kInterleaved, THREADS, HEADS>(p, t0, tid);
+  else rotate_tokens<BF16, kHalves, THREADS, HEADS>(p, t0, tid);
 }
 
-// CTAs of `threads` that turn p's heads: enough units a CTA for every thread's
-// loads in flight, fewer while that leaves SMs idle.
-inline long long rotate_ctas(RotateParams* p, int threads) {
-  const long long per = p->per.d, all = per * p->n_tokens;
-  const long long want = std::min<long long>(8 * threads, std::max<long long>(threads, all / (152 * 4)));
+// Heads of a thread: four where turning is all a kernel does, two beside a store,
+// whose registers leave no room.
+constexpr int kRotateHeads = 4, kAppendHeads = 4;
+
+// CTAs of `threads` that turn p's heads: a few rounds each, fewer while that
+// leaves SMs idle.
+inline long long rotate_ctas(RotateParams* p, int threads, int heads) {
+  p->step = (p->n_heads + heads - 1) / heads;
+  const long long per = static_cast<long long>(p->step) * p->units.d, all = per * p->n_tokens;
+  const long long want = std::min<long long>(2 * threads, std::max<long long>(threads, all / (152 * 4)));
   p->tokens = static_cast<int>(std::max<long long>(1, std::min<long long>(want / per, p->n_tokens)));
-  p->per = divisor(p->per.d, per * p->tokens);
+  p->per = divisor(static_cast<uint32_t>(per), per * p->tokens);
   p->units = divisor(p->units.d, per);
   return (p->n_tokens + p->tokens - 1) / p->tokens;
 }
