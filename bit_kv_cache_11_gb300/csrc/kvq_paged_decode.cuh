@@ -86,6 +86,14 @@ __device__ __forceinline__ uint2 lds64(uint32_t a) {
   return v;
 }
 
+// 16 bytes into shared memory, and the arrival of the thread's copies so far.
+__device__ __forceinline__ void async_copy16(void* dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_addr(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void async_copies_arrive(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(bar)) : "memory");
+}
+
 // Four 8 x 8 matrices of 16-bit units: lane (g, t) gets units 2t, 2t + 1 of row g, or
 // (trans) unit g of rows 2t and 2t + 1.  Lane l names row l % 8 of matrix l / 8.
 __device__ __forceinline__ void ldmatrix4(uint32_t a, uint32_t (&x)[4]) {
@@ -135,6 +143,12 @@ constexpr float kWeightLog2 = 15.f, kWeightInv = 0x1p-15f;  // weights are 2^15 
 __device__ __forceinline__ float row_factor(float l) {
   return l > 0.f ? kWeightInv / l : (l == 0.f ? 0.f : l);
 }
+
+// A truth value that is known at compile time.
+template <bool V>
+struct Known {
+  __device__ __forceinline__ operator bool() const { return V; }
+};
 
 // No page is needed (a table entry is never this: ids are below 2^31 - 1).
 constexpr int kNoPage = 0x7fffffff;
@@ -198,7 +212,7 @@ __global__ void __launch_bounds__(PagedCfg<D, NT, Q4>::NW * 32, 1)
   int* flags = reinterpret_cast<int*>(smem + C::OFF_SEG + NW * 2 * sizeof(PagedSeg));
   int* cum = reinterpret_cast<int*>(smem + C::OFF_CUM);
   if (lane == 0) {
-    for (int s = 0; s < NS; ++s) mbar_init(&bars[s], 1);
+    for (int s = 0; s < NS; ++s) mbar_init(&bars[s], Q4 ? 33 : 1);
     fence_barrier_init();
     segs[2 * warp].u0 = segs[2 * warp + 1].u0 = -1;
     if (warp == 0) {
@@ -341,10 +355,10 @@ __global__ void __launch_bounds__(PagedCfg<D, NT, Q4>::NW * 32, 1)
            : make_float4(ks, fast_log2(vs), kWeightInv / vs, seen ? 1.f : 0.f);
   };
   const int nbox = UT / p.box_rows;  // boxes of a side
-  // lane i < nbox copies key box i, lane nbox + i value box i, and the next 2 nbox
-  // lanes their metadata
+  // lane i < nbox copies key box i, lane nbox + i value box i; every lane copies 16
+  // bytes of the 4-bit pages' metadata a side
   const bool key = lane < nbox;
-  const int part = lane >> (31 - __clz(nbox)), bx = lane & (nbox - 1);
+  const int bx = key ? lane : lane - nbox;
   constexpr int ROW = Q4 ? D / 2 : D;  // bytes of a row of codes
   const uint32_t box_bytes = static_cast<uint32_t>(p.box_rows) * ROW;
   const int box_g = bx * (p.box_rows / 16) & (GR - 1);  // first granule of the lane's box
@@ -373,23 +387,25 @@ __global__ void __launch_bounds__(PagedCfg<D, NT, Q4>::NW * 32, 1)
       granule_scales(nx_page, &nx_ks, &nx_vs);
     }
     const int page = __shfl_sync(0xffffffffu, my_page, gbase + box_g);
-    const bool mine = lane < (Q4 ? 4 : 2) * nbox && page >= 0;
-    const uint32_t who = __ballot_sync(0xffffffffu, mine);
-    if (lane == 0) {
-      const uint32_t n = Q4 ? __popc(who) / 4 * 2 * (box_bytes + box_bytes / 4) : __popc(who) * box_bytes;
-      mbar_arrive_expect_tx(&bars[s], n);
-    }
+    const bool mine = lane < 2 * nbox && page >= 0;
+    const int n = __popc(__ballot_sync(0xffffffffu, mine));
+    if (lane == 0) mbar_arrive_expect_tx(&bars[s], n * box_bytes);
     __syncwarp();
-    if (mine) {
-      const int tok = li.tok0 + (lu - li.u0) * UT + bx * p.box_rows;
-      const int row = ((page * p.H + li.h) << p.lg_ps) + (tok & ((1 << p.lg_ps) - 1));
-      uint8_t* st = stages + s * C::STAGE;
-      if (!Q4 || part < 2) {
-        tma_load_2d(st + (key ? 0 : C::OFF_V) + bx * box_bytes, key ? &kmap : &vmap, 0, row, &bars[s]);
-      } else {
-        bulk_g2s(st + (part == 2 ? C::OFF_KM : C::OFF_VM) + bx * (box_bytes / 4),
-                 p.meta[part - 2] + static_cast<size_t>(row) * (D / kGroup4), box_bytes / 4, &bars[s]);
+    const int tok0 = li.tok0 + (lu - li.u0) * UT;
+    auto row_of = [&](int pg, int tok) { return ((pg * p.H + li.h) << p.lg_ps) + (tok & ((1 << p.lg_ps) - 1)); };
+    uint8_t* st = stages + s * C::STAGE;
+    if (mine)
+      tma_load_2d(st + (key ? 0 : C::OFF_V) + bx * box_bytes, key ? &kmap : &vmap, 0,
+                  row_of(page, tok0 + bx * p.box_rows), &bars[s]);
+    if constexpr (Q4) {
+      const int tok = lane * (128 / D);  // the lane's token of the unit
+      const int pg = __shfl_sync(0xffffffffu, my_page, gbase + tok / 16);
+      if (pg >= 0) {
+        const size_t at = static_cast<size_t>(row_of(pg, tok0 + tok)) * (D / kGroup4);
+        async_copy16(st + C::OFF_KM + lane * 16, p.meta[0] + at);
+        async_copy16(st + C::OFF_VM + lane * 16, p.meta[1] + at);
       }
+      async_copies_arrive(&bars[s]);
     }
     if (fresh) put_record(u_first, rec_first, ks, vs);
     if (gbase == 0) nx_page = granule_page(lu + 32 / GR);
@@ -543,7 +559,8 @@ __global__ void __launch_bounds__(PagedCfg<D, NT, Q4>::NW * 32, 1)
   // One unit from stage memory.  edge: some of its tokens are hidden from some
   // rows (or not there at all).
   float4 rec[GR];  // the unit's granule records
-  auto compute = [&](uint32_t st, int tok, bool edge) {
+  auto compute = [&](uint32_t st, int tok, auto at_edge) {
+    const bool edge = at_edge;
     uint32_t pw[GR][NT][2];
     float s[GR][NT][4];
 #pragma unroll
@@ -865,7 +882,13 @@ __global__ void __launch_bounds__(PagedCfg<D, NT, Q4>::NW * 32, 1)
         rec[i] = ring[(crec + i) & (C::RING - 1)];
         there &= rec[i].w != 0.f;
       }
-      compute(sp, tok, !there || tok < full_lo || tok + UT > full_hi);
+      const bool edge = !there || tok < full_lo || tok + UT > full_hi;
+      if constexpr (Q4) {
+        if (edge) compute(sp, tok, Known<true>{});
+        else compute(sp, tok, Known<false>{});
+      } else {
+        compute(sp, tok, edge);
+      }
     }
     crec += GR;
     __syncwarp();
