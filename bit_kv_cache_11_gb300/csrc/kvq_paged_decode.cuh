@@ -75,11 +75,6 @@ __device__ __forceinline__ uint4 lds128(uint32_t a) {
                : "r"(a));
   return v;
 }
-__device__ __forceinline__ uint32_t lds32(uint32_t a) {
-  uint32_t v;
-  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a));
-  return v;
-}
 __device__ __forceinline__ uint2 lds64(uint32_t a) {
   uint2 v;
   asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
@@ -420,7 +415,6 @@ __global__ void __launch_bounds__(PagedCfg<D, NT, Q4>::NW * 32, 1)
 
   // ---- compute ---------------------------------------------------------------
   uint32_t qf[NT][KS][2];
-  uint32_t qz[NT][2];  // 4-bit pages: the row's sum over group t, in two fp16 parts
   float acc[MT][NT][4];
   float m[NT][2], l[NT][2], cq[NT][2];
   PagedItem it = {};
@@ -461,66 +455,28 @@ __global__ void __launch_bounds__(PagedCfg<D, NT, Q4>::NW * 32, 1)
           w[4 * i + 3] = v.w;
         }
       }
-      if constexpr (Q4) {
-        // The row times a power of two, its largest element in [2^10, 2^11):
-        // elements down to 2^-24 of it keep all their bits.  A code in the low
-        // four bits of a half is the fp16 number code * 2^-24, in the next four
-        // code * 2^-20; the queries of the first are 16 times larger instead.
-        float mx = 0.f;
-        float2 x[KS * 2];
+      if constexpr (BF16) {
+        // The row times a power of two as fp16: its largest element comes to
+        // [2^14, 2^15), so elements down to 2^-22 of it keep all their bits
+        // and the rest an absolute error below 2^-40 of it.
+        uint32_t mg = 0;
 #pragma unroll
-        for (int i = 0; i < KS * 2; ++i) {
-          x[i] = pair_to_float2<BF16>(w[i]);
-          mx = fmaxf(mx, fmaxf(fabsf(x[i].x), fabsf(x[i].y)));
-        }
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-        const int e = max(static_cast<int>(__float_as_uint(mx) >> 23) - 127, -100);
-        const float up = __uint_as_float(static_cast<uint32_t>(127 + 10 - e) << 23);
-        c *= __uint_as_float(static_cast<uint32_t>(127 - 10 + e) << 23) * 0x1p20f;
-        float mine = 0.f;
+        for (int i = 0; i < KS * 2; ++i) mg = __vmaxu2(mg, w[i] & 0x7fff7fffu);
+        uint32_t mx = max(mg & 0xffffu, mg >> 16);
+        mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+        mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+        const int e = max(static_cast<int>(mx >> 7) - 127, -100);
+        const float up = __uint_as_float(static_cast<uint32_t>(127 + 14 - e) << 23);
+        c *= __uint_as_float(static_cast<uint32_t>(127 - 14 + e) << 23);
 #pragma unroll
-        for (int i = 0; i < D / 32; ++i) {
-          // words j of group i: channels 2j and 2j + 1 of the lane's eight
-          float sum = 0.f;
+        for (int i = 0; i < KS * 2; ++i)
+          w[i] = pack_half2(__uint_as_float(w[i] << 16) * up,
+                            __uint_as_float(w[i] & 0xffff0000u) * up);
+      }
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const float2 y = make_float2(x[4 * i + j].x * up, x[4 * i + j].y * up);
-            sum += y.x + y.y;
-            const float k = j & 1 ? 1.f : 16.f;
-            qf[nt][2 * i + (j & 1)][j >> 1] = pack_half2(y.x * k, y.y * k);
-          }
-          sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-          sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-          if (t == i) mine = sum * 0x1p-20f;
-        }
-        const __half hi = __float2half_rn(mine), lo = __float2half_rn(mine - __half2float(hi));
-        qz[nt][0] = as_word(__halves2half2(__ushort_as_half(0), hi));
-        qz[nt][1] = as_word(__halves2half2(__ushort_as_half(0), lo));
-      } else {
-        if constexpr (BF16) {
-          // The row times a power of two as fp16: its largest element comes to
-          // [2^14, 2^15), so elements down to 2^-22 of it keep all their bits
-          // and the rest an absolute error below 2^-40 of it.
-          uint32_t mg = 0;
-#pragma unroll
-          for (int i = 0; i < KS * 2; ++i) mg = __vmaxu2(mg, w[i] & 0x7fff7fffu);
-          uint32_t mx = max(mg & 0xffffu, mg >> 16);
-          mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-          mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-          const int e = max(static_cast<int>(mx >> 7) - 127, -100);
-          const float up = __uint_as_float(static_cast<uint32_t>(127 + 14 - e) << 23);
-          c *= __uint_as_float(static_cast<uint32_t>(127 - 14 + e) << 23);
-#pragma unroll
-          for (int i = 0; i < KS * 2; ++i)
-            w[i] = pack_half2(__uint_as_float(w[i] << 16) * up,
-                              __uint_as_float(w[i] & 0xffff0000u) * up);
-        }
-#pragma unroll
-        for (int i = 0; i < KS; ++i) {
-          qf[nt][i][0] = w[2 * i];
-          qf[nt][i][1] = w[2 * i + 1];
-        }
+      for (int i = 0; i < KS; ++i) {
+        qf[nt][i][0] = w[2 * i];
+        qf[nt][i][1] = w[2 * i + 1];
       }
       // columns 2t, 2t + 1 of the score fragment are rows of other lanes
       cq[nt][0] = __shfl_sync(0xffffffffu, c, 8 * t);
@@ -570,39 +526,26 @@ __global__ void __launch_bounds__(PagedCfg<D, NT, Q4>::NW * 32, 1)
 #pragma unroll
         for (int i = 0; i < 4; ++i) s[mt][nt][i] = 0.f;
       if constexpr (Q4) {
-        // The tokens' minima times the queries' sums over each group start the
-        // scores; then group by group the codes' products times the step.
+        // words of channels 32 w + 8 t .. of tokens g and g + 8, and the tokens'
+        // steps and minima
         const uint32_t meta = st + C::OFF_KM + (mt * 16 + g) * (D / 8);
         Meta4<D> ma, mb;
         ma.load(meta);
         mb.load(meta + D);
-        uint32_t za = 0, zb = 0;
-        if (D == 128 || t < D / 32) {
-          za = lds32(meta + 4 * t);
-          zb = lds32(meta + D + 4 * t);
-        }
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) mma_16816(s[mt][nt], za, zb, za, zb, qz[nt][0], qz[nt][1]);
 #pragma unroll
         for (int w = 0; w < D / 32; w += 2) {
-          uint32_t x[4];  // channels 32 w + 8 t .. of tokens g and g + 8, and of the next group
+          uint32_t x[4];
           ldmatrix4((st + mt * 8 * D + moff) ^ (16 * w), x);
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            const uint32_t a = x[2 * i], b = x[2 * i + 1], a8 = a >> 8, b8 = b >> 8;
-            constexpr uint32_t LO = 0x000f000fu, HI = 0x00f000f0u;
-            const float sa = __low2float(as_half2(ma.m[w + i])), sb = __low2float(as_half2(mb.m[w + i]));
+            uint32_t a[4], b[4];
+            values4(x[2 * i], pair_lo(ma.m[w + i], ma.m[w + i]), pair_hi(ma.m[w + i], ma.m[w + i]), a);
+            values4(x[2 * i + 1], pair_lo(mb.m[w + i], mb.m[w + i]), pair_hi(mb.m[w + i], mb.m[w + i]), b);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-              float d[4] = {0.f, 0.f, 0.f, 0.f};
               const int ks = 2 * (w + i);
-              mma_16816(d, a & LO, b & LO, a8 & LO, b8 & LO, qf[nt][ks][0], qf[nt][ks][1]);
-              mma_16816(d, a & HI, b & HI, a8 & HI, b8 & HI, qf[nt][ks + 1][0], qf[nt][ks + 1][1]);
-              float* y = s[mt][nt];
-              y[0] = fmaf(d[0], sa, y[0]);
-              y[1] = fmaf(d[1], sa, y[1]);
-              y[2] = fmaf(d[2], sb, y[2]);
-              y[3] = fmaf(d[3], sb, y[3]);
+              mma_16816(s[mt][nt], a[0], b[0], a[1], b[1], qf[nt][ks][0], qf[nt][ks][1]);
+              mma_16816(s[mt][nt], a[2], b[2], a[3], b[3], qf[nt][ks + 1][0], qf[nt][ks + 1][1]);
             }
           }
         }

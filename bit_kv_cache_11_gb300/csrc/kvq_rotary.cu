@@ -15,12 +15,16 @@ constexpr int kThreads = 256;
 // ---- angles ---------------------------------------------------------------------
 //
 // position * turn modulo 2^64 is the exact part of a turn; the nearest quarter
-// comes off its top bits, the rest (at most an eighth of a turn) becomes an angle
-// within pi / 4, whose Taylor series to x^9 and x^10 leave 2^-29 and 2^-30.
-__device__ __forceinline__ float2 unit_of(uint64_t phase) {
-  const uint32_t quarter = static_cast<uint32_t>((phase + (1ull << 61)) >> 62);
-  // the 32 bits below the quarter's two, as a signed fraction of it
-  const float x = static_cast<float>(static_cast<int32_t>(phase >> 30)) * 3.65729521e-10f;  // 2 pi / 2^34
+// comes off the top of its upper 32 bits, the rest (at most an eighth of a turn)
+// becomes an angle within pi / 4, whose Taylor series to x^9 and x^10 leave 2^-29
+// and 2^-30.
+__device__ __forceinline__ float2 unit_of(int pos, uint2 turn) {  // turn: low, high word
+  const uint32_t n = static_cast<uint32_t>(pos);
+  uint32_t phase = __umulhi(n, turn.x) + n * turn.y;
+  if (pos < 0) phase -= turn.x;  // n is 2^32 above the position
+  const uint32_t quarter = (phase + (1u << 29)) >> 30;
+  // what the quarter leaves, as a signed fraction of it
+  const float x = static_cast<float>(static_cast<int32_t>(phase << 2)) * 3.65729521e-10f;  // 2 pi / 2^34
   const float y = x * x;
   const float s = fmaf(fmaf(fmaf(fmaf(2.7557319e-6f, y, -1.9841270e-4f), y, 8.3333333e-3f), y, -0.16666667f) * y, x, x);
   const float c = fmaf(fmaf(fmaf(fmaf(fmaf(-2.7557319e-7f, y, 2.4801587e-5f), y, -1.3888889e-3f), y, 4.1666667e-2f), y,
@@ -38,17 +42,17 @@ __global__ void __launch_bounds__(kThreads) rotary_angles_kernel(const AnglesPar
   grid_dep_wait();
   grid_dep_launch();
   if (row >= rows) return;
-  uint64_t turn[V];
+  uint2 turn[V];
 #pragma unroll
-  for (int i = 0; i < V; ++i) turn[i] = static_cast<uint64_t>(p.turns[k + i]);
+  for (int i = 0; i < V; ++i) turn[i] = reinterpret_cast<const uint2*>(p.turns)[k + i];
   const long long step = static_cast<long long>(gridDim.x) * rows;
 #pragma unroll 4
   for (long long t = static_cast<long long>(blockIdx.x) * rows + row; t < p.n_tokens; t += step) {
-    const uint64_t pos = static_cast<uint64_t>(static_cast<int64_t>(p.positions[t]));
+    const int pos = p.positions[t];
     float2 u[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      u[i] = unit_of(pos * turn[i]);
+      u[i] = unit_of(pos, turn[i]);
       u[i].x *= p.magnitude;
       u[i].y *= p.magnitude;
     }
