@@ -379,6 +379,7 @@ kvq_status kvq_paged_append(const kvq_paged_pool* pool, const kvq_rotary* rotary
     if (n_q_heads < 1) return KVQ_ERR_INVALID_ARG;
     s = rotate_params(&p.q, rotary, q, dtype, q_stride, q_out, q_out_stride, n_tokens, n_q_heads, pool->head_dim);
     if (s != KVQ_OK) return s;
+    if (pool->n_kv_heads > 65535 - 512) return KVQ_ERR_UNSUPPORTED;  // grid.y: at most a row of CTAs a chunk's token
   }
   if (n_tokens == 0) return KVQ_OK;
   p.angles = reinterpret_cast<const float2*>(rotary->angles);

@@ -458,7 +458,6 @@ cudaError_t launch_team(PagedStoreParams p, cudaStream_t st) {
   if (ROT && p.q.n_heads > 0) {
     const long long ctas = rotate_ctas(&p.q, THREADS, kAppendHeads);
     cfg.gridDim.y += static_cast<unsigned>((ctas + cfg.gridDim.x - 1) / cfg.gridDim.x);
-    if (cfg.gridDim.y > 65535) return cudaErrorInvalidValue;
   }
   cfg.blockDim = dim3(THREADS);
   cfg.stream = st;

@@ -198,7 +198,7 @@ def check_attention(kvq, case, seed=0, **over):
     seq = np.array(ctx) + np.array(new)
     need = -(-seq // ps)
     n_pages = int(need.sum()) + 2
-    codes, step, mn = pages_of(rng, n_pages, H, ps, D)
+    codes, step, mn = pages_of(rng, n_pages, H, ps, D, over.get("page_amp", 1.0))
     vals = [ref.values(codes[i], step[i], mn[i]) for i in range(2)]
     ids = rng.permutation(n_pages)
     table = np.full((B, max(1, int(need.max())) + 1), -1, np.int32)
@@ -296,6 +296,16 @@ def test_a_mixed_batch(kvq):
 def test_any_softmax_scale(kvq, scale):
     check_attention(kvq, (16, 64, 1, 2, "fp16", [60], [1], 0), scale=scale)
     check_attention(kvq, (16, 64, 1, 1, "bf16", [60], [150], 0), scale=scale, idle=150)
+
+
+@pytest.mark.parametrize("new,idle", [(1, 0), (130, 140)])
+@pytest.mark.parametrize("D", [64, 128])
+def test_large_values_are_attended_as_they_are_held(kvq, D, new, idle):
+    """A value is the fp16 number nearest to code * step + minimum.  At sizes of
+    500 that rounding moves a score by 0.01 .. 0.02 here, thirty times what the
+    bound leaves."""
+    case = (32, D, 2, 2, "fp16", [300, 40], [new, 3], 0)
+    check_attention(kvq, case, page_amp=100.0, amp=0.02 * (128 / D) ** 0.5, idle=idle)
 
 
 def test_max_new_may_be_a_loose_bound(kvq):

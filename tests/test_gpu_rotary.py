@@ -111,6 +111,17 @@ def test_rotate_many_tokens(kvq, inter):
     check_rotate(kvq, 20001, 1, 64, 32, inter, "fp16", pad=8)
 
 
+def test_rotate_beyond_four_gigabytes(kvq):
+    """The last of 2^31 elements and more, in place."""
+    T, H, D = 132000, 128, 128
+    x = torch.zeros(T, H, D, dtype=torch.bfloat16, device="cuda")
+    x[-3:] = torch.randn(3, H, D, device="cuda").bfloat16()
+    ang = torch.randn(T, D // 2, 2, device="cuda")
+    want = torch.from_numpy(ref.rotate(x[-3:].float().cpu().numpy(), ang[-3:].cpu().numpy(), False)).bfloat16()
+    assert kvq.kvq_rotate(x, ang, out=x) is x
+    assert same_bits(x[-3:].cpu(), want) and not x[:1000].any()
+
+
 def test_rotate_nonfinite_stays_in_its_pair(kvq):
     x = torch.randn(4, 2, 64, device="cuda").half()
     ang = torch.randn(4, 32, 2, device="cuda")
