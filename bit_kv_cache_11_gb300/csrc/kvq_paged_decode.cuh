@@ -539,8 +539,8 @@ __global__ void __launch_bounds__(PagedCfg<D, NT, Q4>::NW * 32, 1)
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
             uint32_t a[4], b[4];
-            values4(x[2 * i], pair_lo(ma.m[w + i], ma.m[w + i]), pair_hi(ma.m[w + i], ma.m[w + i]), a);
-            values4(x[2 * i + 1], pair_lo(mb.m[w + i], mb.m[w + i]), pair_hi(mb.m[w + i], mb.m[w + i]), b);
+            values4(x[2 * i], as_word(__low2half2(as_half2(ma.m[w + i]))), as_word(__high2half2(as_half2(ma.m[w + i]))), a);
+            values4(x[2 * i + 1], as_word(__low2half2(as_half2(mb.m[w + i]))), as_word(__high2half2(as_half2(mb.m[w + i]))), b);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
               const int ks = 2 * (w + i);

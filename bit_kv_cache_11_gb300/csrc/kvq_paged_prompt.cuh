@@ -545,7 +545,7 @@ __global__ void __launch_bounds__(PromptCfg<D, Q4>::THREADS, 1)
           const int sw = D == 128 ? w ^ ((row >> 1) & 3) : w ^ ((row >> 2) & 1);
           const uint4 v = *reinterpret_cast<const uint4*>(src + row * C::ROW + (sw << 4));
           const uint32_t x[4] = {v.x, v.y, v.z, v.w};
-          const uint32_t step = __byte_perm(m[w], m[w], 0x1010), least = __byte_perm(m[w], m[w], 0x3232);
+          const uint32_t step = as_word(__low2half2(as_half2(m[w]))), least = as_word(__high2half2(as_half2(m[w])));
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             uint32_t o[4];
