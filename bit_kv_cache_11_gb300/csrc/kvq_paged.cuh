@@ -182,6 +182,7 @@ cudaError_t launch_paged4_prompt(const PagedAttnParams& a, int items_max, const 
 cudaError_t allow_smem(const void* fn, int bytes);
 // Warps per CTA of the decode kernel, its most CTAs (one per SM of a GB300) and
 // the tokens of a unit.
+// (4-bit stages are smaller, and their arithmetic wants more warps)
 constexpr int paged_warps(int nt, bool four) { return four && nt == 1 ? 12 : 8; }
 constexpr int kPagedMaxCtas = 152;
 // A request with at most this many query rows per kv head (new tokens * R) is
@@ -195,7 +196,14 @@ constexpr int kPagedMaxCtas = 152;
 //                             D = 64:  32 rows 45 / 53, 64 rows 74 / 53
 //   512 items of 1000 tokens, D = 128: 64 rows 116 / 85; D = 64: 74 / 71
 // so the turn lies near 32 rows (48 of the narrower ones) where the items fill
-// the SMs, and moves up in proportion where they do not.
+// the SMs, and moves up in proportion where they do not.  Over 4-bit pages:
+//   8 items of 32768 tokens, D = 128: 32 rows 49 / 430, 128 rows 130 / 430
+//                            D = 64:  32 rows 34 / 373, 128 rows 75 / 373
+//   128 items of 4000 tokens, D = 128: 16 rows 46 / 64, 32 rows 75 / 65, 48 rows 102 / 65
+//                             D = 64:  32 rows 47 / 56, 48 rows 60 / 56, 64 rows 76 / 56
+//   512 items of 1000 tokens, D = 128: 32 rows 78 / 83, 48 rows 110 / 84
+//                             D = 64:  32 rows 57 / 69, 48 rows 73 / 70, 64 rows 93 / 69
+// which turns at nearly the same rows.
 constexpr int decode_rows(long long items, int D) {
   const int full = D == 64 ? 48 : 32;
   return items >= 133 ? full : static_cast<int>(full * 133 / items);

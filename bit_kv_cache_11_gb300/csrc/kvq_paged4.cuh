@@ -33,12 +33,6 @@ struct Paged4ReadParams {
   int* err;
 };
 
-// Two codes in the low four bits of a word's halves as fp16.
-__device__ __forceinline__ __half2 codes_to_half2(uint32_t w) {
-  const uint32_t x = (w & 0x000f000fu) | 0x64006400u;  // 1024 + code
-  return __hsub2(*reinterpret_cast<const __half2*>(&x), __float2half2_rn(1024.f));
-}
-
 __device__ __forceinline__ uint32_t pair_lo(uint32_t a, uint32_t b) { return __byte_perm(a, b, 0x5410); }
 __device__ __forceinline__ uint32_t pair_hi(uint32_t a, uint32_t b) { return __byte_perm(a, b, 0x7632); }
 __device__ __forceinline__ __half2 as_half2(uint32_t x) { return *reinterpret_cast<const __half2*>(&x); }

@@ -284,6 +284,15 @@ __device__ __forceinline__ void store_run(const PagedStoreParams& p, int t, int 
 //   one prompt, 16 x 64              3.0/ 2.8   3.6/ 2.8   4.6/ 2.9   7.1/ 2.9
 // The host does not know the runs: the turn lies where prompts lose by short
 // chunks what single tokens gain.
+//
+// With keys that turn (ROT) the partner of a channel comes from the lane that
+// holds it, and the angles from memory, 64 bytes a vector.  Measured (26298 tokens
+// x 8 heads x 128, bf16, halves / interleaved): 27.5 us without turning, 55 / 48
+// with three CTAs an SM (80 registers), 60 / 48 with four (64, spills), 69 / 62 with
+// two (128); with partners from memory 75.  The angles' loads, one step after the
+// other, and the warps of the values that wait for those of the keys take the
+// difference.  With 32 query heads in the same launch, their CTAs evenly among
+// these, 120 / 123 us (floor 89); one after the other 151 / 157.
 template <int TEAM>
 __host__ __device__ constexpr int chunk_threads() {
   return TEAM == 256 ? 512 : 256;
@@ -315,7 +324,7 @@ __global__ void __launch_bounds__(chunk_threads<TEAM>(), (ROT ? 768 : 1024) / ch
     h = blockIdx.y * p.H / gridDim.y;
     if (gridDim.y > p.H && (blockIdx.y + 1) * p.H / gridDim.y == h) {
       const long long t0 = (static_cast<long long>(blockIdx.y - h) * gridDim.x + blockIdx.x) * p.q.tokens;
-      if (t0 < p.q.n_tokens) rotate_any<BF16, THREADS, kAppendHeads>(p.q, t0, tid);
+      if (t0 < p.q.n_tokens) rotate_any<BF16, THREADS>(p.q, t0, tid);
       return;
     }
   }
@@ -456,7 +465,7 @@ cudaError_t launch_team(PagedStoreParams p, cudaStream_t st) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((p.n_tokens + p.chunk - 1) / p.chunk, p.H);
   if (ROT && p.q.n_heads > 0) {
-    const long long ctas = rotate_ctas(&p.q, THREADS, kAppendHeads);
+    const long long ctas = rotate_ctas(&p.q, THREADS);
     cfg.gridDim.y += static_cast<unsigned>((ctas + cfg.gridDim.x - 1) / cfg.gridDim.x);
   }
   cfg.blockDim = dim3(THREADS);

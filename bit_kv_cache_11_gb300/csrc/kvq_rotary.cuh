@@ -194,10 +194,14 @@ __device__ __forceinline__ uint4 turn_chunk(uint4 own, const ChunkTurn& ct, cons
   return turn_single<BF16>(own, head, vec * 8, a, rot, interleaved);
 }
 
+// Heads of a thread.
+constexpr int kHeads = 4;
+
 // Tokens [t0, t0 + p.tokens) by a CTA's THREADS threads.  A thread turns one unit
-// of HEADS heads of a token: their angles are the same, and their loads are on
-// their way at once.
-template <bool BF16, RotateKind KIND, int THREADS, int HEADS>
+// of kHeads heads of a token: their angles are loaded once, and the heads' loads
+// are on their way together.  Measured (26298 tokens x 32 heads x 128, bf16): one
+// head a thread 84 us (the angles' loads fill the L1), two 74, four 66.
+template <bool BF16, RotateKind KIND, int THREADS>
 __device__ __forceinline__ void rotate_tokens(const RotateParams& p, long long t0, int tid) {
   const int n = static_cast<int>(min(static_cast<long long>(p.tokens), p.n_tokens - t0));
   const uint32_t total = static_cast<uint32_t>(n) * p.per.d;
@@ -205,7 +209,7 @@ __device__ __forceinline__ void rotate_tokens(const RotateParams& p, long long t
   const bool copies = p.x != p.out;
   for (uint32_t i = tid; i < total; i += THREADS) {
     const uint32_t t = i / p.per, r = i - t * p.per.d, h0 = r / p.units, u = r - h0 * p.units.d;
-    const int heads = min(HEADS, static_cast<int>((p.n_heads - h0 + p.step - 1) / p.step));  // h0, h0 + step, ...
+    const int heads = min(kHeads, static_cast<int>((p.n_heads - h0 + p.step - 1) / p.step));  // h0, h0 + step, ...
     const uint16_t* x = p.x + (t0 + t) * p.x_stride + h0 * p.D;
     uint16_t* out = p.out + (t0 + t) * p.out_stride + h0 * p.D;
     const float2* a = p.angles + (t0 + t) * half;
@@ -230,9 +234,9 @@ __device__ __forceinline__ void rotate_tokens(const RotateParams& p, long long t
       if (KIND == kHalves && c >= half) c += half;
       const bool turns = c < p.rot;
       if (!turns && !copies) continue;
-      uint4 va[HEADS], vb[HEADS];
+      uint4 va[kHeads], vb[kHeads];
 #pragma unroll
-      for (int k = 0; k < HEADS; ++k) {
+      for (int k = 0; k < kHeads; ++k) {
         if (k < heads) {
           va[k] = *reinterpret_cast<const uint4*>(x + c + k * step);
           if (KIND == kHalves && turns) vb[k] = *reinterpret_cast<const uint4*>(x + c + half + k * step);
@@ -245,7 +249,7 @@ __device__ __forceinline__ void rotate_tokens(const RotateParams& p, long long t
         for (int j = 0; j < (KIND == kHalves ? 4 : 2); ++j) cs[j] = angles2(a + 2 * j);
       }
 #pragma unroll
-      for (int k = 0; k < HEADS; ++k) {
+      for (int k = 0; k < kHeads; ++k) {
         if (k >= heads) break;
         if (turns) {
           if constexpr (KIND == kHalves) {
@@ -268,21 +272,17 @@ __device__ __forceinline__ void rotate_tokens(const RotateParams& p, long long t
 }
 
 // The same where the kind is known at run time only.
-template <bool BF16, int THREADS, int HEADS>
+template <bool BF16, int THREADS>
 __device__ __forceinline__ void rotate_any(const RotateParams& p, long long t0, int tid) {
-  if (!rotate_aligned(p.rot, p.interleaved)) rotate_tokens<BF16, kSingle, THREADS, HEADS>(p, t0, tid);
-  else if (p.interleaved) rotate_tokens<BF16, kInterleaved, THREADS, HEADS>(p, t0, tid);
-  else rotate_tokens<BF16, kHalves, THREADS, HEADS>(p, t0, tid);
+  if (!rotate_aligned(p.rot, p.interleaved)) rotate_tokens<BF16, kSingle, THREADS>(p, t0, tid);
+  else if (p.interleaved) rotate_tokens<BF16, kInterleaved, THREADS>(p, t0, tid);
+  else rotate_tokens<BF16, kHalves, THREADS>(p, t0, tid);
 }
 
-// Heads of a thread: four where turning is all a kernel does, two beside a store,
-// whose registers leave no room.
-constexpr int kRotateHeads = 4, kAppendHeads = 4;
-
-// CTAs of `threads` that turn p's heads: a few rounds each, fewer while that
-// leaves SMs idle.
-inline long long rotate_ctas(RotateParams* p, int threads, int heads) {
-  p->step = (p->n_heads + heads - 1) / heads;
+// CTAs of `threads` that turn p's heads: two rounds each (one or four: 66 and 67 us
+// instead of 66 for the case above), one while that leaves SMs idle.
+inline long long rotate_ctas(RotateParams* p, int threads) {
+  p->step = (p->n_heads + kHeads - 1) / kHeads;
   const long long per = static_cast<long long>(p->step) * p->units.d, all = per * p->n_tokens;
   const long long want = std::min<long long>(2 * threads, std::max<long long>(threads, all / (152 * 4)));
   p->tokens = static_cast<int>(std::max<long long>(1, std::min<long long>(want / per, p->n_tokens)));
