@@ -323,7 +323,8 @@ kvq_status kvq_paged_plan_positions(const int* ctx_len, const int* new_len, int 
     return KVQ_ERR_INVALID_ARG;
   if (n_free_pages > 0 && !dev_ptr(free_pages, 4)) return KVQ_ERR_INVALID_ARG;
   if (n_tokens > 0 && !dev_ptr(slots, 16)) return KVQ_ERR_INVALID_ARG;
-  if (!aligned(positions, 16) || (positions != nullptr && (positions == ctx_len || positions == new_len)))
+  if (!aligned(positions, 16) ||
+      (positions != nullptr && (positions == ctx_len || positions == new_len || positions == slots)))
     return KVQ_ERR_INVALID_ARG;
   // several CTAs read the inputs while the first writes these
   if (seq_len == ctx_len || seq_len == new_len || n_left == n_free || cu_new == ctx_len ||

@@ -57,8 +57,8 @@
 // 64 ragged requests 34.6 us, one of 257 tokens 7.6.  Measured and not kept: eight
 // warps 59 us, sixteen 52 (spills); the metadata by bulk copies 1 % slower; scores
 // from the codes themselves (a product for each group, times the step) 50.2 us, but
-// for keys that are not rounded to fp16, which the definition is: outputs 4.8e-4
-// from it instead of 2.7e-4.
+// for keys that are not rounded to fp16, as a value's definition is: fp16 outputs
+// 4.8e-4 off 64 bits instead of 2.3e-4 (fp32 weights 2.1e-4).
 #pragma once
 
 #include "kvq_decode_mma.cuh"

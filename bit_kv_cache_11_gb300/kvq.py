@@ -320,7 +320,7 @@ def __getattr__(name):
         from . import rotary as home
     else:
         home = None
-    if hasattr(home, name):
+    if home is not None and hasattr(home, name):
         globals()[name] = getattr(home, name)
         return globals()[name]
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

@@ -423,6 +423,29 @@ def test_a_pool_beyond_four_gigabytes(kvq):
 
 # ---------------------------------------------------------------- together
 
+@pytest.mark.parametrize("batch,most_ctx,most_new,short", [(1, 0, 1, 0), (5, 90, 40, 0), (300, 500, 9, 0), (64, 60, 30, 20),
+                                                           (4096, 3, 2, 0)])
+def test_plan_positions(kvq, batch, most_ctx, most_new, short):
+    """Every new token's position, with the plan's other outputs as without; requests
+    that the stack cannot serve get theirs too."""
+    rng = np.random.default_rng(batch + short)
+    ctx, new = rng.integers(0, most_ctx + 1, batch), rng.integers(0, most_new + 1, batch)
+    ps, n = 16, int(new.sum())
+    pages = int((-(-(ctx + new) // ps)).sum())
+    have = -(-ctx // ps)
+    table = rng.integers(0, pages + 1, (batch, int((-(-(ctx + new) // ps)).max()) + 1))
+    stack = pages - int(have.sum()) - short
+    free = ints(rng.permutation(max(stack, 0) + 5))
+    args = (ints(ctx), ints(new))
+    t1, t2 = ints(table), ints(table)
+    pos = torch.full((n + 6,), -9, dtype=torch.int32, device="cuda")
+    a = kvq.kvq_paged_plan(*args, t1, free, ints([max(stack, 0)]), ps, n + 5)
+    b = kvq.kvq_paged_plan(*args, t2, free, ints([max(stack, 0)]), ps, n + 5, positions=pos)
+    assert torch.equal(t1, t2) and all(torch.equal(x, y) for x, y in zip(a, b))
+    want = np.concatenate([c + np.arange(m) for c, m in zip(ctx, new)] + [np.zeros(5), [-9]])
+    assert np.array_equal(f64(pos), want)
+
+
 @pytest.mark.parametrize("cls", ["PagedCache", "PagedCache4"])
 @pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
 def test_serving_steps(kvq, cls, dtype):

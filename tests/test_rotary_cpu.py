@@ -193,3 +193,17 @@ def test_binding_refuses_positions(kvq):
     ok = [i32(3), i32(3), i32(3, 4), i32(9), i32(1), 16, 5]
     refused(kvq, "positions", kvq.kvq_paged_plan, *ok, positions=i32(4))
     refused(kvq, "positions", kvq.kvq_paged_plan, *ok, positions=i32(5).long())
+
+
+def test_plan_positions_refusals(kvq):
+    k = kvq
+    good = dict(ctx=A, new=A + 64, batch=4, table=A, max_pages=8, free=A, n_free_pages=10, n_free=A, ps=16, n_tokens=9,
+                cu=A + 128, seq=A + 192, slots=A, positions=A + 512, left=A + 256, err=None, stream=None)
+
+    def call(**over):
+        return k._lib.kvq_paged_plan_positions(*{**good, **over}.values())
+
+    for over in (dict(positions=A + 516), dict(positions=A), dict(positions=A + 64), dict(slots=A + 512), dict(batch=0),
+                 dict(seq=A)):
+        assert call(**over) == k.KVQ_ERR_INVALID_ARG, over
+    assert call(ps=24) == k.KVQ_ERR_UNSUPPORTED
