@@ -145,3 +145,23 @@ def test_two_appends_at_once(kvq, cls):
     for a, b in zip(one._pool(), two._pool()):
         assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
     two.check()
+
+
+@pytest.mark.parametrize("cls", ["PagedCache", "PagedCache4"])
+def test_many_tokens_at_once(kvq, cls):
+    """A step of 70001 tokens, queries in the same call, against turning and storing."""
+    H, D, ps, T = 2, 64, 64, 70001
+    one, two = (getattr(kvq, cls)(n_pages=1100, page_size=ps, n_q_heads=6, n_kv_heads=H, head_dim=D) for _ in "ab")
+    k, v = (torch.randn(T, H, D, device="cuda").bfloat16() for _ in "kv")
+    q = torch.randn(T, 6, D, device="cuda").bfloat16()
+    ids = torch.randperm(1100, device="cuda")
+    t = torch.arange(T, device="cuda")
+    slots = (ids[t // ps] * ps + t % ps).int()
+    for rot, inter in ((64, False), (32, True), (20, False)):
+        ang = kvq.kvq_rotary_angles(t.int(), kvq.kvq_rotary_turns(rot))
+        got = one.append(k, v, slots, ang, interleaved=inter, q=q)
+        two.store(kvq.kvq_rotate(k, ang, inter), v, slots)
+        assert torch.equal(got, kvq.kvq_rotate(q, ang, inter))
+        for a, b in zip(one._pool(), two._pool()):
+            assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+    one.check()
