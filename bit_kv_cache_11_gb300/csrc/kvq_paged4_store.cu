@@ -7,11 +7,9 @@
 // A thread holds 16 channels, half a group: its neighbour's minimum and maximum
 // complete the statistics, its codes are one 8-byte store.
 //
-// The quotient comes from an approximate reciprocal and the 1.5 * 2^23 rounding
-// trick, two elements an instruction; the exact distance of x - mn from the
-// code's multiple of the step tells where that may be another code than the
-// divide's, and only those divide.  (A tie itself goes by the code's last bit:
-// values of few bits meet ties often.)
+// The divide is three packed operations on two quotients, exact for steps of 11
+// bits, and the rounding one more; ties need no branch, which values of few bits
+// would take often.
 //
 // Bound: arithmetic, about 430 instructions a thread (68 % of the issue slots,
 // 60 % of the L1's throughput with keys turned).  Measured (us; 26298 tokens x 8
@@ -104,15 +102,15 @@ __device__ __forceinline__ uint2 quantize16(uint32_t (&w)[8], uint32_t pair, uin
   const __half sh = __float2half_rn(fifteenth(range));
   const float step = __half2float(sh);
   *meta = as_word(__halves2half2(sh, __float2half_rn(mn)));
-  // rint by the fp32 numbers around 1.5 * 2^23, whose last bit is 1 and whose bits
-  // are this one's plus the code.  `far` is the largest distance of a difference
-  // from its code's multiple of the step (exact): up to half a step, less what the
-  // reciprocal errs by, the code is the nearest.  A tie, or a step that is no
-  // normal fp16 number and so may be far too small, needs another look.
+  // The divide, correctly rounded: with an approximate reciprocal (2^-22), q + (d -
+  // q step) inv errs by less than 2^-18 of its last place (the remainder is exact),
+  // and a quotient by a step of 11 bits is no nearer than 2^-12 to the middle
+  // between two fp32 numbers.  Then rint by the fp32 numbers around 1.5 * 2^23,
+  // whose last bit is 1 and whose bits are this one's plus the code.  (A step that
+  // is no normal fp16 number may be far too small: codes end at 15.)
   constexpr float kRint = 12582912.f;
   constexpr uint32_t kBits = 0x4b400000u, kAll = 0x11111111u;
   const float inv = step > 0.f ? about_inverse(step) : 0.f;
-  float far = 0.f;
   uint32_t o[2];
 #pragma unroll
   for (int c = 0; c < 2; ++c) {
@@ -120,33 +118,13 @@ __device__ __forceinline__ uint2 quantize16(uint32_t (&w)[8], uint32_t pair, uin
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const float2 d = add2(__half22float2(as_half2(w[4 * c + j])), twice(-mn));
-      const float2 r = fma2(d, twice(inv), twice(kRint));
-      const float2 e = fma2(add2(r, twice(-kRint)), twice(-step), d);
-      far = fmaxf(far, fmaxf(fabsf(e.x), fabsf(e.y)));
-      word += __float_as_uint(r.x) << (KEY ? 4 * j : 8 * j);
-      word += __float_as_uint(r.y) << (KEY ? 4 * j + 16 : 8 * j + 4);
+      float2 q = fma2(d, twice(inv), twice(0.f));
+      q = fma2(fma2(q, twice(-step), d), twice(inv), q);
+      const float2 r = add2(q, twice(kRint));
+      word += __float_as_uint(fminf(r.x, kRint + 15.f)) << (KEY ? 4 * j : 8 * j);
+      word += __float_as_uint(fminf(r.y, kRint + 15.f)) << (KEY ? 4 * j + 16 : 8 * j + 4);
     }
     o[c] = word;
-  }
-  if (step > 0.f && (far > 0.49999f * step || step < 0x1p-14f)) {
-#pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      o[c] = 0;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float2 f = __half22float2(as_half2(w[4 * c + (j >> 1)]));
-        const float d = (j & 1 ? f.y : f.x) - mn;
-        float code = rintf(d * inv);
-        const float e = fmaf(-code, step, d);
-        // an exact tie goes to the even code; near one (or far off) divide
-        if (fabsf(e) == 0.5f * step && step >= 0x1p-14f) {
-          code += static_cast<int>(code) & 1 ? copysignf(1.f, e) : 0.f;
-        } else if (fabsf(e) > 0.49999f * step) {
-          code = rintf(__fdiv_rn(d, step));
-        }
-        o[c] |= static_cast<uint32_t>(min(static_cast<int>(code), 15)) << (KEY ? 4 * (j >> 1) + 16 * (j & 1) : 4 * j);
-      }
-    }
   }
   return make_uint2(o[0], o[1]);
 }
