@@ -75,11 +75,11 @@ __device__ __forceinline__ float2 bounds(const uint32_t (&w)[8]) {
   }
 }
 
-// The two words of codes of 16 channels w and the {step, minimum} pair of their
-// group, whose other half the lane's neighbour holds.  *odd: one of the 16 is
+// Step and minimum of a group, of which the lane holds the 16 channels w (turned to
+// fp16 here) and its neighbour the others; by whole warps.  *odd: one of the 16 is
 // infinite or NaN.
-template <bool BF16, bool KEY>
-__device__ __forceinline__ uint2 quantize16(uint32_t (&w)[8], uint32_t pair, uint32_t* meta, bool* odd) {
+template <bool BF16>
+__device__ __forceinline__ __half2 group_of(uint32_t (&w)[8], bool* odd) {
   float2 b = bounds<BF16>(w);
   *odd = false;
   if (!(b.x >= -kMost4 && b.y <= kMost4)) {  // beyond the bounds, infinite or NaN
@@ -97,11 +97,15 @@ __device__ __forceinline__ uint2 quantize16(uint32_t (&w)[8], uint32_t pair, uin
     b = make_float2(__half2float(__float2half_rn(b.x)), __half2float(__float2half_rn(b.y)));
   }
   // (a minimum or a range of -0 is stored as 0)
-  const float mn = fminf(b.x, __shfl_xor_sync(pair, b.x, 1)) + 0.f;
-  const float range = fmaxf(b.y, __shfl_xor_sync(pair, b.y, 1)) - mn + 0.f;
-  const __half sh = __float2half_rn(fifteenth(range));
-  const float step = __half2float(sh);
-  *meta = as_word(__halves2half2(sh, __float2half_rn(mn)));
+  const float mn = fminf(b.x, __shfl_xor_sync(~0u, b.x, 1)) + 0.f;
+  const float range = fmaxf(b.y, __shfl_xor_sync(~0u, b.y, 1)) - mn + 0.f;
+  return __floats2half2_rn(fifteenth(range), mn);
+}
+
+// The two words of codes of 16 channels.
+template <bool KEY>
+__device__ __forceinline__ uint2 codes16(const uint32_t (&w)[8], __half2 meta) {
+  const float step = __low2float(meta), mn = __high2float(meta);
   // The divide, correctly rounded: with an approximate reciprocal (2^-22), q + (d -
   // q step) inv errs by less than 2^-18 of its last place (the remainder is exact),
   // and a quotient by a step of 11 bits is no nearer than 2^-12 to the middle
@@ -156,8 +160,8 @@ __device__ __forceinline__ void append_tokens(const Paged4StoreParams& p, const 
   constexpr int TPR = D / 16;  // threads of a row
   const int n = static_cast<int>(min(static_cast<long long>(g.tokens), p.n_tokens - t0));
   const uint32_t total = static_cast<uint32_t>(n) * 2 * g.per.d;
-  const uint32_t pair = 3u << (tid & 30);
-  for (uint32_t i = tid; i < total; i += kThreads) {
+  for (uint32_t i0 = tid; (i0 & ~31u) < total; i0 += kThreads) {
+    const uint32_t i = min(i0, total - 1);  // (whole warps shuffle)
     const uint32_t st = i / g.per, r = i - st * g.per.d, t = st >> 1, side = st & 1;
     const uint32_t h = r / TPR, c = 16 * (r - h * TPR);
     const uint16_t* head = static_cast<const uint16_t*>(side ? p.x[1] : p.x[0]) +
@@ -171,19 +175,20 @@ __device__ __forceinline__ void append_tokens(const Paged4StoreParams& p, const 
 #pragma unroll
       for (int j = 0; j < 2; ++j) v[j] = turned<BF16>(v[j], head, c + 8 * j, a, p.rot, p.interleaved);
     }
+    uint32_t w[8] = {v[0].x, v[0].y, v[0].z, v[0].w, v[1].x, v[1].y, v[1].z, v[1].w};
+    bool odd;
+    const __half2 meta = group_of<BF16>(w, &odd);
     const int page = slot >> p.lg_ps;
-    if (slot < 0) continue;
+    if (slot < 0 || i0 >= total) continue;
     if (page >= p.n_pages) {
       if (r == 0) set_err(p.err, KVQ_PAGED_ERR_BAD_PAGE);
       continue;
     }
-    uint32_t w[8] = {v[0].x, v[0].y, v[0].z, v[0].w, v[1].x, v[1].y, v[1].z, v[1].w}, meta;
-    bool odd;
-    const uint2 codes = side ? quantize16<BF16, false>(w, pair, &meta, &odd) : quantize16<BF16, true>(w, pair, &meta, &odd);
+    const uint2 codes = side ? codes16<false>(w, meta) : codes16<true>(w, meta);
     if (odd) set_err(p.err, KVQ_PAGED_ERR_NONFINITE);
     const size_t at = (((static_cast<size_t>(page) * p.H + h) << p.lg_ps) + (slot & ((1 << p.lg_ps) - 1))) * (D / 2) + c / 2;
     *reinterpret_cast<uint2*>((side ? p.codes[1] : p.codes[0]) + at) = codes;
-    if ((c & 16) == 0) (side ? p.meta[1] : p.meta[0])[at / 16] = meta;
+    if ((c & 16) == 0) (side ? p.meta[1] : p.meta[0])[at / 16] = as_word(meta);
   }
 }
 
