@@ -173,17 +173,17 @@ __device__ __forceinline__ const uint4* vec_ptr(const PagedStoreParams& p, int s
                                         t * (side ? p.stride[1] : p.stride[0]) + h * D) + vec;
 }
 
-// Vector `vec` of token t's key (side 0, turned by its angles when ROT) or value; a
-// row's vectors are in the consecutive lanes of `mask`.
+// Vector `vec` of token t's key (side 0, turned by its angles when ROT) or value, 0
+// for a lane that is not `live`; a row's vectors are in consecutive lanes.
 template <int D, bool BF16, bool ROT>
 __device__ __forceinline__ uint4 load_vec(const PagedStoreParams& p, int side, long long t, int h, int vec, int lane,
-                                          uint32_t mask) {
-  const uint4 v = __ldg(vec_ptr(p, side, t, h, D, vec));
+                                          bool live) {
+  const uint4 v = live ? __ldg(vec_ptr(p, side, t, h, D, vec)) : make_uint4(0, 0, 0, 0);
   if constexpr (ROT) {
-    if (side == 0)
-      return turn_chunk<BF16>(v, ChunkTurn(vec, lane, p.rot, p.interleaved),
-                              static_cast<const uint16_t*>(p.x[0]) + t * p.stride[0] + h * D, vec,
-                              p.angles + t * (p.rot >> 1), p.rot, p.interleaved, mask);
+    const uint4 k = turn_chunk<BF16>(v, ChunkTurn(vec, lane, p.rot, p.interleaved),
+                                     static_cast<const uint16_t*>(p.x[0]) + t * p.stride[0] + h * D, vec,
+                                     p.angles + t * (p.rot >> 1), p.rot, p.interleaved, live && side == 0);
+    if (side == 0) return k;
   }
   return v;
 }
@@ -202,7 +202,6 @@ __device__ __forceinline__ void store_run(const PagedStoreParams& p, int t, int 
     return;
   }
   const int side = lane >> 4, l = lane & 15, sub = l / VPR, vec = l % VPR;
-  const uint32_t mask = (VPR == 16 ? 0xffffu : 0xffu) << (lane & ~(VPR - 1));  // the lanes of a row
   // rows of the run: until the page ends or the slots stop following
   const int most = min((1 << p.lg_ps) - row0, p.n_tokens - t);
   int n = 1;
@@ -218,10 +217,10 @@ __device__ __forceinline__ void store_run(const PagedStoreParams& p, int t, int 
   }
   float* scale = (side ? p.scale[1] : p.scale[0]) + static_cast<size_t>(page) * p.H + h;
   const float was = *scale;
-  const uint4 zero = make_uint4(0, 0, 0, 0);
-  const uint4 first = sub < n ? load_vec<D, BF16, ROT>(p, side, t + sub, h, vec, lane, mask) : zero;
+  auto load = [&](int i) { return load_vec<D, BF16, ROT>(p, side, t + i, h, vec, lane, i < n); };
+  const uint4 first = load(sub);
   uint32_t m2 = vec_max(first, 0);
-  for (int i = sub + RPS; i < n; i += RPS) m2 = vec_max(load_vec<D, BF16, ROT>(p, side, t + i, h, vec, lane, mask), m2);
+  for (int i = RPS; i < n; i += RPS) m2 = vec_max(load(i + sub), m2);
   auto side_max = [](uint32_t x) {  // over the side's sixteen lanes
 #pragma unroll
     for (int o = 1; o < 16; o <<= 1) x = max(x, __shfl_xor_sync(0xffffffffu, x, o));
@@ -231,8 +230,7 @@ __device__ __forceinline__ void store_run(const PagedStoreParams& p, int t, int 
   const bool odd = mag >= inf_bits<BF16>();  // the side holds a NaN or an infinity
   if (__any_sync(0xffffffffu, odd)) {
     m2 = 0;
-    for (int i = sub; i < n; i += RPS)
-      m2 = vec_max_finite<BF16>(load_vec<D, BF16, ROT>(p, side, t + i, h, vec, lane, mask), m2);
+    for (int i = 0; i < n; i += RPS) m2 = vec_max_finite<BF16>(load(i + sub), m2);
     mag = side_max(fold2(m2));
     if (odd && l == 0) set_err(p.err, KVQ_PAGED_ERR_NONFINITE);
   }
@@ -253,9 +251,10 @@ __device__ __forceinline__ void store_run(const PagedStoreParams& p, int t, int 
   const float inv = exp2i(-e);
   const bool plain = plain_codes<BF16>(odd, e);
   if (sub < n) *reinterpret_cast<uint2*>(base + static_cast<size_t>(row0 + sub) * D) = codes8<BF16>(first, inv, plain);
-  for (int i = sub + RPS; i < n; i += RPS)
-    *reinterpret_cast<uint2*>(base + static_cast<size_t>(row0 + i) * D) =
-        codes8<BF16>(load_vec<D, BF16, ROT>(p, side, t + i, h, vec, lane, mask), inv, plain);
+  for (int i = RPS + sub; i - sub < n; i += RPS) {
+    const uint2 c = codes8<BF16>(load(i), inv, plain);
+    if (i < n) *reinterpret_cast<uint2*>(base + static_cast<size_t>(row0 + i) * D) = c;
+  }
   if (l == 0) *scale = exp2i(e);
 }
 
@@ -394,16 +393,15 @@ __global__ void __launch_bounds__(chunk_threads<TEAM>(), (ROT ? 768 : 1024) / ch
       if ((rows >> s) & 1) x[s] = __ldg(vec_ptr(p, side, t + s * RPS + sub, h, D, vec));
     }
     if constexpr (ROT) {
-      // (a row's lanes hold it together, or none of them)
-      const uint32_t mask = (VPR == 16 ? 0xffffu : 0xffu) << (lane & ~(VPR - 1));
       const ChunkTurn ct(vec, lane, p.rot, p.interleaved);
-      if (side == 0) {
+      if (TEAM < 32 || side == 0) {  // whole warps
 #pragma unroll
         for (int s = 0; s < kSteps; ++s) {
           const long long tok = t + s * RPS + sub;
-          if ((rows >> s) & 1)
-            x[s] = turn_chunk<BF16>(x[s], ct, static_cast<const uint16_t*>(p.x[0]) + tok * p.stride[0] + h * D, vec,
-                                    p.angles + tok * (p.rot >> 1), p.rot, p.interleaved, mask);
+          const uint4 k = turn_chunk<BF16>(x[s], ct, static_cast<const uint16_t*>(p.x[0]) + tok * p.stride[0] + h * D,
+                                           vec, p.angles + tok * (p.rot >> 1), p.rot, p.interleaved,
+                                           side == 0 && ((rows >> s) & 1));
+          if (side == 0) x[s] = k;
         }
       }
     }

@@ -161,35 +161,40 @@ struct ChunkTurn {
   bool pairs;   // aligned halves: the partner is a lane's whole chunk
   int src;      // that lane
   int angle;    // first angle
-  float sign;
+  bool second;  // of the two chunks of a pair
   __device__ __forceinline__ ChunkTurn(int vec, int lane, int rot, int interleaved) {
     const int c = vec * 8, half = rot >> 1;
     turns = c < rot;
     pairs = !interleaved && rotate_aligned(rot, interleaved);
-    const bool second = !interleaved && c >= half;
+    second = !interleaved && c >= half;
     angle = interleaved ? c >> 1 : second ? c - half : c;
     src = !turns || !pairs ? lane : second ? lane - (half >> 3) : lane + (half >> 3);
-    sign = second ? 1.f : -1.f;
   }
 };
 
-// The chunk `own` of `head` after the turn by angles a [rot / 2].  Every lane of
-// `mask` takes part.
+// The chunk `own` of `head` after the turn by angles a [rot / 2].  Whole warps take
+// part; a lane that is not `live` loads nothing.  Of two chunks whose channels are
+// pairs, the first's lane turns the first four pairs and the second's the last four,
+// so that each loads the half of the angles.
 template <bool BF16>
 __device__ __forceinline__ uint4 turn_chunk(uint4 own, const ChunkTurn& ct, const uint16_t* head, int vec,
-                                            const float2* a, int rot, int interleaved, uint32_t mask) {
+                                            const float2* a, int rot, int interleaved, bool live) {
   if (ct.pairs) {
-    uint4 o;
-    o.x = __shfl_sync(mask, own.x, ct.src);
-    o.y = __shfl_sync(mask, own.y, ct.src);
-    o.z = __shfl_sync(mask, own.z, ct.src);
-    o.w = __shfl_sync(mask, own.w, ct.src);
+    const uint32_t x = __shfl_sync(~0u, ct.second ? own.x : own.z, ct.src);
+    const uint32_t y = __shfl_sync(~0u, ct.second ? own.y : own.w, ct.src);
+    uint32_t va[2] = {ct.second ? x : own.x, ct.second ? y : own.y};
+    uint32_t vb[2] = {ct.second ? own.z : x, ct.second ? own.w : y};
+    if (ct.turns && live) {
+      a += ct.angle + (ct.second ? 4 : 0);
+      turn_words<BF16>(va[0], vb[0], angles2(a));
+      turn_words<BF16>(va[1], vb[1], angles2(a + 2));
+    }
+    const uint32_t z = __shfl_sync(~0u, ct.second ? va[0] : vb[0], ct.src);
+    const uint32_t w = __shfl_sync(~0u, ct.second ? va[1] : vb[1], ct.src);
     if (!ct.turns) return own;
-    a += ct.angle;
-    return make_uint4(turn_own<BF16>(own.x, o.x, angles2(a), ct.sign), turn_own<BF16>(own.y, o.y, angles2(a + 2), ct.sign),
-                      turn_own<BF16>(own.z, o.z, angles2(a + 4), ct.sign), turn_own<BF16>(own.w, o.w, angles2(a + 6), ct.sign));
+    return ct.second ? make_uint4(z, w, vb[0], vb[1]) : make_uint4(va[0], va[1], z, w);
   }
-  if (!ct.turns) return own;
+  if (!ct.turns || !live) return own;
   if (rotate_aligned(rot, interleaved)) return turn_interleaved<BF16>(own, a + ct.angle);
   return turn_single<BF16>(own, head, vec * 8, a, rot, interleaved);
 }
