@@ -262,8 +262,8 @@ __device__ __forceinline__ void store_run(const PagedStoreParams& p, int t, int 
 //
 // It lists the chunk's leaders.  Where runs are short (more than an eighth of
 // the tokens lead), each warp stores whole runs.  Where they are long, a team
-// of TEAM = page_size * D / 64 threads stores one side of a run: eight 16-byte
-// vectors a thread cover a whole page, stay in registers between the maximum
+// of TEAM = page_size * D / 32 threads stores a run: four 16-byte vectors of
+// either side a thread cover a whole page, stay in registers between the maximum
 // and the codes, and are all on their way at once; a CTA holds as many teams
 // as fit 256 threads (512 for the largest page).
 //
@@ -294,22 +294,21 @@ __device__ __forceinline__ void store_run(const PagedStoreParams& p, int t, int 
 // these, 120 / 123 us (floor 89); one after the other 151 / 157.
 template <int TEAM>
 __host__ __device__ constexpr int chunk_threads() {
-  return TEAM == 256 ? 512 : 256;
+  return TEAM == 512 ? 512 : 256;
 }
-constexpr int kSteps = 8;
+constexpr int kSteps = 4;
 constexpr int kShortChunks = 8192;
 
 template <int D, bool BF16, bool ROT, int TEAM>
 __global__ void __launch_bounds__(chunk_threads<TEAM>(), (ROT ? 768 : 1024) / chunk_threads<TEAM>())
     paged_store_kernel(const PagedStoreParams p) {
-  constexpr int THREADS = chunk_threads<TEAM>(), TEAMS = THREADS / (2 * TEAM);
-  constexpr int VPR = D / 8, RPS = TEAM / VPR, CHUNK = TEAM * 64 / D * TEAMS;  // the most
-  constexpr int WPT = TEAM > 32 ? TEAM / 32 : 1;  // warps of a team's side
+  constexpr int THREADS = chunk_threads<TEAM>(), TEAMS = THREADS / TEAM, WARPS = TEAM / 32;
+  constexpr int VPR = D / 8, RPS = TEAM / VPR, CHUNK = RPS * kSteps * TEAMS;  // the most
   __shared__ int s_list[CHUNK];
   __shared__ int s_count;
-  __shared__ uint32_t s_max[TEAMS][2][2][WPT];  // [team][pass][side][warp]
+  __shared__ uint32_t s_max[TEAMS][2][2][WARPS];  // [team][pass][side][warp]
   const int tid = threadIdx.x, lane = tid & 31;
-  const int side = tid / TEAM & 1, team = tid / (2 * TEAM), l = tid % TEAM;
+  const int team = tid / TEAM, l = tid % TEAM;
   const int sub = l / VPR, vec = l % VPR;
   const int tb = blockIdx.x * p.chunk;
   int h = blockIdx.y;
@@ -339,126 +338,131 @@ __global__ void __launch_bounds__(chunk_threads<TEAM>(), (ROT ? 768 : 1024) / ch
     for (int i = tid >> 5; i < count; i += THREADS / 32) store_run<D, BF16, ROT>(p, s_list[i], h, lane);
     return;
   }
-  // Threads of a run's two sides wait for one another (whole warps when a
-  // side is 16 or 32 threads).
   auto team_sync = [&]() {
-    if constexpr (TEAM > 32)
-      asm volatile("bar.sync %0, %1;" ::"r"(1 + team), "n"(2 * TEAM) : "memory");
+    if constexpr (WARPS > 1) asm volatile("bar.sync %0, %1;" ::"r"(1 + team), "n"(TEAM) : "memory");
     else __syncwarp();
   };
-  // The side's largest value of x; *both: the larger one of the two sides.
-  auto side_max = [&](int pass, uint32_t x, uint32_t* both) {
-    if constexpr (TEAM > 32) {
-      x = __reduce_max_sync(0xffffffffu, x);
-      if (lane == 0) s_max[team][pass][side][l >> 5] = x;
-      team_sync();
-      uint32_t m[2] = {0, 0};
+  // The largest values of either side over the team.
+  auto team_max = [&](int pass, uint32_t (&x)[2]) {
 #pragma unroll
-      for (int w = 0; w < WPT; ++w) {
-        m[0] = max(m[0], s_max[team][pass][0][w]);
-        m[1] = max(m[1], s_max[team][pass][1][w]);
+    for (int side = 0; side < 2; ++side) x[side] = __reduce_max_sync(~0u, x[side]);
+    if constexpr (WARPS > 1) {
+      if (lane == 0) {
+        s_max[team][pass][0][l >> 5] = x[0];
+        s_max[team][pass][1][l >> 5] = x[1];
       }
-      *both = max(m[0], m[1]);
-      return side ? m[1] : m[0];
-    } else {
+      team_sync();
 #pragma unroll
-      for (int o = 1; o < TEAM; o <<= 1) x = max(x, __shfl_xor_sync(0xffffffffu, x, o));
-      *both = __reduce_max_sync(0xffffffffu, x);  // the warp's: it decides for its lanes
-      return x;
+      for (int w = 0; w < WARPS; ++w) {
+        x[0] = max(x[0], s_max[team][pass][0][w]);
+        x[1] = max(x[1], s_max[team][pass][1][w]);
+      }
     }
   };
-  // (all lanes of a warp make the same number of rounds)
-  const int rounds = TEAM >= 32 ? (count - team + TEAMS - 1) / TEAMS : (count + TEAMS - 1) / TEAMS;
-  for (int k = 0; k < rounds; ++k) {
-    const int i_run = k * TEAMS + team;
-    const bool has = i_run < count;
-    const int t = has ? s_list[i_run] : 0;
-    const int slot = has ? p.slots[t] : 0;
+  for (int i_run = team; i_run < count; i_run += TEAMS) {
+    const int t = s_list[i_run];
+    const int slot = p.slots[t];
     const int page = slot >> p.lg_ps, row0 = slot & (ps - 1);
-    const bool good = has && page < p.n_pages;
-    if (has && !good && l == 0 && side == 0) set_err(p.err, KVQ_PAGED_ERR_BAD_PAGE);
+    if (page >= p.n_pages) {
+      if (l == 0) set_err(p.err, KVQ_PAGED_ERR_BAD_PAGE);
+      continue;
+    }
     // rows that follow the leader: token t + i in row row0 + i of the page
-    const int most = good ? min(ps - row0, p.n_tokens - t) : 0;
-    float* scale = (side ? p.scale[1] : p.scale[0]) + static_cast<size_t>(good ? page : 0) * p.H + h;
-    uint4 x[kSteps];
-    uint32_t rows = 0;  // bit s: this thread holds a vector of step s
+    const int most = min(ps - row0, p.n_tokens - t);
+    uint4 x[2][kSteps];
+    uint32_t rows = 0;  // bit s: this thread holds vectors of step s
 #pragma unroll
     for (int s = 0; s < kSteps; ++s) {
       const int i = s * RPS + sub;
       if (i < most && (i == 0 || p.slots[t + i] == slot + i)) rows |= 1u << s;
     }
 #pragma unroll
-    for (int s = 0; s < kSteps; ++s) {
-      x[s] = make_uint4(0, 0, 0, 0);
-      if ((rows >> s) & 1) x[s] = __ldg(vec_ptr(p, side, t + s * RPS + sub, h, D, vec));
+    for (int side = 0; side < 2; ++side) {
+#pragma unroll
+      for (int s = 0; s < kSteps; ++s) {
+        x[side][s] = make_uint4(0, 0, 0, 0);
+        if ((rows >> s) & 1) x[side][s] = __ldg(vec_ptr(p, side, t + s * RPS + sub, h, D, vec));
+      }
+    }
+    float was[2] = {0.f, 0.f};
+    const size_t head = static_cast<size_t>(page) * p.H + h;
+    if (row0 > 0) {
+      was[0] = p.scale[0][head];
+      was[1] = p.scale[1][head];
     }
     if constexpr (ROT) {
       const ChunkTurn ct(vec, lane, p.rot, p.interleaved);
-      if (TEAM < 32 || side == 0) {  // whole warps
 #pragma unroll
-        for (int s = 0; s < kSteps; ++s) {
-          const long long tok = t + s * RPS + sub;
-          const uint4 k = turn_chunk<BF16>(x[s], ct, static_cast<const uint16_t*>(p.x[0]) + tok * p.stride[0] + h * D,
-                                           vec, p.angles + tok * (p.rot >> 1), p.rot, p.interleaved,
-                                           side == 0 && ((rows >> s) & 1));
-          if (side == 0) x[s] = k;
-        }
+      for (int s = 0; s < kSteps; ++s) {
+        const long long tok = t + s * RPS + sub;
+        x[0][s] = turn_chunk<BF16>(x[0][s], ct, static_cast<const uint16_t*>(p.x[0]) + tok * p.stride[0] + h * D, vec,
+                                   p.angles + tok * (p.rot >> 1), p.rot, p.interleaved, (rows >> s) & 1);
       }
     }
-    const float was = good && row0 > 0 ? *scale : 0.f;
-    uint32_t m2 = 0, both;
+    uint32_t mag[2];
 #pragma unroll
-    for (int s = 0; s < kSteps; ++s) m2 = vec_max(x[s], m2);
-    uint32_t mag = side_max(0, fold2(m2), &both);
-    const bool odd = mag >= inf_bits<BF16>();  // the side holds a NaN or an infinity
-    if (both >= inf_bits<BF16>()) {
-      m2 = 0;
+    for (int side = 0; side < 2; ++side) {
+      uint32_t m2 = 0;
 #pragma unroll
-      for (int s = 0; s < kSteps; ++s) m2 = vec_max_finite<BF16>(x[s], m2);
-      mag = side_max(1, fold2(m2), &both);
-      if (odd && l == 0) set_err(p.err, KVQ_PAGED_ERR_NONFINITE);
+      for (int s = 0; s < kSteps; ++s) m2 = vec_max(x[side][s], m2);
+      mag[side] = fold2(m2);
     }
-    int e = exp_for_bits<BF16>(mag);
-    if (good) {
-      uint8_t* base = (side ? p.pages[1] : p.pages[0]) +
-                      ((static_cast<size_t>(page) * p.H + h) << p.lg_ps) * D + vec * 8;
+    team_max(0, mag);
+    // a side holds a NaN or an infinity
+    const bool odd[2] = {mag[0] >= inf_bits<BF16>(), mag[1] >= inf_bits<BF16>()};
+    if (odd[0] || odd[1]) {
+#pragma unroll
+      for (int side = 0; side < 2; ++side) {
+        uint32_t m2 = 0;
+#pragma unroll
+        for (int s = 0; s < kSteps; ++s) m2 = vec_max_finite<BF16>(x[side][s], m2);
+        mag[side] = fold2(m2);
+      }
+      team_max(1, mag);
+      if (l == 0) set_err(p.err, KVQ_PAGED_ERR_NONFINITE);
+    }
+    int e[2];
+#pragma unroll
+    for (int side = 0; side < 2; ++side) {
+      e[side] = exp_for_bits<BF16>(mag[side]);
+      uint8_t* base = (side ? p.pages[1] : p.pages[0]) + (head << p.lg_ps) * D + vec * 8;
       if (row0 > 0) {
-        e = max(e, exp_of_scale(was));
-        const float now = exp2i(e);
-        if (was != now && was > 0.f) {
-          const float f = was / now;
+        e[side] = max(e[side], exp_of_scale(was[side]));
+        const float now = exp2i(e[side]);
+        if (was[side] != now && was[side] > 0.f) {
+          const float f = was[side] / now;
           for (int i = sub; i < row0; i += RPS) {
             uint2* c = reinterpret_cast<uint2*>(base + static_cast<size_t>(i) * D);
             *c = rescale8(*c, f);
           }
         }
       }
-      const float inv = exp2i(-e);
-      if (plain_codes<BF16>(odd, e)) {
+      const float inv = exp2i(-e[side]);
+      if (plain_codes<BF16>(odd[side], e[side])) {
 #pragma unroll
         for (int s = 0; s < kSteps; ++s) {
           if ((rows >> s) & 1)
             *reinterpret_cast<uint2*>(base + static_cast<size_t>(row0 + s * RPS + sub) * D) =
-                codes8<BF16>(x[s], inv, true);
+                codes8<BF16>(x[side][s], inv, true);
         }
       } else {
 #pragma unroll
         for (int s = 0; s < kSteps; ++s) {
           if ((rows >> s) & 1)
             *reinterpret_cast<uint2*>(base + static_cast<size_t>(row0 + s * RPS + sub) * D) =
-                codes8<BF16>(x[s], inv, false);
+                codes8<BF16>(x[side][s], inv, false);
         }
       }
     }
     team_sync();  // s_max and `was` are read
-    if (good && l == 0) *scale = exp2i(e);
+    if (l < 2) (l ? p.scale[1] : p.scale[0])[head] = exp2i(l ? e[1] : e[0]);
   }
 }
 
 template <int D, bool BF16, bool ROT, int TEAM>
 cudaError_t launch_team(PagedStoreParams p, cudaStream_t st) {
   constexpr int THREADS = chunk_threads<TEAM>();
-  const int most = TEAM * 64 / D * (THREADS / (2 * TEAM));
+  const int most = kSteps * TEAM * 8 / D * (THREADS / TEAM);
   p.chunk = static_cast<long long>(p.n_tokens) * p.H <= kShortChunks ? 8 : most;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((p.n_tokens + p.chunk - 1) / p.chunk, p.H);
@@ -478,15 +482,15 @@ cudaError_t launch_team(PagedStoreParams p, cudaStream_t st) {
 
 template <int D, bool BF16, bool ROT>
 cudaError_t launch(const PagedStoreParams& p, cudaStream_t st) {
-  switch ((D << p.lg_ps) / 64) {
-    case 16:
-      if constexpr (D == 64) return launch_team<D, BF16, ROT, 16>(p, st);
+  switch ((D << p.lg_ps) / (8 * kSteps)) {
+    case 32:
+      if constexpr (D == 64) return launch_team<D, BF16, ROT, 32>(p, st);
       break;
-    case 32: return launch_team<D, BF16, ROT, 32>(p, st);
     case 64: return launch_team<D, BF16, ROT, 64>(p, st);
     case 128: return launch_team<D, BF16, ROT, 128>(p, st);
-    case 256:
-      if constexpr (D == 128) return launch_team<D, BF16, ROT, 256>(p, st);
+    case 256: return launch_team<D, BF16, ROT, 256>(p, st);
+    case 512:
+      if constexpr (D == 128) return launch_team<D, BF16, ROT, 512>(p, st);
       break;
   }
   return cudaErrorInvalidValue;
