@@ -11,12 +11,14 @@
 // bits, and the rounding one more; ties need no branch, which values of few bits
 // would take often.
 //
-// Bound: arithmetic, about 430 instructions a thread (68 % of the issue slots,
-// 60 % of the L1's throughput with keys turned).  Measured (us; 26298 tokens x 8
-// heads x 128, bf16: 142 MB, floor 20.8): 44 without turning, 54 with, 27 to read
-// back (78 % of the measured copy rate); 8, 16 or 32 channels a thread 71, 44 and 60;
-// the next item's loads ahead 56, places worked out once a thread 59 (both cost
-// registers, 48 -> 75, and with them a third of the threads).  64 tokens 2.6 us.
+// Bound: arithmetic, about 300 instructions a thread (73 % of the issue slots; the
+// L1 takes 73 % of its time with keys turned).  Measured (us; 26298 tokens x 8 heads
+// x 128, bf16: 142 MB, floor 20.8): 35 without turning, 48 with halves, 42 with
+// interleaved pairs, 27 to read back (78 % of the measured copy rate); 64 tokens 1.9
+// and 2.5.  Partners by shuffles and half of the angles a lane 49; places worked out
+// once a thread 55, the next item's loads ahead no better (both cost registers, 48 ->
+// 64 and more, and with them threads); shuffles by the masks of the pairs, not of the
+// warp, 2 us more.
 #include <algorithm>
 
 #include "kvq_paged4.cuh"
@@ -198,7 +200,7 @@ __global__ void __launch_bounds__(kThreads) paged4_append_kernel(const Paged4Sto
   grid_dep_launch();
   // CTAs for keys and values lie evenly among those for the step's queries, so that
   // the ones' arithmetic runs beside the others' traffic (16000 tokens, a half of
-  // each head turned, interleaved: 58 us; one after the other 63)
+  // each head turned, interleaved: 55 us; one after the other 63)
   const unsigned kv = static_cast<unsigned>(static_cast<unsigned long long>(blockIdx.x) * g.kv_ctas / gridDim.x);
   if ((static_cast<unsigned long long>(blockIdx.x) + 1) * g.kv_ctas / gridDim.x != kv) {
     append_tokens<D, BF16>(p, g, static_cast<long long>(kv) * g.tokens, threadIdx.x);

@@ -285,13 +285,14 @@ __device__ __forceinline__ void store_run(const PagedStoreParams& p, int t, int 
 // chunks what single tokens gain.
 //
 // With keys that turn (ROT) the partner of a channel comes from the lane that
-// holds it, and the angles from memory, 64 bytes a vector.  Measured (26298 tokens
-// x 8 heads x 128, bf16, halves / interleaved): 27.5 us without turning, 55 / 48
-// with three CTAs an SM (80 registers), 60 / 48 with four (64, spills), 69 / 62 with
-// two (128); with partners from memory 75.  The angles' loads, one step after the
-// other, and the warps of the values that wait for those of the keys take the
-// difference.  With 32 query heads in the same launch, their CTAs evenly among
-// these, 120 / 123 us (floor 89); one after the other 151 / 157.
+// holds it, and the angles from memory, 32 bytes a vector.  Measured (26298 tokens
+// x 8 heads x 128, bf16, halves / interleaved): 27.4 us without turning, 44 / 41
+// with it.  Warps that held one side each took 53 / 48: those of the values waited
+// for those of the keys.  What is left of the difference are the angles' loads, one
+// step after the other.  With 32 query heads in the same launch, their CTAs evenly
+// among these, 106 / 111 us (floor 87) with three CTAs an SM (80 registers); with
+// four (64) 43 / 39 and, with the queries, 114 / 103, with two (128) 54 / 50 and
+// 129 / 139.
 template <int TEAM>
 __host__ __device__ constexpr int chunk_threads() {
   return TEAM == 512 ? 512 : 256;
