@@ -43,6 +43,12 @@ std::atomic<uint32_t> g_wait_limit{UINT32_MAX};
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 bool dev_ptr(const void* p, uintptr_t a) { return p != nullptr && aligned(p, a); }
 
+// Whether two arrays of 32-bit numbers share an element.
+bool overlap(const int* a, size_t n_a, const int* b, size_t n_b) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + 4 * n_b && y < x + 4 * n_a;
+}
+
 int log2_of(int v) {
   int l = 0;
   while ((1 << l) < v) ++l;
@@ -323,9 +329,25 @@ kvq_status kvq_paged_plan_positions(const int* ctx_len, const int* new_len, int 
     return KVQ_ERR_INVALID_ARG;
   if (n_free_pages > 0 && !dev_ptr(free_pages, 4)) return KVQ_ERR_INVALID_ARG;
   if (n_tokens > 0 && !dev_ptr(slots, 16)) return KVQ_ERR_INVALID_ARG;
-  if (!aligned(positions, 16) ||
-      (positions != nullptr && (positions == ctx_len || positions == new_len || positions == slots)))
-    return KVQ_ERR_INVALID_ARG;
+  if (!aligned(positions, 16)) return KVQ_ERR_INVALID_ARG;
+  // every CTA writes positions while others read the inputs and write the outputs
+  if (positions != nullptr) {
+    const struct {
+      const int* at;
+      size_t n;
+    } others[] = {{ctx_len, static_cast<size_t>(batch)},
+                  {new_len, static_cast<size_t>(batch)},
+                  {block_table, static_cast<size_t>(batch) * max_pages},
+                  {free_pages, static_cast<size_t>(n_free_pages)},
+                  {n_free, 1},
+                  {cu_new, static_cast<size_t>(batch) + 1},
+                  {seq_len, static_cast<size_t>(batch)},
+                  {slots, static_cast<size_t>(n_tokens)},
+                  {n_left, 1},
+                  {device_error, 1}};
+    for (const auto& x : others)
+      if (x.at != nullptr && overlap(positions, static_cast<size_t>(n_tokens), x.at, x.n)) return KVQ_ERR_INVALID_ARG;
+  }
   // several CTAs read the inputs while the first writes these
   if (seq_len == ctx_len || seq_len == new_len || n_left == n_free || cu_new == ctx_len ||
       cu_new == new_len)

@@ -64,7 +64,7 @@ def kvq_paged_plan(ctx_len, new_len, block_table, free_pages, n_free, page_size:
     seq_len = ctx_len and gets slots -1: its rows of the attention's output
     mean nothing, and its step can be made again when pages are free.
     `positions`, an int32 tensor [n_tokens], gets every new token's position
-    (0 behind the last one)."""
+    (0 behind the last one); it overlaps none of the other tensors."""
     return _plan(ctx_len, new_len, block_table, free_pages, n_free, page_size, n_tokens, cu_new,
                  seq_len, slots, n_left, error, stream, positions)
 

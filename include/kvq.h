@@ -497,7 +497,8 @@ KVQ_API kvq_status kvq_paged_attention(const kvq_paged_pool* pool, const void* q
 
 /* kvq_paged_plan that also writes positions [n_tokens] (device, 16-byte
  * aligned): the position of every new token within its request, 0 behind the
- * last one.  A request that gets no pages still gets its positions. */
+ * last one.  A request that gets no pages still gets its positions.  The array
+ * overlaps none of the call's others (KVQ_ERR_INVALID_ARG). */
 KVQ_API kvq_status kvq_paged_plan_positions(const int* ctx_len, const int* new_len, int batch,
                                             int* block_table, int max_pages, const int* free_pages,
                                             int n_free_pages, const int* n_free, int page_size,

@@ -1,0 +1,45 @@
+"""Host-side limits of the rotary calls and of the appends: arrays that overlap,
+sizes at the ends of their ranges (no GPU)."""
+import os
+import sys
+
+import pytest
+
+sys.path.insert(0, os.path.dirname(os.path.abspath(__file__)))
+
+torch = pytest.importorskip("torch")
+
+A = 1 << 20  # an aligned address that no call may touch
+
+
+@pytest.fixture(scope="module")
+def kvq():
+    from bit_kv_cache_11_gb300 import build
+    build.build()
+    from bit_kv_cache_11_gb300 import kvq as k
+    return k
+
+
+# the arrays of a plan and their elements, each in a place of its own
+PLAN = dict(ctx=(A, 4), new=(A + 1024, 4), table=(A + 2048, 4 * 8), free=(A + 4096, 10), n_free=(A + 5120, 1),
+            cu=(A + 6144, 5), seq=(A + 7168, 4), slots=(A + 8192, 9), left=(A + 9216, 1), err=(A + 10240, 1))
+
+
+@pytest.mark.parametrize("name", PLAN)
+def test_positions_overlap_no_array_of_the_plan(kvq, name):
+    """Positions are 9 elements at a multiple of 16 bytes: at an array's start, and
+    where only the last of one and the first of the other meet."""
+    at = {k: v[0] for k, v in PLAN.items()}
+
+    def call(positions, ps=16):
+        return kvq._lib.kvq_paged_plan_positions(
+            at["ctx"], at["new"], 4, at["table"], 8, at["free"], 10, at["n_free"], ps, 9, at["cu"], at["seq"],
+            at["slots"], positions, at["left"], at["err"], None)
+
+    start, n = PLAN[name]
+    last = (start + 4 * (n - 1)) & ~15
+    for bad in (start, last, start - 32):  # (start - 32: elements -8 .. 0)
+        assert call(bad) == kvq.KVQ_ERR_INVALID_ARG, bad - start
+    # beside it: nothing is refused before the page size is looked at
+    for good in (start - 48, (start + 4 * n + 15) & ~15):
+        assert call(good, ps=24) == kvq.KVQ_ERR_UNSUPPORTED, good - start
