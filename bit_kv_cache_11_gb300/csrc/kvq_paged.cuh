@@ -39,6 +39,10 @@ struct PagedPlanParams {
   int* err;
 };
 
+// Most tokens of a store into E4M3 pages: its CTAs look at up to 512 tokens from a
+// 32-bit one on.
+constexpr int kPagedMaxStore = 0x7fffffff - 512;
+
 // Attention over the pages.  Work is a flat sequence of units: request b's
 // query rows (row r = new token r / R, query head r % R of the kv head's
 // group) form groups of RG rows, and item (b, kv head, group) owns nu_b

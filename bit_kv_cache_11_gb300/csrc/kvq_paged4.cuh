@@ -33,6 +33,23 @@ struct Paged4ReadParams {
   int* err;
 };
 
+// CTAs of `threads` for `per` threads' work a token of both sides: `rounds` of it
+// each, fewer while that leaves SMs idle.
+struct Grid4 {
+  int tokens;   // of a CTA
+  Divisor per;  // threads of a token and side
+  unsigned kv_ctas;
+};
+inline Grid4 grid4(int n_tokens, long long per, int rounds, int threads) {
+  const long long all = per * n_tokens;
+  const long long want = std::min<long long>(static_cast<long long>(rounds) * threads, std::max<long long>(threads, all / (152 * 4)));
+  Grid4 g = {};
+  g.tokens = static_cast<int>(std::max<long long>(1, std::min<long long>(want / per, n_tokens)));
+  g.per = divisor(static_cast<uint32_t>(per / 2), per * g.tokens);
+  g.kv_ctas = static_cast<unsigned>(ctas_of(n_tokens, g.tokens));
+  return g;
+}
+
 __device__ __forceinline__ uint32_t pair_lo(uint32_t a, uint32_t b) { return __byte_perm(a, b, 0x5410); }
 __device__ __forceinline__ uint32_t pair_hi(uint32_t a, uint32_t b) { return __byte_perm(a, b, 0x7632); }
 __device__ __forceinline__ __half2 as_half2(uint32_t x) { return *reinterpret_cast<const __half2*>(&x); }

@@ -135,12 +135,6 @@ __device__ __forceinline__ uint2 codes16(const uint32_t (&w)[8], __half2 meta) {
   return make_uint2(o[0], o[1]);
 }
 
-struct Grid4 {
-  int tokens;  // of a CTA
-  Divisor per;  // threads of a token and side
-  unsigned kv_ctas;
-};
-
 // Channels c .. c + 7 of a key at `head`, in `own`, after the turn by angles a.
 template <bool BF16>
 __device__ __forceinline__ uint4 turned(uint4 own, const uint16_t* head, int c, const float2* a, int rot, int interleaved) {
@@ -271,22 +265,10 @@ cudaError_t launch(void (*fn)(K...), long long ctas, cudaStream_t st, A... args)
   return cudaLaunchKernelEx(&cfg, fn, args...);
 }
 
-// CTAs that take `per` threads' work a token: `rounds` of it each, fewer while that
-// leaves SMs idle.
-Grid4 grid_of(int n_tokens, long long per, int rounds) {
-  const long long all = per * n_tokens;
-  const long long want = std::min<long long>(static_cast<long long>(rounds) * kThreads, std::max<long long>(kThreads, all / (152 * 4)));
-  Grid4 g = {};
-  g.tokens = static_cast<int>(std::max<long long>(1, std::min<long long>(want / per, n_tokens)));
-  g.per = divisor(static_cast<uint32_t>(per / 2), per * g.tokens);
-  g.kv_ctas = static_cast<unsigned>((n_tokens + g.tokens - 1) / g.tokens);
-  return g;
-}
-
 template <int D, bool BF16>
 cudaError_t append(Paged4StoreParams p, cudaStream_t st) {
-  const Grid4 g = grid_of(p.n_tokens, 2LL * p.H * (D / 16), 2);
-  const long long ctas = g.kv_ctas + (p.q.n_heads ? rotate_ctas(&p.q, kThreads) : 0);
+  const Grid4 g = grid4(p.n_tokens, 2LL * p.H * (D / 16), 2, kThreads);
+  const long long ctas = static_cast<long long>(g.kv_ctas) + (p.q.n_heads ? rotate_ctas(&p.q, kThreads) : 0);
   switch (p.q.n_heads ? rotate_kind(p.q.rot, p.q.interleaved) : kInterleaved) {
     case kInterleaved: return launch(paged4_append_kernel<D, BF16, kInterleaved>, ctas, st, p, g);
     case kHalves: return launch(paged4_append_kernel<D, BF16, kHalves>, ctas, st, p, g);
@@ -303,7 +285,7 @@ cudaError_t launch_paged4_append(const Paged4StoreParams& p, int D, int dtype, c
 }
 
 cudaError_t launch_paged4_read(const Paged4ReadParams& p, int D, cudaStream_t st) {
-  const Grid4 g = grid_of(p.n_tokens, 2LL * p.H * (D / 8), 16);
+  const Grid4 g = grid4(p.n_tokens, 2LL * p.H * (D / 8), 16, kThreads);
   return D == 128 ? launch(paged4_read_kernel<128>, g.kv_ctas, st, p, g)
                   : launch(paged4_read_kernel<64>, g.kv_ctas, st, p, g);
 }

@@ -385,6 +385,7 @@ kvq_status kvq_paged_store(const kvq_paged_pool* pool, const void* k, const void
   PagedStoreParams p;
   const kvq_status s = store_params(&p, pool, k, v, dtype, k_stride, v_stride, slots, n_tokens, device_error);
   if (s != KVQ_OK || n_tokens == 0) return s;
+  if (n_tokens > kPagedMaxStore) return KVQ_ERR_UNSUPPORTED;
   return store(p, pool->head_dim, dtype, stream);
 }
 
@@ -405,6 +406,7 @@ kvq_status kvq_paged_append(const kvq_paged_pool* pool, const kvq_rotary* rotary
     if (pool->n_kv_heads > 65535 - 512) return KVQ_ERR_UNSUPPORTED;  // grid.y: at most a row of CTAs a chunk's token
   }
   if (n_tokens == 0) return KVQ_OK;
+  if (n_tokens > kPagedMaxStore) return KVQ_ERR_UNSUPPORTED;
   p.angles = reinterpret_cast<const float2*>(rotary->angles);
   p.rot = rotary->rotary_dim;
   p.interleaved = rotary->interleaved;
@@ -455,6 +457,7 @@ kvq_status kvq_paged4_append(const kvq_paged4_pool* pool, const kvq_rotary* rota
     if (rotary == nullptr || n_q_heads < 1) return KVQ_ERR_INVALID_ARG;
     s = rotate_params(&p.q, rotary, q, dtype, q_stride, q_out, q_out_stride, n_tokens, n_q_heads, c.head_dim);
     if (s != KVQ_OK) return s;
+    if (n_tokens > INT_MAX / 2) return KVQ_ERR_UNSUPPORTED;  // grid.x: at most two CTAs a token
   }
   if (n_tokens == 0) return KVQ_OK;
   for (int i = 0; i < 2; ++i) {

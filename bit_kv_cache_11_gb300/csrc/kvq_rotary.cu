@@ -149,8 +149,7 @@ cudaError_t launch_rotary_angles(AnglesParams p, cudaStream_t st) {
   const int v = p.half % 2 == 0 ? 2 : 1, lanes = p.half / v;  // (at most 128 pairs: 256 threads hold a token)
   p.lanes = divisor(lanes, kThreads + 1);
   const int rows = kThreads / lanes;
-  // four tokens a thread where there are many
-  const long long ctas = std::min<long long>((p.n_tokens + rows - 1) / rows, std::max<long long>(152 * 8, (p.n_tokens + 4LL * rows - 1) / (4 * rows)));
+  const long long ctas = angles_ctas(p.n_tokens, rows);
   return v == 2 ? launch(rotary_angles_kernel<2>, p, ctas, st) : launch(rotary_angles_kernel<1>, p, ctas, st);
 }
 

@@ -21,6 +21,9 @@ __device__ __forceinline__ uint32_t operator/(uint32_t n, const Divisor& v) {
   return v.m ? __umulhi(n, v.m) : n / v.d;
 }
 
+// CTAs of `tokens` each (64 bits: token counts go up to 2^31 - 1).
+inline long long ctas_of(int n_tokens, int tokens) { return (static_cast<long long>(n_tokens) + tokens - 1) / tokens; }
+
 // x -> out, heads of D channels whose first `rot` turn by angles
 // [token][rot / 2] (cos, sin).
 struct RotateParams {
@@ -293,7 +296,11 @@ inline long long rotate_ctas(RotateParams* p, int threads) {
   p->tokens = static_cast<int>(std::max<long long>(1, std::min<long long>(want / per, p->n_tokens)));
   p->per = divisor(static_cast<uint32_t>(per), per * p->tokens);
   p->units = divisor(p->units.d, per);
-  return (p->n_tokens + p->tokens - 1) / p->tokens;
+  return ctas_of(p->n_tokens, p->tokens);
+}
+// CTAs that make `rows` tokens' angles at a time: four rounds each where there are many.
+inline long long angles_ctas(int n_tokens, int rows) {
+  return std::min(ctas_of(n_tokens, rows), std::max(152LL * 8, ctas_of(n_tokens, 4 * rows)));
 }
 
 struct PagedStoreParams {

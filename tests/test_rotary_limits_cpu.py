@@ -1,13 +1,15 @@
 """Host-side limits of the rotary calls and of the appends: arrays that overlap,
 sizes at the ends of their ranges (no GPU)."""
+import ctypes
 import os
-import sys
+import shutil
+import subprocess
 
 import pytest
 
-sys.path.insert(0, os.path.dirname(os.path.abspath(__file__)))
-
 torch = pytest.importorskip("torch")
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 A = 1 << 20  # an aligned address that no call may touch
 
@@ -43,3 +45,33 @@ def test_positions_overlap_no_array_of_the_plan(kvq, name):
     # beside it: nothing is refused before the page size is looked at
     for good in (start - 48, (start + 4 * n + 15) & ~15):
         assert call(good, ps=24) == kvq.KVQ_ERR_UNSUPPORTED, good - start
+
+
+def test_grids_of_every_token_count(tmp_path):
+    """Token counts up to 2^31 - 1, on the host code that sizes the launches."""
+    nvcc = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
+    if not (os.path.exists(nvcc) or shutil.which("nvcc")):
+        pytest.skip("no nvcc")
+    exe = tmp_path / "grid_check"
+    subprocess.check_call([nvcc, "-std=c++17", "-O1", "-I", os.path.join(ROOT, "bit_kv_cache_11_gb300", "csrc"),
+                           "-I", os.path.join(ROOT, "include"),
+                           os.path.join(ROOT, "tests", "harness", "grid_check.cu"), "-o", str(exe)])
+    out = subprocess.run([str(exe)], capture_output=True, text=True, timeout=120)
+    assert out.returncode == 0, out.stdout + out.stderr
+    assert "failures 0" in out.stdout
+
+
+def test_token_counts_that_no_launch_takes(kvq):
+    k = kvq
+    r = k.kvq_rotary(A, 64, 0)
+    sizes = dict(n_pages=8, n_kv_heads=2, page_size=16, head_dim=64)
+    p8 = k.kvq_paged_pool(A, A, A, A, *sizes.values())
+    p4 = k.kvq_paged4_pool(A, A, A, A, *sizes.values())
+    ref = ctypes.byref
+    most = (1 << 31) - 1
+    assert k._lib.kvq_paged_store(ref(p8), A, A, 0, 128, 128, A, most, None, None) == k.KVQ_ERR_UNSUPPORTED
+    for q in ((None, 0, None, 0, 0), (A, 256, A + 8192, 256, 4)):
+        args = (ref(r), A, A, 0, 128, 128, A, most, *q, None, None)
+        assert k._lib.kvq_paged_append(ref(p8), *args) == k.KVQ_ERR_UNSUPPORTED
+        if q[0]:
+            assert k._lib.kvq_paged4_append(ref(p4), *args) == k.KVQ_ERR_UNSUPPORTED
