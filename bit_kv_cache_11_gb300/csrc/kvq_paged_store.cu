@@ -191,21 +191,31 @@ __device__ __forceinline__ uint4 load_vec(const PagedStoreParams& p, int side, l
 // ---- short runs: a warp stores a whole run of one head ------------------------
 //
 // Lanes [0, 16) serve K and [16, 32) V; a side's lanes hold a row as 16-byte
-// vectors (D / 8 of them, 16 / (D / 8) rows at a time).
+// vectors (D / 8 of them, 16 / (D / 8) rows at a time).  What does not depend on where
+// the run ends is asked for first: one load gives its slot and the 31 behind it, and
+// the scale is on its way before they are compared (1024 single tokens x 8 heads: 4.7
+// -> 4.3 us, 5.0 -> 4.3 in pages of 16 x 64; the rows asked for as early: 10 % more for
+// runs of five tokens).
 template <int D, bool BF16, bool ROT>
 __device__ __forceinline__ void store_run(const PagedStoreParams& p, int t, int h, int lane) {
   constexpr int VPR = D / 8, RPS = 16 / VPR;  // vectors of a row, rows a step
-  const int slot = p.slots[t];
+  const int left = p.n_tokens - t;
+  const int mine = lane < left ? p.slots[t + lane] : -1;
+  const int slot = __shfl_sync(0xffffffffu, mine, 0);
   const int page = slot >> p.lg_ps, row0 = slot & ((1 << p.lg_ps) - 1);
   if (page >= p.n_pages) {
     if (lane == 0) set_err(p.err, KVQ_PAGED_ERR_BAD_PAGE);
     return;
   }
   const int side = lane >> 4, l = lane & 15, sub = l / VPR, vec = l % VPR;
-  // rows of the run: until the page ends or the slots stop following
-  const int most = min((1 << p.lg_ps) - row0, p.n_tokens - t);
-  int n = 1;
-  while (n < most) {
+  float* scale = (side ? p.scale[1] : p.scale[0]) + static_cast<size_t>(page) * p.H + h;
+  const float was = *scale;
+  // rows of the run: until the page ends or the slots stop following (the first 32 are
+  // at hand)
+  const int most = min((1 << p.lg_ps) - row0, left);
+  const uint32_t ends = __ballot_sync(0xffffffffu, lane >= most || mine != slot + lane);
+  int n = ends ? __ffs(ends) - 1 : 32;
+  while (!ends && n < most) {
     const int i = n + lane;
     const bool ok = i < most && p.slots[t + i] == slot + i;
     const uint32_t m = __ballot_sync(0xffffffffu, !ok);
@@ -215,12 +225,12 @@ __device__ __forceinline__ void store_run(const PagedStoreParams& p, int t, int 
     }
     n += 32;
   }
-  float* scale = (side ? p.scale[1] : p.scale[0]) + static_cast<size_t>(page) * p.H + h;
-  const float was = *scale;
-  auto load = [&](int i) { return load_vec<D, BF16, ROT>(p, side, t + i, h, vec, lane, i < n); };
-  const uint4 first = load(sub);
+  auto load = [&](int i, bool live) { return load_vec<D, BF16, ROT>(p, side, t + i, h, vec, lane, live); };
+  // a lane's rows begin at `sub`; lanes that turn keys make their rounds together
+  const int lo = ROT ? 0 : sub, up = sub - lo;
+  const uint4 first = load(sub, sub < n);
   uint32_t m2 = vec_max(first, 0);
-  for (int i = RPS; i < n; i += RPS) m2 = vec_max(load(i + sub), m2);
+  for (int i = lo + RPS; i < n; i += RPS) m2 = vec_max(load(i + up, i + up < n), m2);
   auto side_max = [](uint32_t x) {  // over the side's sixteen lanes
 #pragma unroll
     for (int o = 1; o < 16; o <<= 1) x = max(x, __shfl_xor_sync(0xffffffffu, x, o));
@@ -230,7 +240,7 @@ __device__ __forceinline__ void store_run(const PagedStoreParams& p, int t, int 
   const bool odd = mag >= inf_bits<BF16>();  // the side holds a NaN or an infinity
   if (__any_sync(0xffffffffu, odd)) {
     m2 = 0;
-    for (int i = 0; i < n; i += RPS) m2 = vec_max_finite<BF16>(load(i + sub), m2);
+    for (int i = lo; i < n; i += RPS) m2 = vec_max_finite<BF16>(load(i + up, i + up < n), m2);
     mag = side_max(fold2(m2));
     if (odd && l == 0) set_err(p.err, KVQ_PAGED_ERR_NONFINITE);
   }
@@ -243,7 +253,7 @@ __device__ __forceinline__ void store_run(const PagedStoreParams& p, int t, int 
     if (was != now && was > 0.f) {
       const float f = was / now;
       for (int i = sub; i < row0; i += RPS) {
-        uint2* c = reinterpret_cast<uint2*>(base + static_cast<size_t>(i) * D);
+        uint2* c = reinterpret_cast<uint2*>(base + i * D);
         *c = rescale8(*c, f);
       }
     }
@@ -251,9 +261,9 @@ __device__ __forceinline__ void store_run(const PagedStoreParams& p, int t, int 
   const float inv = exp2i(-e);
   const bool plain = plain_codes<BF16>(odd, e);
   if (sub < n) *reinterpret_cast<uint2*>(base + static_cast<size_t>(row0 + sub) * D) = codes8<BF16>(first, inv, plain);
-  for (int i = RPS + sub; i - sub < n; i += RPS) {
-    const uint2 c = codes8<BF16>(load(i), inv, plain);
-    if (i < n) *reinterpret_cast<uint2*>(base + static_cast<size_t>(row0 + i) * D) = c;
+  for (int i = lo + RPS; i < n; i += RPS) {
+    const uint2 c = codes8<BF16>(load(i + up, i + up < n), inv, plain);
+    if (i + up < n) *reinterpret_cast<uint2*>(base + static_cast<size_t>(row0 + i + up) * D) = c;
   }
   if (l == 0) *scale = exp2i(e);
 }
@@ -268,19 +278,19 @@ __device__ __forceinline__ void store_run(const PagedStoreParams& p, int t, int 
 // as fit 256 threads (512 for the largest page).
 //
 // Measured with either way alone (8 heads of 128, pages of 64, us): 256 single
-// tokens 2.5 by warps and 75 by teams, 2048 single tokens 6.8 and 94; four
-// prompts of 256 tokens 20 and 5.0, of 1024 tokens 29 and 7.6.
+// tokens 2.4 by warps and 12 by teams, 2048 single tokens 8.7 and 88; four
+// prompts of 256 tokens 19 and 4.1, of 1024 tokens 18 and 4.3.
 //
 // A call of up to kShortChunks tokens x heads takes chunks of 8 tokens, so that
 // its runs spread over the SMs; a larger one takes chunks of as many rows as its
 // teams hold.  Measured (8 heads, short / whole chunks, us of a graph's call):
 //   tokens x heads                       2048       4096       8192      16384
-//   single tokens, 64 x 128          2.5/ 7.7   3.0/ 7.8   4.6/ 7.8   7.8/ 9.0
-//   single tokens, 16 x 64           2.5/13.8   3.0/13.9   4.6/14.2   7.9/14.7
-//   runs of 5, 64 x 128              3.2/ 4.5   3.9/ 4.6   6.0/ 4.6   9.5/ 5.4
-//   runs of 5, 16 x 64               3.0/ 7.6   3.5/ 7.8   5.5/ 8.1   8.4/ 8.5
-//   one prompt, 64 x 128             3.2/ 3.0   3.8/ 3.0   4.6/ 3.1   5.9/ 3.7
-//   one prompt, 16 x 64              3.0/ 2.8   3.6/ 2.8   4.6/ 2.9   7.1/ 2.9
+//   single tokens, 64 x 128          2.4/ 8.0   2.7/ 7.9   4.3/ 8.0   7.5/ 8.7
+//   single tokens, 16 x 64           2.4/15.1   2.8/15.3   4.4/15.4   7.7/15.7
+//   runs of 5, 64 x 128              3.2/ 4.3   4.0/ 4.4   6.0/ 4.5   9.2/ 5.5
+//   runs of 5, 16 x 64               2.8/ 6.9   2.8/ 7.0   4.7/ 7.1   7.1/ 7.2
+//   one prompt, 64 x 128             3.0/ 2.7   3.6/ 2.8   4.2/ 2.7   5.5/ 3.3
+//   one prompt, 16 x 64              2.7/ 2.7   2.7/ 2.8   3.4/ 2.7   4.9/ 2.9
 // The host does not know the runs: the turn lies where prompts lose by short
 // chunks what single tokens gain.
 //
@@ -433,7 +443,7 @@ __global__ void __launch_bounds__(chunk_threads<TEAM>(), (ROT ? 768 : 1024) / ch
         if (was[side] != now && was[side] > 0.f) {
           const float f = was[side] / now;
           for (int i = sub; i < row0; i += RPS) {
-            uint2* c = reinterpret_cast<uint2*>(base + static_cast<size_t>(i) * D);
+            uint2* c = reinterpret_cast<uint2*>(base + i * D);
             *c = rescale8(*c, f);
           }
         }
