@@ -19,7 +19,7 @@ import ctypes
 import torch
 
 from . import kvq
-from .kvq import KVQ_ERR_INVALID_ARG, KvqError
+from .kvq import KVQ_ERR_INVALID_ARG, KVQ_ERR_UNSUPPORTED, KvqError
 from .paged import _paged_bind
 
 _angles = _paged_bind.angles
@@ -35,9 +35,15 @@ def kvq_rotary_turns(rotary_dim: int, base: float = 10000.0, factor: float = 1.0
     factor > 1 slows the pairs down for longer contexts: all of them where
     original_len is 0, else those that make few turns in original_len positions
     (all the way at `low` turns, not at all from `high` on)."""
-    n = int(rotary_dim)
-    if n < 2 or n % 2:
+    try:
+        n = int(rotary_dim)
+        whole = n == rotary_dim
+    except (TypeError, ValueError, OverflowError):
+        whole = False
+    if not whole or n < 2 or n % 2:
         raise KvqError(KVQ_ERR_INVALID_ARG, "kvq_rotary_turns: rotary_dim must be even and positive")
+    if n > 256:
+        raise KvqError(KVQ_ERR_UNSUPPORTED, "kvq_rotary_turns: rotary_dim must be at most 256")
     turns = (ctypes.c_int64 * (n // 2))()
     kvq._check(kvq._lib.kvq_rotary_turns(turns, n, float(base), float(factor), float(original_len),
                                          float(low), float(high)), "kvq_rotary_turns")

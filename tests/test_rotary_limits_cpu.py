@@ -75,3 +75,18 @@ def test_token_counts_that_no_launch_takes(kvq):
         assert k._lib.kvq_paged_append(ref(p8), *args) == k.KVQ_ERR_UNSUPPORTED
         if q[0]:
             assert k._lib.kvq_paged4_append(ref(p4), *args) == k.KVQ_ERR_UNSUPPORTED
+
+
+@pytest.mark.parametrize("dim,status", [(258, "UNSUPPORTED"), ((1 << 31) + 2, "UNSUPPORTED"), ((1 << 32) + 64, "UNSUPPORTED"),
+                                        (1 << 70, "UNSUPPORTED"), (64.5, "INVALID_ARG"), (float("nan"), "INVALID_ARG"),
+                                        (float("inf"), "INVALID_ARG"), (None, "INVALID_ARG"), ("64", "INVALID_ARG")])
+def test_rotary_dims_that_no_call_takes(kvq, dim, status):
+    """Looked at before anything is allocated or cut to 32 bits."""
+    with pytest.raises(kvq.KvqError, match="rotary_dim") as e:
+        kvq.kvq_rotary_turns(dim, device="cpu")
+    assert e.value.status == getattr(kvq, f"KVQ_ERR_{status}")
+
+
+def test_rotary_dims_that_are_taken(kvq):
+    assert kvq.kvq_rotary_turns(256, device="cpu").shape == (128,)
+    assert torch.equal(kvq.kvq_rotary_turns(64.0, device="cpu"), kvq.kvq_rotary_turns(64, device="cpu"))
