@@ -33,18 +33,21 @@ _attention = _paged_bind.attention
 _append = _paged_bind.append
 
 
+def _sizes(*sizes):
+    """A pool's sizes as C ints: those beyond 32 bits as its ends, which no call takes."""
+    return (max(-(1 << 31), min(int(n), (1 << 31) - 1)) for n in sizes)
+
+
 def kvq_paged_pool_check(n_pages: int, n_kv_heads: int, page_size: int, head_dim: int) -> int:
     """Status of a pool's sizes (KVQ_OK when the calls take such a pool)."""
-    pool = kvq_paged_pool(None, None, None, None, int(n_pages), int(n_kv_heads), int(page_size),
-                          int(head_dim))
+    pool = kvq_paged_pool(None, None, None, None, *_sizes(n_pages, n_kv_heads, page_size, head_dim))
     return kvq._lib.kvq_paged_pool_check(ctypes.byref(pool))
 
 
 def kvq_paged_workspace_bytes(n_pages: int, n_kv_heads: int, page_size: int,
                               head_dim: int) -> int:
     """Bytes of the attention's workspace for such a pool."""
-    pool = kvq_paged_pool(None, None, None, None, int(n_pages), int(n_kv_heads), int(page_size),
-                          int(head_dim))
+    pool = kvq_paged_pool(None, None, None, None, *_sizes(n_pages, n_kv_heads, page_size, head_dim))
     n = ctypes.c_size_t(0)
     kvq._check(kvq._lib.kvq_paged_workspace_bytes(ctypes.byref(pool), ctypes.byref(n)),
                "kvq_paged_workspace_bytes")

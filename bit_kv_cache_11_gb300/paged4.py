@@ -15,7 +15,7 @@ import torch
 
 from . import kvq
 from .kvq import kvq_paged4_pool
-from .paged import PagedCache, _paged_bind
+from .paged import PagedCache, _paged_bind, _sizes
 
 _append = _paged_bind.append4
 _read = _paged_bind.read4
@@ -24,16 +24,14 @@ _attention = _paged_bind.attention4
 
 def kvq_paged4_pool_check(n_pages: int, n_kv_heads: int, page_size: int, head_dim: int) -> int:
     """Status of a pool's sizes (KVQ_OK when the calls take such a pool)."""
-    pool = kvq_paged4_pool(None, None, None, None, int(n_pages), int(n_kv_heads), int(page_size),
-                           int(head_dim))
+    pool = kvq_paged4_pool(None, None, None, None, *_sizes(n_pages, n_kv_heads, page_size, head_dim))
     return kvq._lib.kvq_paged4_pool_check(ctypes.byref(pool))
 
 
 def kvq_paged4_workspace_bytes(n_pages: int, n_kv_heads: int, page_size: int,
                                head_dim: int) -> int:
     """Bytes of the attention's workspace for such a pool."""
-    pool = kvq_paged4_pool(None, None, None, None, int(n_pages), int(n_kv_heads), int(page_size),
-                           int(head_dim))
+    pool = kvq_paged4_pool(None, None, None, None, *_sizes(n_pages, n_kv_heads, page_size, head_dim))
     n = ctypes.c_size_t(0)
     kvq._check(kvq._lib.kvq_paged4_workspace_bytes(ctypes.byref(pool), ctypes.byref(n)),
                "kvq_paged4_workspace_bytes")

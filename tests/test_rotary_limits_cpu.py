@@ -90,3 +90,23 @@ def test_rotary_dims_that_no_call_takes(kvq, dim, status):
 def test_rotary_dims_that_are_taken(kvq):
     assert kvq.kvq_rotary_turns(256, device="cpu").shape == (128,)
     assert torch.equal(kvq.kvq_rotary_turns(64.0, device="cpu"), kvq.kvq_rotary_turns(64, device="cpu"))
+
+
+@pytest.mark.parametrize("at", range(4))
+def test_pool_sizes_beyond_32_bits(kvq, at):
+    """No size is cut to its low 32 bits, neither where a pool is checked nor made."""
+    good = [8, 2, 16, 64]
+    for check, nbytes, cache in ((kvq.kvq_paged_pool_check, kvq.kvq_paged_workspace_bytes, kvq.PagedCache),
+                                 (kvq.kvq_paged4_pool_check, kvq.kvq_paged4_workspace_bytes, kvq.PagedCache4)):
+        assert check(*good) == kvq.KVQ_OK and nbytes(*good) > 1024
+        for beyond in (1 << 32, 1 << 70):
+            bad = list(good)
+            bad[at] += beyond
+            assert check(*bad) == kvq.KVQ_ERR_UNSUPPORTED
+            bad[at] = good[at] - beyond
+            assert check(*bad) == kvq.KVQ_ERR_INVALID_ARG
+            bad[at] = good[at] + beyond
+            for call in (lambda: nbytes(*bad), lambda: cache(bad[0], bad[2], 2 * bad[1], bad[1], bad[3], device="cpu")):
+                with pytest.raises(kvq.KvqError) as e:
+                    call()
+                assert e.value.status == kvq.KVQ_ERR_UNSUPPORTED
