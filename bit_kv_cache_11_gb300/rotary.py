@@ -30,7 +30,7 @@ def kvq_rotary_turns(rotary_dim: int, base: float = 10000.0, factor: float = 1.0
                      original_len: float = 0.0, low: float = 1.0, high: float = 32.0,
                      device="cuda"):
     """Frequencies base^(-2 i / rotary_dim) as int64 parts of a turn, units of
-    2^-64, [rotary_dim / 2].
+    2^-64, [rotary_dim / 2], within 2^-51 of a turn (float64's roundings).
 
     factor > 1 slows the pairs down for longer contexts: all of them where
     original_len is 0, else those that make few turns in original_len positions

@@ -515,9 +515,12 @@ KVQ_API kvq_status kvq_paged_plan_positions(const int* ctx_len, const int* new_l
  * position; the others stay as they are.  Pair i moves f_i radians a position:
  *   f_i = base^(-2 i / rotary_dim), scaled for contexts longer than the model's
  * (kvq_rotary_turns).  Its channels are (i, i + rotary_dim / 2), or (2 i,
- * 2 i + 1) when interleaved.  A frequency is held as the whole number
- * f_i / (2 pi) * 2^64, so that position * frequency modulo 2^64 is the exact
- * part of a turn, however far the position.
+ * 2 i + 1) when interleaved.  A frequency is held as the whole number nearest
+ * to f_i / (2 pi) * 2^64 as float64 has it, so that position * frequency modulo
+ * 2^64 is the exact part of a turn that the held frequency makes, however far
+ * the position.  The held frequency is within 2^-51 of a turn a position of its
+ * definition (float64's roundings; scaled by parts, where high >= 2 low): an
+ * angle at position 2^20 within 2^-31 of a turn, at 2^31 within 2^-20.
  *
  * A step's cosines and sines are computed once for all layers
  * (kvq_rotary_angles) and passed to the calls that turn queries and keys:
@@ -539,8 +542,8 @@ KVQ_API kvq_status kvq_rotary_turns(int64_t* turns, int rotary_dim, double base,
 
 /* Cosine and sine of every token's angles, times magnitude: angles fp32
  * [n_tokens][rotary_dim / 2][2], 16-byte aligned.  positions: device int32
- * [n_tokens], any values; turns: device int64 [rotary_dim / 2].  Errors are
- * below 2^-22 of magnitude. */
+ * [n_tokens], any values; turns: device int64 [rotary_dim / 2].  Errors, against
+ * the frequencies as they are held, are below 2^-22 of magnitude. */
 KVQ_API kvq_status kvq_rotary_angles(const int* positions, int n_tokens, const int64_t* turns,
                                      int rotary_dim, float magnitude, float* angles, void* stream);
 
