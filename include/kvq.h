@@ -594,9 +594,10 @@ KVQ_API kvq_status kvq_paged_append(const kvq_paged_pool* pool, const kvq_rotary
  * channels (turned keys are first rounded to their own type):
  *   x     = the value as fp16, within +-65408 (NaN: 0)
  *   mn,mx = minimum and maximum of the group
- *   step  = fp16((mx - mn) / 15), the divide in fp32
+ *   step  = fp16((mx - mn) / 15)
  *   code  = round((x - mn) / step), half to even, within [0, 15]; 0 if step is 0
- * and a value is fp16(code * step + mn), rounded once.  (The bound keeps the
+ * where differences and quotients are fp32 numbers, each rounded by itself, and a
+ * value is fp16(code * step + mn), rounded once.  (The bound keeps the
  * largest code of the widest group a finite number.)  Infinities and NaN set
  * KVQ_PAGED_ERR_NONFINITE.
  *
