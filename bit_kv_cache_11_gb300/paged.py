@@ -186,4 +186,4 @@ class PagedCache:
                  (KVQ_PAGED_ERR_LENGTH, "a length breaks the call's contract"),
                  (KVQ_PAGED_ERR_NONFINITE, "a non-finite key or value"))
         what = ", ".join(n for b, n in names if bits & b)
-        raise KvqError(KVQ_ERR_DEVICE_CHECK, f"PagedCache.check: {what}")
+        raise KvqError(KVQ_ERR_DEVICE_CHECK, f"{type(self).__name__}.check: {what}")

@@ -110,3 +110,14 @@ def test_pool_sizes_beyond_32_bits(kvq, at):
                 with pytest.raises(kvq.KvqError) as e:
                     call()
                 assert e.value.status == kvq.KVQ_ERR_UNSUPPORTED
+
+
+@pytest.mark.parametrize("cls", ["PagedCache", "PagedCache4"])
+def test_check_names_its_class(kvq, monkeypatch, cls):
+    monkeypatch.setattr(torch.cuda, "synchronize", lambda *a: None)
+    c = getattr(kvq, cls)(8, 16, 4, 2, 64, device="cpu")
+    c.check()
+    c.error.fill_(kvq.KVQ_PAGED_ERR_BAD_PAGE)
+    with pytest.raises(kvq.KvqError, match=rf"{cls}\.check: a page id outside the pool"):
+        c.check()
+    c.check()
