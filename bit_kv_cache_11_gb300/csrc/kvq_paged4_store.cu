@@ -193,8 +193,14 @@ __global__ void __launch_bounds__(kThreads) paged4_append_kernel(const Paged4Sto
   grid_dep_wait();
   grid_dep_launch();
   // CTAs for keys and values lie evenly among those for the step's queries, so that
-  // the ones' arithmetic runs beside the others' traffic (16000 tokens, a half of
-  // each head turned, interleaved: 55 us; one after the other 63)
+  // the ones' arithmetic runs beside the others' traffic.  Both sides (us in a graph;
+  // with the queries / the append alone, plus kvq_rotate alone; halves, interleaved):
+  //   64 tokens, 8 + 32 heads of 128                   2.4/  4.6    2.3/  4.0
+  //   256 tokens, 8 + 32 heads of 128                  3.1/  4.7    2.6/  4.2
+  //   4861 tokens, 32 + 32 heads of 64, 16 turned     25.0/ 22.5   18.7/ 19.2
+  //   16000 tokens, 8 + 32 heads of 64                34.2/ 33.7   29.5/ 30.9
+  //   16000 tokens, 8 + 32 heads of 128, 64 turned    69.9/ 67.2   54.9/ 64.2
+  //   26298 tokens, 8 + 32 heads of 128              105.4/114.1   90.0/107.6
   const unsigned kv = static_cast<unsigned>(static_cast<unsigned long long>(blockIdx.x) * g.kv_ctas / gridDim.x);
   if ((static_cast<unsigned long long>(blockIdx.x) + 1) * g.kv_ctas / gridDim.x != kv) {
     append_tokens<D, BF16>(p, g, static_cast<long long>(kv) * g.tokens, threadIdx.x);

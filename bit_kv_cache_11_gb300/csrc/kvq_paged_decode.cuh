@@ -29,8 +29,8 @@
 // read 7.4 TB/s), latency around that: 4 us from the start of a launch to the
 // first data (lengths, table, page, copy, one after the other) and 3 .. 6 us of
 // joins.  Measured (us, and the share of the measured copy rate): 131072 tokens
-// 49.5 (81 %), 8 x 4113 tokens of 32 heads 53.5 (75 %), 64 ragged requests of up to
-// 2048 tokens 43.6 (57 %), five drafted tokens with a window 28.  Eight warps of
+// 49.7 (80 %), 8 x 4113 tokens of 32 heads 52.2 (76 %), 64 ragged requests of up to
+// 2048 tokens 43.3 (57 %), five drafted tokens with a window 29.  Eight warps of
 // three 8 KB stages were 3 % faster than twelve of two.  Code that runs once a
 // launch is fetched as it runs: the joins are small loops, and one body of the
 // unit serves edges too (together with the joins' loads in flight that took 15 %
@@ -51,10 +51,12 @@
 // token's 16 bytes of metadata hold) and, transposed, the codes of two tokens of
 // four value channels in the halves of a word, so that no byte moves between
 // lanes.  A unit is 5 KB; twelve warps of three stages (NT = 1) or eight of four.
-// Bound: instructions, about 450 for 16 tokens of a head (E4M3: 310), 0.6 an issue
-// slot while it streams: 131072 tokens of 8 heads, 168 MB, 51.4 us (48 % of the
-// measured copy rate; 36 without the arithmetic, 42 without the values' conversion),
-// 64 ragged requests 34.6 us, one of 257 tokens 7.6.  Measured and not kept: eight
+// Bound: the chain from a shared-memory read over conversion and products to the
+// softmax, which twelve warps of 168 registers do not hide: 456 instructions for 16
+// tokens of a head (E4M3: 312), 2.07 of four issued a cycle, no pipe above 40 %.
+// 131072 tokens of 8 heads, 168 MB, 52 us (47 % of the measured copy rate; 36 without
+// the arithmetic, 42 without the values' conversion), no less than over E4M3 pages, 64
+// ragged requests 38 us, one of 257 tokens 7.6.  Measured and not kept: eight
 // warps 59 us, sixteen 52 (spills); the metadata by bulk copies 1 % slower; scores
 // from the codes themselves (a product for each group, times the step) 50.2 us, but
 // for keys that are not rounded to fp16, as a value's definition is: fp16 outputs

@@ -16,11 +16,11 @@
 // whole run, so no two CTAs touch the same page and head.
 //
 // Bound: HBM for prompts (3 bytes a value: 2 read, 1 written), latency for
-// single tokens.  Measured: 26298 tokens x 8 heads x 128, 162 MB, 28.9 us (84 %
+// single tokens.  Measured: 26298 tokens x 8 heads x 128, 162 MB, 28.8 us (83 %
 // of the measured copy rate); 4861 tokens x 32 heads x 64 in 16-row pages, 60 MB,
-// 14.5 us (62 %; the launch and the last CTAs take the rest); 256 single tokens
-// 2.5 us.  One test per side for NaN instead of two selects a value, and fp16
-// codes without a step through fp32, took 31.0 -> 28.9 and 16.0 -> 14.5 us.
+// 14.3 us (62 %; the launch and the last CTAs take the rest); 256 single tokens
+// 2.4 us.  One test per side for NaN instead of two selects a value, and fp16
+// codes without a step through fp32, took 31 -> 29 and 16 -> 14.5 us.
 #include "kvq_rotary.cuh"
 
 namespace kvq {
@@ -296,13 +296,24 @@ __device__ __forceinline__ void store_run(const PagedStoreParams& p, int t, int 
 //
 // With keys that turn (ROT) the partner of a channel comes from the lane that
 // holds it, and the angles from memory, 32 bytes a vector.  Measured (26298 tokens
-// x 8 heads x 128, bf16, halves / interleaved): 27.4 us without turning, 44 / 41
-// with it.  Warps that held one side each took 53 / 48: those of the values waited
-// for those of the keys.  What is left of the difference are the angles' loads, one
-// step after the other.  With 32 query heads in the same launch, their CTAs evenly
-// among these, 106 / 111 us (floor 87) with three CTAs an SM (80 registers); with
-// four (64) 43 / 39 and, with the queries, 114 / 103, with two (128) 54 / 50 and
-// 129 / 139.
+// x 8 heads x 128, bf16, halves / interleaved): 27.6 us without turning, 44 / 41
+// with it (120 channels of 128 turned, one by one: 63).  Warps that held one side each
+// took 53 / 48: those of the values waited for those of the keys.  What is left of the
+// difference are the angles' loads, one step after the other.  With 32 query heads in
+// the same launch, their CTAs evenly among these, 106 / 111 us (floor 87) with three
+// CTAs an SM (80 registers); with four (64) 43 / 39 and, with the queries, 114 / 103,
+// with two (128) 54 / 50 and 129 / 139.
+//
+// One launch for a step's keys, values and queries saves single tokens a launch and
+// gains little or loses on prompts, whose query CTAs have this kernel's registers.  Both
+// sides (us in a graph; the append with its queries / alone, plus kvq_rotate alone):
+//   64 tokens, 8 + 32 heads of 128                  halves   2.7/  4.9   interleaved   2.7/  4.4
+//   256 tokens, 8 + 32 heads of 128                          3.9/  5.4                 3.1/  5.1
+//   4861 tokens, 32 + 32 heads of 64, 16 turned             22.9/ 21.3                20.8/ 17.9
+//   16000 tokens, 8 + 32 heads of 64                        33.1/ 32.5                34.6/ 30.6
+//   16000 tokens, 8 + 32 heads of 128, 64 turned            66.1/ 66.0                64.0/ 63.6
+//   26298 tokens, 8 + 32 heads of 128                      105.9/110.6               110.9/106.7
+// A caller who has such prompts may call kvq_rotate for the queries: the bits are equal.
 template <int TEAM>
 __host__ __device__ constexpr int chunk_threads() {
   return TEAM == 512 ? 512 : 256;

@@ -4,11 +4,15 @@
 //   a' = a cos - b sin,  b' = b cos + a sin,  angle = position * f_i
 //
 // Cosines and sines are computed once a step and not once a head or layer: 64
-// pairs are 512 bytes a token, a tenth of what its 8 + 8 + 32 heads of 128 move.
+// pairs are 512 bytes a token, 1/24 of what its 8 + 8 + 32 heads of 128 read, and
+// fifty instructions a pair would come to each of those heads.
 // Bound: HBM for prompts, a launch for decodes.  Measured: 16003 tokens x 40
 // heads of 128 (half of each turned, interleaved, 328 MB) 49.4 us, 98 % of the
 // measured copy rate; 26298 tokens x 32 heads (halves, 443 MB) 66 us, 99 %; 64
-// tokens x 32 heads 2.1 us in a graph.
+// tokens x 32 heads 2.1 us in a graph.  Pairs that do not lie in aligned chunks are
+// turned channel by channel, two bytes a load: 16003 tokens x 40 heads of 96, 24 of
+// them turned, 188 us (32 of them, aligned halves, 41); 26298 x 32 heads of 128, 120
+// turned, 211; 64 tokens x 32 heads 4.7.
 #include <algorithm>
 #include <cmath>
 
@@ -26,7 +30,7 @@ constexpr int kThreads = 256;
 // position * turn modulo 2^64 is the exact part of a turn; the nearest quarter
 // comes off the top of its upper 32 bits, the rest (at most an eighth of a turn)
 // becomes an angle within pi / 4, whose Taylor series to x^9 and x^10 leave 2^-29
-// and 2^-30.
+// and 2^-33.
 __device__ __forceinline__ float2 unit_of(int pos, uint2 turn) {  // turn: low, high word
   const uint32_t n = static_cast<uint32_t>(pos);
   uint32_t phase = __umulhi(n, turn.x) + n * turn.y;
@@ -42,8 +46,9 @@ __device__ __forceinline__ float2 unit_of(int pos, uint2 turn) {  // turn: low, 
   return make_float2(quarter == 1 || quarter == 2 ? -a : a, quarter & 2 ? -b : b);
 }
 
-// Bound: 131072 positions of 64 pairs write 67 MB (10 us) and take some thirty
-// instructions a pair; 14.7 us, 69 % of the measured copy rate (16.3 with the
+// Bound: 131072 positions of 64 pairs write 67 MB (10 us) and take fifty
+// instructions a pair, 10 us at full issue (71 % of the slots are used, by 3.4 rounds of
+// CTAs); 14.7 us, 69 % of the measured copy rate (16.3 with the
 // phase as one 64-bit product, 38.6 with a pair a thread and its place by 64-bit
 // division).  64 positions: 1.3 us in a graph.
 //

@@ -44,7 +44,8 @@ struct RotateParams {
 // aligned a unit is
 //   kInterleaved  one chunk, its four pairs or (from rot on) its copy
 //   kHalves       two chunks of eight pairs, or a chunk to copy
-// and else (kSingle) four pairs of single channels, or eight channels to copy.
+// and else (kSingle) four pairs of single channels, or eight channels to copy, which
+// takes three to five times as long on prompts (figures in kvq_rotary.cu).
 enum RotateKind { kInterleaved, kHalves, kSingle };
 inline __host__ __device__ bool rotate_aligned(int rot, int interleaved) {
   return rot % (interleaved ? 8 : 16) == 0;
