@@ -30,10 +30,10 @@
 // (about 1900 cycles) and the hand-overs to it and back lie between its scores
 // and its output product, and only one other row tile's products fit beside
 // them: about 3300 cycles a key tile, the tensor pipe 59 % active.  Measured: 2048
-// new tokens behind 32768 (32 heads, D = 128) 943 us, 1.20 PFLOP/s, 62 % of the
+// new tokens behind 32768 (32 heads, D = 128) 946 us, 1.20 PFLOP/s, 62 % of the
 // measured bf16 rate (two rounds of CTAs over 152 SMs: 84 % of a full one);
 // without the softmax 805 us, without the conversion 885 us, without either
-// 756 us.  Three prompts of up to 4001 tokens (40 heads) 254 us, where the
+// 756 us.  Three prompts of up to 4001 tokens (40 heads) 257 us, where the
 // causal half and 9 us a CTA of start and end weigh more.  Lanes that wait by a
 // vote, so that the compiler knows a warp as converged, took 956 -> 943 and
 // 262 -> 254 us.
@@ -50,7 +50,7 @@
 // 4-bit pages (Q4): the converters turn codes and metadata into the same fp16 tiles
 // (a thread a row: eight lanes read and write on different banks), three raw tiles
 // of 10 KB are in flight, and the rest is the same.  2048 new tokens behind 32768
-// 976 us, 1.16 PFLOP/s: the converters' 1.7 instructions a value instead of 0.6
+// 987 us, 1.15 PFLOP/s: the converters' 1.7 instructions a value instead of 0.6
 // share the issue slots with the softmax.
 #pragma once
 

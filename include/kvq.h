@@ -691,8 +691,9 @@ KVQ_API uint64_t kvq_launch_count(void);
  *   records the error without writing `out`; limit < 0 restores the normal
  *   limit.  Applies to launches enqueued afterwards.
  * kvq_debug_set_paged_wait_limit: the same for the main-loop waits of
- *   kvq_paged_attention and kvq_paged4_attention, which then set KVQ_PAGED_ERR_WAIT and leave `out`
- *   incomplete (rows may be written).  Process-wide. */
+ *   kvq_paged_attention and kvq_paged4_attention, which then set
+ *   KVQ_PAGED_ERR_WAIT and leave `out` incomplete (rows may be written).
+ *   Process-wide. */
 KVQ_API kvq_status kvq_debug_fail_allocations(int after, int n);
 KVQ_API kvq_status kvq_debug_set_device_error(kvq_cache* cache, int value);
 KVQ_API kvq_status kvq_debug_set_wait_limit(kvq_cache* cache, int limit);
