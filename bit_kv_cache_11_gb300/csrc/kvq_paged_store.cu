@@ -253,7 +253,7 @@ __device__ __forceinline__ void store_run(const PagedStoreParams& p, int t, int 
     if (was != now && was > 0.f) {
       const float f = was / now;
       for (int i = sub; i < row0; i += RPS) {
-        uint2* c = reinterpret_cast<uint2*>(base + i * D);
+        uint2* c = reinterpret_cast<uint2*>(base + static_cast<size_t>(i) * D);
         *c = rescale8(*c, f);
       }
     }
@@ -454,7 +454,7 @@ __global__ void __launch_bounds__(chunk_threads<TEAM>(), (ROT ? 768 : 1024) / ch
         if (was[side] != now && was[side] > 0.f) {
           const float f = was[side] / now;
           for (int i = sub; i < row0; i += RPS) {
-            uint2* c = reinterpret_cast<uint2*>(base + i * D);
+            uint2* c = reinterpret_cast<uint2*>(base + static_cast<size_t>(i) * D);
             *c = rescale8(*c, f);
           }
         }
